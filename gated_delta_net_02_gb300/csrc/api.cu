@@ -7,31 +7,18 @@
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
-#include <string>
 #include <vector>
 
+#include "api_util.h"
 #include "common.cuh"
 #include "gdn.h"
 #include "kernels.h"
 
 namespace {
 
-thread_local std::string g_msg;
-
-__attribute__((format(printf, 2, 3))) gdn_status fail(gdn_status st, const char *fmt, ...);
-gdn_status fail(gdn_status st, const char *fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_msg = buf;
-  return st;
-}
+thread_local char g_msg[512];
 
 gdn_status ok() { return GDN_OK; }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool head_size_ok(int d) { return d == 64 || d == 128; }
 
@@ -45,6 +32,19 @@ namespace {
 constexpr int kMaxDevices = 64;
 std::mutex g_err_mu;
 int *g_err_ptr[kMaxDevices] = {};
+
+}  // namespace
+
+namespace gdn {
+namespace api {
+
+gdn_status fail(gdn_status st, const char *fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
+  va_end(ap);
+  return st;
+}
 
 // Device address of the current device's error word, looked up once per
 // device with that device current.
@@ -74,11 +74,14 @@ gdn_status check_launch(cudaError_t e, const char *what) {
   return GDN_OK;
 }
 
-}  // namespace
+}  // namespace api
+}  // namespace gdn
+
+using namespace gdn::api;
 
 extern "C" {
 
-const char *gdn_last_error(void) { return g_msg.c_str(); }
+const char *gdn_last_error(void) { return g_msg; }
 
 const char *gdn_version(void) { return "libgdn 0.2.0 (sm_103a)"; }
 
@@ -297,11 +300,6 @@ gdn_status gdn_forward_chunked(const gdn_varlen_shape *shape,
                       workspace_bytes, stream);
 }
 
-static bool ranges_overlap(const void *a, size_t na, const void *b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-
 gdn_status gdn_forward_chunked_checkpointed(
     const gdn_varlen_shape *shape, const int32_t *cu_seqlens, const void *q, const void *k,
     const void *v, const float *g, const float *beta, const float *const *state_in,
@@ -505,6 +503,13 @@ gdn_status gdn_decode_device_error(int word) {
       return fail(GDN_ERR_DEVICE_ARG, "cu_seqlens is not a valid offset table");
     case gdn::kDevOverlap:
       return fail(GDN_ERR_DEVICE_ARG, "a state_in pointer points into state_slots");
+    case gdn::kDevBadSlot:
+      return fail(GDN_ERR_DEVICE_ARG, "a slot index is beyond the cache's pages (that token's "
+                                      "k and v were not written)");
+    case gdn::kDevBadPage:
+      return fail(GDN_ERR_DEVICE_ARG, "a page table entry is not a page of the cache, or a "
+                                      "sequence is longer than its page table (its missing "
+                                      "keys were left out)");
     case gdn::kDevGateRange:
       return fail(GDN_ERR_DEVICE_ARG,
                   "a gate decays (or grows) by more than e^80 inside one 64-token chunk, or "

@@ -16,6 +16,8 @@ enum DevErr : int {
   kDevBadSeqlens = 2,  // cu_seqlens is not a valid offset table
   kDevOverlap = 3,     // a state_in pointer points into the slot buffer
   kDevGateRange = 4,   // a chunk's cumulative log-gate leaves [-80, 80] (chunked path)
+  kDevBadSlot = 5,     // a slot index beyond the key-value cache
+  kDevBadPage = 6,     // a page table entry or a length beyond the key-value cache
 };
 
 // Where a bounded wait ran out: bits 8..15 of a timeout error word. The host

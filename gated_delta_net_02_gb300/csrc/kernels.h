@@ -78,4 +78,16 @@ cudaError_t launch_chunked(const ChunkedArgs &a, cudaStream_t stream);
 size_t static_scratch_bytes();
 cudaError_t launch_chunked_static(ChunkedArgs a, cudaStream_t stream, size_t *need);
 
+// RMS norm with residual and an e4m3 output; see norm_fp8.cu.
+struct NormArgs {
+  const void *x, *residual, *weight;  // [rows][cols], same, [cols]; the last two may be NULL
+  void *residual_out, *out;           // [rows][cols] or NULL
+  unsigned char *out_fp8;             // [rows][cols] or NULL, with
+  float *out_scale;                   // [rows][ceil(cols / 128)]
+  int rows, cols;
+  bool bf16, normalize;
+  float eps, weight_offset;
+};
+cudaError_t launch_norm_fp8(const NormArgs &a, cudaStream_t stream);
+
 }  // namespace gdn

@@ -54,6 +54,12 @@ class gdn_varlen_shape(ctypes.Structure):
                 ("H_qk", ctypes.c_int), ("qk_map", ctypes.c_int)]
 
 
+class gdn_norm_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("cols", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("normalize", ctypes.c_int), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libgdn.so is not built ({LIB_PATH}); run "
                       "gated_delta_net_02_gb300/build.py or __graft_entry__.build()")
@@ -88,6 +94,9 @@ lib.gdn_checkpoint_select.argtypes = [_i, _i, _i, _i, _i, ctypes.POINTER(_i),
                                       ctypes.POINTER(_i), ctypes.POINTER(_i)]
 lib.gdn_noalloc_scratch_bytes.restype = ctypes.c_size_t
 lib.gdn_noalloc_scratch_bytes.argtypes = []
+lib.gdn_rmsnorm_fp8.restype = _st
+lib.gdn_rmsnorm_fp8.argtypes = [ctypes.POINTER(gdn_norm_shape), _vp, _vp, _vp, _vp, _vp, _vp,
+                                _vp, _vp]
 lib.gdn_seq_table_create.restype = _st
 lib.gdn_seq_table_create.argtypes = [_i, _i, ctypes.POINTER(_vp)]
 lib.gdn_seq_table_destroy.restype = None
@@ -214,6 +223,15 @@ def gdn_checkpoint_select(n_keep: int, L: int, n_slots: int, ckpt_every: int,
 
 def gdn_noalloc_scratch_bytes() -> int:
     return int(lib.gdn_noalloc_scratch_bytes())
+
+
+def gdn_rmsnorm_fp8(shape: gdn_norm_shape, x, residual, weight, residual_out, out, out_fp8,
+                    out_scale, stream=None) -> None:
+    """residual, weight, residual_out and out may be None, and out_fp8 with
+    out_scale when out is given. out_fp8: a float8_e4m3fn (or uint8) tensor."""
+    _check(lib.gdn_rmsnorm_fp8(ctypes.byref(shape), _addr(x), _addr(residual), _addr(weight),
+                               _addr(residual_out), _addr(out), _addr(out_fp8),
+                               _addr(out_scale), _stream(stream)))
 
 
 def gdn_check_device_error(stream=None) -> None:

@@ -286,6 +286,50 @@ gdn_status gdn_checkpoint_select(int n_keep, int L, int n_slots, int ckpt_every,
                                  int *replay_from);
 
 /* ------------------------------------------------------------------------
+ * The attention layer between the recurrent ones. A hybrid model runs full
+ * attention every few layers, and a norm and projections around every layer;
+ * the calls below are that layer's work for the two shapes gdn_forward serves
+ * (T = 1 and T = draft_max + 1). "Every buffer" conventions above hold:
+ * dense unless a stride is given, 16-byte aligned, nothing allocated, no
+ * synchronisation. Each kernel is a programmatic dependent launch like
+ * gdn_forward's: stream order holds as usual.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Root-mean-square norm with the residual's addition and an 8-bit output.
+ * Per row (all arithmetic and sums in fp32):
+ *   h = x + residual                      (residual NULL: h = x)
+ *   y = h / sqrt(mean(h^2) + eps) * (weight_offset + weight)
+ *                                         (weight NULL: without that factor;
+ *                                          normalize = 0: y = h)
+ *   scale[b] = max(max |y| over columns [128 b, 128 b + 128) / 448, 2^-100)
+ *   fp8      = y / scale[b], rounded to e4m3 (to nearest even, saturating)
+ * so y is about fp8 * scale. NaNs take no part in the maximum and stay NaN.
+ */
+typedef struct {
+  int rows, cols;      /* rows >= 0, cols >= 1 */
+  gdn_dtype dtype;     /* of x, residual, weight, residual_out and out */
+  int normalize;       /* 1: as above; 0: y = h (a plain quantiser) */
+  float eps;           /* finite, >= 0 */
+  float weight_offset; /* 0, or 1 for weights stored around zero */
+} gdn_norm_shape;
+
+/*
+ * x, residual   device [rows][cols] dtype (residual may be NULL)
+ * weight        device [cols] dtype (may be NULL; must be with normalize = 0)
+ * residual_out  device [rows][cols] dtype, receives h; may be NULL
+ * out           device [rows][cols] dtype, receives y; may be NULL
+ * out_fp8       device e4m3 [rows][cols], one byte each
+ * out_scale     device fp32 [rows][ceil(cols / 128)]
+ *               (both NULL when only `out` is wanted, never one alone)
+ * residual_out and out may each be x or residual itself (in place); any
+ * other overlap of an output with another buffer is refused.
+ */
+gdn_status gdn_rmsnorm_fp8(const gdn_norm_shape *shape, const void *x, const void *residual,
+                           const void *weight, void *residual_out, void *out, void *out_fp8,
+                           float *out_scale, gdn_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Rollback bookkeeping: a host-side table with one entry per sequence (the
  * recurrent memory's per-sequence record of which stored state is live,
  * "llama-memory-recurrent: clear rs_idx in clear", koboldcpp commits, tag
