@@ -33,6 +33,62 @@ gdn_status check_apart(const char *fn, const Buf &out, const Buf &b) {
 
 bool dtype_ok(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
 
+// Checks a cache layout and resolves its strides; *bytes is the extent of
+// each of its two buffers.
+gdn_status kv_layout(const char *fn, const gdn_kv_cache *cache, gdn::KvLayout *l, size_t *bytes) {
+  if (!cache) return fail(GDN_ERR_INVALID_ARG, "%s: cache is NULL", fn);
+  const gdn_kv_cache &c = *cache;
+  if (c.n_pages < 0 || c.page_size < 1 || c.H_kv < 1)
+    return fail(GDN_ERR_INVALID_ARG, "%s: n_pages=%d page_size=%d H_kv=%d", fn, c.n_pages,
+                c.page_size, c.H_kv);
+  if (!dtype_ok(c.dtype))
+    return fail(GDN_ERR_INVALID_ARG, "%s: cache dtype %d", fn, (int)c.dtype);
+  if (c.D != 64 && c.D != 128 && c.D != 256)
+    return fail(c.D < 1 ? GDN_ERR_INVALID_ARG : GDN_ERR_UNSUPPORTED,
+                "%s: head size D=%d (supported: 64, 128, 256)", fn, c.D);
+  if (c.H_kv > (1 << 20))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: H_kv=%d is above 2^20", fn, c.H_kv);
+  const long long most = 1LL << 60;
+  long long ps = c.page_stride, ts = c.token_stride, hs = c.head_stride;
+  if (!ps && !ts && !hs) {
+    hs = c.D;
+    ts = (long long)c.H_kv * c.D;
+    ps = ts * c.page_size;
+    if (c.n_pages && ps > most / c.n_pages)
+      return fail(GDN_ERR_UNSUPPORTED, "%s: the cache is too large", fn);
+  } else {
+    const long long m = c.dtype == GDN_BF16 ? 8 : 4;
+    if (ps <= 0 || ts <= 0 || hs <= 0 || ps % m || ts % m || hs % m)
+      return fail(GDN_ERR_INVALID_ARG,
+                  "%s: cache strides %lld, %lld, %lld (need positive multiples of 16 bytes)", fn,
+                  ps, ts, hs);
+    if (ps > most / (c.n_pages + 1LL) || ts > most / c.page_size || hs > most / c.H_kv)
+      return fail(GDN_ERR_UNSUPPORTED, "%s: the cache is too large", fn);
+    // each (page, token, head) has D elements of its own: true when, in the
+    // order of their strides, each level steps over all of the level below
+    struct { long long stride, n; } lv[3] = {{ps, c.n_pages}, {ts, c.page_size}, {hs, c.H_kv}};
+    for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < 2 - i; ++j)
+        if (lv[j].stride > lv[j + 1].stride) {
+          const auto t = lv[j];
+          lv[j] = lv[j + 1];
+          lv[j + 1] = t;
+        }
+    long long span = c.D;
+    for (int i = 0; i < 3; ++i) {
+      if (lv[i].n > 1 && lv[i].stride < span)
+        return fail(GDN_ERR_INVALID_ARG, "%s: the cache's strides make its rows overlap", fn);
+      if (lv[i].n > 1) span += (lv[i].n - 1) * lv[i].stride;
+    }
+  }
+  *l = gdn::KvLayout{c.n_pages, c.page_size, c.H_kv, c.D, c.dtype == GDN_BF16, ps, ts, hs};
+  const size_t e = c.dtype == GDN_BF16 ? 2 : 4;
+  *bytes = c.n_pages == 0 ? 0
+                          : e * (size_t)((c.n_pages - 1) * ps + (c.page_size - 1) * ts +
+                                         (c.H_kv - 1) * hs + c.D);
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -92,6 +148,95 @@ gdn_status gdn_rmsnorm_fp8(const gdn_norm_shape *shape, const void *x, const voi
   a.eps = s.eps; a.weight_offset = s.weight_offset;
   return check_launch(gdn::launch_norm_fp8(a, reinterpret_cast<cudaStream_t>(stream)),
                       "gdn_rmsnorm_fp8 launch");
+}
+
+gdn_status gdn_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cache, const void *q,
+                           const void *k, const void *v, const int32_t *positions,
+                           const float *inv_freq, const int64_t *slots, void *q_out,
+                           void *k_cache, void *v_cache, gdn_stream_t stream) {
+  const char *fn = "gdn_rope_append";
+  if (!shape) return fail(GDN_ERR_INVALID_ARG, "%s: shape is NULL", fn);
+  const gdn_rope_shape &s = *shape;
+  gdn::RopeArgs a{};
+  size_t cache_bytes = 0;
+  gdn_status st = kv_layout(fn, cache, &a.cache, &cache_bytes);
+  if (st != GDN_OK) return st;
+  const int D = a.cache.D, H_kv = a.cache.H_kv;
+  if (s.n_tokens < 0 || s.H < 1)
+    return fail(GDN_ERR_INVALID_ARG, "%s: n_tokens=%d H=%d", fn, s.n_tokens, s.H);
+  if (s.H > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "%s: H=%d is above 2^20", fn, s.H);
+  if (s.rot_dim < 0 || s.rot_dim > D || (s.rot_dim & 1))
+    return fail(GDN_ERR_INVALID_ARG, "%s: rot_dim=%d (need even, 0 to D=%d)", fn, s.rot_dim, D);
+  if (s.pairs != GDN_ROPE_HALVES && s.pairs != GDN_ROPE_NEIGHBOURS)
+    return fail(GDN_ERR_INVALID_ARG, "%s: pairs %d", fn, (int)s.pairs);
+  if (s.axes != GDN_ROPE_AXES_SECTIONED && s.axes != GDN_ROPE_AXES_INTERLEAVED)
+    return fail(GDN_ERR_INVALID_ARG, "%s: axes %d", fn, (int)s.axes);
+  if (s.n_axes < 1 || s.n_axes > 4)
+    return fail(GDN_ERR_INVALID_ARG, "%s: n_axes=%d (need 1 to 4)", fn, s.n_axes);
+  const int half = s.rot_dim / 2;
+  int left = half;
+  for (int i = 0; i < s.n_axes; ++i) {
+    if (s.section[i] < 0 || s.section[i] > left)
+      return fail(GDN_ERR_INVALID_ARG, "%s: the sections do not sum to rot_dim / 2 = %d", fn, half);
+    // taking turns, axis i > 0 has the frequencies i, i + n_axes, ... below half
+    if (s.axes == GDN_ROPE_AXES_INTERLEAVED && i > 0 &&
+        s.section[i] > (half - i + s.n_axes - 1) / s.n_axes)
+      return fail(GDN_ERR_INVALID_ARG, "%s: section[%d]=%d is more than the axis's turns", fn, i,
+                  s.section[i]);
+    left -= s.section[i];
+  }
+  if (left)
+    return fail(GDN_ERR_INVALID_ARG, "%s: the sections do not sum to rot_dim / 2 = %d", fn, half);
+  const long long m = a.cache.bf16 ? 8 : 4;
+  const long long dense[3] = {(long long)s.H * D, (long long)H_kv * D, (long long)H_kv * D};
+  long long stride[3] = {s.q_stride, s.k_stride, s.v_stride};
+  const char *names[3] = {"q_stride", "k_stride", "v_stride"};
+  for (int i = 0; i < 3; ++i) {
+    if (stride[i] == 0) stride[i] = dense[i];
+    if (stride[i] < dense[i] || stride[i] % m || stride[i] > (1LL << 28))
+      return fail(GDN_ERR_INVALID_ARG,
+                  "%s: %s=%lld (need a multiple of 16 bytes from %lld to 2^28)", fn, names[i],
+                  stride[i], dense[i]);
+  }
+  if (s.n_tokens == 0) return GDN_OK;
+  const size_t e = a.cache.bf16 ? 2 : 4, n = (size_t)s.n_tokens;
+  const Buf in[] = {{"q", q, e * ((n - 1) * (size_t)stride[0] + (size_t)dense[0])},
+                    {"k", k, e * ((n - 1) * (size_t)stride[1] + (size_t)dense[1])},
+                    {"v", v, e * ((n - 1) * (size_t)stride[2] + (size_t)dense[2])},
+                    {"positions", positions, 4 * n * s.n_axes},
+                    {"slots", slots, 8 * n},
+                    {"inv_freq", inv_freq, 4 * (size_t)half}};
+  const Buf outs[] = {{"q_out", q_out, e * n * (size_t)dense[0]},
+                      {"k_cache", k_cache, cache_bytes},
+                      {"v_cache", v_cache, cache_bytes}};
+  for (const Buf &b : in) {
+    if (!b.p && !(b.p == inv_freq && half == 0))
+      return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, b.name);
+    if ((st = check_aligned(fn, b)) != GDN_OK) return st;
+  }
+  for (int i = 0; i < 3; ++i) {
+    if (!outs[i].p) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, outs[i].name);
+    if ((st = check_aligned(fn, outs[i])) != GDN_OK) return st;
+    for (const Buf &b : in)
+      if ((st = check_apart(fn, outs[i], b)) != GDN_OK) return st;
+  }
+  // one buffer may hold both caches interleaved (strides twice as long), so
+  // the two are compared only where they would be the same rows
+  if (k_cache == v_cache)
+    return fail(GDN_ERR_INVALID_ARG, "%s: k_cache and v_cache are the same", fn);
+  for (int i = 1; i < 3; ++i)
+    if ((st = check_apart(fn, outs[0], outs[i])) != GDN_OK) return st;
+  if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;
+  a.q = q; a.k = k; a.v = v;
+  a.q_stride = stride[0]; a.k_stride = stride[1]; a.v_stride = stride[2];
+  a.positions = positions; a.inv_freq = inv_freq; a.slots = slots;
+  a.q_out = q_out; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.n_tokens = s.n_tokens; a.H = s.H; a.rot_dim = s.rot_dim; a.n_axes = s.n_axes;
+  for (int i = 0; i < 4; ++i) a.section[i] = i < s.n_axes ? s.section[i] : 0;
+  a.neighbours = s.pairs == GDN_ROPE_NEIGHBOURS;
+  a.interleaved = s.axes == GDN_ROPE_AXES_INTERLEAVED;
+  return check_launch(gdn::launch_rope_append(a, reinterpret_cast<cudaStream_t>(stream)),
+                      "gdn_rope_append launch");
 }
 
 }  // extern "C"

@@ -90,4 +90,27 @@ struct NormArgs {
 };
 cudaError_t launch_norm_fp8(const NormArgs &a, cudaStream_t stream);
 
+// Paged key-value cache layout (strides in elements, resolved).
+struct KvLayout {
+  int n_pages, page_size, H_kv, D;
+  bool bf16;
+  long long page_stride, token_stride, head_stride;
+};
+
+// Rotary positions and the cache append; see rope_append.cu.
+struct RopeArgs {
+  KvLayout cache;
+  const void *q, *k, *v;
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t *positions;                // [n_axes][n_tokens]
+  const float *inv_freq;                   // [rot_dim / 2]
+  const int64_t *slots;                    // [n_tokens]
+  void *q_out, *k_cache, *v_cache;
+  int n_tokens, H, rot_dim, n_axes;
+  int section[4];
+  bool neighbours, interleaved;            // pairs (2i, 2i+1); axes taking turns
+  int *err;
+};
+cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t stream);
+
 }  // namespace gdn

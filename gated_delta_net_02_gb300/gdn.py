@@ -60,6 +60,27 @@ class gdn_norm_shape(ctypes.Structure):
                 ("weight_offset", ctypes.c_float)]
 
 
+GDN_ROPE_HALVES, GDN_ROPE_NEIGHBOURS = 0, 1
+GDN_ROPE_AXES_SECTIONED, GDN_ROPE_AXES_INTERLEAVED = 0, 1
+c_int = ctypes.c_int    # (c_int * 4)(...) builds gdn_rope_shape's sections
+
+
+class gdn_kv_cache(ctypes.Structure):
+    # all three strides 0 (the default) means dense [n_pages][page_size][H_kv][D]
+    _fields_ = [("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("H_kv", ctypes.c_int), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("page_stride", ctypes.c_longlong), ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong)]
+
+
+class gdn_rope_shape(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int), ("H", ctypes.c_int), ("rot_dim", ctypes.c_int),
+                ("pairs", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("section", ctypes.c_int * 4), ("axes", ctypes.c_int),
+                ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+                ("v_stride", ctypes.c_longlong)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libgdn.so is not built ({LIB_PATH}); run "
                       "gated_delta_net_02_gb300/build.py or __graft_entry__.build()")
@@ -97,6 +118,9 @@ lib.gdn_noalloc_scratch_bytes.argtypes = []
 lib.gdn_rmsnorm_fp8.restype = _st
 lib.gdn_rmsnorm_fp8.argtypes = [ctypes.POINTER(gdn_norm_shape), _vp, _vp, _vp, _vp, _vp, _vp,
                                 _vp, _vp]
+lib.gdn_rope_append.restype = _st
+lib.gdn_rope_append.argtypes = [ctypes.POINTER(gdn_rope_shape), ctypes.POINTER(gdn_kv_cache),
+                                _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
 lib.gdn_seq_table_create.restype = _st
 lib.gdn_seq_table_create.argtypes = [_i, _i, ctypes.POINTER(_vp)]
 lib.gdn_seq_table_destroy.restype = None
@@ -127,6 +151,26 @@ def _addr(x):
         return x
     if not x.is_contiguous():
         raise ValueError("gdn: tensor arguments must be contiguous (packed row-major)")
+    return x.data_ptr()
+
+
+def _rows_addr(x, stride, width):
+    """Device address of rows [n][heads][D] that lie `stride` elements apart
+    (0 = dense): a column range of a wider matrix is such a view."""
+    if x is None or isinstance(x, int):
+        return x
+    st = x.stride()
+    if x.shape[0] > 1 and st[0] != (stride or width) or st[2] != 1 or st[1] != x.shape[2]:
+        raise ValueError("gdn: rows must be packed, and apart by the shape's stride")
+    return x.data_ptr()
+
+
+def _cache_addr(x, cache):
+    """Device address of a cache tensor; a strided one must say so in `cache`."""
+    if x is None or isinstance(x, int):
+        return x
+    if not (cache.token_stride or x.is_contiguous()):
+        raise ValueError("gdn: a strided cache needs its strides in gdn_kv_cache")
     return x.data_ptr()
 
 
@@ -232,6 +276,19 @@ def gdn_rmsnorm_fp8(shape: gdn_norm_shape, x, residual, weight, residual_out, ou
     _check(lib.gdn_rmsnorm_fp8(ctypes.byref(shape), _addr(x), _addr(residual), _addr(weight),
                                _addr(residual_out), _addr(out), _addr(out_fp8),
                                _addr(out_scale), _stream(stream)))
+
+
+def gdn_rope_append(shape: gdn_rope_shape, cache: gdn_kv_cache, q, k, v, positions, inv_freq,
+                    slots, q_out, k_cache, v_cache, stream=None) -> None:
+    """q, k and v may be column ranges of one wider matrix (the shape's
+    strides); k_cache and v_cache have the layout of `cache`."""
+    kv = cache.H_kv * cache.D
+    _check(lib.gdn_rope_append(
+        ctypes.byref(shape), ctypes.byref(cache),
+        _rows_addr(q, shape.q_stride, shape.H * cache.D), _rows_addr(k, shape.k_stride, kv),
+        _rows_addr(v, shape.v_stride, kv), _addr(positions), _addr(inv_freq), _addr(slots),
+        _addr(q_out), _cache_addr(k_cache, cache), _cache_addr(v_cache, cache),
+        _stream(stream)))
 
 
 def gdn_check_device_error(stream=None) -> None:

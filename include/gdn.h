@@ -329,6 +329,67 @@ gdn_status gdn_rmsnorm_fp8(const gdn_norm_shape *shape, const void *x, const voi
                            const void *weight, void *residual_out, void *out, void *out_fp8,
                            float *out_scale, gdn_stream_t stream);
 
+/* A key-value cache in pages: token j of a page's page_size tokens, head h:
+ *   element p * page_stride + j * token_stride + h * head_stride + d
+ * of the k (or v) buffer, for page p. Strides are in elements and multiples
+ * of 16 bytes; all three 0 means dense [n_pages][page_size][H_kv][D]. The k
+ * and the v buffer share one layout. */
+typedef struct {
+  int n_pages, page_size; /* >= 0, >= 1 */
+  int H_kv;               /* key-value heads */
+  int D;                  /* head size: 64, 128 or 256 */
+  gdn_dtype dtype;        /* of the cache, and of q, k, v and out with it */
+  long long page_stride, token_stride, head_stride;
+} gdn_kv_cache;
+
+/* Which elements of a head form the pairs that are rotated: (i, i + rot/2),
+ * or the neighbours (2i, 2i + 1). */
+typedef enum { GDN_ROPE_HALVES = 0, GDN_ROPE_NEIGHBOURS = 1 } gdn_rope_pairs;
+
+/* Which axis turns frequency i of rot_dim/2, with n_i = section[] frequencies
+ * for each axis: one run for each axis in turn, or the axes taking turns
+ * (axis a = i % n_axes while i / n_axes < section[a], axis 0 otherwise). */
+typedef enum { GDN_ROPE_AXES_SECTIONED = 0, GDN_ROPE_AXES_INTERLEAVED = 1 } gdn_rope_axes;
+
+/*
+ * Rotary positions with several axes (time, height, width), and the cache
+ * append. For token t, pair i of the first rot_dim elements of every q and k
+ * head turns by the angle positions[axis(i)][t] * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, a sin + b cos)
+ * and the other elements pass unchanged. The angle is reduced to one turn
+ * beyond fp32 (error below 2e-6 for positions up to 2^24, in proportion to
+ * the position beyond), so long positions lose nothing. The rotated q goes to q_out; the rotated k and v go to slot
+ * slots[t] of the cache (page slot / page_size, token slot % page_size).
+ * A negative slot (padding) writes no cache entry; one beyond the cache is
+ * skipped and reported as GDN_ERR_DEVICE_ARG by gdn_check_device_error. Of
+ * two tokens with one slot, either may stay.
+ */
+typedef struct {
+  int n_tokens;             /* >= 0 */
+  int H;                    /* query heads (the cache has the key-value heads) */
+  int rot_dim;              /* even, 0 .. D */
+  gdn_rope_pairs pairs;
+  int n_axes;               /* 1 .. 4 */
+  int section[4];           /* frequencies of each axis; they sum to rot_dim / 2 */
+  gdn_rope_axes axes;
+  long long q_stride, k_stride, v_stride; /* elements between tokens, multiples of 16
+                                             bytes; 0 = dense (heads * D) */
+} gdn_rope_shape;
+
+/*
+ * q          device [n_tokens] rows of [H][D], q_stride apart (k, v: [H_kv][D]),
+ *            for example column ranges of one projection's output
+ * positions  device int32 [n_axes][n_tokens]
+ * inv_freq   device fp32 [rot_dim / 2]
+ * slots      device int64 [n_tokens]
+ * q_out      device [n_tokens][H][D]; overlaps no other buffer
+ * k_cache, v_cache  device buffers of the layout `cache`
+ */
+gdn_status gdn_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cache, const void *q,
+                           const void *k, const void *v, const int32_t *positions,
+                           const float *inv_freq, const int64_t *slots, void *q_out,
+                           void *k_cache, void *v_cache, gdn_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Rollback bookkeeping: a host-side table with one entry per sequence (the
  * recurrent memory's per-sequence record of which stored state is live,

@@ -56,3 +56,65 @@ def test_norm_refuses_buffers(gdn, ptrs, word):
 def test_norm_of_no_rows(gdn):
     norm(gdn, dict(rows=0), x=0)
     assert gdn.lib.gdn_rmsnorm_fp8(None, *[0] * 8) == gdn.GDN_ERR_INVALID_ARG
+
+
+def kv(gdn, **kw):
+    c = dict(n_pages=10, page_size=16, H_kv=2, D=128, dtype=gdn.GDN_BF16, page_stride=0,
+             token_stride=0, head_stride=0)
+    c.update(kw)
+    return gdn.gdn_kv_cache(*(c[f[0]] for f in gdn.gdn_kv_cache._fields_))
+
+
+BAD_CACHES = [
+    (dict(n_pages=-1), 1), (dict(page_size=0), 1), (dict(H_kv=0), 1), (dict(dtype=5), 1),
+    (dict(D=0), 1), (dict(D=96), 2), (dict(D=512), 2),
+    (dict(page_stride=4096), 1), (dict(page_stride=4096, token_stride=256, head_stride=129), 1),
+    (dict(page_stride=4096, token_stride=256, head_stride=120), 1),   # heads overlap
+    (dict(page_stride=4088, token_stride=256, head_stride=128), 1),   # pages overlap
+    (dict(page_stride=1 << 59, token_stride=256, head_stride=128), 2)]
+
+
+def rope(gdn, shape=None, cache=None, **kw):
+    sh = dict(n_tokens=5, H=4, rot_dim=128, pairs=0, n_axes=3, section=(32, 16, 16), axes=0,
+              q_stride=0, k_stride=0, v_stride=0)
+    sh.update(shape or {})
+    sh["section"] = (ctypes.c_int * 4)(*sh["section"])
+    p = {n: FAKE + i * STEP for i, n in enumerate(
+        ("q", "k", "v", "positions", "inv_freq", "slots", "q_out", "k_cache", "v_cache"))}
+    p.update(kw)
+    gdn.gdn_rope_append(gdn.gdn_rope_shape(*(sh[f[0]] for f in gdn.gdn_rope_shape._fields_)),
+                        kv(gdn, **(cache or {})), *p.values())
+
+
+@pytest.mark.parametrize("cache,status", BAD_CACHES)
+def test_rope_refuses_caches(gdn, cache, status):
+    st, msg = refused(gdn, lambda: rope(gdn, cache=cache))
+    assert st == status and "gdn_rope_append" in msg
+
+
+@pytest.mark.parametrize("shape", [
+    dict(n_tokens=-1), dict(H=0), dict(rot_dim=127), dict(rot_dim=130), dict(rot_dim=-2),
+    dict(pairs=2), dict(axes=2), dict(n_axes=0), dict(n_axes=5), dict(section=(32, 16, 15)),
+    dict(section=(65, 0, 0)), dict(section=(65, -1, 0)), dict(axes=1, section=(10, 22, 32)),
+    dict(q_stride=512 - 8), dict(k_stride=260), dict(v_stride=(1 << 28) + 8)])
+def test_rope_refuses_shapes(gdn, shape):
+    st, msg = refused(gdn, lambda: rope(gdn, shape))
+    assert st == gdn.GDN_ERR_INVALID_ARG and "gdn_rope_append" in msg
+
+
+@pytest.mark.parametrize("ptrs,word", [
+    (dict(q=0), "q is NULL"), (dict(v_cache=0), "v_cache is NULL"),
+    (dict(inv_freq=0), "inv_freq is NULL"), (dict(slots=FAKE + 8), "slots is not 16-byte"),
+    (dict(q_out=FAKE), "q_out overlaps q"), (dict(k_cache=FAKE + STEP), "k_cache overlaps k"),
+    (dict(v_cache=FAKE + 7 * STEP), "are the same"),
+    (dict(q_out=FAKE + 8 * STEP), "q_out overlaps v_cache")])
+def test_rope_refuses_buffers(gdn, ptrs, word):
+    st, msg = refused(gdn, lambda: rope(gdn, **ptrs))
+    assert st == gdn.GDN_ERR_INVALID_ARG and word in msg
+
+
+def test_rope_of_no_tokens_and_null_structs(gdn):
+    rope(gdn, dict(n_tokens=0), q=0)
+    assert gdn.lib.gdn_rope_append(None, None, *[0] * 10) == gdn.GDN_ERR_INVALID_ARG
+    assert gdn.lib.gdn_rope_append(ctypes.byref(gdn.gdn_rope_shape()), None,
+                                   *[0] * 10) == gdn.GDN_ERR_INVALID_ARG
