@@ -508,8 +508,7 @@ gdn_status gdn_decode_device_error(int word) {
                                       "k and v were not written)");
     case gdn::kDevBadPage:
       return fail(GDN_ERR_DEVICE_ARG, "a page table entry is not a page of the cache, or a "
-                                      "sequence is longer than its page table (its missing "
-                                      "keys were left out)");
+                                      "sequence is longer than its page table");
     case gdn::kDevGateRange:
       return fail(GDN_ERR_DEVICE_ARG,
                   "a gate decays (or grows) by more than e^80 inside one 64-token chunk, or "

@@ -89,6 +89,27 @@ gdn_status kv_layout(const char *fn, const gdn_kv_cache *cache, gdn::KvLayout *l
   return GDN_OK;
 }
 
+// Checks the sizes of an attention call; cache layout as kv_layout.
+gdn_status attn_shape(const char *fn, const gdn_attn_shape *shape, const gdn_kv_cache *cache,
+                      gdn::KvLayout *l, size_t *cache_bytes) {
+  if (!shape) return fail(GDN_ERR_INVALID_ARG, "%s: shape is NULL", fn);
+  const gdn_attn_shape &s = *shape;
+  const gdn_status st = kv_layout(fn, cache, l, cache_bytes);
+  if (st != GDN_OK) return st;
+  if (s.n_seqs < 0 || s.T < 0 || s.H < 1 || s.max_pages < 0)
+    return fail(GDN_ERR_INVALID_ARG, "%s: n_seqs=%d T=%d H=%d max_pages=%d", fn, s.n_seqs, s.T,
+                s.H, s.max_pages);
+  if (s.H % l->H_kv != 0)
+    return fail(GDN_ERR_INVALID_ARG, "%s: H_kv=%d must divide H=%d", fn, l->H_kv, s.H);
+  if (s.kv_map != GDN_QK_TILED && s.kv_map != GDN_QK_GROUPED)
+    return fail(GDN_ERR_INVALID_ARG, "%s: kv_map %d", fn, (int)s.kv_map);
+  if (!std::isfinite(s.scale)) return fail(GDN_ERR_INVALID_ARG, "%s: scale is not finite", fn);
+  if ((long long)s.n_seqs * s.T > (1LL << 30) / s.H)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: %d x %d tokens x %d heads too large", fn, s.n_seqs, s.T,
+                s.H);
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -237,6 +258,62 @@ gdn_status gdn_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cach
   a.interleaved = s.axes == GDN_ROPE_AXES_INTERLEAVED;
   return check_launch(gdn::launch_rope_append(a, reinterpret_cast<cudaStream_t>(stream)),
                       "gdn_rope_append launch");
+}
+
+size_t gdn_paged_attention_workspace_size(const gdn_attn_shape *shape, const gdn_kv_cache *cache) {
+  gdn::KvLayout l;
+  size_t cache_bytes = 0;
+  if (attn_shape("gdn_paged_attention_workspace_size", shape, cache, &l, &cache_bytes) != GDN_OK)
+    return 0;
+  if (shape->n_seqs == 0 || shape->T == 0) return 0;
+  return gdn::attn_workspace_size(l, shape->n_seqs, shape->T, shape->H, shape->max_pages);
+}
+
+gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const gdn_kv_cache *cache,
+                               const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *page_table, const int32_t *lens, void *out,
+                               void *workspace, size_t workspace_bytes, gdn_stream_t stream) {
+  const char *fn = "gdn_paged_attention";
+  gdn::AttnArgs a{};
+  size_t cache_bytes = 0;
+  gdn_status st = attn_shape(fn, shape, cache, &a.cache, &cache_bytes);
+  if (st != GDN_OK) return st;
+  const gdn_attn_shape &s = *shape;
+  if (s.n_seqs == 0 || s.T == 0) return GDN_OK;
+  const size_t e = a.cache.bf16 ? 2 : 4, rows = (size_t)s.n_seqs * s.T * s.H;
+  const size_t need = gdn::attn_workspace_size(a.cache, s.n_seqs, s.T, s.H, s.max_pages);
+  const Buf in[] = {{"q", q, e * rows * a.cache.D},
+                    {"k_cache", k_cache, cache_bytes},
+                    {"v_cache", v_cache, cache_bytes},
+                    {"page_table", page_table, 4 * (size_t)s.n_seqs * s.max_pages},
+                    {"lens", lens, 4 * (size_t)s.n_seqs}};
+  const Buf outs[] = {{"out", out, e * rows * a.cache.D}, {"workspace", workspace, need}};
+  for (const Buf &b : in) {
+    // no pages: every sequence is empty, and nothing of them is read
+    if (!b.p && !(b.bytes == 0 && &b != &in[0]))
+      return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, b.name);
+    if ((st = check_aligned(fn, b)) != GDN_OK) return st;
+  }
+  for (const Buf &o : outs) {
+    if (!o.p) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, o.name);
+    if ((st = check_aligned(fn, o)) != GDN_OK) return st;
+    for (const Buf &b : in)
+      if ((st = check_apart(fn, o, b)) != GDN_OK) return st;
+  }
+  if ((st = check_apart(fn, outs[0], outs[1])) != GDN_OK) return st;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(GDN_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+  if (workspace_bytes < need)
+    return fail(GDN_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes,
+                need);
+  if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;
+  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.table = page_table; a.lens = lens; a.out = out; a.workspace = workspace;
+  a.n_seqs = s.n_seqs; a.T = s.T; a.H = s.H; a.max_pages = s.max_pages;
+  a.grouped = s.kv_map == GDN_QK_GROUPED;
+  a.scale = s.scale != 0.f ? s.scale : 1.0f / std::sqrt((float)a.cache.D);
+  return check_launch(gdn::launch_paged_attention(a, reinterpret_cast<cudaStream_t>(stream)),
+                      "gdn_paged_attention launch");
 }
 
 }  // extern "C"

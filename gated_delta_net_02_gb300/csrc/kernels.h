@@ -113,4 +113,19 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t stream);
 
+// Attention over a paged cache; see paged_attention.cu.
+struct AttnArgs {
+  KvLayout cache;
+  const void *q, *k_cache, *v_cache;
+  const int32_t *table, *lens;  // [n_seqs][max_pages], [n_seqs]
+  void *out;
+  void *workspace;
+  int n_seqs, T, H, max_pages;
+  bool grouped;                 // query head h reads kv head h / (H / H_kv), else h % H_kv
+  float scale;
+  int *err;
+};
+size_t attn_workspace_size(const KvLayout &c, int n_seqs, int T, int H, int max_pages);
+cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream);
+
 }  // namespace gdn

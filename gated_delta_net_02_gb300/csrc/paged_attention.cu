@@ -1,0 +1,782 @@
+// paged_attention.cu -- attention of the last T tokens of each sequence over
+// a paged key-value cache, split over the cache's length and joined.
+//
+//   out[t] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q_t . k_j - m),
+//   j = 0 .. len - T + t
+//
+// One pass over the keys with a running maximum m and sum l (fp32). Bound by
+// HBM: a key and its value are read once for the G = H / H_kv query heads of
+// their kv head and for the T tokens, 4 G T D flops for 2 D elements.
+//
+//  * Rows: the T x G (token, query head) pairs of a kv head are the rows of
+//    one matrix product, in blocks of 16, 32 or 64, so that the cache is read
+//    once for all of them.
+//  * Work: an item is one (sequence, kv head, row block); its keys are cut
+//    into tiles. All items' tiles form one line, and each block of the grid
+//    takes an equal run of it, whatever the lengths (every block reads the
+//    lengths and finds its place by a scan). An item that one block holds
+//    whole is finished there; of a cut item each block writes its (m, l,
+//    sum p v) to the workspace and a second kernel joins them, in the fixed
+//    order of the line.
+//  * bf16: products on the warp-level matrix instruction (m16n8k16): with
+//    at most 64 rows the tensor-memory path would leave most of its 128 rows
+//    idle. p is rounded to bf16 for the second product (the sum l takes the
+//    unrounded p): 2^-9 relative on each term, as the inputs are.
+//    fp32: fp32 products on the CUDA cores.
+//  * Keys reach shared memory by 16-byte asynchronous copies, several tiles
+//    ahead; each key's address comes from its page, looked up a tile earlier.
+//    Rows beyond the length are filled with zeros, so what an unused part of
+//    a page holds (NaN included) reaches no result.
+#include <cuda_bf16.h>
+#include <limits.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kMinTiles = 2;  // shortest run of tiles worth a block of its own
+
+struct AttnParams {
+  const void *q, *k, *v;
+  void *out;
+  const int32_t *table, *lens;
+  float *part_o;    // [2 grid][rows][D] unnormalised sums of cut items
+  float2 *part_ml;  // [2 grid][rows]
+  int4 *cut;        // [grid] joins: x = item (-1: none), y, z = first and last block
+  long long page_stride, token_stride, head_stride;
+  int n_seqs, T, H, H_kv, n_pages, page_size, max_pages, row_blocks, grouped;
+  float scale_log2;  // scale * log2(e)
+  int *err;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+  const int n = live ? 16 : 0;  // 0 source bytes: filled with zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// Tile geometry. WM: warps along the rows (bf16), 16 rows each; the other
+// warps share out the tile's keys.
+template <typename T, int D_, int WM_>
+struct Cfg {
+  using In = T;
+  static constexpr bool kBf16 = sizeof(T) == 2;
+  static constexpr int D = D_, WM = WM_;
+  static constexpr int ROWS = kBf16 ? 16 * WM : 16;
+  static constexpr int WK = kBf16 ? 4 / WM : 1;  // key groups with their own m, l and sum
+  static constexpr int KT = kBf16 ? 64 : 32;     // keys of a tile
+  static constexpr int ROW_BYTES = D * (int)sizeof(T);
+  static constexpr int CH = ROW_BYTES / 16;      // 16-byte chunks of a row
+  static constexpr int TILE = KT * ROW_BYTES;    // K or V
+  static constexpr int STAGES = 3;
+  static constexpr int Q_BYTES = ROWS * ROW_BYTES;
+  static constexpr int P_BYTES = kBf16 ? 0 : ROWS * KT * 4;
+  // q fragments stay in registers up to D = 128: q then only passes through
+  // the last stage's place before that stage is first used
+  static constexpr bool QREG = kBf16 && D <= 128;
+  static constexpr int SMEM = STAGES * 2 * TILE + (QREG ? 0 : Q_BYTES) + P_BYTES;
+  static constexpr int PER_SM = SMEM <= 110 * 1024 ? 2 : 1;
+  static_assert(!QREG || Q_BYTES <= 2 * TILE, "q fits a stage");
+  static_assert(WK * ROWS * D * 4 <= STAGES * 2 * TILE, "the join reuses the tiles");
+};
+
+// Chunk c of row r: rows are at least 128 bytes, and eight consecutive rows
+// place one chunk in eight different bank groups.
+template <class C>
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+  return (uint32_t)(row * C::ROW_BYTES + ((c ^ (row & 7)) << 4));
+}
+
+constexpr long long kMaxLen = 1LL << 30;  // key indexes of a few tiles beyond it still fit
+
+__device__ __forceinline__ int seq_len(const AttnParams &p, int s, bool report) {
+  const int len = p.lens[s];
+  const long long most = min((long long)p.max_pages * p.page_size, kMaxLen);
+  if (len > most) {
+    if (report) set_error(p.err, kDevBadPage);
+    return (int)most;
+  }
+  return len < 0 ? 0 : len;
+}
+
+// Tiles of one item of a sequence: at least one, so that an empty sequence
+// still has its zeros written.
+__device__ __forceinline__ int item_tiles(int len, int kt) {
+  return len <= 0 ? 1 : (len - 1) / kt + 1;
+}
+
+struct Place {
+  int seq;          // sequence of the block's first tile
+  long long first;  // line position of that sequence's first tile
+  long long total;  // tiles of all items
+};
+
+// Block-wide: finds where line position begin(total) lies. Each thread sums
+// a run of sequences; the thread whose run holds the position walks it.
+template <class F>
+__device__ Place find_place(const AttnParams &p, int kt, int items_per_seq, F begin,
+                            long long (&warp_sum)[4], Place &shared) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.n_seqs + kThreads - 1) / kThreads;
+  const int s0 = min(tid * per, p.n_seqs), s1 = min(s0 + per, p.n_seqs);
+  long long sum = 0;
+  for (int s = s0; s < s1; ++s)
+    sum += (long long)item_tiles(seq_len(p, s, blockIdx.x == 0), kt) * items_per_seq;
+  long long scan = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, scan, off);
+    if (lane >= off) scan += up;
+  }
+  if (lane == 31) warp_sum[warp] = scan;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  before += scan - sum;
+  const long long x = begin(total);
+  if (x >= before && x < before + sum) {
+    long long at = before;
+    for (int s = s0; s < s1; ++s) {
+      const long long n = (long long)item_tiles(seq_len(p, s, false), kt) * items_per_seq;
+      if (x < at + n) {
+        shared = Place{s, at, total};
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  Place r = shared;
+  r.total = total;
+  return r;
+}
+
+// ---- one tile on the matrix instruction (bf16) -------------------------------
+
+template <class C>
+struct TileBf16 {
+  static constexpr int D = C::D, KW = C::KT / C::WK;  // keys of a warp
+  static constexpr bool QREG = C::QREG;
+  float o[D / 8][4];
+  float m[2], l[2];
+  uint32_t qf[QREG ? D / 16 : 1][4];
+  uint32_t q_addr;
+
+  __device__ __forceinline__ void start(uint32_t q_s) {
+    const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % C::WM;
+    const int row = wm * 16 + (lane & 15);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+    q_addr = q_s;
+    if constexpr (QREG) {
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        ldsm4(qf[ks], q_s + chunk_at<C>(row, ks * 2 + (lane >> 4)));
+    }
+  }
+
+  // Keys key0 .. of the tile; `lim` = keys the lane's two rows see.
+  __device__ __forceinline__ void tile(uint32_t k_s, uint32_t v_s, int key0, const int (&lim)[2],
+                                       float scale_log2, float *) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int kbase = warp / C::WM * KW;
+    const int qrow = warp % C::WM * 16 + (lane & 15);
+    float s[KW / 8][4];
+#pragma unroll
+    for (int i = 0; i < KW / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+    const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks) {
+      uint32_t a[4];
+      if constexpr (QREG) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = qf[ks][i];
+      } else {
+        ldsm4(a, q_addr + chunk_at<C>(qrow, ks * 2 + (lane >> 4)));
+      }
+#pragma unroll
+      for (int n = 0; n < KW / 16; ++n) {
+        uint32_t b[4];
+        ldsm4(b, k_s + chunk_at<C>(kbase + n * 16 + krow, ks * 2 + kch));
+        mma16816(s[2 * n], a, b[0], b[1]);
+        mma16816(s[2 * n + 1], a, b[2], b[3]);
+      }
+    }
+    // scaled scores, masked beyond each row's last key; running maximum
+    const int col = key0 + kbase + (lane & 3) * 2;
+    const bool cut = key0 + C::KT > min(lim[0], lim[1]);
+    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x = s[i][e] * scale_log2;
+        if (cut && col + i * 8 + (e & 1) >= lim[e >> 1]) x = -INFINITY;
+        s[i][e] = x;
+        mx[e >> 1] = fmaxf(mx[e >> 1], x);
+      }
+    float ref[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+      mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+      const float mn = fmaxf(m[r], mx[r]);
+      ref[r] = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every p is 0
+      const float alpha = exp2f(m[r] - ref[r]);
+      m[r] = mn;
+      l[r] *= alpha;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        o[i][2 * r] *= alpha;
+        o[i][2 * r + 1] *= alpha;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < KW / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[i][e] = exp2f(s[i][e] - ref[e >> 1]);
+        l[e >> 1] += s[i][e];
+      }
+    const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vch = lane >> 4;
+#pragma unroll
+    for (int n = 0; n < KW / 16; ++n) {
+      const uint32_t a[4] = {bf16x2(s[2 * n][0], s[2 * n][1]), bf16x2(s[2 * n][2], s[2 * n][3]),
+                             bf16x2(s[2 * n + 1][0], s[2 * n + 1][1]),
+                             bf16x2(s[2 * n + 1][2], s[2 * n + 1][3])};
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        uint32_t b[4];
+        ldsm4_t(b, v_s + chunk_at<C>(kbase + n * 16 + vrow, d * 2 + vch));
+        mma16816(o[2 * d], a, b[0], b[1]);
+        mma16816(o[2 * d + 1], a, b[2], b[3]);
+      }
+    }
+  }
+
+  // Row limits of the lane's two rows, as tile() takes them.
+  template <class F>
+  static __device__ __forceinline__ void limits(F limit_of, int (&lim)[2]) {
+    const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % C::WM;
+    lim[0] = limit_of(wm * 16 + (lane >> 2));
+    lim[1] = limit_of(wm * 16 + (lane >> 2) + 8);
+  }
+
+  // Sums to shared memory: so[key group][row][D], sml[key group][row].
+  __device__ __forceinline__ void flush(float *so, float2 *sml) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wk = warp / C::WM, wm = warp % C::WM;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float t = l[r];
+      t += __shfl_xor_sync(0xffffffffu, t, 1);
+      t += __shfl_xor_sync(0xffffffffu, t, 2);
+      const int row = wk * C::ROWS + wm * 16 + (lane >> 2) + 8 * r;
+      if ((lane & 3) == 0) sml[row] = make_float2(m[r], t);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<float2 *>(so + row * D + i * 8 + (lane & 3) * 2) =
+            make_float2(o[i][2 * r], o[i][2 * r + 1]);
+    }
+  }
+};
+
+// ---- one tile on the CUDA cores (fp32) -----------------------------------------
+// A warp has 4 rows. Scores: a lane has one key of the 32, and reads its row
+// of K in 16-byte chunks (eight lanes, eight bank groups) beside broadcast
+// chunks of q. Sums: a lane has D / 32 columns, and reads V rows beside
+// broadcast p.
+template <class C>
+struct TileF32 {
+  static constexpr int D = C::D, VL = D / 32;
+  float o[4][VL];
+  float m[4], l[4];
+  uint32_t q_addr;
+
+  __device__ __forceinline__ void start(uint32_t q_s) {
+    q_addr = q_s;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int i = 0; i < VL; ++i) o[r][i] = 0.f;
+    }
+  }
+  static __device__ __forceinline__ float4 lds4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a));
+    return v;
+  }
+  // column i of the lane: chunk (lane * VL + i) / 4; two-column lanes read half a chunk
+  static __device__ __forceinline__ void lds_v(uint32_t v_s, int row, float (&x)[VL]) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (VL == 2) {
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(x[0]), "=f"(x[1])
+                   : "r"(v_s + chunk_at<C>(row, lane >> 1) + (lane & 1) * 8));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VL / 4; ++i) {
+        const float4 t = lds4(v_s + chunk_at<C>(row, i * 32 + lane));
+        x[4 * i] = t.x; x[4 * i + 1] = t.y; x[4 * i + 2] = t.z; x[4 * i + 3] = t.w;
+      }
+    }
+  }
+  template <class F>
+  static __device__ __forceinline__ void limits(F limit_of, int (&lim)[4]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) lim[r] = limit_of((threadIdx.x >> 5) * 4 + r);
+  }
+  __device__ __forceinline__ void tile(uint32_t k_s, uint32_t v_s, int key0, const int (&lim)[4],
+                                       float scale_log2, float *p_s) {
+    const int lane = threadIdx.x & 31, row0 = (threadIdx.x >> 5) * 4;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int c = 0; c < C::CH; ++c) {
+      const float4 k = lds4(k_s + chunk_at<C>(lane, c));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float4 q = lds4(q_addr + chunk_at<C>(row0 + r, c));
+        s[r] = fmaf(q.x, k.x, s[r]);
+        s[r] = fmaf(q.y, k.y, s[r]);
+        s[r] = fmaf(q.z, k.z, s[r]);
+        s[r] = fmaf(q.w, k.w, s[r]);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float x = key0 + lane < lim[r] ? s[r] * scale_log2 : -INFINITY;
+      float mx = x;
+#pragma unroll
+      for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const float mn = fmaxf(m[r], mx), ref = mn == -INFINITY ? 0.f : mn;
+      const float alpha = exp2f(m[r] - ref), e = exp2f(x - ref);
+      m[r] = mn;
+      l[r] = l[r] * alpha + e;  // this lane's keys; summed over the lanes at the end
+      p_s[(row0 + r) * C::KT + lane] = e;
+#pragma unroll
+      for (int i = 0; i < VL; ++i) o[r][i] *= alpha;
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int j = 0; j < C::KT; j += 4) {
+      float4 pj[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        pj[r] = *reinterpret_cast<const float4 *>(p_s + (row0 + r) * C::KT + j);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        float x[VL];
+        lds_v(v_s, j + jj, x);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = jj == 0 ? pj[r].x : jj == 1 ? pj[r].y : jj == 2 ? pj[r].z : pj[r].w;
+#pragma unroll
+          for (int i = 0; i < VL; ++i) o[r][i] = fmaf(e, x[i], o[r][i]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void flush(float *so, float2 *sml) {
+    const int lane = threadIdx.x & 31, row0 = (threadIdx.x >> 5) * 4;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float t = l[r];
+#pragma unroll
+      for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+      if (lane == 0) sml[row0 + r] = make_float2(m[r], t);
+#pragma unroll
+      for (int i = 0; i < VL; ++i) {
+        const int col = VL == 2 ? lane * 2 + i : (i / 4) * 128 + lane * 4 + (i & 3);
+        so[(row0 + r) * D + col] = o[r][i];
+      }
+    }
+  }
+};
+
+template <class C>
+struct TileOf {
+  using type = TileF32<C>;
+};
+template <int D, int WM>
+struct TileOf<Cfg<__nv_bfloat16, D, WM>> {
+  using type = TileBf16<Cfg<__nv_bfloat16, D, WM>>;
+};
+
+// Output row (element offset / D) of row r of an item, or -1 beyond its rows.
+__device__ __forceinline__ long long out_row(const AttnParams &p, int item, int r, int rows) {
+  const int per_seq = p.H_kv * p.row_blocks, s = item / per_seq, x = item % per_seq;
+  const int kvh = x / p.row_blocks, row = x % p.row_blocks * rows + r;
+  const int G = p.H / p.H_kv;
+  if (row >= p.T * G) return -1;
+  const int t = row / G, g = row % G;
+  const int h = p.grouped ? kvh * G + g : g * p.H_kv + kvh;
+  return ((long long)s * p.T + t) * p.H + h;
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T *p, float4 v) {
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint2 *>(p) = make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+  else
+    *reinterpret_cast<float4 *>(p) = v;
+}
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnParams p) {
+  using T = typename C::In;
+  using Tile = typename TileOf<C>::type;
+  constexpr int D = C::D, KT = C::KT, ROWS = C::ROWS, WK = C::WK, S = C::STAGES;
+  constexpr bool Q_IN_STAGE = C::QREG;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ long long offs[2][KT], warp_sum[4];
+  __shared__ Place place;
+  __shared__ float2 sml[WK * ROWS];
+  const int tid = threadIdx.x;
+  const uint32_t tiles_s = smem_u32(smem);
+  const uint32_t q_s = tiles_s + (Q_IN_STAGE ? S - 1 : S) * 2 * C::TILE;
+  float *p_s = reinterpret_cast<float *>(smem + S * 2 * C::TILE + C::Q_BYTES);  // fp32 only
+  float *so = reinterpret_cast<float *>(smem);
+  const int G = p.H / p.H_kv, items_per_seq = p.H_kv * p.row_blocks;
+  const T *kc = static_cast<const T *>(p.k), *vc = static_cast<const T *>(p.v);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  long long run = 0;  // tiles of a block
+  const Place at = find_place(
+      p, KT, items_per_seq,
+      [&](long long total) {
+        run = (total + gridDim.x - 1) / gridDim.x;
+        if (run < kMinTiles) run = kMinTiles;
+        return run * blockIdx.x;
+      },
+      warp_sum, place);
+  long long pos = run * blockIdx.x;
+  const long long end = min(pos + run, at.total);
+  if (pos >= end) {
+    if (tid == 0) p.cut[blockIdx.x].x = -1;
+    return;
+  }
+  int s = at.seq;
+  int len = seq_len(p, s, false), nt = item_tiles(len, KT);
+  const long long in_seq = pos - at.first;
+  int x = (int)(in_seq / nt), tile0 = (int)(in_seq % nt);  // item of the sequence, its tile
+
+  if (tid == 0) {
+    // the first block that starts inside an item has it joined
+    const long long a = pos - tile0, before = pos - run;
+    const bool joins = tile0 > 0 && before <= a;
+    p.cut[blockIdx.x] = make_int4(joins ? s * items_per_seq + x : -1, (int)(a / run),
+                                  (int)((a + nt - 1) / run), a == before ? 0 : 1);
+  }
+
+  for (int seg = 0; pos < end; ++seg) {
+    const int n = (int)min((long long)(nt - tile0), end - pos);  // tiles of this item here
+    const int kvh = x / p.row_blocks, r0 = x % p.row_blocks * ROWS;
+    const int item = s * items_per_seq + x;
+    const long long head = (long long)kvh * p.head_stride;
+    const int32_t *table = p.table + (long long)s * p.max_pages;
+
+    // address of key tid of tile i, for its turn in offs (-1: zeros)
+    auto page_of = [&](int i) -> int {
+      const int key = (tile0 + i) * KT + tid;
+      return tid < KT && i < n && key < len ? table[(unsigned)key / (unsigned)p.page_size] : -1;
+    };
+    auto put_offs = [&](int i, int page) {
+      if (tid >= KT) return;
+      const int key = (tile0 + i) * KT + tid;
+      long long off = -1;
+      if (i < n && key < len) {
+        if (page < 0 || page >= p.n_pages) set_error(p.err, kDevBadPage);
+        else
+          off = page * p.page_stride +
+                (long long)((unsigned)key % (unsigned)p.page_size) * p.token_stride + head;
+      }
+      offs[i & 1][tid] = off;
+    };
+    auto load_tile = [&](int i) {
+      if (i < n) {
+        const uint32_t st = tiles_s + (uint32_t)(i % S) * 2 * C::TILE;
+        constexpr int RSTEP = kThreads / C::CH;
+        const int c = tid % C::CH;
+#pragma unroll
+        for (int j = 0; j < KT / RSTEP; ++j) {
+          const int row = tid / C::CH + j * RSTEP;
+          const long long off = offs[i & 1][row];
+          const bool live = off >= 0;
+          const long long e = (live ? off : 0) + c * (16 / (int)sizeof(T));
+          cp_async16(st + chunk_at<C>(row, c), kc + e, live);
+          cp_async16(st + C::TILE + chunk_at<C>(row, c), vc + e, live);
+        }
+      }
+      cp_async_commit();
+    };
+
+    // q rows of the item (zeros beyond them) join the first tile's copies
+    for (int e = tid; e < ROWS * C::CH; e += kThreads) {
+      const int r = e / C::CH, c = e % C::CH;
+      const long long row = out_row(p, item, r, ROWS);
+      cp_async16(q_s + chunk_at<C>(r, c),
+                 static_cast<const T *>(p.q) + (row < 0 ? 0 : row) * D + c * (16 / (int)sizeof(T)),
+                 row >= 0);
+    }
+    int page = page_of(0);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      put_offs(i, page);
+      page = page_of(i + 1);
+      __syncthreads();
+      load_tile(i);
+    }
+    put_offs(S - 1, page);
+    page = page_of(S);
+
+    int lim[sizeof(Tile::m) / sizeof(float)];
+    Tile::limits(
+        [&](int r) {
+          const int row = r0 + r;
+          // rows beyond the item's are not stored: no mask for their sake
+          return row < p.T * G ? len - p.T + row / G + 1 : INT_MAX;
+        },
+        lim);
+    Tile acc;
+    for (int i = 0; i < n; ++i) {
+      cp_async_wait<S - 2>();
+      __syncthreads();
+      if (i == 0) {
+        acc.start(q_s);
+        if (Q_IN_STAGE) __syncthreads();  // q is in registers before its place is loaded
+      }
+      load_tile(i + S - 1);
+      put_offs(i + S, page);
+      page = page_of(i + S + 1);
+      const uint32_t st = tiles_s + (uint32_t)(i % S) * 2 * C::TILE;
+      acc.tile(st, st + C::TILE, (tile0 + i) * KT, lim, p.scale_log2, p_s);
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // the tiles are free: the key groups' sums take their place
+    acc.flush(so, sml);
+    __syncthreads();
+
+    const bool whole = n == nt;
+    const long long slot = (long long)blockIdx.x * 2 + (seg > 0);
+    for (int e = tid; e < ROWS * (D / 4); e += kThreads) {
+      const int r = e / (D / 4), c = e % (D / 4) * 4;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WK; ++w) mm = fmaxf(mm, sml[w * ROWS + r].x);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WK; ++w) {
+        const float2 ml = sml[w * ROWS + r];
+        const float f = exp2f(ml.x - ref);
+        const float4 v = *reinterpret_cast<const float4 *>(so + (w * ROWS + r) * D + c);
+        ll += f * ml.y;
+        sum.x = fmaf(f, v.x, sum.x);
+        sum.y = fmaf(f, v.y, sum.y);
+        sum.z = fmaf(f, v.z, sum.z);
+        sum.w = fmaf(f, v.w, sum.w);
+      }
+      const long long row = out_row(p, item, r, ROWS);
+      if (row < 0) continue;
+      if (whole) {
+        // a row without keys has ll = 0 and sum = 0: its output is 0
+        const float inv = 1.f / (ll == 0.f ? 1.f : ll);
+        store4(static_cast<T *>(p.out) + row * D + c,
+               make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
+      } else {
+        *reinterpret_cast<float4 *>(p.part_o + (slot * ROWS + r) * D + c) = sum;
+        if (c == 0) p.part_ml[slot * ROWS + r] = make_float2(mm, ll);
+      }
+    }
+    __syncthreads();  // before the next item's copies reuse the tiles
+
+    pos += n;
+    tile0 = 0;
+    if (++x == items_per_seq && pos < end) {
+      x = 0;
+      len = seq_len(p, ++s, false);
+      nt = item_tiles(len, KT);
+    }
+  }
+}
+
+// Joins the cut items: block (i, r) row r of the item that the main kernel's
+// block i listed. The warps take the pieces in turn, a lane D / 32 columns.
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads) join_kernel(const AttnParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int VL = D / 32;
+  const int4 cut = p.cut[blockIdx.x];
+  if (cut.x < 0) return;
+  const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long row = out_row(p, cut.x, r, ROWS);
+  if (row < 0) return;
+  const int np = cut.z - cut.y + 1;
+  // the item is the first block's last item (its only one if it starts there),
+  // and the first of all later blocks
+  auto slot = [&](int i) { return 2LL * (cut.y + i) + (i == 0 && cut.w); };
+  float mm = -INFINITY;
+  for (int i = lane; i < np; i += 32) mm = fmaxf(mm, p.part_ml[slot(i) * ROWS + r].x);
+#pragma unroll
+  for (int off = 16; off; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
+  const float ref = mm == -INFINITY ? 0.f : mm;
+  float sum[VL], ll = 0.f;
+#pragma unroll
+  for (int j = 0; j < VL; ++j) sum[j] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < np; i += 4) {
+    const float2 ml = p.part_ml[slot(i) * ROWS + r];
+    const float f = exp2f(ml.x - ref);
+    ll += f * ml.y;
+    const float *o = p.part_o + (slot(i) * ROWS + r) * D;
+#pragma unroll
+    for (int j = 0; j < VL; ++j) sum[j] = fmaf(f, o[j * 32 + lane], sum[j]);
+  }
+  __shared__ float so[4][D], sl[4];
+#pragma unroll
+  for (int j = 0; j < VL; ++j) so[warp][j * 32 + lane] = sum[j];
+  if (lane == 0) sl[warp] = ll;
+  __syncthreads();
+  const float l4 = sl[0] + sl[1] + sl[2] + sl[3], inv = 1.f / (l4 == 0.f ? 1.f : l4);
+  for (int c = threadIdx.x; c < D; c += kThreads) {
+    const float v = (so[0][c] + so[1][c] + so[2][c] + so[3][c]) * inv;
+    T *out = static_cast<T *>(p.out) + row * D + c;
+    if constexpr (sizeof(T) == 2) *out = __float2bfloat16_rn(v);
+    else *out = v;
+  }
+}
+
+// ---- host side ------------------------------------------------------------------
+
+// Rows of a block: as few blocks of 16, 32 or 64 as hold all of an item's
+// rows (each block reads the keys again), the smallest that do.
+int rows_of(bool bf16, int rows) { return !bf16 || rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+constexpr int kSms = 152;
+
+int grid_of(const KvLayout &c, int n_seqs, int max_pages, int row_blocks, bool two_per_sm) {
+  const int kt = c.bf16 ? 64 : 32;
+  const long long tiles = ((long long)max_pages * c.page_size + kt - 1) / kt;
+  const long long most = two_per_sm ? 2 * kSms : kSms;
+  const long long items = (long long)n_seqs * c.H_kv * row_blocks;
+  // more blocks than tiles have nothing to do
+  if (tiles < most && items * (tiles < 1 ? 1 : tiles) < most)
+    return (int)(items * (tiles < 1 ? 1 : tiles));
+  return (int)most;
+}
+
+template <class C>
+cudaError_t launch_cfg(const AttnParams &p, int grid, cudaStream_t stream) {
+  static_assert(C::SMEM <= 227 * 1024 - 2048, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::SMEM);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(attn_kernel<C>, dim3(grid), dim3(kThreads), C::SMEM, stream, p);
+  if (e != cudaSuccess || grid == 1) return e;
+  const int rows = p.row_blocks > 1 ? C::ROWS : p.T * (p.H / p.H_kv);
+  return launch_pdl(join_kernel<typename C::In, C::D, C::ROWS>, dim3(grid, rows),
+                    dim3(kThreads), 0, stream, p);
+}
+
+template <int D>
+cudaError_t launch_d(const AttnParams &p, bool bf16, int rows, int grid, cudaStream_t stream) {
+  if (!bf16) return launch_cfg<Cfg<float, D, 1>>(p, grid, stream);
+  if (rows == 16) return launch_cfg<Cfg<__nv_bfloat16, D, 1>>(p, grid, stream);
+  if (rows == 32) return launch_cfg<Cfg<__nv_bfloat16, D, 2>>(p, grid, stream);
+  return launch_cfg<Cfg<__nv_bfloat16, D, 4>>(p, grid, stream);
+}
+
+bool two_per_sm(const KvLayout &c, int rows) {
+  if (!c.bf16)
+    return c.D == 64 ? Cfg<float, 64, 1>::PER_SM == 2
+                     : c.D == 128 ? Cfg<float, 128, 1>::PER_SM == 2 : false;
+  if (c.D == 64) return true;
+  if (c.D == 128)
+    return rows == 64 ? Cfg<__nv_bfloat16, 128, 4>::PER_SM == 2
+                      : Cfg<__nv_bfloat16, 128, 1>::PER_SM == 2;
+  return false;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t attn_workspace_size(const KvLayout &c, int n_seqs, int T, int H, int max_pages) {
+  const int total = T * (H / c.H_kv), rows = rows_of(c.bf16, total);
+  const size_t g = (size_t)grid_of(c, n_seqs, max_pages, (total + rows - 1) / rows,
+                                   two_per_sm(c, rows));
+  return up256(g * 16) + up256(g * 2 * rows * 8) + g * 2 * rows * c.D * 4;
+}
+
+cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream) {
+  const KvLayout &c = a.cache;
+  const int total = a.T * (a.H / c.H_kv), rows = rows_of(c.bf16, total);
+  AttnParams p{};
+  p.q = a.q; p.k = a.k_cache; p.v = a.v_cache; p.out = a.out;
+  p.table = a.table; p.lens = a.lens;
+  p.page_stride = c.page_stride; p.token_stride = c.token_stride; p.head_stride = c.head_stride;
+  p.n_seqs = a.n_seqs; p.T = a.T; p.H = a.H; p.H_kv = c.H_kv;
+  p.n_pages = c.n_pages; p.page_size = c.page_size; p.max_pages = a.max_pages;
+  p.row_blocks = (total + rows - 1) / rows;
+  p.grouped = a.grouped;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.err = a.err;
+  const int grid = grid_of(c, a.n_seqs, a.max_pages, p.row_blocks, two_per_sm(c, rows));
+  unsigned char *ws = static_cast<unsigned char *>(a.workspace);
+  p.cut = reinterpret_cast<int4 *>(ws);
+  p.part_ml = reinterpret_cast<float2 *>(ws + up256((size_t)grid * 16));
+  p.part_o = reinterpret_cast<float *>(ws + up256((size_t)grid * 16) +
+                                       up256((size_t)grid * 2 * rows * 8));
+  if (c.D == 64) return launch_d<64>(p, c.bf16, rows, grid, stream);
+  if (c.D == 128) return launch_d<128>(p, c.bf16, rows, grid, stream);
+  return launch_d<256>(p, c.bf16, rows, grid, stream);
+}
+
+}  // namespace gdn

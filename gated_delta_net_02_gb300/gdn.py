@@ -81,6 +81,12 @@ class gdn_rope_shape(ctypes.Structure):
                 ("v_stride", ctypes.c_longlong)]
 
 
+class gdn_attn_shape(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("scale", ctypes.c_float),
+                ("kv_map", ctypes.c_int)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libgdn.so is not built ({LIB_PATH}); run "
                       "gated_delta_net_02_gb300/build.py or __graft_entry__.build()")
@@ -121,6 +127,13 @@ lib.gdn_rmsnorm_fp8.argtypes = [ctypes.POINTER(gdn_norm_shape), _vp, _vp, _vp, _
 lib.gdn_rope_append.restype = _st
 lib.gdn_rope_append.argtypes = [ctypes.POINTER(gdn_rope_shape), ctypes.POINTER(gdn_kv_cache),
                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+lib.gdn_paged_attention_workspace_size.restype = ctypes.c_size_t
+lib.gdn_paged_attention_workspace_size.argtypes = [ctypes.POINTER(gdn_attn_shape),
+                                                   ctypes.POINTER(gdn_kv_cache)]
+lib.gdn_paged_attention.restype = _st
+lib.gdn_paged_attention.argtypes = [ctypes.POINTER(gdn_attn_shape),
+                                    ctypes.POINTER(gdn_kv_cache), _vp, _vp, _vp, _vp, _vp, _vp,
+                                    _vp, ctypes.c_size_t, _vp]
 lib.gdn_seq_table_create.restype = _st
 lib.gdn_seq_table_create.argtypes = [_i, _i, ctypes.POINTER(_vp)]
 lib.gdn_seq_table_destroy.restype = None
@@ -289,6 +302,20 @@ def gdn_rope_append(shape: gdn_rope_shape, cache: gdn_kv_cache, q, k, v, positio
         _rows_addr(v, shape.v_stride, kv), _addr(positions), _addr(inv_freq), _addr(slots),
         _addr(q_out), _cache_addr(k_cache, cache), _cache_addr(v_cache, cache),
         _stream(stream)))
+
+
+def gdn_paged_attention_workspace_size(shape: gdn_attn_shape, cache: gdn_kv_cache) -> int:
+    return int(lib.gdn_paged_attention_workspace_size(ctypes.byref(shape), ctypes.byref(cache)))
+
+
+def gdn_paged_attention(shape: gdn_attn_shape, cache: gdn_kv_cache, q, k_cache, v_cache,
+                        page_table, lens, out, workspace, workspace_bytes: int,
+                        stream=None) -> None:
+    """Attention of the last T tokens of each sequence over its pages."""
+    _check(lib.gdn_paged_attention(
+        ctypes.byref(shape), ctypes.byref(cache), _addr(q), _cache_addr(k_cache, cache),
+        _cache_addr(v_cache, cache), _addr(page_table), _addr(lens), _addr(out),
+        _addr(workspace), int(workspace_bytes), _stream(stream)))
 
 
 def gdn_check_device_error(stream=None) -> None:

@@ -390,6 +390,56 @@ gdn_status gdn_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cach
                            const float *inv_freq, const int64_t *slots, void *q_out,
                            void *k_cache, void *v_cache, gdn_stream_t stream);
 
+/*
+ * Attention of the last T tokens of each sequence over its pages (T = 1:
+ * decode; T = draft_max + 1: verify). Sequence s has lens[s] tokens in the
+ * cache, the new ones included; its token j is at page
+ * page_table[s][j / page_size], token j % page_size. Row t of its T rows
+ * stands at position lens[s] - T + t and sees the keys 0 up to itself:
+ *   out = sum_j softmax_j(scale q . k_j) v_j
+ * with statistics and sums in fp32 (bf16: the probabilities are rounded to
+ * bf16 before the product with v). A row that sees no key (lens[s] = 0, or
+ * lens[s] < T) is 0. What pages hold beyond lens[s] is not used, whatever it
+ * is; a NaN or infinity in v of one of the last T tokens reaches all T rows.
+ * Query head h reads kv head h / (H / H_kv) (GDN_QK_GROUPED) or h % H_kv
+ * (GDN_QK_TILED).
+ * The result does not depend on what ran before, bit for bit: the cache is
+ * cut by the lengths alone and the parts are joined in order.
+ */
+typedef struct {
+  int n_seqs;        /* >= 0 */
+  int T;             /* new tokens of each sequence, >= 0 */
+  int H;             /* query heads, a multiple of the cache's H_kv */
+  int max_pages;     /* columns of page_table, >= 0 */
+  float scale;       /* 0 means 1/sqrt(D) */
+  gdn_qk_map kv_map; /* query head -> kv head */
+} gdn_attn_shape;
+
+/* Bytes of device workspace gdn_paged_attention needs (at most 64 MiB); 0 for
+ * arguments that it refuses. Depends on the shapes alone, not on lens. */
+size_t gdn_paged_attention_workspace_size(const gdn_attn_shape *shape, const gdn_kv_cache *cache);
+
+/*
+ * q           device [n_seqs*T][H][D] (token s*T+t is token t of sequence s)
+ * k_cache, v_cache  device buffers of the layout `cache`
+ * page_table  device int32 [n_seqs][max_pages]; entries that no token needs
+ *             are not read
+ * lens        device int32 [n_seqs], 0 <= lens[s] <= max_pages * page_size
+ *             and at most 2^30 (a longer one is cut to that, a negative one
+ *             is 0)
+ * out         device [n_seqs*T][H][D]
+ * workspace   device buffer of at least gdn_paged_attention_workspace_size
+ *             bytes, 256-byte aligned; its contents on entry do not matter.
+ *             Calls that can overlap on the GPU need one each.
+ * A page table entry outside the cache, or a length that was cut, is reported
+ * as GDN_ERR_DEVICE_ARG by gdn_check_device_error; nothing out of range is
+ * read, and that sequence's output is undefined.
+ */
+gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const gdn_kv_cache *cache,
+                               const void *q, const void *k_cache, const void *v_cache,
+                               const int32_t *page_table, const int32_t *lens, void *out,
+                               void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * Rollback bookkeeping: a host-side table with one entry per sequence (the
  * recurrent memory's per-sequence record of which stored state is live,

@@ -118,3 +118,52 @@ def test_rope_of_no_tokens_and_null_structs(gdn):
     assert gdn.lib.gdn_rope_append(None, None, *[0] * 10) == gdn.GDN_ERR_INVALID_ARG
     assert gdn.lib.gdn_rope_append(ctypes.byref(gdn.gdn_rope_shape()), None,
                                    *[0] * 10) == gdn.GDN_ERR_INVALID_ARG
+
+
+def attend(gdn, shape=None, cache=None, nbytes=1 << 23, **kw):
+    sh = dict(n_seqs=3, T=2, H=8, max_pages=4, scale=0.0, kv_map=1)
+    sh.update(shape or {})
+    p = {n: FAKE + i * STEP for i, n in enumerate(
+        ("q", "k_cache", "v_cache", "page_table", "lens", "out", "workspace"))}
+    p.update(kw)
+    gdn.gdn_paged_attention(gdn.gdn_attn_shape(*(sh[f[0]] for f in gdn.gdn_attn_shape._fields_)),
+                            kv(gdn, **(cache or {})), *p.values(), nbytes)
+
+
+@pytest.mark.parametrize("cache,status", BAD_CACHES)
+def test_attention_refuses_caches(gdn, cache, status):
+    st, msg = refused(gdn, lambda: attend(gdn, cache=cache))
+    assert st == status and "gdn_paged_attention" in msg
+    assert gdn.gdn_paged_attention_workspace_size(gdn.gdn_attn_shape(3, 2, 8, 4, 0.0, 1),
+                                                  kv(gdn, **cache)) == 0
+
+
+@pytest.mark.parametrize("shape,status", [
+    (dict(n_seqs=-1), 1), (dict(T=-1), 1), (dict(H=0), 1), (dict(H=3), 1), (dict(max_pages=-1), 1),
+    (dict(kv_map=2), 1), (dict(scale=float("inf")), 1), (dict(n_seqs=1 << 28), 2)])
+def test_attention_refuses_shapes(gdn, shape, status):
+    st, msg = refused(gdn, lambda: attend(gdn, shape))
+    assert st == status and "gdn_paged_attention" in msg
+
+
+@pytest.mark.parametrize("ptrs,word", [
+    (dict(q=0), "q is NULL"), (dict(lens=0), "lens is NULL"), (dict(workspace=0), "workspace is"),
+    (dict(k_cache=FAKE + STEP + 4), "k_cache is not 16-byte"), (dict(out=FAKE), "out overlaps q"),
+    (dict(workspace=FAKE + 6 * STEP + 16), "256-byte"),
+    (dict(workspace=FAKE + STEP), "workspace overlaps k_cache"), (dict(nbytes=1000), "needed")])
+def test_attention_refuses_buffers(gdn, ptrs, word):
+    st, msg = refused(gdn, lambda: attend(gdn, **ptrs))
+    assert st == gdn.GDN_ERR_INVALID_ARG and word in msg
+
+
+def test_attention_of_nothing(gdn):
+    attend(gdn, dict(n_seqs=0), q=0)
+    attend(gdn, dict(T=0), q=0)
+    assert gdn.lib.gdn_paged_attention(None, None, *[0] * 9) == gdn.GDN_ERR_INVALID_ARG
+
+
+def test_attention_workspace_goes_by_the_shapes(gdn):
+    size = gdn.gdn_paged_attention_workspace_size
+    small = size(gdn.gdn_attn_shape(1, 1, 8, 1, 0.0, 1), kv(gdn))
+    large = size(gdn.gdn_attn_shape(64, 8, 16, 512, 0.0, 1), kv(gdn))
+    assert 0 < small < large <= 64 << 20
