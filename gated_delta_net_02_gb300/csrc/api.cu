@@ -485,6 +485,10 @@ static const char *wait_site_name(int site) {
     case gdn::kSiteScanStage: return "chunk scan, stage copies";
     case gdn::kSiteScanS0: return "chunk scan, state operand";
     case gdn::kSiteScanD: return "chunk scan, D tile";
+    case gdn::kSiteGemmEmpty: return "e4m3 product, stage release";
+    case gdn::kSiteGemmStage: return "e4m3 product, stage copies";
+    case gdn::kSiteGemmAcc: return "e4m3 product, accumulator buffer";
+    case gdn::kSiteGemmScale: return "e4m3 product, scale vector";
     default: return "unnamed wait";
   }
 }

@@ -171,6 +171,43 @@ gdn_status gdn_rmsnorm_fp8(const gdn_norm_shape *shape, const void *x, const voi
                       "gdn_rmsnorm_fp8 launch");
 }
 
+gdn_status gdn_gemm_fp8(const gdn_gemm_shape *shape, const void *a, const float *a_scale,
+                        const void *b, const float *b_scale, void *out, gdn_stream_t stream) {
+  const char *fn = "gdn_gemm_fp8";
+  if (!shape) return fail(GDN_ERR_INVALID_ARG, "%s: shape is NULL", fn);
+  const gdn_gemm_shape &s = *shape;
+  if (s.M < 0 || s.N < 0 || s.K < 1)
+    return fail(GDN_ERR_INVALID_ARG, "%s: M=%d N=%d K=%d", fn, s.M, s.N, s.K);
+  if (!dtype_ok(s.out_dtype))
+    return fail(GDN_ERR_INVALID_ARG, "%s: out_dtype %d", fn, (int)s.out_dtype);
+  if (s.K % 16)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: K=%d is no multiple of 16", fn, s.K);
+  if (s.M > (1 << 21) || s.N > (1 << 21) || s.K > (1 << 21))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: M=%d N=%d K=%d above 2^21", fn, s.M, s.N, s.K);
+  if (s.M == 0 || s.N == 0) return GDN_OK;
+  const size_t M = (size_t)s.M, N = (size_t)s.N, K = (size_t)s.K, kb = (K + 127) / 128;
+  const Buf in[] = {{"a", a, M * K},
+                    {"a_scale", a_scale, 4 * M * kb},
+                    {"b", b, N * K},
+                    {"b_scale", b_scale, 4 * ((N + 127) / 128) * kb}};
+  const Buf o = {"out", out, M * N * (s.out_dtype == GDN_BF16 ? 2 : 4)};
+  gdn_status st;
+  for (const Buf &x : in) {
+    if (!x.p) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, x.name);
+    if ((st = check_aligned(fn, x)) != GDN_OK) return st;
+  }
+  if (!o.p) return fail(GDN_ERR_INVALID_ARG, "%s: out is NULL", fn);
+  if ((st = check_aligned(fn, o)) != GDN_OK) return st;
+  for (const Buf &x : in)
+    if ((st = check_apart(fn, o, x)) != GDN_OK) return st;
+  gdn::GemmArgs g{};
+  if ((st = device_err_ptr(&g.err)) != GDN_OK) return st;
+  g.a = a; g.a_scale = a_scale; g.b = b; g.b_scale = b_scale; g.out = out;
+  g.M = s.M; g.N = s.N; g.K = s.K; g.bf16_out = s.out_dtype == GDN_BF16;
+  return check_launch(gdn::launch_gemm_fp8(g, reinterpret_cast<cudaStream_t>(stream)),
+                      "gdn_gemm_fp8 launch");
+}
+
 gdn_status gdn_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cache, const void *q,
                            const void *k, const void *v, const int32_t *positions,
                            const float *inv_freq, const int64_t *slots, void *q_out,

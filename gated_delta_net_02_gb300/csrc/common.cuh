@@ -36,6 +36,10 @@ enum WaitSite : int {
   kSiteScanStage = 52,    // chunk scan, MMA issuer: a stage's copies
   kSiteScanS0 = 53,       // chunk scan, MMA issuer: the state operand
   kSiteScanD = 54,        // chunk scan, MMA issuer: the D tile
+  kSiteGemmEmpty = 61,    // e4m3 product, producer: a stage released by its products
+  kSiteGemmStage = 62,    // e4m3 product, MMA issuer: a stage's copies
+  kSiteGemmAcc = 63,      // e4m3 product: a tensor-memory buffer filled or taken
+  kSiteGemmScale = 64,    // e4m3 product: a scale vector filled or taken
 };
 
 // Largest |cumulative log-gate| inside one chunk that the chunked kernels

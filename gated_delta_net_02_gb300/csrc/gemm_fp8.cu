@@ -1,0 +1,549 @@
+// gemm_fp8.cu -- product of two e4m3 matrices with fp32 scales: one for each
+// row and 128 columns of A, one for each 128 x 128 block of B.
+//
+//   out[m][n] = sum_b sa[m][b] sb[n/128][b] sum_{k in block b} A[m][k] B[n][k]
+//
+// The scales change every 128 elements of k, so a block's product (four
+// tcgen05 instructions of K = 32, fp32 accumulators in tensor memory) is
+// taken to registers and added there as acc += (sa sb) * product: one load
+// from tensor memory and one fused multiply-add for every 128 products of
+// the tensor cores. Two tensor-memory buffers let the tensor cores form one
+// block while the epilogue warps take the other.
+//
+// Roles of a block of threads: one thread issues TMA loads into a ring of
+// 128-byte-swizzled stages (one scale block of k each), one the tensor-core
+// instructions, one warp brings the stages' scales into a ring of their own,
+// and the epilogue warps keep the fp32 sums of the whole k in registers.
+//
+// Two forms:
+//  * few rows of A: the rows of B are the instruction's 128 rows and the rows
+//    of A its 16 to 128 columns, so that no tensor-core row idles. Bound by
+//    the read of B: k is split over a cluster of up to 8 blocks, which add
+//    their sums through distributed shared memory in rank order.
+//  * many rows of A: 128 x 256 tiles, persistent blocks. Bound by the tensor
+//    cores.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tensor_map.h"
+#include "umma.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kBlockK = 128;      // k of a stage, of a scale and of a swizzle row
+constexpr int kScaleSlots = 8;    // ring of scale vectors
+
+struct GemmParams {
+  const float *a_scale, *b_scale;
+  void *out;
+  int M, N, KB;  // KB = blocks of k
+  int split;     // blocks of a cluster along k (few rows)
+  int bf16_out;
+  int *err;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t local, uint32_t rank) {
+  float4 v;
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(remote)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) { return pack_bf16(lo, hi); }
+
+// Four consecutive outputs of one row; `full` when all four exist and the
+// address allows one store.
+__device__ __forceinline__ void store_out4(const GemmParams &p, long long at, float4 v, int n_left,
+                                           bool vec) {
+  if (p.bf16_out) {
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at;
+    if (vec && n_left >= 4) {
+      *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(v.x, v.y), pack2(v.z, v.w));
+    } else {
+      if (n_left > 0) o[0] = __float2bfloat16_rn(v.x);
+      if (n_left > 1) o[1] = __float2bfloat16_rn(v.y);
+      if (n_left > 2) o[2] = __float2bfloat16_rn(v.z);
+      if (n_left > 3) o[3] = __float2bfloat16_rn(v.w);
+    }
+  } else {
+    float *o = static_cast<float *>(p.out) + at;
+    if (vec && n_left >= 4) {
+      *reinterpret_cast<float4 *>(o) = v;
+    } else {
+      if (n_left > 0) o[0] = v.x;
+      if (n_left > 1) o[1] = v.y;
+      if (n_left > 2) o[2] = v.z;
+      if (n_left > 3) o[3] = v.w;
+    }
+  }
+}
+
+struct Bars {
+  uint64_t sfull[kScaleSlots], sempty[kScaleSlots];  // scale ring
+  uint64_t tfull[2], tempty[2];                      // tensor-memory buffers
+};
+
+// ---- few rows of A -------------------------------------------------------------
+
+template <int NT>
+struct SmallCfg {
+  static constexpr int A_BYTES = 128 * kBlockK;  // rows of B, the instruction's rows
+  static constexpr int STAGE = A_BYTES + NT * kBlockK;
+  static constexpr int STAGES = NT <= 32 ? 5 : 4;
+  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static constexpr int TCOLS = NT < 16 ? 32 : 2 * NT;  // two buffers
+  static_assert(NT * 128 * 4 <= STAGES * STAGE, "the sums reuse the stages");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(256) gemm_small_kernel(const GemmParams p,
+                                                         const __grid_constant__ CUtensorMap mb,
+                                                         const __grid_constant__ CUtensorMap ma) {
+  using C = SmallCfg<NT>;
+  constexpr int S = C::STAGES;
+  extern __shared__ unsigned char raw[];
+  unsigned char *sm =
+      reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[S], empty[S];
+  __shared__ Bars bars;
+  __shared__ __align__(16) float sc[kScaleSlots][NT];
+  __shared__ uint32_t tm_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % p.split, n0 = blockIdx.x / p.split * 128, m0 = blockIdx.y * NT;
+  const int kb0 = (int)((long long)rank * p.KB / p.split);
+  const int nk = (int)((long long)(rank + 1) * p.KB / p.split) - kb0;
+
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(&bars.sfull[i], 32);
+      mbar_init(&bars.sempty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.tfull[i], 1);
+      mbar_init(&bars.tempty[i], 4);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&mb);
+    prefetch_tmap(&ma);
+  }
+  // Tensor memory only once the kernel before has completed, and the next
+  // kernel only once this one has its own: of two kernels on one SM that both
+  // allocate, the earlier never waits for the later.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 2) {
+    tmem_alloc(&tm_s, C::TCOLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tm = tm_s;
+
+  float acc[NT];
+  if (warp == 0) {
+    if (lane == 0)
+      for (int i = 0; i < nk; ++i) {
+        const int s = i % S;
+        if (i >= S && !mbar_wait(&empty[s], (i / S - 1) & 1, p.err, kSiteGemmEmpty)) break;
+        unsigned char *st = sm + s * C::STAGE;
+        mbar_arrive_expect_tx(&full[s], C::STAGE);
+        tma_load_2d(st, &mb, (kb0 + i) * kBlockK, n0, &full[s]);
+        tma_load_2d(st + C::A_BYTES, &ma, (kb0 + i) * kBlockK, m0, &full[s]);
+      }
+  } else if (warp == 1) {
+    if (lane == 0)
+      for (int i = 0; i < nk; ++i) {
+        const int s = i % S, b = i & 1;
+        if (i >= 2 && !mbar_wait(&bars.tempty[b], ((i >> 1) - 1) & 1, p.err, kSiteGemmAcc)) break;
+        if (!mbar_wait(&full[s], (i / S) & 1, p.err, kSiteGemmStage)) break;
+        tc_fence_after();
+        const uint32_t st = smem_u32(sm + s * C::STAGE);
+#pragma unroll
+        for (int q = 0; q < kBlockK / 32; ++q)
+          umma_e4m3(tm + b * NT, sdesc_kmajor(st + q * 32), sdesc_kmajor(st + C::A_BYTES + q * 32),
+                    idesc_e4m3_f32(128, NT), q > 0);
+        umma_commit(&empty[s]);
+        umma_commit(&bars.tfull[b]);
+      }
+  } else if (warp == 2) {
+    // scales of the tile's columns (rows of A), times the tile's block of B
+    constexpr int PER = (NT + 31) / 32, AHEAD = 4;
+    const float *bs = p.b_scale + (long long)(n0 >> 7) * p.KB + kb0;
+    bool ok = true;
+    for (int i0 = 0; i0 < nk && ok; i0 += AHEAD) {
+      float v[AHEAD][PER];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+        for (int c = 0; c < PER; ++c) {
+          const int j = c * 32 + lane;
+          v[u][c] = 0.f;
+          if (i0 + u < nk && j < NT && m0 + j < p.M)
+            v[u][c] = p.a_scale[(long long)(m0 + j) * p.KB + kb0 + i0 + u] * bs[i0 + u];
+        }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int i = i0 + u, s = i % kScaleSlots;
+        if (i >= nk) break;
+        if (i >= kScaleSlots &&
+            !mbar_wait(&bars.sempty[s], (i / kScaleSlots - 1) & 1, p.err, kSiteGemmScale)) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+          if (c * 32 + lane < NT) sc[s][c * 32 + lane] = v[u][c];
+        mbar_arrive(&bars.sfull[s]);
+      }
+    }
+  } else if (warp >= 4) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[j] = 0.f;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    for (int i = 0; i < nk; ++i) {
+      const int b = i & 1, s = i % kScaleSlots;
+      if (!mbar_wait(&bars.sfull[s], (i / kScaleSlots) & 1, p.err, kSiteGemmScale)) break;
+      if (!mbar_wait(&bars.tfull[b], (i >> 1) & 1, p.err, kSiteGemmAcc)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < NT; c += 16) {
+        float t[16];
+        tmem_ld16(tm + lanes + b * NT + c, t);
+        if (c + 16 >= NT) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.tempty[b]);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(&sc[s][c + j]);
+          acc[c + j] = fmaf(t[j], f.x, acc[c + j]);
+          acc[c + j + 1] = fmaf(t[j + 1], f.y, acc[c + j + 1]);
+          acc[c + j + 2] = fmaf(t[j + 2], f.z, acc[c + j + 2]);
+          acc[c + j + 3] = fmaf(t[j + 3], f.w, acc[c + j + 3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.sempty[s]);
+    }
+  }
+  __syncthreads();  // every stage has been read by the tensor cores
+  float *sums = reinterpret_cast<float *>(sm);  // [NT][128]
+  if (warp >= 4) {
+    const int row = (warp & 3) * 32 + lane;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) sums[j * 128 + row] = acc[j];
+  }
+  if (p.split > 1) cluster_sync();
+  else __syncthreads();
+  const int cols = NT / p.split;  // columns that this block finishes
+  const bool vec = (p.N & 3) == 0;
+  for (int e = tid; e < cols * 32; e += 256) {
+    const int j = rank * cols + (e >> 5), r = (e & 31) * 4;
+    const uint32_t at = smem_u32(sums + j * 128 + r);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < p.split; ++c) {
+      const float4 t = p.split > 1 ? ld_cluster_f4(at, c)
+                                   : *reinterpret_cast<const float4 *>(sums + j * 128 + r);
+      v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
+    }
+    if (m0 + j < p.M && n0 + r < p.N)
+      store_out4(p, (long long)(m0 + j) * p.N + n0 + r, v, p.N - n0 - r, vec);
+  }
+  if (p.split > 1) cluster_sync();  // no block leaves while its sums are read
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) tmem_dealloc(tm, C::TCOLS);
+}
+
+// ---- many rows of A --------------------------------------------------------------
+
+struct LargeCfg {
+  static constexpr int TM = 128, TN = 256;
+  static constexpr int A_BYTES = TM * kBlockK, STAGE = (TM + TN) * kBlockK;
+  static constexpr int STAGES = 4;
+  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static constexpr int THREADS = 384;  // four warps of roles, eight of epilogue
+};
+
+__global__ void __launch_bounds__(LargeCfg::THREADS, 1)
+    gemm_large_kernel(const GemmParams p, const __grid_constant__ CUtensorMap ma,
+                      const __grid_constant__ CUtensorMap mb, int m_tiles, int n_tiles) {
+  using C = LargeCfg;
+  constexpr int S = C::STAGES;
+  extern __shared__ unsigned char raw[];
+  unsigned char *sm =
+      reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[S], empty[S];
+  __shared__ Bars bars;
+  __shared__ float sc[kScaleSlots][C::TM + 2];  // rows of A, then the two blocks of B
+  __shared__ uint32_t tm_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(&bars.sfull[i], 32);
+      mbar_init(&bars.sempty[i], 8);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.tfull[i], 1);
+      mbar_init(&bars.tempty[i], 8);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&mb);
+    prefetch_tmap(&ma);
+  }
+  // Tensor memory only once the kernel before has completed, and the next
+  // kernel only once this one has its own: of two kernels on one SM that both
+  // allocate, the earlier never waits for the later.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 2) {
+    tmem_alloc(&tm_s, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tm = tm_s;
+  const int tiles = m_tiles * n_tiles;
+
+  // registers: 384 x 168 at launch = 128 x 72 + 256 x 216
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+      if (lane == 0) {
+        int i = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+          const int m0 = t % m_tiles * C::TM, n0 = t / m_tiles * C::TN;
+          for (int kb = 0; kb < p.KB; ++kb, ++i) {
+            const int s = i % S;
+            if (i >= S && !mbar_wait(&empty[s], (i / S - 1) & 1, p.err, kSiteGemmEmpty)) {
+              ok = false;
+              break;
+            }
+            unsigned char *st = sm + s * C::STAGE;
+            mbar_arrive_expect_tx(&full[s], C::STAGE);
+            tma_load_2d(st, &ma, kb * kBlockK, m0, &full[s]);
+            tma_load_2d(st + C::A_BYTES, &mb, kb * kBlockK, n0, &full[s]);
+          }
+        }
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        int i = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x)
+          for (int kb = 0; kb < p.KB; ++kb, ++i) {
+            const int s = i % S, b = i & 1;
+            if ((i >= 2 && !mbar_wait(&bars.tempty[b], ((i >> 1) - 1) & 1, p.err, kSiteGemmAcc)) ||
+                !mbar_wait(&full[s], (i / S) & 1, p.err, kSiteGemmStage)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t st = smem_u32(sm + s * C::STAGE);
+  #pragma unroll
+            for (int q = 0; q < kBlockK / 32; ++q)
+              umma_e4m3(tm + b * C::TN, sdesc_kmajor(st + q * 32),
+                        sdesc_kmajor(st + C::A_BYTES + q * 32), idesc_e4m3_f32(C::TM, C::TN), q > 0);
+            umma_commit(&empty[s]);
+            umma_commit(&bars.tfull[b]);
+          }
+      }
+    } else if (warp == 2) {
+      constexpr int AHEAD = 4;
+      int i = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const int m0 = t % m_tiles * C::TM, n0 = t / m_tiles * C::TN;
+        for (int k0 = 0; k0 < p.KB && ok; k0 += AHEAD) {
+          float v[AHEAD][5];
+  #pragma unroll
+          for (int u = 0; u < AHEAD; ++u) {
+            const int kb = k0 + u;
+  #pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int m = m0 + c * 32 + lane;
+              v[u][c] = kb < p.KB && m < p.M ? p.a_scale[(long long)m * p.KB + kb] : 0.f;
+            }
+            const int nb = (n0 >> 7) + lane;
+            v[u][4] = kb < p.KB && lane < 2 && nb * 128 < p.N ? p.b_scale[(long long)nb * p.KB + kb]
+                                                              : 0.f;
+          }
+  #pragma unroll
+          for (int u = 0; u < AHEAD; ++u) {
+            if (k0 + u >= p.KB) break;
+            const int s = i % kScaleSlots;
+            if (i >= kScaleSlots &&
+                !mbar_wait(&bars.sempty[s], (i / kScaleSlots - 1) & 1, p.err, kSiteGemmScale)) {
+              ok = false;
+              break;
+            }
+  #pragma unroll
+            for (int c = 0; c < 4; ++c) sc[s][c * 32 + lane] = v[u][c];
+            if (lane < 2) sc[s][C::TM + lane] = v[u][4];
+            mbar_arrive(&bars.sfull[s]);
+            ++i;
+          }
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t taddr = tm + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
+    int i = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+      for (int kb = 0; kb < p.KB; ++kb, ++i) {
+        const int b = i & 1, s = i % kScaleSlots;
+        if (!mbar_wait(&bars.sfull[s], (i / kScaleSlots) & 1, p.err, kSiteGemmScale) ||
+            !mbar_wait(&bars.tfull[b], (i >> 1) & 1, p.err, kSiteGemmAcc)) {
+          ok = false;
+          break;
+        }
+        const float f = sc[s][row] * sc[s][C::TM + half];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.sempty[s]);
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          float v[32];
+          tmem_ld32(taddr + b * C::TN + c, v);
+          if (c + 32 >= 128) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.tempty[b]);
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(v[j], f, acc[c + j]);
+        }
+      }
+      if (!ok) break;
+      const int m = t % m_tiles * C::TM + row, n0 = t / m_tiles * C::TN + half * 128;
+      if (m < p.M) {
+        const long long at = (long long)m * p.N + n0;
+        if (p.bf16_out && (p.N & 7) == 0) {
+          __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at;
+#pragma unroll
+          for (int j = 0; j < 128; j += 8)
+            if (n0 + j < p.N)
+              *reinterpret_cast<uint4 *>(o + j) =
+                  make_uint4(pack2(acc[j], acc[j + 1]), pack2(acc[j + 2], acc[j + 3]),
+                             pack2(acc[j + 4], acc[j + 5]), pack2(acc[j + 6], acc[j + 7]));
+        } else {
+          const bool vec = (p.N & 3) == 0;
+#pragma unroll
+          for (int j = 0; j < 128; j += 4)
+            if (n0 + j < p.N)
+              store_out4(p, at + j, make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]),
+                         p.N - n0 - j, vec);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) tmem_dealloc(tm, 512);
+}
+
+// ---- host side ------------------------------------------------------------------
+
+// e4m3 [rows][K], boxes of 128 bytes x box_rows, 128-byte swizzle; what lies
+// beyond the matrix reads as zeros.
+bool map_e4m3(CUtensorMap *m, const void *base, int rows, int K, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)K};
+  const cuuint32_t box[2] = {kBlockK, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides,
+                     box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kSms = 152;
+
+template <int NT>
+cudaError_t launch_small(const GemmArgs &a, GemmParams p, cudaStream_t stream) {
+  using C = SmallCfg<NT>;
+  CUtensorMap ma, mb;
+  if (!map_e4m3(&ma, a.a, a.M, a.K, NT) || !map_e4m3(&mb, a.b, a.N, a.K, 128))
+    return cudaErrorInvalidValue;
+  const int nt = (a.N + 127) / 128, mt = (a.M + NT - 1) / NT;
+  // as many blocks of k as keep the grid within the GPU, two stages each at least
+  p.split = 1;
+  while (p.split < 8 && (long long)nt * mt * p.split * 2 <= kSms && p.KB >= 4 * p.split)
+    p.split *= 2;
+  cudaError_t e = cudaFuncSetAttribute(gemm_small_kernel<NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(nt * p.split, mt);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gemm_small_kernel<NT>, p, mb, ma);
+}
+
+cudaError_t launch_large(const GemmArgs &a, const GemmParams &p, cudaStream_t stream) {
+  using C = LargeCfg;
+  CUtensorMap ma, mb;
+  if (!map_e4m3(&ma, a.a, a.M, a.K, C::TM) || !map_e4m3(&mb, a.b, a.N, a.K, C::TN))
+    return cudaErrorInvalidValue;
+  const int mt = (a.M + C::TM - 1) / C::TM, nt = (a.N + C::TN - 1) / C::TN;
+  cudaError_t e = cudaFuncSetAttribute(gemm_large_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (long long)mt * nt;
+  return launch_pdl(gemm_large_kernel, dim3(tiles < kSms ? (unsigned)tiles : kSms),
+                    dim3(C::THREADS), C::SMEM, stream, p, ma, mb, mt, nt);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8(const GemmArgs &a, cudaStream_t stream) {
+  if (!encode_fn()) return cudaErrorNotSupported;
+  GemmParams p{};
+  p.a_scale = a.a_scale; p.b_scale = a.b_scale; p.out = a.out;
+  p.M = a.M; p.N = a.N; p.KB = (a.K + kBlockK - 1) / kBlockK;
+  p.bf16_out = a.bf16_out; p.err = a.err; p.split = 1;
+  if (a.M <= 16) return launch_small<16>(a, p, stream);
+  if (a.M <= 32) return launch_small<32>(a, p, stream);
+  if (a.M <= 64) return launch_small<64>(a, p, stream);
+  if (a.M <= 256) return launch_small<128>(a, p, stream);
+  return launch_large(a, p, stream);
+}
+
+}  // namespace gdn

@@ -90,6 +90,17 @@ struct NormArgs {
 };
 cudaError_t launch_norm_fp8(const NormArgs &a, cudaStream_t stream);
 
+// Product of e4m3 matrices with block scales; see gemm_fp8.cu.
+struct GemmArgs {
+  const void *a, *b;               // e4m3 [M][K], [N][K]
+  const float *a_scale, *b_scale;  // [M][KB], [ceil(N / 128)][KB], KB = ceil(K / 128)
+  void *out;                       // [M][N]
+  int M, N, K;
+  bool bf16_out;
+  int *err;
+};
+cudaError_t launch_gemm_fp8(const GemmArgs &a, cudaStream_t stream);
+
 // Paged key-value cache layout (strides in elements, resolved).
 struct KvLayout {
   int n_pages, page_size, H_kv, D;

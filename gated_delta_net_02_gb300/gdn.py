@@ -60,6 +60,11 @@ class gdn_norm_shape(ctypes.Structure):
                 ("weight_offset", ctypes.c_float)]
 
 
+class gdn_gemm_shape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
+                ("out_dtype", ctypes.c_int)]
+
+
 GDN_ROPE_HALVES, GDN_ROPE_NEIGHBOURS = 0, 1
 GDN_ROPE_AXES_SECTIONED, GDN_ROPE_AXES_INTERLEAVED = 0, 1
 c_int = ctypes.c_int    # (c_int * 4)(...) builds gdn_rope_shape's sections
@@ -124,6 +129,8 @@ lib.gdn_noalloc_scratch_bytes.argtypes = []
 lib.gdn_rmsnorm_fp8.restype = _st
 lib.gdn_rmsnorm_fp8.argtypes = [ctypes.POINTER(gdn_norm_shape), _vp, _vp, _vp, _vp, _vp, _vp,
                                 _vp, _vp]
+lib.gdn_gemm_fp8.restype = _st
+lib.gdn_gemm_fp8.argtypes = [ctypes.POINTER(gdn_gemm_shape), _vp, _vp, _vp, _vp, _vp, _vp]
 lib.gdn_rope_append.restype = _st
 lib.gdn_rope_append.argtypes = [ctypes.POINTER(gdn_rope_shape), ctypes.POINTER(gdn_kv_cache),
                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
@@ -289,6 +296,13 @@ def gdn_rmsnorm_fp8(shape: gdn_norm_shape, x, residual, weight, residual_out, ou
     _check(lib.gdn_rmsnorm_fp8(ctypes.byref(shape), _addr(x), _addr(residual), _addr(weight),
                                _addr(residual_out), _addr(out), _addr(out_fp8),
                                _addr(out_scale), _stream(stream)))
+
+
+def gdn_gemm_fp8(shape: gdn_gemm_shape, a, a_scale, b, b_scale, out, stream=None) -> None:
+    """out = A B^T of e4m3 matrices (float8_e4m3fn or uint8 tensors) with a
+    scale for each row and 128 columns of A and each 128 x 128 block of B."""
+    _check(lib.gdn_gemm_fp8(ctypes.byref(shape), _addr(a), _addr(a_scale), _addr(b),
+                            _addr(b_scale), _addr(out), _stream(stream)))
 
 
 def gdn_rope_append(shape: gdn_rope_shape, cache: gdn_kv_cache, q, k, v, positions, inv_freq,

@@ -329,6 +329,31 @@ gdn_status gdn_rmsnorm_fp8(const gdn_norm_shape *shape, const void *x, const voi
                            const void *weight, void *residual_out, void *out, void *out_fp8,
                            float *out_scale, gdn_stream_t stream);
 
+/*
+ * Product of two 8-bit matrices with block scales, for example of
+ * gdn_rmsnorm_fp8's output and a projection's weights:
+ *   out[m][n] = sum_b a_scale[m][b] b_scale[n / 128][b]
+ *                     sum_{k in [128 b, 128 b + 128)} a[m][k] b[n][k]
+ * on the tensor cores, sums in fp32 (each block's products exactly as the
+ * tensor cores add them in fp32, then in fp32 over the blocks), rounded once
+ * to out_dtype. Nothing but the order of those sums depends on the sizes.
+ */
+typedef struct {
+  int M, N;            /* >= 0 */
+  int K;               /* >= 1, a multiple of 16 (a row starts on 16 bytes) */
+  gdn_dtype out_dtype;
+} gdn_gemm_shape;
+
+/*
+ * a        device e4m3 [M][K];  a_scale  device fp32 [M][ceil(K / 128)]
+ * b        device e4m3 [N][K];  b_scale  device fp32 [ceil(N / 128)][ceil(K / 128)]
+ * out      device [M][N] out_dtype; overlaps no other buffer
+ * The last blocks of N and K may be partial. GDN_ERR_UNSUPPORTED for another K
+ * and for sizes above 2^21.
+ */
+gdn_status gdn_gemm_fp8(const gdn_gemm_shape *shape, const void *a, const float *a_scale,
+                        const void *b, const float *b_scale, void *out, gdn_stream_t stream);
+
 /* A key-value cache in pages: token j of a page's page_size tokens, head h:
  *   element p * page_stride + j * token_stride + h * head_stride + d
  * of the k (or v) buffer, for page p. Strides are in elements and multiples

@@ -167,3 +167,35 @@ def test_attention_workspace_goes_by_the_shapes(gdn):
     small = size(gdn.gdn_attn_shape(1, 1, 8, 1, 0.0, 1), kv(gdn))
     large = size(gdn.gdn_attn_shape(64, 8, 16, 512, 0.0, 1), kv(gdn))
     assert 0 < small < large <= 64 << 20
+
+
+def gemm(gdn, shape=None, **kw):
+    sh = dict(M=40, N=300, K=512, out_dtype=gdn.GDN_BF16)
+    sh.update(shape or {})
+    p = {n: FAKE + i * STEP for i, n in enumerate(("a", "a_scale", "b", "b_scale", "out"))}
+    p.update(kw)
+    gdn.gdn_gemm_fp8(gdn.gdn_gemm_shape(*(sh[f[0]] for f in gdn.gdn_gemm_shape._fields_)),
+                     *p.values())
+
+
+@pytest.mark.parametrize("shape,status", [
+    (dict(M=-1), 1), (dict(N=-1), 1), (dict(K=0), 1), (dict(out_dtype=3), 1), (dict(K=520), 2),
+    (dict(K=8), 2), (dict(M=(1 << 21) + 1), 2), (dict(K=(1 << 21) + 16), 2)])
+def test_gemm_refuses_shapes(gdn, shape, status):
+    st, msg = refused(gdn, lambda: gemm(gdn, shape))
+    assert st == status and "gdn_gemm_fp8" in msg
+
+
+@pytest.mark.parametrize("ptrs,word", [
+    (dict(a=0), "a is NULL"), (dict(b_scale=0), "b_scale is NULL"), (dict(out=0), "out is NULL"),
+    (dict(b=FAKE + 2 * STEP + 8), "b is not 16-byte"), (dict(out=FAKE + 4 * STEP + 2), "out is not"),
+    (dict(out=FAKE), "out overlaps a"), (dict(out=FAKE + 3 * STEP - 32), "out overlaps b_scale")])
+def test_gemm_refuses_buffers(gdn, ptrs, word):
+    st, msg = refused(gdn, lambda: gemm(gdn, **ptrs))
+    assert st == gdn.GDN_ERR_INVALID_ARG and word in msg
+
+
+def test_gemm_of_nothing(gdn):
+    gemm(gdn, dict(M=0), a=0)
+    gemm(gdn, dict(N=0), b=0)
+    assert gdn.lib.gdn_gemm_fp8(None, *[0] * 6) == gdn.GDN_ERR_INVALID_ARG
