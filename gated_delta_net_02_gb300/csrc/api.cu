@@ -485,6 +485,8 @@ static const char *wait_site_name(int site) {
     case gdn::kSiteScanStage: return "chunk scan, stage copies";
     case gdn::kSiteScanS0: return "chunk scan, state operand";
     case gdn::kSiteScanD: return "chunk scan, D tile";
+    case gdn::kSiteNormRow: return "RMS norm, a group of rows";
+    case gdn::kSiteRopeRow: return "rotary positions, a token's rows";
     case gdn::kSiteGemmEmpty: return "e4m3 product, stage release";
     case gdn::kSiteGemmStage: return "e4m3 product, stage copies";
     case gdn::kSiteGemmAcc: return "e4m3 product, accumulator buffer";

@@ -36,6 +36,8 @@ enum WaitSite : int {
   kSiteScanStage = 52,    // chunk scan, MMA issuer: a stage's copies
   kSiteScanS0 = 53,       // chunk scan, MMA issuer: the state operand
   kSiteScanD = 54,        // chunk scan, MMA issuer: the D tile
+  kSiteNormRow = 55,      // RMS norm: a group of rows
+  kSiteRopeRow = 56,      // rotary positions: a token's rows
   kSiteGemmEmpty = 61,    // e4m3 product, producer: a stage released by its products
   kSiteGemmStage = 62,    // e4m3 product, MMA issuer: a stage's copies
   kSiteGemmAcc = 63,      // e4m3 product: a tensor-memory buffer filled or taken

@@ -148,6 +148,13 @@ def test_counts_and_dense_rows(gdn, n, H, H_kv):
     run(gdn, n, H, H_kv, 64, 64, (32,), False, False, 16, torch.bfloat16, fused=False, seed=n)
 
 
+@pytest.mark.parametrize("neighbours", [False, True])
+@pytest.mark.parametrize("rot", [256, 90])
+@pytest.mark.parametrize("n,H,H_kv,dtype", [(40, 70, 2, torch.float32), (3, 128, 64, torch.bfloat16)])
+def test_rows_of_many_wide_heads(gdn, neighbours, rot, n, H, H_kv, dtype):
+    run(gdn, n, H, H_kv, 256, rot, (rot // 2 - 9, 9), True, neighbours, 16, dtype, seed=n)
+
+
 @pytest.mark.parametrize("max_pos", [131072, 1 << 24])
 def test_long_positions_keep_their_angles(gdn, max_pos):
     run(gdn, 500, 2, 1, 128, 128, (64,), False, False, 16, torch.float32, max_pos=max_pos)
