@@ -161,6 +161,7 @@ gdn_status gdn_rmsnorm_fp8(const gdn_norm_shape *shape, const void *x, const voi
   }
 
   gdn::NormArgs a{};
+  if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;
   a.x = x; a.residual = residual; a.weight = weight;
   a.residual_out = residual_out; a.out = out;
   a.out_fp8 = static_cast<unsigned char *>(out_fp8); a.out_scale = out_scale;

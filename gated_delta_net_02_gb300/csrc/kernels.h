@@ -87,6 +87,7 @@ struct NormArgs {
   int rows, cols;
   bool bf16, normalize;
   float eps, weight_offset;
+  int *err;
 };
 cudaError_t launch_norm_fp8(const NormArgs &a, cudaStream_t stream);
 

@@ -85,6 +85,28 @@ def test_against_the_formula(gdn, rows, cols, dtype):
     check_fp8(q, s, y)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,cols", [(40001, 16), (20001, 272), (5003, 2048), (3001, 2064),
+                                       (2001, 4096), (1501, 8192), (700, 10000)])
+def test_many_rows(gdn, rows, cols, residual, dtype):
+    x, r, w = inputs_of(rows, cols, dtype, rows + cols)
+    r = r if residual else None
+    out = torch.empty_like(x)
+    res = torch.empty_like(x) if residual else None
+    q, s = call(gdn, x, r, w, res_out=res, out=out, w_off=0.5)
+    h, y = formula(x, r, w, w_off=0.5)
+    if residual:
+        close(res, h, OUT[dtype])
+    close(out, y, OUT[dtype])
+    check_fp8(q, s, y)
+    # in place, and outputs that start on 16 bytes only
+    wide = torch.empty(rows * cols + 16, device="cuda", dtype=dtype)
+    off = wide[16 // wide.element_size():][:rows * cols].view(rows, cols)
+    call(gdn, x, r, w, res_out=r, out=off, w_off=0.5)
+    assert torch.equal(off, out) and (not residual or torch.equal(r, res))
+
+
 @pytest.mark.parametrize("cols", [1024, 1001])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_options(gdn, dtype, cols):
