@@ -20,8 +20,13 @@
 //    of A its 16 to 128 columns, so that no tensor-core row idles. Bound by
 //    the read of B: k is split over a cluster of up to 8 blocks, which add
 //    their sums through distributed shared memory in rank order.
-//  * many rows of A: 128 x 256 tiles, persistent blocks. Bound by the tensor
-//    cores.
+//  * many rows of A: 256 x 256 tiles of a pair of blocks (cta_group::2),
+//    persistent. Should be bound by the tensor cores; 8192 x 8192 x 4096 with
+//    bf16 output takes 210 us (2620 TFLOP/s). Its instructions alone take 123,
+//    with their stages' loads and barriers 163: two tensor-memory buffers are
+//    all there is, and a block's product cannot start before the buffer of
+//    two blocks ago has been read in both blocks of the pair, which takes
+//    about as long again as the product.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -85,6 +90,23 @@ __device__ __forceinline__ void store_out4(const GemmParams &p, long long at, fl
       if (n_left > 2) o[2] = v.z;
       if (n_left > 3) o[3] = v.w;
     }
+  }
+}
+
+// acc += v * f for two neighbours in one instruction (each rounds alone).
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float f, float g) {
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\t"
+      "mov.b64 w, {%4, %5};\n\tfma.rn.f32x2 u, v, w, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(f), "f"(g));
+}
+// acc[at ..] += v f for 32 loaded columns. The empty statement keeps each use
+// behind the wait that stands before it.
+__device__ __forceinline__ void add_part(float (&acc)[128], float (&v)[32], float f, int at) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    asm volatile("" : "+f"(v[j]), "+f"(v[j + 1]));
+    fma2(acc[at + j], acc[at + j + 1], v[j], v[j + 1], f, f);
   }
 }
 
@@ -166,20 +188,16 @@ __global__ void __launch_bounds__(256) gemm_small_kernel(const GemmParams p,
         tma_load_2d(st + C::A_BYTES, &ma, (kb0 + i) * kBlockK, m0, &full[s]);
       }
   } else if (warp == 1) {
-    if (lane == 0)
-      for (int i = 0; i < nk; ++i) {
-        const int s = i % S, b = i & 1;
-        if (i >= 2 && !mbar_wait(&bars.tempty[b], ((i >> 1) - 1) & 1, p.err, kSiteGemmAcc)) break;
-        if (!mbar_wait(&full[s], (i / S) & 1, p.err, kSiteGemmStage)) break;
-        tc_fence_after();
-        const uint32_t st = smem_u32(sm + s * C::STAGE);
-#pragma unroll
-        for (int q = 0; q < kBlockK / 32; ++q)
-          umma_e4m3(tm + b * NT, sdesc_kmajor(st + q * 32), sdesc_kmajor(st + C::A_BYTES + q * 32),
-                    idesc_e4m3_f32(128, NT), q > 0);
-        umma_commit(&empty[s]);
-        umma_commit(&bars.tfull[b]);
-      }
+    for (int i = 0; i < nk; ++i) {
+      const int s = i % S, b = i & 1;
+      bool ok = i < 2 || mbar_wait(&bars.tempty[b], ((i >> 1) - 1) & 1, p.err, kSiteGemmAcc);
+      ok = ok && mbar_wait(&full[s], (i / S) & 1, p.err, kSiteGemmStage);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t st = smem_u32(sm) + s * C::STAGE;
+      umma_e4m3_k128(tm + b * NT, sdesc_kmajor(st), sdesc_kmajor(st + C::A_BYTES),
+                     idesc_e4m3_f32(128, NT), smem_u32(&empty[s]), smem_u32(&bars.tfull[b]));
+    }
   } else if (warp == 2) {
     // scales of the tile's columns (rows of A), times the tile's block of B
     constexpr int PER = (NT + 31) / 32, AHEAD = 4;
@@ -273,27 +291,62 @@ __global__ void __launch_bounds__(256) gemm_small_kernel(const GemmParams p,
 
 // ---- many rows of A --------------------------------------------------------------
 
+// A pair of blocks on one 256 x 256 tile: each holds 128 rows of A and 128 of
+// B a stage (half of what a block alone would load for the same products) and
+// the sums of its own 128 rows.
 struct LargeCfg {
-  static constexpr int TM = 128, TN = 256;
-  static constexpr int A_BYTES = TM * kBlockK, STAGE = (TM + TN) * kBlockK;
+  static constexpr int TM = 256, TN = 256;
+  static constexpr int HALF = 128 * kBlockK, STAGE = 2 * HALF;
   static constexpr int STAGES = 4;
-  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static constexpr int BOX = 32 * 128;  // output box of a warp: 32 rows of 128 bytes
+  static constexpr int SMEM = STAGES * STAGE + 8 * 2 * BOX + 1024;
   static constexpr int THREADS = 384;  // four warps of roles, eight of epilogue
 };
 
-__global__ void __launch_bounds__(LargeCfg::THREADS, 1)
+// Two boxes of the warp's 32 rows: columns c0 .. c0 + 128 (bf16) or + 64
+// (fp32) of acc, lane = row. The warp's earlier boxes have left first.
+template <bool BF16>
+__device__ __forceinline__ void store_box(unsigned char *box, int lane, const CUtensorMap &mo,
+                                          int n0, int m0, const float (&acc)[128], int c0) {
+  if (lane == 0) bulk_wait_read();
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = BF16 ? pack2(acc[(i * 8 + c) * 8 + 2 * k], acc[(i * 8 + c) * 8 + 2 * k + 1])
+                    : __float_as_uint(acc[c0 + (i * 8 + c) * 4 + k]);
+      *reinterpret_cast<uint4 *>(box + i * LargeCfg::BOX + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  fence_proxy_async();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(&mo, n0, m0, box);
+    tma_store_2d(&mo, n0 + (BF16 ? 64 : 32), m0, box + LargeCfg::BOX);
+    bulk_commit();
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1)
     gemm_large_kernel(const GemmParams p, const __grid_constant__ CUtensorMap ma,
-                      const __grid_constant__ CUtensorMap mb, int m_tiles, int n_tiles) {
+                      const __grid_constant__ CUtensorMap mb,
+                      const __grid_constant__ CUtensorMap mo, int m_tiles, int n_tiles,
+                      bool boxes) {
   using C = LargeCfg;
   constexpr int S = C::STAGES;
   extern __shared__ unsigned char raw[];
   unsigned char *sm =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[S], empty[S];
+  __shared__ uint64_t full[S], empty[S];  // full and tempty: those of rank 0 serve the pair
   __shared__ Bars bars;
-  __shared__ float sc[kScaleSlots][C::TM + 2];  // rows of A, then the two blocks of B
+  __shared__ float sc[kScaleSlots][130];  // 128 rows of A, then the two blocks of B
   __shared__ uint32_t tm_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&full[i], 1);
@@ -305,7 +358,7 @@ __global__ void __launch_bounds__(LargeCfg::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.tfull[i], 1);
-      mbar_init(&bars.tempty[i], 8);
+      mbar_init(&bars.tempty[i], 16);
     }
     fence_mbar_init();
     prefetch_tmap(&mb);
@@ -315,12 +368,11 @@ __global__ void __launch_bounds__(LargeCfg::THREADS, 1)
   // kernel only once this one has its own: of two kernels on one SM that both
   // allocate, the earlier never waits for the later.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == 2) {
-    tmem_alloc(&tm_s, 512);
-    tmem_relinquish();
-  }
+  __syncthreads();
+  if (warp == 2) tmem_alloc_pair(&tm_s, 512);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both blocks' barriers stand
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tm = tm_s;
@@ -333,8 +385,8 @@ __global__ void __launch_bounds__(LargeCfg::THREADS, 1)
       if (lane == 0) {
         int i = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-          const int m0 = t % m_tiles * C::TM, n0 = t / m_tiles * C::TN;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+          const int m0 = t % m_tiles * C::TM + rank * 128, n0 = t / m_tiles * C::TN + rank * 128;
           for (int kb = 0; kb < p.KB; ++kb, ++i) {
             const int s = i % S;
             if (i >= S && !mbar_wait(&empty[s], (i / S - 1) & 1, p.err, kSiteGemmEmpty)) {
@@ -342,55 +394,53 @@ __global__ void __launch_bounds__(LargeCfg::THREADS, 1)
               break;
             }
             unsigned char *st = sm + s * C::STAGE;
-            mbar_arrive_expect_tx(&full[s], C::STAGE);
-            tma_load_2d(st, &ma, kb * kBlockK, m0, &full[s]);
-            tma_load_2d(st + C::A_BYTES, &mb, kb * kBlockK, n0, &full[s]);
+            const uint32_t bar = cluster_addr(&full[s], 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE);
+            tma_load_2d_pair(st, &ma, kb * kBlockK, m0, bar);
+            tma_load_2d_pair(st + C::HALF, &mb, kb * kBlockK, n0, bar);
           }
         }
       }
     } else if (warp == 1) {
-      if (lane == 0) {
+      if (rank == 0) {
         int i = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x)
+        for (int t = pair; t < tiles && ok; t += pairs)
           for (int kb = 0; kb < p.KB; ++kb, ++i) {
             const int s = i % S, b = i & 1;
-            if ((i >= 2 && !mbar_wait(&bars.tempty[b], ((i >> 1) - 1) & 1, p.err, kSiteGemmAcc)) ||
-                !mbar_wait(&full[s], (i / S) & 1, p.err, kSiteGemmStage)) {
-              ok = false;
-              break;
-            }
+            ok = i < 2 || mbar_wait(&bars.tempty[b], ((i >> 1) - 1) & 1, p.err, kSiteGemmAcc);
+            ok = ok && mbar_wait(&full[s], (i / S) & 1, p.err, kSiteGemmStage);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t st = smem_u32(sm + s * C::STAGE);
-  #pragma unroll
-            for (int q = 0; q < kBlockK / 32; ++q)
-              umma_e4m3(tm + b * C::TN, sdesc_kmajor(st + q * 32),
-                        sdesc_kmajor(st + C::A_BYTES + q * 32), idesc_e4m3_f32(C::TM, C::TN), q > 0);
-            umma_commit(&empty[s]);
-            umma_commit(&bars.tfull[b]);
+            const uint32_t st = smem_u32(sm) + s * C::STAGE;
+            umma_e4m3_k128_pair(tm + b * C::TN, sdesc_kmajor(st), sdesc_kmajor(st + C::HALF),
+                                idesc_e4m3_f32(C::TM, C::TN), smem_u32(&empty[s]),
+                                smem_u32(&bars.tfull[b]));
           }
       }
     } else if (warp == 2) {
       constexpr int AHEAD = 4;
       int i = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-        const int m0 = t % m_tiles * C::TM, n0 = t / m_tiles * C::TN;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const int m0 = t % m_tiles * C::TM + rank * 128, n0 = t / m_tiles * C::TN;
         for (int k0 = 0; k0 < p.KB && ok; k0 += AHEAD) {
           float v[AHEAD][5];
-  #pragma unroll
+#pragma unroll
           for (int u = 0; u < AHEAD; ++u) {
             const int kb = k0 + u;
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int m = m0 + c * 32 + lane;
               v[u][c] = kb < p.KB && m < p.M ? p.a_scale[(long long)m * p.KB + kb] : 0.f;
             }
             const int nb = (n0 >> 7) + lane;
-            v[u][4] = kb < p.KB && lane < 2 && nb * 128 < p.N ? p.b_scale[(long long)nb * p.KB + kb]
-                                                              : 0.f;
+            v[u][4] = kb < p.KB && lane < 2 && nb * 128 < p.N
+                          ? p.b_scale[(long long)nb * p.KB + kb]
+                          : 0.f;
           }
-  #pragma unroll
+#pragma unroll
           for (int u = 0; u < AHEAD; ++u) {
             if (k0 + u >= p.KB) break;
             const int s = i % kScaleSlots;
@@ -399,9 +449,9 @@ __global__ void __launch_bounds__(LargeCfg::THREADS, 1)
               ok = false;
               break;
             }
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < 4; ++c) sc[s][c * 32 + lane] = v[u][c];
-            if (lane < 2) sc[s][C::TM + lane] = v[u][4];
+            if (lane < 2) sc[s][128 + lane] = v[u][4];
             mbar_arrive(&bars.sfull[s]);
             ++i;
           }
@@ -412,9 +462,11 @@ __global__ void __launch_bounds__(LargeCfg::THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t taddr = tm + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
+    unsigned char *box = sm + S * C::STAGE + (warp - 4) * 2 * C::BOX;
+    const uint32_t freed[2] = {cluster_addr(&bars.tempty[0], 0), cluster_addr(&bars.tempty[1], 0)};
     int i = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int t = pair; t < tiles && ok; t += pairs) {
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.f;
@@ -425,49 +477,59 @@ __global__ void __launch_bounds__(LargeCfg::THREADS, 1)
           ok = false;
           break;
         }
-        const float f = sc[s][row] * sc[s][C::TM + half];
+        const float f = sc[s][row] * sc[s][128 + half];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.sempty[s]);
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) {
-          float v[32];
-          tmem_ld32(taddr + b * C::TN + c, v);
-          if (c + 32 >= 128) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.tempty[b]);
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) acc[c + j] = fmaf(v[j], f, acc[c + j]);
-        }
+        // Columns in four parts, two in registers at a time: the third and
+        // fourth are under way while the first two are added, and the buffer
+        // is given back before the last two are.
+        const uint32_t src = taddr + b * C::TN;
+        float v0[32], v1[32];
+        tmem_ld32_async(src, v0);
+        tmem_ld32_async(src + 32, v1);
+        tmem_wait_ld();
+        add_part(acc, v0, f, 0);
+        tmem_ld32_async(src + 64, v0);
+        add_part(acc, v1, f, 32);
+        tmem_ld32_async(src + 96, v1);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(b ? freed[1] : freed[0]);
+        add_part(acc, v0, f, 64);
+        add_part(acc, v1, f, 96);
       }
       if (!ok) break;
-      const int m = t % m_tiles * C::TM + row, n0 = t / m_tiles * C::TN + half * 128;
-      if (m < p.M) {
-        const long long at = (long long)m * p.N + n0;
-        if (p.bf16_out && (p.N & 7) == 0) {
-          __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at;
-#pragma unroll
-          for (int j = 0; j < 128; j += 8)
-            if (n0 + j < p.N)
-              *reinterpret_cast<uint4 *>(o + j) =
-                  make_uint4(pack2(acc[j], acc[j + 1]), pack2(acc[j + 2], acc[j + 3]),
-                             pack2(acc[j + 4], acc[j + 5]), pack2(acc[j + 6], acc[j + 7]));
+      const int m0 = t % m_tiles * C::TM + rank * 128 + (warp & 3) * 32;
+      const int n0 = t / m_tiles * C::TN + half * 128, m = m0 + lane;
+      if (boxes) {
+        // through shared memory in swizzled boxes of 32 rows x 128 bytes, which
+        // bulk copies take to the output while the next tile begins (stores
+        // from registers, 32 rows at a time, took a sixth of the whole call)
+        if (p.bf16_out) {
+          store_box<true>(box, lane, mo, n0, m0, acc, 0);
         } else {
-          const bool vec = (p.N & 3) == 0;
-#pragma unroll
-          for (int j = 0; j < 128; j += 4)
-            if (n0 + j < p.N)
-              store_out4(p, at + j, make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]),
-                         p.N - n0 - j, vec);
+          store_box<false>(box, lane, mo, n0, m0, acc, 0);
+          store_box<false>(box, lane, mo, n0 + 64, m0, acc, 64);
         }
+      } else if (m < p.M) {
+        const long long at = (long long)m * p.N + n0;
+        const bool vec = (p.N & 3) == 0;
+#pragma unroll
+        for (int j = 0; j < 128; j += 4)
+          if (n0 + j < p.N)
+            store_out4(p, at + j, make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]),
+                       p.N - n0 - j, vec);
       }
     }
+    if (boxes && lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 2) tmem_dealloc(tm, 512);
+  cluster_sync();  // nothing of the pair arrives in a block that has left
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc_pair(tm, 512);
 }
 
 // ---- host side ------------------------------------------------------------------
@@ -481,6 +543,18 @@ bool map_e4m3(CUtensorMap *m, const void *base, int rows, int K, int box_rows) {
   return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides,
                      box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Output [M][N], boxes of 128 bytes x 32 rows, 128-byte swizzle; rows must
+// start on 16 bytes. What a box has beyond the matrix is not written.
+bool map_out(CUtensorMap *m, void *out, int M, int N, bool bf16) {
+  const cuuint64_t e = bf16 ? 2 : 4;
+  const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M}, strides[1] = {N * e};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / e), 32}, es[2] = {1, 1};
+  return encode_fn()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                     2, out, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -519,16 +593,19 @@ cudaError_t launch_small(const GemmArgs &a, GemmParams p, cudaStream_t stream) {
 
 cudaError_t launch_large(const GemmArgs &a, const GemmParams &p, cudaStream_t stream) {
   using C = LargeCfg;
-  CUtensorMap ma, mb;
-  if (!map_e4m3(&ma, a.a, a.M, a.K, C::TM) || !map_e4m3(&mb, a.b, a.N, a.K, C::TN))
+  CUtensorMap ma, mb, mo{};
+  const bool boxes = a.N % (a.bf16_out ? 8 : 4) == 0;
+  if (!map_e4m3(&ma, a.a, a.M, a.K, 128) || !map_e4m3(&mb, a.b, a.N, a.K, 128) ||
+      (boxes && !map_out(&mo, a.out, a.M, a.N, a.bf16_out)))
     return cudaErrorInvalidValue;
   const int mt = (a.M + C::TM - 1) / C::TM, nt = (a.N + C::TN - 1) / C::TN;
   cudaError_t e = cudaFuncSetAttribute(gemm_large_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const long long tiles = (long long)mt * nt;
-  return launch_pdl(gemm_large_kernel, dim3(tiles < kSms ? (unsigned)tiles : kSms),
-                    dim3(C::THREADS), C::SMEM, stream, p, ma, mb, mt, nt);
+  return launch_pdl(gemm_large_kernel, dim3(2 * (tiles < kSms / 2 ? (unsigned)tiles : kSms / 2)),
+                    dim3(C::THREADS), C::SMEM, stream, p, ma, mb, mo, mt, nt,
+                    boxes);
 }
 
 }  // namespace
