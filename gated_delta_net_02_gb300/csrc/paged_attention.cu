@@ -36,8 +36,24 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kJoinThreads = 128;
 constexpr int kMinTiles = 2;  // shortest run of tiles worth a block of its own
+
+// Division by a number fixed at launch: n / d for 0 <= n < 2^31 as one high
+// product and a shift (Granlund and Montgomery 1994: mul = floor(2^32 (2^s -
+// d) / d) + 1 with s = ceil(log2 d), q = (mulhi(mul, n) + n) >> s).
+struct FastDiv {
+  uint32_t mul, shift, d;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div) {
+    shift = 0;
+    while ((1ull << shift) < d) ++shift;
+    mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift);
+  }
+};
 
 struct AttnParams {
   const void *q, *k, *v;
@@ -47,7 +63,8 @@ struct AttnParams {
   float2 *part_ml;  // [2 grid][rows]
   int4 *cut;        // [grid] joins: x = item (-1: none), y, z = first and last block
   long long page_stride, token_stride, head_stride;
-  int n_seqs, T, H, H_kv, n_pages, page_size, max_pages, row_blocks, grouped;
+  FastDiv page_size, G, row_blocks;
+  int n_seqs, T, H, H_kv, n_pages, max_pages, grouped;
   float scale_log2;  // scale * log2(e)
   int *err;
 };
@@ -96,7 +113,12 @@ struct Cfg {
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int D = D_, WM = WM_;
   static constexpr int ROWS = kBf16 ? 16 * WM : 16;
-  static constexpr int WK = kBf16 ? 4 / WM : 1;  // key groups with their own m, l and sum
+  // Two warps for each of an SM's schedulers: two blocks of four, or one of
+  // eight where the tiles leave room for one block only and a warp has at
+  // least 16 keys of its own.
+  static constexpr int WARPS = kBf16 && D == 256 && WM > 1 ? 8 : 4;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int WK = kBf16 ? WARPS / WM : 1;  // key groups with their own m, l and sum
   static constexpr int KT = kBf16 ? 64 : 32;     // keys of a tile
   static constexpr int ROW_BYTES = D * (int)sizeof(T);
   static constexpr int CH = ROW_BYTES / 16;      // 16-byte chunks of a row
@@ -124,7 +146,7 @@ constexpr long long kMaxLen = 1LL << 30;  // key indexes of a few tiles beyond i
 
 __device__ __forceinline__ int seq_len(const AttnParams &p, int s, bool report) {
   const int len = p.lens[s];
-  const long long most = min((long long)p.max_pages * p.page_size, kMaxLen);
+  const long long most = min((long long)p.max_pages * p.page_size.d, kMaxLen);
   if (len > most) {
     if (report) set_error(p.err, kDevBadPage);
     return (int)most;
@@ -139,22 +161,31 @@ __device__ __forceinline__ int item_tiles(int len, int kt) {
 }
 
 struct Place {
-  int seq;          // sequence of the block's first tile
+  int seq, len;     // sequence of the block's first tile
   long long first;  // line position of that sequence's first tile
-  long long total;  // tiles of all items
 };
+
+// Quotient of line positions, in 32 bits where they fit (a 64-bit division
+// costs some hundred instructions at the head of every block).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
 // Block-wide: finds where line position begin(total) lies. Each thread sums
 // a run of sequences; the thread whose run holds the position walks it.
-template <class F>
-__device__ Place find_place(const AttnParams &p, int kt, int items_per_seq, F begin,
-                            long long (&warp_sum)[4], Place &shared) {
+// False when the position is beyond the line.
+template <int THREADS, class F>
+__device__ bool find_place(const AttnParams &p, int kt, int items_per_seq, F begin,
+                           long long (&warp_sum)[THREADS / 32], Place &found) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.n_seqs + kThreads - 1) / kThreads;
+  const int per = (p.n_seqs + THREADS - 1) / THREADS;
   const int s0 = min(tid * per, p.n_seqs), s1 = min(s0 + per, p.n_seqs);
   long long sum = 0;
-  for (int s = s0; s < s1; ++s)
-    sum += (long long)item_tiles(seq_len(p, s, blockIdx.x == 0), kt) * items_per_seq;
+  int len = 0;
+  for (int s = s0; s < s1; ++s) {
+    len = seq_len(p, s, blockIdx.x == 0);
+    sum += (long long)item_tiles(len, kt) * items_per_seq;
+  }
   long long scan = sum;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -165,7 +196,7 @@ __device__ Place find_place(const AttnParams &p, int kt, int items_per_seq, F be
   __syncthreads();
   long long before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     if (w < warp) before += warp_sum[w];
     total += warp_sum[w];
   }
@@ -174,18 +205,17 @@ __device__ Place find_place(const AttnParams &p, int kt, int items_per_seq, F be
   if (x >= before && x < before + sum) {
     long long at = before;
     for (int s = s0; s < s1; ++s) {
-      const long long n = (long long)item_tiles(seq_len(p, s, false), kt) * items_per_seq;
+      if (per > 1) len = seq_len(p, s, false);
+      const long long n = (long long)item_tiles(len, kt) * items_per_seq;
       if (x < at + n) {
-        shared = Place{s, at, total};
+        found = Place{s, len, at};
         break;
       }
       at += n;
     }
   }
   __syncthreads();
-  Place r = shared;
-  r.total = total;
-  return r;
+  return x < total;
 }
 
 // ---- one tile on the matrix instruction (bf16) -------------------------------
@@ -446,13 +476,12 @@ struct TileOf<Cfg<__nv_bfloat16, D, WM>> {
   using type = TileBf16<Cfg<__nv_bfloat16, D, WM>>;
 };
 
-// Output row (element offset / D) of row r of an item, or -1 beyond its rows.
-__device__ __forceinline__ long long out_row(const AttnParams &p, int item, int r, int rows) {
-  const int per_seq = p.H_kv * p.row_blocks, s = item / per_seq, x = item % per_seq;
-  const int kvh = x / p.row_blocks, row = x % p.row_blocks * rows + r;
-  const int G = p.H / p.H_kv;
-  if (row >= p.T * G) return -1;
-  const int t = row / G, g = row % G;
+// Row of q and out (in units of D elements) of row r of an item's block of
+// rows, or -1 beyond the item's rows.
+__device__ __forceinline__ long long out_row(const AttnParams &p, int s, int kvh, int r) {
+  const int G = p.G.d;
+  if (r >= p.T * G) return -1;
+  const int t = p.G.div(r), g = r - t * G;
   const int h = p.grouped ? kvh * G + g : g * p.H_kv + kvh;
   return ((long long)s * p.T + t) * p.H + h;
 }
@@ -466,86 +495,81 @@ __device__ __forceinline__ void store4(T *p, float4 v) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnParams p) {
   using T = typename C::In;
   using Tile = typename TileOf<C>::type;
   constexpr int D = C::D, KT = C::KT, ROWS = C::ROWS, WK = C::WK, S = C::STAGES;
   constexpr bool Q_IN_STAGE = C::QREG;
+  constexpr int NT = C::THREADS;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long offs[2][KT], warp_sum[4];
+  __shared__ long long offs[4][KT], rows[ROWS], warp_sum[NT / 32];
   __shared__ Place place;
-  __shared__ float2 sml[WK * ROWS];
+  // the key groups' (m, l) at the end of an item take the place of its keys' addresses
+  static_assert(WK * ROWS * sizeof(float2) <= sizeof(offs), "m and l fit");
+  float2 *sml = reinterpret_cast<float2 *>(offs);
   const int tid = threadIdx.x;
   const uint32_t tiles_s = smem_u32(smem);
   const uint32_t q_s = tiles_s + (Q_IN_STAGE ? S - 1 : S) * 2 * C::TILE;
   float *p_s = reinterpret_cast<float *>(smem + S * 2 * C::TILE + C::Q_BYTES);  // fp32 only
   float *so = reinterpret_cast<float *>(smem);
-  const int G = p.H / p.H_kv, items_per_seq = p.H_kv * p.row_blocks;
+  const int items_per_seq = p.H_kv * p.row_blocks.d;
   const T *kc = static_cast<const T *>(p.k), *vc = static_cast<const T *>(p.v);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  long long run = 0;  // tiles of a block
-  const Place at = find_place(
+  long long run = 0, total = 0;  // tiles of a block, of all items
+  const bool any = find_place<NT>(
       p, KT, items_per_seq,
-      [&](long long total) {
-        run = (total + gridDim.x - 1) / gridDim.x;
-        if (run < kMinTiles) run = kMinTiles;
+      [&](long long n) {
+        total = n;
+        run = max(quotient(n + gridDim.x - 1, gridDim.x), (long long)kMinTiles);
         return run * blockIdx.x;
       },
       warp_sum, place);
-  long long pos = run * blockIdx.x;
-  const long long end = min(pos + run, at.total);
-  if (pos >= end) {
+  if (!any) {
     if (tid == 0) p.cut[blockIdx.x].x = -1;
     return;
   }
-  int s = at.seq;
-  int len = seq_len(p, s, false), nt = item_tiles(len, KT);
-  const long long in_seq = pos - at.first;
-  int x = (int)(in_seq / nt), tile0 = (int)(in_seq % nt);  // item of the sequence, its tile
-
-  if (tid == 0) {
-    // the first block that starts inside an item has it joined
-    const long long a = pos - tile0, before = pos - run;
-    const bool joins = tile0 > 0 && before <= a;
-    p.cut[blockIdx.x] = make_int4(joins ? s * items_per_seq + x : -1, (int)(a / run),
-                                  (int)((a + nt - 1) / run), a == before ? 0 : 1);
-  }
+  long long pos = run * blockIdx.x;
+  const long long end = min(pos + run, total);
+  int s = place.seq, len = place.len, nt = item_tiles(len, KT);
+  int x = (int)quotient(pos - place.first, nt);  // item of the sequence
+  int tile0 = (int)(pos - place.first - (long long)x * nt);
 
   for (int seg = 0; pos < end; ++seg) {
     const int n = (int)min((long long)(nt - tile0), end - pos);  // tiles of this item here
-    const int kvh = x / p.row_blocks, r0 = x % p.row_blocks * ROWS;
-    const int item = s * items_per_seq + x;
+    const int kvh = p.row_blocks.div(x), r0 = (x - kvh * (int)p.row_blocks.d) * ROWS;
     const long long head = (long long)kvh * p.head_stride;
     const int32_t *table = p.table + (long long)s * p.max_pages;
 
     // address of key tid of tile i, for its turn in offs (-1: zeros)
     auto page_of = [&](int i) -> int {
       const int key = (tile0 + i) * KT + tid;
-      return tid < KT && i < n && key < len ? table[(unsigned)key / (unsigned)p.page_size] : -1;
+      return tid < KT && i < n && key < len ? table[p.page_size.div(key)] : -1;
     };
     auto put_offs = [&](int i, int page) {
       if (tid >= KT) return;
       const int key = (tile0 + i) * KT + tid;
       long long off = -1;
       if (i < n && key < len) {
-        if (page < 0 || page >= p.n_pages) set_error(p.err, kDevBadPage);
-        else
-          off = page * p.page_stride +
-                (long long)((unsigned)key % (unsigned)p.page_size) * p.token_stride + head;
+        if (page < 0 || page >= p.n_pages) {
+          set_error(p.err, kDevBadPage);
+        } else {
+          const int in_page = key - p.page_size.div(key) * (int)p.page_size.d;
+          off = page * p.page_stride + in_page * p.token_stride + head;
+        }
       }
-      offs[i & 1][tid] = off;
+      offs[i & 3][tid] = off;
     };
     auto load_tile = [&](int i) {
       if (i < n) {
         const uint32_t st = tiles_s + (uint32_t)(i % S) * 2 * C::TILE;
-        constexpr int RSTEP = kThreads / C::CH;
+        constexpr int RSTEP = NT / C::CH;
         const int c = tid % C::CH;
 #pragma unroll
         for (int j = 0; j < KT / RSTEP; ++j) {
           const int row = tid / C::CH + j * RSTEP;
-          const long long off = offs[i & 1][row];
+          const long long off = offs[i & 3][row];
           const bool live = off >= 0;
           const long long e = (live ? off : 0) + c * (16 / (int)sizeof(T));
           cp_async16(st + chunk_at<C>(row, c), kc + e, live);
@@ -555,31 +579,43 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnPar
       cp_async_commit();
     };
 
+    // the first tiles' pages are looked up together
+    int page[S + 1];
+#pragma unroll
+    for (int i = 0; i <= S; ++i) page[i] = page_of(i);
+    for (int r = tid; r < ROWS; r += NT) rows[r] = out_row(p, s, kvh, r0 + r);
+#pragma unroll
+    for (int i = 0; i < S; ++i) put_offs(i, page[i]);
+    __syncthreads();
     // q rows of the item (zeros beyond them) join the first tile's copies
-    for (int e = tid; e < ROWS * C::CH; e += kThreads) {
+    for (int e = tid; e < ROWS * C::CH; e += NT) {
       const int r = e / C::CH, c = e % C::CH;
-      const long long row = out_row(p, item, r, ROWS);
+      const long long row = rows[r];
       cp_async16(q_s + chunk_at<C>(r, c),
                  static_cast<const T *>(p.q) + (row < 0 ? 0 : row) * D + c * (16 / (int)sizeof(T)),
                  row >= 0);
     }
-    int page = page_of(0);
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-      put_offs(i, page);
-      page = page_of(i + 1);
-      __syncthreads();
-      load_tile(i);
+    for (int i = 0; i < S - 1; ++i) load_tile(i);
+    int next_page = page[S];
+
+    if (seg == 0 && tid == NT - 1) {
+      // the first block that starts inside an item has it joined
+      const long long a = pos - tile0, before = pos - run;
+      const bool joins = tile0 > 0 && before <= a;
+      int4 cut = make_int4(-1, 0, 0, 0);
+      if (joins)
+        cut = make_int4(s * items_per_seq + x, (int)quotient(a, run),
+                        (int)quotient(a + nt - 1, run), a == before ? 0 : 1);
+      p.cut[blockIdx.x] = cut;
     }
-    put_offs(S - 1, page);
-    page = page_of(S);
 
     int lim[sizeof(Tile::m) / sizeof(float)];
     Tile::limits(
         [&](int r) {
           const int row = r0 + r;
           // rows beyond the item's are not stored: no mask for their sake
-          return row < p.T * G ? len - p.T + row / G + 1 : INT_MAX;
+          return row < p.T * (int)p.G.d ? len - p.T + p.G.div(row) + 1 : INT_MAX;
         },
         lim);
     Tile acc;
@@ -591,8 +627,8 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnPar
         if (Q_IN_STAGE) __syncthreads();  // q is in registers before its place is loaded
       }
       load_tile(i + S - 1);
-      put_offs(i + S, page);
-      page = page_of(i + S + 1);
+      put_offs(i + S, next_page);
+      next_page = page_of(i + S + 1);
       const uint32_t st = tiles_s + (uint32_t)(i % S) * 2 * C::TILE;
       acc.tile(st, st + C::TILE, (tile0 + i) * KT, lim, p.scale_log2, p_s);
     }
@@ -603,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnPar
 
     const bool whole = n == nt;
     const long long slot = (long long)blockIdx.x * 2 + (seg > 0);
-    for (int e = tid; e < ROWS * (D / 4); e += kThreads) {
+    for (int e = tid; e < ROWS * (D / 4); e += NT) {
       const int r = e / (D / 4), c = e % (D / 4) * 4;
       float mm = -INFINITY;
 #pragma unroll
@@ -622,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnPar
         sum.z = fmaf(f, v.z, sum.z);
         sum.w = fmaf(f, v.w, sum.w);
       }
-      const long long row = out_row(p, item, r, ROWS);
+      const long long row = rows[r];
       if (row < 0) continue;
       if (whole) {
         // a row without keys has ll = 0 and sum = 0: its output is 0
@@ -649,14 +685,16 @@ __global__ void __launch_bounds__(kThreads, C::PER_SM) attn_kernel(const AttnPar
 // Joins the cut items: block (i, r) row r of the item that the main kernel's
 // block i listed. The warps take the pieces in turn, a lane D / 32 columns.
 template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads) join_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int VL = D / 32;
   const int4 cut = p.cut[blockIdx.x];
   if (cut.x < 0) return;
   const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long row = out_row(p, cut.x, r, ROWS);
+  const int per_seq = p.H_kv * (int)p.row_blocks.d, s = cut.x / per_seq, x = cut.x - s * per_seq;
+  const int kvh = p.row_blocks.div(x), rb = x - kvh * (int)p.row_blocks.d;
+  const long long row = out_row(p, s, kvh, rb * ROWS + r);
   if (row < 0) return;
   const int np = cut.z - cut.y + 1;
   // the item is the first block's last item (its only one if it starts there),
@@ -685,7 +723,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const AttnParams p) {
   if (lane == 0) sl[warp] = ll;
   __syncthreads();
   const float l4 = sl[0] + sl[1] + sl[2] + sl[3], inv = 1.f / (l4 == 0.f ? 1.f : l4);
-  for (int c = threadIdx.x; c < D; c += kThreads) {
+  for (int c = threadIdx.x; c < D; c += kJoinThreads) {
     const float v = (so[0][c] + so[1][c] + so[2][c] + so[3][c]) * inv;
     T *out = static_cast<T *>(p.out) + row * D + c;
     if constexpr (sizeof(T) == 2) *out = __float2bfloat16_rn(v);
@@ -714,15 +752,15 @@ int grid_of(const KvLayout &c, int n_seqs, int max_pages, int row_blocks, bool t
 
 template <class C>
 cudaError_t launch_cfg(const AttnParams &p, int grid, cudaStream_t stream) {
-  static_assert(C::SMEM <= 227 * 1024 - 2048, "shared memory");
+  static_assert(C::SMEM + 4 * C::KT * 8 + 8 * C::ROWS + 128 <= 227 * 1024, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_kernel<C>, dim3(grid), dim3(kThreads), C::SMEM, stream, p);
+  e = launch_pdl(attn_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, p);
   if (e != cudaSuccess || grid == 1) return e;
-  const int rows = p.row_blocks > 1 ? C::ROWS : p.T * (p.H / p.H_kv);
+  const int rows = p.row_blocks.d > 1 ? C::ROWS : p.T * (int)p.G.d;
   return launch_pdl(join_kernel<typename C::In, C::D, C::ROWS>, dim3(grid, rows),
-                    dim3(kThreads), 0, stream, p);
+                    dim3(kJoinThreads), 0, stream, p);
 }
 
 template <int D>
@@ -763,12 +801,14 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream) {
   p.table = a.table; p.lens = a.lens;
   p.page_stride = c.page_stride; p.token_stride = c.token_stride; p.head_stride = c.head_stride;
   p.n_seqs = a.n_seqs; p.T = a.T; p.H = a.H; p.H_kv = c.H_kv;
-  p.n_pages = c.n_pages; p.page_size = c.page_size; p.max_pages = a.max_pages;
-  p.row_blocks = (total + rows - 1) / rows;
+  p.n_pages = c.n_pages; p.max_pages = a.max_pages;
+  p.page_size = FastDiv(c.page_size);
+  p.G = FastDiv(a.H / c.H_kv);
+  p.row_blocks = FastDiv((total + rows - 1) / rows);
   p.grouped = a.grouped;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.err = a.err;
-  const int grid = grid_of(c, a.n_seqs, a.max_pages, p.row_blocks, two_per_sm(c, rows));
+  const int grid = grid_of(c, a.n_seqs, a.max_pages, p.row_blocks.d, two_per_sm(c, rows));
   unsigned char *ws = static_cast<unsigned char *>(a.workspace);
   p.cut = reinterpret_cast<int4 *>(ws);
   p.part_ml = reinterpret_cast<float2 *>(ws + up256((size_t)grid * 16));
