@@ -105,14 +105,14 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// Tile geometry. WM: warps along the rows (bf16), 16 rows each; the other
-// warps share out the tile's keys.
+// Tile geometry. bf16: WM warps along the rows, 16 rows each; the other warps
+// share out the tile's keys. fp32: WM rows of each warp, all warps on all keys.
 template <typename T, int D_, int WM_>
 struct Cfg {
   using In = T;
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int D = D_, WM = WM_;
-  static constexpr int ROWS = kBf16 ? 16 * WM : 16;
+  static constexpr int ROWS = kBf16 ? 16 * WM : 4 * WM;
   // Two warps for each of an SM's schedulers: two blocks of four, or one of
   // eight where the tiles leave room for one block only and a warp has at
   // least 16 keys of its own.
@@ -130,7 +130,9 @@ struct Cfg {
   // the last stage's place before that stage is first used
   static constexpr bool QREG = kBf16 && D <= 128;
   static constexpr int SMEM = STAGES * 2 * TILE + (QREG ? 0 : Q_BYTES) + P_BYTES;
-  static constexpr int PER_SM = SMEM <= 110 * 1024 ? 2 : 1;
+  // blocks of an SM: what its shared memory holds, up to four of them
+  static constexpr int FIT = 224 * 1024 / (SMEM + 4 * 1024);
+  static constexpr int PER_SM = FIT > 4 ? 4 : FIT < 1 ? 1 : FIT;
   static_assert(!QREG || Q_BYTES <= 2 * TILE, "q fits a stage");
   static_assert(WK * ROWS * D * 4 <= STAGES * 2 * TILE, "the join reuses the tiles");
 };
@@ -263,12 +265,15 @@ struct TileBf16 {
       } else {
         ldsm4(a, q_addr + chunk_at<C>(qrow, ks * 2 + (lane >> 4)));
       }
+      // a step's fragments are all under way before its first product
+      uint32_t b[KW / 16][4];
+#pragma unroll
+      for (int n = 0; n < KW / 16; ++n)
+        ldsm4(b[n], k_s + chunk_at<C>(kbase + n * 16 + krow, ks * 2 + kch));
 #pragma unroll
       for (int n = 0; n < KW / 16; ++n) {
-        uint32_t b[4];
-        ldsm4(b, k_s + chunk_at<C>(kbase + n * 16 + krow, ks * 2 + kch));
-        mma16816(s[2 * n], a, b[0], b[1]);
-        mma16816(s[2 * n + 1], a, b[2], b[3]);
+        mma16816(s[2 * n], a, b[n][0], b[n][1]);
+        mma16816(s[2 * n + 1], a, b[n][2], b[n][3]);
       }
     }
     // scaled scores, masked beyond each row's last key; running maximum
@@ -284,21 +289,23 @@ struct TileBf16 {
         s[i][e] = x;
         mx[e >> 1] = fmaxf(mx[e >> 1], x);
       }
-    float ref[2];
+    float ref[2], alpha[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
       mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
       const float mn = fmaxf(m[r], mx[r]);
       ref[r] = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every p is 0
-      const float alpha = exp2f(m[r] - ref[r]);
+      alpha[r] = exp2f(m[r] - ref[r]);
       m[r] = mn;
-      l[r] *= alpha;
+      l[r] *= alpha[r];
+    }
+    // the sums are only touched when some row's maximum has moved
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        o[i][2 * r] *= alpha;
-        o[i][2 * r + 1] *= alpha;
-      }
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] *= alpha[e >> 1];
     }
 #pragma unroll
     for (int i = 0; i < KW / 8; ++i)
@@ -314,11 +321,16 @@ struct TileBf16 {
                              bf16x2(s[2 * n + 1][0], s[2 * n + 1][1]),
                              bf16x2(s[2 * n + 1][2], s[2 * n + 1][3])};
 #pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        uint32_t b[4];
-        ldsm4_t(b, v_s + chunk_at<C>(kbase + n * 16 + vrow, d * 2 + vch));
-        mma16816(o[2 * d], a, b[0], b[1]);
-        mma16816(o[2 * d + 1], a, b[2], b[3]);
+      for (int d0 = 0; d0 < D / 16; d0 += 4) {
+        uint32_t b[4][4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          ldsm4_t(b[d], v_s + chunk_at<C>(kbase + n * 16 + vrow, (d0 + d) * 2 + vch));
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          mma16816(o[2 * (d0 + d)], a, b[d][0], b[d][1]);
+          mma16816(o[2 * (d0 + d) + 1], a, b[d][2], b[d][3]);
+        }
       }
     }
   }
@@ -351,21 +363,28 @@ struct TileBf16 {
 };
 
 // ---- one tile on the CUDA cores (fp32) -----------------------------------------
-// A warp has 4 rows. Scores: a lane has one key of the 32, and reads its row
+// A warp has R rows. Scores: a lane has one key of the 32, and reads its row
 // of K in 16-byte chunks (eight lanes, eight bank groups) beside broadcast
 // chunks of q. Sums: a lane has D / 32 columns, and reads V rows beside
-// broadcast p.
+// broadcast p. Products go two to an instruction.
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float c, float d) {
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\t"
+      "mov.b64 w, {%4, %5};\n\tfma.rn.f32x2 u, v, w, u;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
 template <class C>
 struct TileF32 {
-  static constexpr int D = C::D, VL = D / 32;
-  float o[4][VL];
-  float m[4], l[4];
+  static constexpr int D = C::D, VL = D / 32, R = C::WM;
+  float o[R][VL];
+  float m[R], l[R];
   uint32_t q_addr;
 
   __device__ __forceinline__ void start(uint32_t q_s) {
     q_addr = q_s;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
       m[r] = -INFINITY;
       l[r] = 0.f;
 #pragma unroll
@@ -379,7 +398,7 @@ struct TileF32 {
                  : "r"(a));
     return v;
   }
-  // column i of the lane: chunk (lane * VL + i) / 4; two-column lanes read half a chunk
+  // the lane's columns of a row of V: chunks lane, 32 + lane, or half a chunk
   static __device__ __forceinline__ void lds_v(uint32_t v_s, int row, float (&x)[VL]) {
     const int lane = threadIdx.x & 31;
     if constexpr (VL == 2) {
@@ -395,30 +414,30 @@ struct TileF32 {
     }
   }
   template <class F>
-  static __device__ __forceinline__ void limits(F limit_of, int (&lim)[4]) {
+  static __device__ __forceinline__ void limits(F limit_of, int (&lim)[R]) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) lim[r] = limit_of((threadIdx.x >> 5) * 4 + r);
+    for (int r = 0; r < R; ++r) lim[r] = limit_of((threadIdx.x >> 5) * R + r);
   }
-  __device__ __forceinline__ void tile(uint32_t k_s, uint32_t v_s, int key0, const int (&lim)[4],
+  __device__ __forceinline__ void tile(uint32_t k_s, uint32_t v_s, int key0, const int (&lim)[R],
                                        float scale_log2, float *p_s) {
-    const int lane = threadIdx.x & 31, row0 = (threadIdx.x >> 5) * 4;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
+    const int lane = threadIdx.x & 31, row0 = (threadIdx.x >> 5) * R;
+    float s[R], s2[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r] = s2[r] = 0.f;
+#pragma unroll(R > 4 ? 2 : 4)
     for (int c = 0; c < C::CH; ++c) {
       const float4 k = lds4(k_s + chunk_at<C>(lane, c));
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < R; ++r) {
         const float4 q = lds4(q_addr + chunk_at<C>(row0 + r, c));
-        s[r] = fmaf(q.x, k.x, s[r]);
-        s[r] = fmaf(q.y, k.y, s[r]);
-        s[r] = fmaf(q.z, k.z, s[r]);
-        s[r] = fmaf(q.w, k.w, s[r]);
+        fma2(s[r], s2[r], q.x, q.y, k.x, k.y);
+        fma2(s[r], s2[r], q.z, q.w, k.z, k.w);
       }
     }
     __syncwarp();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float x = key0 + lane < lim[r] ? s[r] * scale_log2 : -INFINITY;
+    for (int r = 0; r < R; ++r) {
+      const float x = key0 + lane < lim[r] ? (s[r] + s2[r]) * scale_log2 : -INFINITY;
       float mx = x;
 #pragma unroll
       for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -431,29 +450,29 @@ struct TileF32 {
       for (int i = 0; i < VL; ++i) o[r][i] *= alpha;
     }
     __syncwarp();
-#pragma unroll 4
-    for (int j = 0; j < C::KT; j += 4) {
-      float4 pj[4];
+#pragma unroll(R > 4 ? 2 : 4)
+    for (int j = 0; j < C::KT; j += 2) {
+      float2 pj[R];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        pj[r] = *reinterpret_cast<const float4 *>(p_s + (row0 + r) * C::KT + j);
+      for (int r = 0; r < R; ++r)
+        pj[r] = *reinterpret_cast<const float2 *>(p_s + (row0 + r) * C::KT + j);
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
+      for (int jj = 0; jj < 2; ++jj) {
         float x[VL];
         lds_v(v_s, j + jj, x);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float e = jj == 0 ? pj[r].x : jj == 1 ? pj[r].y : jj == 2 ? pj[r].z : pj[r].w;
+        for (int r = 0; r < R; ++r) {
+          const float e = jj ? pj[r].y : pj[r].x;
 #pragma unroll
-          for (int i = 0; i < VL; ++i) o[r][i] = fmaf(e, x[i], o[r][i]);
+          for (int i = 0; i < VL; i += 2) fma2(o[r][i], o[r][i + 1], x[i], x[i + 1], e, e);
         }
       }
     }
   }
   __device__ __forceinline__ void flush(float *so, float2 *sml) {
-    const int lane = threadIdx.x & 31, row0 = (threadIdx.x >> 5) * 4;
+    const int lane = threadIdx.x & 31, row0 = (threadIdx.x >> 5) * R;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < R; ++r) {
       float t = l[r];
 #pragma unroll
       for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
@@ -733,18 +752,42 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnParams p) 
 
 // ---- host side ------------------------------------------------------------------
 
-// Rows of a block: as few blocks of 16, 32 or 64 as hold all of an item's
-// rows (each block reads the keys again), the smallest that do.
-int rows_of(bool bf16, int rows) { return !bf16 || rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Calls f with the configuration of a head size, type and number of rows (T
+// x G of an item): the smallest block of rows that holds them all, or the
+// largest there is (each block of rows reads the keys again).
+template <typename T, int D, class F>
+auto with_rows(int rows, F f) {
+  if constexpr (sizeof(T) == 2) {
+    if (rows <= 16) return f(Cfg<T, D, 1>{});
+    if (rows <= 32) return f(Cfg<T, D, 2>{});
+    return f(Cfg<T, D, 4>{});
+  } else {
+    if (rows <= 4) return f(Cfg<T, D, 1>{});
+    if (rows <= 8) return f(Cfg<T, D, 2>{});
+    if constexpr (D < 256)  // q and the tiles of 32 rows of 256 fill more than an SM has
+      if (rows > 16) return f(Cfg<T, D, 8>{});
+    return f(Cfg<T, D, 4>{});
+  }
+}
+template <typename T, class F>
+auto with_d(int D, int rows, F f) {
+  if (D == 64) return with_rows<T, 64>(rows, f);
+  if (D == 128) return with_rows<T, 128>(rows, f);
+  return with_rows<T, 256>(rows, f);
+}
+template <class F>
+auto with_cfg(const KvLayout &c, int rows, F f) {
+  return c.bf16 ? with_d<__nv_bfloat16>(c.D, rows, f) : with_d<float>(c.D, rows, f);
+}
 
 constexpr int kSms = 152;
 
-int grid_of(const KvLayout &c, int n_seqs, int max_pages, int row_blocks, bool two_per_sm) {
-  const int kt = c.bf16 ? 64 : 32;
-  const long long tiles = ((long long)max_pages * c.page_size + kt - 1) / kt;
-  const long long most = two_per_sm ? 2 * kSms : kSms;
+// Blocks of the grid: all that fit the GPU, or as many as there can be tiles.
+template <class C>
+int grid_of(const KvLayout &c, int n_seqs, int max_pages, int row_blocks) {
+  const long long tiles = ((long long)max_pages * c.page_size + C::KT - 1) / C::KT;
+  const long long most = (long long)C::PER_SM * kSms;
   const long long items = (long long)n_seqs * c.H_kv * row_blocks;
-  // more blocks than tiles have nothing to do
   if (tiles < most && items * (tiles < 1 ? 1 : tiles) < most)
     return (int)(items * (tiles < 1 ? 1 : tiles));
   return (int)most;
@@ -763,39 +806,22 @@ cudaError_t launch_cfg(const AttnParams &p, int grid, cudaStream_t stream) {
                     dim3(kJoinThreads), 0, stream, p);
 }
 
-template <int D>
-cudaError_t launch_d(const AttnParams &p, bool bf16, int rows, int grid, cudaStream_t stream) {
-  if (!bf16) return launch_cfg<Cfg<float, D, 1>>(p, grid, stream);
-  if (rows == 16) return launch_cfg<Cfg<__nv_bfloat16, D, 1>>(p, grid, stream);
-  if (rows == 32) return launch_cfg<Cfg<__nv_bfloat16, D, 2>>(p, grid, stream);
-  return launch_cfg<Cfg<__nv_bfloat16, D, 4>>(p, grid, stream);
-}
-
-bool two_per_sm(const KvLayout &c, int rows) {
-  if (!c.bf16)
-    return c.D == 64 ? Cfg<float, 64, 1>::PER_SM == 2
-                     : c.D == 128 ? Cfg<float, 128, 1>::PER_SM == 2 : false;
-  if (c.D == 64) return true;
-  if (c.D == 128)
-    return rows == 64 ? Cfg<__nv_bfloat16, 128, 4>::PER_SM == 2
-                      : Cfg<__nv_bfloat16, 128, 1>::PER_SM == 2;
-  return false;
-}
-
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
 size_t attn_workspace_size(const KvLayout &c, int n_seqs, int T, int H, int max_pages) {
-  const int total = T * (H / c.H_kv), rows = rows_of(c.bf16, total);
-  const size_t g = (size_t)grid_of(c, n_seqs, max_pages, (total + rows - 1) / rows,
-                                   two_per_sm(c, rows));
-  return up256(g * 16) + up256(g * 2 * rows * 8) + g * 2 * rows * c.D * 4;
+  const int rows = T * (H / c.H_kv);
+  return with_cfg(c, rows, [&](auto cfg) -> size_t {
+    using C = decltype(cfg);
+    const size_t g = (size_t)grid_of<C>(c, n_seqs, max_pages, (rows + C::ROWS - 1) / C::ROWS);
+    return up256(g * 16) + up256(g * 2 * C::ROWS * 8) + g * 2 * C::ROWS * c.D * 4;
+  });
 }
 
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream) {
   const KvLayout &c = a.cache;
-  const int total = a.T * (a.H / c.H_kv), rows = rows_of(c.bf16, total);
+  const int rows = a.T * (a.H / c.H_kv);
   AttnParams p{};
   p.q = a.q; p.k = a.k_cache; p.v = a.v_cache; p.out = a.out;
   p.table = a.table; p.lens = a.lens;
@@ -804,19 +830,20 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream) {
   p.n_pages = c.n_pages; p.max_pages = a.max_pages;
   p.page_size = FastDiv(c.page_size);
   p.G = FastDiv(a.H / c.H_kv);
-  p.row_blocks = FastDiv((total + rows - 1) / rows);
   p.grouped = a.grouped;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.err = a.err;
-  const int grid = grid_of(c, a.n_seqs, a.max_pages, p.row_blocks.d, two_per_sm(c, rows));
-  unsigned char *ws = static_cast<unsigned char *>(a.workspace);
-  p.cut = reinterpret_cast<int4 *>(ws);
-  p.part_ml = reinterpret_cast<float2 *>(ws + up256((size_t)grid * 16));
-  p.part_o = reinterpret_cast<float *>(ws + up256((size_t)grid * 16) +
-                                       up256((size_t)grid * 2 * rows * 8));
-  if (c.D == 64) return launch_d<64>(p, c.bf16, rows, grid, stream);
-  if (c.D == 128) return launch_d<128>(p, c.bf16, rows, grid, stream);
-  return launch_d<256>(p, c.bf16, rows, grid, stream);
+  return with_cfg(c, rows, [&](auto cfg) -> cudaError_t {
+    using C = decltype(cfg);
+    p.row_blocks = FastDiv((rows + C::ROWS - 1) / C::ROWS);
+    const int grid = grid_of<C>(c, a.n_seqs, a.max_pages, (int)p.row_blocks.d);
+    unsigned char *ws = static_cast<unsigned char *>(a.workspace);
+    p.cut = reinterpret_cast<int4 *>(ws);
+    ws += up256((size_t)grid * 16);
+    p.part_ml = reinterpret_cast<float2 *>(ws);
+    p.part_o = reinterpret_cast<float *>(ws + up256((size_t)grid * 2 * C::ROWS * 8));
+    return launch_cfg<C>(p, grid, stream);
+  });
 }
 
 }  // namespace gdn
