@@ -117,6 +117,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
   return mbar_wait_n(bar, parity, err, site, kMaxPolls);
 }
 
+// Waits for two phases at once: a poll takes some 150 cycles even of a phase
+// that has completed, and the two polls of a round overlap.
+__device__ __forceinline__ bool mbar_wait_both(uint64_t *bar0, uint32_t parity0, uint64_t *bar1,
+                                               uint32_t parity1, int *err, int site) {
+  for (uint32_t i = 0; i < kMaxPolls; ++i) {
+    const bool a = mbar_try_wait(bar0, parity0), b = mbar_try_wait(bar1, parity1);
+    if (a && b) return true;
+  }
+  set_error(err, kDevTimeout | (site << 8));
+  return false;
+}
+
 // Orders this thread's generic-proxy shared-memory accesses before later
 // async-proxy accesses (TMA copies and stores, tcgen05.mma operands).
 __device__ __forceinline__ void fence_proxy_async() {

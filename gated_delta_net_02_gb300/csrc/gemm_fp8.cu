@@ -11,19 +11,24 @@
 // block while the epilogue warps take the other.
 //
 // Roles of a block of threads: one thread issues TMA loads into a ring of
-// 128-byte-swizzled stages (one scale block of k each), one the tensor-core
-// instructions, one warp brings the stages' scales into a ring of their own,
-// and the epilogue warps keep the fp32 sums of the whole k in registers.
+// 128-byte-swizzled stages (one scale block of k each), one warp the
+// tensor-core instructions, and the epilogue warps keep the fp32 sums of the
+// whole k in registers; scales reach them a group of stages at a time.
 //
-// Two forms:
-//  * few rows of A: the rows of B are the instruction's 128 rows and the rows
-//    of A its 16 to 128 columns, so that no tensor-core row idles. Bound by
-//    the read of B: k is split over a cluster of up to 8 blocks, which add
-//    their sums through distributed shared memory in rank order.
-//  * many rows of A: 256 x 256 tiles of a pair of blocks (cta_group::2),
-//    persistent. Should be bound by the tensor cores; 8192 x 8192 x 4096 with
-//    bf16 output takes 210 us (2620 TFLOP/s). Its instructions alone take 123,
-//    with their stages' loads and barriers 163: two tensor-memory buffers are
+// Three forms, by the sizes (figures: one GB300, bf16 output):
+//  * up to 64 rows of A: the rows of B are the instruction's 128 rows and the
+//    rows of A its 16 to 64 columns, so that no tensor-core row idles. Bound
+//    by the read of B: k is split over a cluster of up to 8 blocks, which add
+//    their sums through distributed shared memory in rank order. 64 x 2560 x
+//    2048 6.0 us, 16 x 8192 x 4096 7.3 us (4.6 TB/s).
+//  * at most one 128 x 128 tile for each SM: rows of A as the instruction's
+//    rows (a row's scale is then a lane's own, not a read for each column);
+//    split and joined alike. 256 x 4096 x 4096 10.3 us, 512 x 4096 x 4096
+//    13.5 us (17.7 us as 256 x 256 tiles).
+//  * more: 256 x 256 tiles of a pair of blocks (cta_group::2), persistent.
+//    8192 x 8192 x 4096 198 us (2770 TFLOP/s), 1024 x 4096 x 4096 17.2 us. It
+//    should be bound by the tensor cores: its instructions alone take 123 us,
+//    with the stages' loads and barriers 163. Two tensor-memory buffers are
 //    all there is, and a block's product cannot start before the buffer of
 //    two blocks ago has been read in both blocks of the pair, which takes
 //    about as long again as the product.
@@ -38,7 +43,7 @@ namespace gdn {
 namespace {
 
 constexpr int kBlockK = 128;      // k of a stage, of a scale and of a swizzle row
-constexpr int kScaleSlots = 8;    // ring of scale vectors
+constexpr int kScaleGroup = 8;    // stages whose scales share one barrier
 
 struct GemmParams {
   const float *a_scale, *b_scale;
@@ -111,34 +116,67 @@ __device__ __forceinline__ void add_part(float (&acc)[128], float (&v)[32], floa
 }
 
 struct Bars {
-  uint64_t sfull[kScaleSlots], sempty[kScaleSlots];  // scale ring
-  uint64_t tfull[2], tempty[2];                      // tensor-memory buffers
+  uint64_t sfull[2], sempty[2];  // two groups of scale vectors
+  uint64_t tfull[4], tempty[4];  // tensor-memory buffers
 };
 
-// ---- few rows of A -------------------------------------------------------------
+// The scales of a lane's row of A and of a block of B, four stages at a time
+// and the next four under way. (Brought by a warp of their own through shared
+// memory they cost each stage a barrier, and a wait some 150 cycles.)
+struct RowScales {
+  const float *a, *b;  // NULL a: no such row
+  int n;               // stages
+  float next_a[4], next_b[4], cur[4];
+  __device__ __forceinline__ void fetch(int i0) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool in = i0 + u < n && a;
+      next_a[u] = in ? a[i0 + u] : 0.f;
+      next_b[u] = in ? b[i0 + u] : 0.f;
+    }
+  }
+  // Scales of stages i0 .. i0 + 3 into cur.
+  __device__ __forceinline__ void advance(int i0) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) cur[u] = next_a[u] * next_b[u];
+    fetch(i0 + 4);
+  }
+};
 
-template <int NT>
+// ---- few rows of A, and few tiles -----------------------------------------------
+
+// TOKENS: the instruction's 128 rows are rows of A, its NT = 128 columns rows
+// of B; otherwise the other way round, with NT rows of A.
+template <int NT, bool TOKENS>
 struct SmallCfg {
-  static constexpr int A_BYTES = 128 * kBlockK;  // rows of B, the instruction's rows
+  static_assert(!TOKENS || NT == 128, "square tiles");
+  static constexpr int A_BYTES = 128 * kBlockK;  // the instruction's rows
   static constexpr int STAGE = A_BYTES + NT * kBlockK;
   static constexpr int STAGES = NT <= 32 ? 5 : 4;
+  static constexpr int GROUPS = NT >= 64 ? 2 : 1;  // of four epilogue warps, each on its columns
+  static constexpr int COLS = NT / GROUPS;
+  static constexpr int THREADS = 128 + 128 * GROUPS;
   static constexpr int SMEM = STAGES * STAGE + 1024;
-  static constexpr int TCOLS = NT < 16 ? 32 : 2 * NT;  // two buffers
-  static_assert(NT * 128 * 4 <= STAGES * STAGE, "the sums reuse the stages");
+  static constexpr int BUFS = 4, TCOLS = BUFS * NT;  // tensor-memory buffers
+  // The sums on their way out: [NT][128], or [128][NT + 4] so that a lane's
+  // 16-byte stores of its own row and the reads along rows meet no conflict.
+  static constexpr int PITCH = TOKENS ? NT + 4 : 128;
+  static_assert(4 * PITCH * (TOKENS ? 128 : NT) <= STAGES * STAGE, "the sums reuse the stages");
 };
 
-template <int NT>
-__global__ void __launch_bounds__(256) gemm_small_kernel(const GemmParams p,
+template <int NT, bool TOKENS>
+__global__ void __launch_bounds__(SmallCfg<NT, TOKENS>::THREADS)
+    gemm_small_kernel(const GemmParams p,
                                                          const __grid_constant__ CUtensorMap mb,
                                                          const __grid_constant__ CUtensorMap ma) {
-  using C = SmallCfg<NT>;
-  constexpr int S = C::STAGES;
+  using C = SmallCfg<NT, TOKENS>;
+  constexpr int S = C::STAGES, NB = C::BUFS, SG = kScaleGroup;
   extern __shared__ unsigned char raw[];
   unsigned char *sm =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[S], empty[S];
   __shared__ Bars bars;
-  __shared__ __align__(16) float sc[kScaleSlots][NT];
+  __shared__ __align__(16) float sc[2][TOKENS ? 1 : SG][NT];
   __shared__ uint32_t tm_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x % p.split, n0 = blockIdx.x / p.split * 128, m0 = blockIdx.y * NT;
@@ -150,13 +188,13 @@ __global__ void __launch_bounds__(256) gemm_small_kernel(const GemmParams p,
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(&bars.sfull[i], 32);
-      mbar_init(&bars.sempty[i], 4);
-    }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.sfull[i], 32);
+      mbar_init(&bars.sempty[i], 4 * C::GROUPS);
+    }
+    for (int i = 0; i < NB; ++i) {
       mbar_init(&bars.tfull[i], 1);
-      mbar_init(&bars.tempty[i], 4);
+      mbar_init(&bars.tempty[i], 4 * C::GROUPS);
     }
     fence_mbar_init();
     prefetch_tmap(&mb);
@@ -165,6 +203,10 @@ __global__ void __launch_bounds__(256) gemm_small_kernel(const GemmParams p,
   // Tensor memory only once the kernel before has completed, and the next
   // kernel only once this one has its own: of two kernels on one SM that both
   // allocate, the earlier never waits for the later.
+  // The first tiles of B start for the L2 while the kernel before still runs:
+  // a hint, which changes nothing if that kernel writes them.
+  if (tid == 0)
+    for (int i = 0; i < min(nk, S); ++i) tma_prefetch_2d(&mb, (kb0 + i) * kBlockK, n0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 2) {
     tmem_alloc(&tm_s, C::TCOLS);
@@ -176,7 +218,8 @@ __global__ void __launch_bounds__(256) gemm_small_kernel(const GemmParams p,
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tm = tm_s;
 
-  float acc[NT];
+  float acc[C::COLS];
+  const int col0 = warp < 4 ? 0 : (warp - 4) / 4 * C::COLS;  // the epilogue warp's columns
   if (warp == 0) {
     if (lane == 0)
       for (int i = 0; i < nk; ++i) {
@@ -184,100 +227,130 @@ __global__ void __launch_bounds__(256) gemm_small_kernel(const GemmParams p,
         if (i >= S && !mbar_wait(&empty[s], (i / S - 1) & 1, p.err, kSiteGemmEmpty)) break;
         unsigned char *st = sm + s * C::STAGE;
         mbar_arrive_expect_tx(&full[s], C::STAGE);
-        tma_load_2d(st, &mb, (kb0 + i) * kBlockK, n0, &full[s]);
-        tma_load_2d(st + C::A_BYTES, &ma, (kb0 + i) * kBlockK, m0, &full[s]);
+        tma_load_2d(TOKENS ? st + C::A_BYTES : st, &mb, (kb0 + i) * kBlockK, n0, &full[s]);
+        tma_load_2d(TOKENS ? st : st + C::A_BYTES, &ma, (kb0 + i) * kBlockK, m0, &full[s]);
       }
   } else if (warp == 1) {
     for (int i = 0; i < nk; ++i) {
-      const int s = i % S, b = i & 1;
-      bool ok = i < 2 || mbar_wait(&bars.tempty[b], ((i >> 1) - 1) & 1, p.err, kSiteGemmAcc);
-      ok = ok && mbar_wait(&full[s], (i / S) & 1, p.err, kSiteGemmStage);
+      const int s = i % S, b = i % NB;
+      // a buffer never used yet counts as the phase before the first: given back
+      const bool ok = mbar_wait_both(&bars.tempty[b], (i / NB + 1) & 1, &full[s], (i / S) & 1,
+                                     p.err, kSiteGemmStage);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t st = smem_u32(sm) + s * C::STAGE;
       umma_e4m3_k128(tm + b * NT, sdesc_kmajor(st), sdesc_kmajor(st + C::A_BYTES),
                      idesc_e4m3_f32(128, NT), smem_u32(&empty[s]), smem_u32(&bars.tfull[b]));
     }
-  } else if (warp == 2) {
-    // scales of the tile's columns (rows of A), times the tile's block of B
-    constexpr int PER = (NT + 31) / 32, AHEAD = 4;
+  } else if (warp == 2 && !TOKENS) {
+    // Scales of the tile's rows of A times that of its block of B, a group of
+    // stages at a time; the next group's loads are under way while this one
+    // waits for its place.
+    constexpr int PER = (NT + 31) / 32;
     const float *bs = p.b_scale + (long long)(n0 >> 7) * p.KB + kb0;
-    bool ok = true;
-    for (int i0 = 0; i0 < nk && ok; i0 += AHEAD) {
-      float v[AHEAD][PER];
+    float v[SG][PER], next[SG][PER];
+    auto fetch = [&](int i0) {
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u)
+      for (int u = 0; u < SG; ++u)
 #pragma unroll
         for (int c = 0; c < PER; ++c) {
           const int j = c * 32 + lane;
-          v[u][c] = 0.f;
+          next[u][c] = 0.f;
           if (i0 + u < nk && j < NT && m0 + j < p.M)
-            v[u][c] = p.a_scale[(long long)(m0 + j) * p.KB + kb0 + i0 + u] * bs[i0 + u];
+            next[u][c] = p.a_scale[(long long)(m0 + j) * p.KB + kb0 + i0 + u] * bs[i0 + u];
         }
+    };
+    fetch(0);
+    for (int g = 0; g * SG < nk; ++g) {
 #pragma unroll
-      for (int u = 0; u < AHEAD; ++u) {
-        const int i = i0 + u, s = i % kScaleSlots;
-        if (i >= nk) break;
-        if (i >= kScaleSlots &&
-            !mbar_wait(&bars.sempty[s], (i / kScaleSlots - 1) & 1, p.err, kSiteGemmScale)) {
-          ok = false;
-          break;
-        }
+      for (int u = 0; u < SG; ++u)
+#pragma unroll
+        for (int c = 0; c < PER; ++c) v[u][c] = next[u][c];
+      fetch((g + 1) * SG);
+      const int s = g & 1;
+      if (g >= 2 && !mbar_wait(&bars.sempty[s], (g / 2 - 1) & 1, p.err, kSiteGemmScale)) break;
+#pragma unroll
+      for (int u = 0; u < SG; ++u)
 #pragma unroll
         for (int c = 0; c < PER; ++c)
-          if (c * 32 + lane < NT) sc[s][c * 32 + lane] = v[u][c];
-        mbar_arrive(&bars.sfull[s]);
-      }
+          if (c * 32 + lane < NT) sc[s][u][c * 32 + lane] = v[u][c];
+      mbar_arrive(&bars.sfull[s]);
     }
   } else if (warp >= 4) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j] = 0.f;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    for (int i = 0; i < nk; ++i) {
-      const int b = i & 1, s = i % kScaleSlots;
-      if (!mbar_wait(&bars.sfull[s], (i / kScaleSlots) & 1, p.err, kSiteGemmScale)) break;
-      if (!mbar_wait(&bars.tfull[b], (i >> 1) & 1, p.err, kSiteGemmAcc)) break;
-      tc_fence_after();
+    for (int j = 0; j < C::COLS; ++j) acc[j] = 0.f;
+    const uint32_t src = tm + ((uint32_t)((warp & 3) * 32) << 16) + col0;
+    RowScales rs;
+    if (TOKENS) {
+      const int m = m0 + (warp & 3) * 32 + lane;
+      rs.a = m < p.M ? p.a_scale + (long long)m * p.KB + kb0 : nullptr;
+      rs.b = p.b_scale + (long long)(n0 >> 7) * p.KB + kb0;
+      rs.n = nk;
+      rs.fetch(0);
+    }
+    bool ok = true;
+    for (int i0 = 0; i0 < nk && ok; i0 += 4) {
+      if (TOKENS) rs.advance(i0);
 #pragma unroll
-      for (int c = 0; c < NT; c += 16) {
-        float t[16];
-        tmem_ld16(tm + lanes + b * NT + c, t);
-        if (c + 16 >= NT) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.tempty[b]);
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u, b = i % NB, g = i / SG;
+        if (i >= nk) break;
+        if (!TOKENS && i % SG == 0)
+          ok = mbar_wait(&bars.sfull[g & 1], (g / 2) & 1, p.err, kSiteGemmScale);
+        ok = ok && mbar_wait(&bars.tfull[b], (i / NB) & 1, p.err, kSiteGemmAcc);
+        if (!ok) break;
+        tc_fence_after();
+        float v[C::COLS];
+        if constexpr (C::COLS == 16) {
+          tmem_ld16(src + b * NT, v);
+        } else {
+#pragma unroll
+          for (int c = 0; c < C::COLS; c += 32) tmem_ld32_async(src + b * NT + c, v + c);
+          tmem_wait_ld();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.tempty[b]);
+        float4 f;
+        if (TOKENS) f.x = f.y = f.z = f.w = rs.cur[u];
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 f = *reinterpret_cast<const float4 *>(&sc[s][c + j]);
-          acc[c + j] = fmaf(t[j], f.x, acc[c + j]);
-          acc[c + j + 1] = fmaf(t[j + 1], f.y, acc[c + j + 1]);
-          acc[c + j + 2] = fmaf(t[j + 2], f.z, acc[c + j + 2]);
-          acc[c + j + 3] = fmaf(t[j + 3], f.w, acc[c + j + 3]);
+        for (int j = 0; j < C::COLS; j += 4) {
+          if (!TOKENS) f = *reinterpret_cast<const float4 *>(&sc[g & 1][TOKENS ? 0 : i % SG][col0 + j]);
+          asm volatile("" : "+f"(v[j]), "+f"(v[j + 1]), "+f"(v[j + 2]), "+f"(v[j + 3]));
+          fma2(acc[j], acc[j + 1], v[j], v[j + 1], f.x, f.y);
+          fma2(acc[j + 2], acc[j + 3], v[j + 2], v[j + 3], f.z, f.w);
+        }
+        if (!TOKENS && (i % SG == SG - 1 || i == nk - 1)) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.sempty[g & 1]);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.sempty[s]);
     }
   }
   __syncthreads();  // every stage has been read by the tensor cores
-  float *sums = reinterpret_cast<float *>(sm);  // [NT][128]
+  float *sums = reinterpret_cast<float *>(sm);
   if (warp >= 4) {
     const int row = (warp & 3) * 32 + lane;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) sums[j * 128 + row] = acc[j];
+    for (int j = 0; j < C::COLS; j += TOKENS ? 4 : 1) {
+      if (TOKENS)
+        *reinterpret_cast<float4 *>(sums + row * C::PITCH + col0 + j) =
+            make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+      else
+        sums[(col0 + j) * C::PITCH + row] = acc[j];
+    }
   }
   if (p.split > 1) cluster_sync();
   else __syncthreads();
-  const int cols = NT / p.split;  // columns that this block finishes
+  const int mine = NT / p.split;  // rows of A that this block finishes, 128 columns each
   const bool vec = (p.N & 3) == 0;
-  for (int e = tid; e < cols * 32; e += 256) {
-    const int j = rank * cols + (e >> 5), r = (e & 31) * 4;
-    const uint32_t at = smem_u32(sums + j * 128 + r);
+  for (int e = tid; e < mine * 32; e += C::THREADS) {
+    const int j = rank * mine + (e >> 5), r = (e & 31) * 4;
+    const float *at = sums + j * C::PITCH + r;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = 0; c < p.split; ++c) {
-      const float4 t = p.split > 1 ? ld_cluster_f4(at, c)
-                                   : *reinterpret_cast<const float4 *>(sums + j * 128 + r);
+      const float4 t = p.split > 1 ? ld_cluster_f4(smem_u32(at), c)
+                                   : *reinterpret_cast<const float4 *>(at);
       v.x += t.x; v.y += t.y; v.z += t.z; v.w += t.w;
     }
     if (m0 + j < p.M && n0 + r < p.N)
@@ -297,37 +370,40 @@ __global__ void __launch_bounds__(256) gemm_small_kernel(const GemmParams p,
 struct LargeCfg {
   static constexpr int TM = 256, TN = 256;
   static constexpr int HALF = 128 * kBlockK, STAGE = 2 * HALF;
-  static constexpr int STAGES = 4;
+  static constexpr int STAGES = 4, BOXES = 2;
   static constexpr int BOX = 32 * 128;  // output box of a warp: 32 rows of 128 bytes
-  static constexpr int SMEM = STAGES * STAGE + 8 * 2 * BOX + 1024;
+  static constexpr int SMEM = STAGES * STAGE + 8 * BOXES * BOX + 1024;
   static constexpr int THREADS = 384;  // four warps of roles, eight of epilogue
 };
 
-// Two boxes of the warp's 32 rows: columns c0 .. c0 + 128 (bf16) or + 64
-// (fp32) of acc, lane = row. The warp's earlier boxes have left first.
+// The warp's 32 rows x 128 columns of acc, lane = row, in boxes of 128 bytes.
 template <bool BF16>
-__device__ __forceinline__ void store_box(unsigned char *box, int lane, const CUtensorMap &mo,
-                                          int n0, int m0, const float (&acc)[128], int c0) {
-  if (lane == 0) bulk_wait_read();
-  __syncwarp();
+__device__ __forceinline__ void store_boxes(unsigned char *box, int lane, const CUtensorMap &mo,
+                                            int n0, int m0, const float (&acc)[128]) {
+  constexpr int COLS = BF16 ? 64 : 32;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 128 / COLS; ++i) {
+    unsigned char *at = box + i % LargeCfg::BOXES * LargeCfg::BOX;
+    if (i % LargeCfg::BOXES == 0) {  // the boxes' last contents have left
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
+    }
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        w[k] = BF16 ? pack2(acc[(i * 8 + c) * 8 + 2 * k], acc[(i * 8 + c) * 8 + 2 * k + 1])
-                    : __float_as_uint(acc[c0 + (i * 8 + c) * 4 + k]);
-      *reinterpret_cast<uint4 *>(box + i * LargeCfg::BOX + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        w[k] = BF16 ? pack2(acc[i * 64 + c * 8 + 2 * k], acc[i * 64 + c * 8 + 2 * k + 1])
+                    : __float_as_uint(acc[i * 32 + c * 4 + k]);
+      *reinterpret_cast<uint4 *>(at + lane * 128 + ((c ^ (lane & 7)) << 4)) =
           make_uint4(w[0], w[1], w[2], w[3]);
     }
-  fence_proxy_async();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_2d(&mo, n0, m0, box);
-    tma_store_2d(&mo, n0 + (BF16 ? 64 : 32), m0, box + LargeCfg::BOX);
-    bulk_commit();
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(&mo, n0 + i * COLS, m0, at);
+      bulk_commit();
+    }
   }
 }
 
@@ -337,13 +413,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
                       const __grid_constant__ CUtensorMap mo, int m_tiles, int n_tiles,
                       bool boxes) {
   using C = LargeCfg;
-  constexpr int S = C::STAGES;
+  constexpr int S = C::STAGES, SG = kScaleGroup;
   extern __shared__ unsigned char raw[];
   unsigned char *sm =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[S], empty[S];  // full and tempty: those of rank 0 serve the pair
   __shared__ Bars bars;
-  __shared__ float sc[kScaleSlots][130];  // 128 rows of A, then the two blocks of B
+  __shared__ float sc[2][SG][130];  // a stage's 128 rows of A, then the two blocks of B
   __shared__ uint32_t tm_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -352,11 +428,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kScaleSlots; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.sfull[i], 32);
       mbar_init(&bars.sempty[i], 8);
-    }
-    for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.tfull[i], 1);
       mbar_init(&bars.tempty[i], 16);
     }
@@ -408,8 +482,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
         for (int t = pair; t < tiles && ok; t += pairs)
           for (int kb = 0; kb < p.KB; ++kb, ++i) {
             const int s = i % S, b = i & 1;
-            ok = i < 2 || mbar_wait(&bars.tempty[b], ((i >> 1) - 1) & 1, p.err, kSiteGemmAcc);
-            ok = ok && mbar_wait(&full[s], (i / S) & 1, p.err, kSiteGemmStage);
+            ok = mbar_wait_both(&bars.tempty[b], ((i >> 1) + 1) & 1, &full[s], (i / S) & 1, p.err,
+                                kSiteGemmStage);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
@@ -420,41 +494,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
           }
       }
     } else if (warp == 2) {
-      constexpr int AHEAD = 4;
-      int i = 0;
+      // scales of the block's rows of A and of the tile's two blocks of B, a
+      // group of stages at a time (registers are short for the epilogue warps
+      // to load them, which is how the square tiles have it)
+      int g = 0;
       bool ok = true;
       for (int t = pair; t < tiles && ok; t += pairs) {
-        const int m0 = t % m_tiles * C::TM + rank * 128, n0 = t / m_tiles * C::TN;
-        for (int k0 = 0; k0 < p.KB && ok; k0 += AHEAD) {
-          float v[AHEAD][5];
-#pragma unroll
-          for (int u = 0; u < AHEAD; ++u) {
-            const int kb = k0 + u;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int m = m0 + c * 32 + lane;
-              v[u][c] = kb < p.KB && m < p.M ? p.a_scale[(long long)m * p.KB + kb] : 0.f;
-            }
-            const int nb = (n0 >> 7) + lane;
-            v[u][4] = kb < p.KB && lane < 2 && nb * 128 < p.N
-                          ? p.b_scale[(long long)nb * p.KB + kb]
-                          : 0.f;
+        const int m0 = t % m_tiles * C::TM + rank * 128, nb = (t / m_tiles * C::TN >> 7) + lane;
+        for (int k0 = 0; k0 < p.KB; k0 += SG, ++g) {
+          const int s = g & 1;
+          if (g >= 2 && !mbar_wait(&bars.sempty[s], (g / 2 - 1) & 1, p.err, kSiteGemmScale)) {
+            ok = false;
+            break;
           }
+          for (int u0 = 0; u0 < SG; u0 += 4) {
+            float v[4][5];
 #pragma unroll
-          for (int u = 0; u < AHEAD; ++u) {
-            if (k0 + u >= p.KB) break;
-            const int s = i % kScaleSlots;
-            if (i >= kScaleSlots &&
-                !mbar_wait(&bars.sempty[s], (i / kScaleSlots - 1) & 1, p.err, kSiteGemmScale)) {
-              ok = false;
-              break;
+            for (int u = 0; u < 4; ++u) {
+              const int kb = k0 + u0 + u;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const int m = m0 + c * 32 + lane;
+                v[u][c] = kb < p.KB && m < p.M ? p.a_scale[(long long)m * p.KB + kb] : 0.f;
+              }
+              v[u][4] = kb < p.KB && lane < 2 && nb * 128 < p.N
+                            ? p.b_scale[(long long)nb * p.KB + kb]
+                            : 0.f;
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sc[s][c * 32 + lane] = v[u][c];
-            if (lane < 2) sc[s][128 + lane] = v[u][4];
-            mbar_arrive(&bars.sfull[s]);
-            ++i;
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) sc[s][u0 + u][c * 32 + lane] = v[u][c];
+              if (lane < 2) sc[s][u0 + u][128 + lane] = v[u][4];
+            }
           }
+          mbar_arrive(&bars.sfull[s]);
         }
       }
     }
@@ -462,43 +536,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t taddr = tm + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
-    unsigned char *box = sm + S * C::STAGE + (warp - 4) * 2 * C::BOX;
+    unsigned char *box = sm + S * C::STAGE + (warp - 4) * C::BOXES * C::BOX;
     const uint32_t freed[2] = {cluster_addr(&bars.tempty[0], 0), cluster_addr(&bars.tempty[1], 0)};
-    int i = 0;
+    int i = 0, g = 0;
     bool ok = true;
     for (int t = pair; t < tiles && ok; t += pairs) {
       float acc[128];
 #pragma unroll
       for (int j = 0; j < 128; ++j) acc[j] = 0.f;
-      for (int kb = 0; kb < p.KB; ++kb, ++i) {
-        const int b = i & 1, s = i % kScaleSlots;
-        if (!mbar_wait(&bars.sfull[s], (i / kScaleSlots) & 1, p.err, kSiteGemmScale) ||
-            !mbar_wait(&bars.tfull[b], (i >> 1) & 1, p.err, kSiteGemmAcc)) {
-          ok = false;
-          break;
+      for (int k0 = 0; k0 < p.KB && ok; k0 += SG, ++g) {
+        const int s = g & 1;
+        ok = mbar_wait(&bars.sfull[s], (g / 2) & 1, p.err, kSiteGemmScale);
+        for (int u = 0; u < SG && k0 + u < p.KB; ++u, ++i) {
+          const int b = i & 1;
+          ok = ok && mbar_wait(&bars.tfull[b], (i >> 1) & 1, p.err, kSiteGemmAcc);
+          if (!ok) break;
+          const float f = sc[s][u][row] * sc[s][u][128 + half];
+          tc_fence_after();
+          // Columns in four parts, two in registers at a time: the third and
+          // fourth are under way while the first two are added, and the buffer
+          // is given back before the last two are.
+          const uint32_t src = taddr + b * C::TN;
+          float v0[32], v1[32];
+          tmem_ld32_async(src, v0);
+          tmem_ld32_async(src + 32, v1);
+          tmem_wait_ld();
+          add_part(acc, v0, f, 0);
+          tmem_ld32_async(src + 64, v0);
+          add_part(acc, v1, f, 32);
+          tmem_ld32_async(src + 96, v1);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(b ? freed[1] : freed[0]);
+          add_part(acc, v0, f, 64);
+          add_part(acc, v1, f, 96);
         }
-        const float f = sc[s][row] * sc[s][128 + half];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.sempty[s]);
-        tc_fence_after();
-        // Columns in four parts, two in registers at a time: the third and
-        // fourth are under way while the first two are added, and the buffer
-        // is given back before the last two are.
-        const uint32_t src = taddr + b * C::TN;
-        float v0[32], v1[32];
-        tmem_ld32_async(src, v0);
-        tmem_ld32_async(src + 32, v1);
-        tmem_wait_ld();
-        add_part(acc, v0, f, 0);
-        tmem_ld32_async(src + 64, v0);
-        add_part(acc, v1, f, 32);
-        tmem_ld32_async(src + 96, v1);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(b ? freed[1] : freed[0]);
-        add_part(acc, v0, f, 64);
-        add_part(acc, v1, f, 96);
       }
       if (!ok) break;
       const int m0 = t % m_tiles * C::TM + rank * 128 + (warp & 3) * 32;
@@ -507,12 +582,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
         // through shared memory in swizzled boxes of 32 rows x 128 bytes, which
         // bulk copies take to the output while the next tile begins (stores
         // from registers, 32 rows at a time, took a sixth of the whole call)
-        if (p.bf16_out) {
-          store_box<true>(box, lane, mo, n0, m0, acc, 0);
-        } else {
-          store_box<false>(box, lane, mo, n0, m0, acc, 0);
-          store_box<false>(box, lane, mo, n0 + 64, m0, acc, 64);
-        }
+        if (p.bf16_out) store_boxes<true>(box, lane, mo, n0, m0, acc);
+        else store_boxes<false>(box, lane, mo, n0, m0, acc);
       } else if (m < p.M) {
         const long long at = (long long)m * p.N + n0;
         const bool vec = (p.N & 3) == 0;
@@ -560,9 +631,9 @@ bool map_out(CUtensorMap *m, void *out, int M, int N, bool bf16) {
 
 constexpr int kSms = 152;
 
-template <int NT>
+template <int NT, bool TOKENS>
 cudaError_t launch_small(const GemmArgs &a, GemmParams p, cudaStream_t stream) {
-  using C = SmallCfg<NT>;
+  using C = SmallCfg<NT, TOKENS>;
   CUtensorMap ma, mb;
   if (!map_e4m3(&ma, a.a, a.M, a.K, NT) || !map_e4m3(&mb, a.b, a.N, a.K, 128))
     return cudaErrorInvalidValue;
@@ -571,12 +642,13 @@ cudaError_t launch_small(const GemmArgs &a, GemmParams p, cudaStream_t stream) {
   p.split = 1;
   while (p.split < 8 && (long long)nt * mt * p.split * 2 <= kSms && p.KB >= 4 * p.split)
     p.split *= 2;
-  cudaError_t e = cudaFuncSetAttribute(gemm_small_kernel<NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  auto kernel = gemm_small_kernel<NT, TOKENS>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nt * p.split, mt);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -588,7 +660,7 @@ cudaError_t launch_small(const GemmArgs &a, GemmParams p, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_small_kernel<NT>, p, mb, ma);
+  return cudaLaunchKernelEx(&cfg, kernel, p, mb, ma);
 }
 
 cudaError_t launch_large(const GemmArgs &a, const GemmParams &p, cudaStream_t stream) {
@@ -616,10 +688,11 @@ cudaError_t launch_gemm_fp8(const GemmArgs &a, cudaStream_t stream) {
   p.a_scale = a.a_scale; p.b_scale = a.b_scale; p.out = a.out;
   p.M = a.M; p.N = a.N; p.KB = (a.K + kBlockK - 1) / kBlockK;
   p.bf16_out = a.bf16_out; p.err = a.err; p.split = 1;
-  if (a.M <= 16) return launch_small<16>(a, p, stream);
-  if (a.M <= 32) return launch_small<32>(a, p, stream);
-  if (a.M <= 64) return launch_small<64>(a, p, stream);
-  if (a.M <= 256) return launch_small<128>(a, p, stream);
+  if (a.M <= 16) return launch_small<16, false>(a, p, stream);
+  if (a.M <= 32) return launch_small<32, false>(a, p, stream);
+  if (a.M <= 64) return launch_small<64, false>(a, p, stream);
+  const long long tiles = (long long)((a.M + 127) / 128) * ((a.N + 127) / 128);
+  if (tiles <= kSms) return launch_small<128, true>(a, p, stream);
   return launch_large(a, p, stream);
 }
 

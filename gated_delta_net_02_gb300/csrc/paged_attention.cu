@@ -69,6 +69,13 @@ struct AttnParams {
   int *err;
 };
 
+// 2^x, 0 below the normal numbers: no probability that small reaches a sum.
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
   const int n = live ? 16 : 0;  // 0 source bytes: filled with zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
@@ -296,7 +303,7 @@ struct TileBf16 {
       mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
       const float mn = fmaxf(m[r], mx[r]);
       ref[r] = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every p is 0
-      alpha[r] = exp2f(m[r] - ref[r]);
+      alpha[r] = exp2_ftz(m[r] - ref[r]);
       m[r] = mn;
       l[r] *= alpha[r];
     }
@@ -311,7 +318,7 @@ struct TileBf16 {
     for (int i = 0; i < KW / 8; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[i][e] = exp2f(s[i][e] - ref[e >> 1]);
+        s[i][e] = exp2_ftz(s[i][e] - ref[e >> 1]);
         l[e >> 1] += s[i][e];
       }
     const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3), vch = lane >> 4;
@@ -442,7 +449,7 @@ struct TileF32 {
 #pragma unroll
       for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float mn = fmaxf(m[r], mx), ref = mn == -INFINITY ? 0.f : mn;
-      const float alpha = exp2f(m[r] - ref), e = exp2f(x - ref);
+      const float alpha = exp2_ftz(m[r] - ref), e = exp2_ftz(x - ref);
       m[r] = mn;
       l[r] = l[r] * alpha + e;  // this lane's keys; summed over the lanes at the end
       p_s[(row0 + r) * C::KT + lane] = e;
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
 #pragma unroll
       for (int w = 0; w < WK; ++w) {
         const float2 ml = sml[w * ROWS + r];
-        const float f = exp2f(ml.x - ref);
+        const float f = exp2_ftz(ml.x - ref);
         const float4 v = *reinterpret_cast<const float4 *>(so + (w * ROWS + r) * D + c);
         ll += f * ml.y;
         sum.x = fmaf(f, v.x, sum.x);
@@ -730,7 +737,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnParams p) 
 #pragma unroll 4
   for (int i = warp; i < np; i += 4) {
     const float2 ml = p.part_ml[slot(i) * ROWS + r];
-    const float f = exp2f(ml.x - ref);
+    const float f = exp2_ftz(ml.x - ref);
     ll += f * ml.y;
     const float *o = p.part_o + (slot(i) * ROWS + r) * D;
 #pragma unroll
