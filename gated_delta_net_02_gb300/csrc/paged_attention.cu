@@ -614,6 +614,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
     for (int i = 0; i < S; ++i) put_offs(i, page[i]);
     __syncthreads();
     // q rows of the item (zeros beyond them) join the first tile's copies
+#pragma unroll 1
     for (int e = tid; e < ROWS * C::CH; e += NT) {
       const int r = e / C::CH, c = e % C::CH;
       const long long row = rows[r];
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
                  static_cast<const T *>(p.q) + (row < 0 ? 0 : row) * D + c * (16 / (int)sizeof(T)),
                  row >= 0);
     }
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < S - 1; ++i) load_tile(i);
     int next_page = page[S];
 
@@ -665,6 +666,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
 
     const bool whole = n == nt;
     const long long slot = (long long)blockIdx.x * 2 + (seg > 0);
+#pragma unroll 1
     for (int e = tid; e < ROWS * (D / 4); e += NT) {
       const int r = e / (D / 4), c = e % (D / 4) * 4;
       float mm = -INFINITY;
