@@ -487,6 +487,9 @@ static const char *wait_site_name(int site) {
     case gdn::kSiteScanD: return "chunk scan, D tile";
     case gdn::kSiteNormRow: return "RMS norm, a group of rows";
     case gdn::kSiteRopeRow: return "rotary positions, a token's rows";
+    case gdn::kSiteAttnTile: return "attention, tile of keys";
+    case gdn::kSiteAttnScore: return "attention, scores";
+    case gdn::kSiteAttnSum: return "attention, sums";
     case gdn::kSiteGemmEmpty: return "e4m3 product, stage release";
     case gdn::kSiteGemmStage: return "e4m3 product, stage copies";
     case gdn::kSiteGemmAcc: return "e4m3 product, accumulator buffer";

@@ -36,6 +36,9 @@ enum WaitSite : int {
   kSiteScanStage = 52,    // chunk scan, MMA issuer: a stage's copies
   kSiteScanS0 = 53,       // chunk scan, MMA issuer: the state operand
   kSiteScanD = 54,        // chunk scan, MMA issuer: the D tile
+  kSiteAttnTile = 57,     // attention: a tile of keys copied or used
+  kSiteAttnScore = 58,    // attention: scores formed or taken
+  kSiteAttnSum = 59,      // attention: probabilities taken into the sums
   kSiteNormRow = 55,      // RMS norm: a group of rows
   kSiteRopeRow = 56,      // rotary positions: a token's rows
   kSiteGemmEmpty = 61,    // e4m3 product, producer: a stage released by its products

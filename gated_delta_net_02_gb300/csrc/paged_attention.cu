@@ -32,6 +32,8 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tensor_map.h"
+#include "umma.cuh"
 
 namespace gdn {
 namespace {
@@ -117,6 +119,7 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 template <typename T, int D_, int WM_>
 struct Cfg {
   using In = T;
+  static constexpr bool kTensorMemory = false;
   static constexpr bool kBf16 = sizeof(T) == 2;
   static constexpr int D = D_, WM = WM_;
   static constexpr int ROWS = kBf16 ? 16 * WM : 4 * WM;
@@ -520,6 +523,100 @@ __device__ __forceinline__ void store4(T *p, float4 v) {
     *reinterpret_cast<float4 *>(p) = v;
 }
 
+// The end of an item's tiles in a block: the key groups' sums so[group][row]
+// (pitch floats apart) and (m, l) become output rows, or a piece for the join.
+template <class C>
+__device__ __forceinline__ void finish_item(const AttnParams &p, const float *so, int pitch,
+                                            const float2 *sml, const long long *rows, bool whole,
+                                            long long slot) {
+  using T = typename C::In;
+  constexpr int D = C::D, ROWS = C::ROWS, WK = C::WK;
+#pragma unroll 1
+  for (int e = threadIdx.x; e < ROWS * (D / 4); e += C::THREADS) {
+    const int r = e / (D / 4), c = e % (D / 4) * 4;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) mm = fmaxf(mm, sml[w * ROWS + r].x);
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    float ll = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < WK; ++w) {
+      const float2 ml = sml[w * ROWS + r];
+      const float f = exp2_ftz(ml.x - ref);
+      const float4 v = *reinterpret_cast<const float4 *>(so + (w * ROWS + r) * pitch + c);
+      ll += f * ml.y;
+      sum.x = fmaf(f, v.x, sum.x);
+      sum.y = fmaf(f, v.y, sum.y);
+      sum.z = fmaf(f, v.z, sum.z);
+      sum.w = fmaf(f, v.w, sum.w);
+    }
+    const long long row = rows[r];
+    if (row < 0) continue;
+    if (whole) {
+      // a row without keys has ll = 0 and sum = 0: its output is 0
+      const float inv = 1.f / (ll == 0.f ? 1.f : ll);
+      store4(static_cast<T *>(p.out) + row * D + c,
+             make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
+    } else {
+      *reinterpret_cast<float4 *>(p.part_o + (slot * ROWS + r) * D + c) = sum;
+      if (c == 0) p.part_ml[slot * ROWS + r] = make_float2(mm, ll);
+    }
+  }
+}
+
+// What a block holds: tiles of a run of items, walked item by item.
+struct Walk {
+  long long pos, end, run;
+  int s, len, nt, x, tile0;
+  // The block's first item; false when there is nothing for this block.
+  template <int KT, int NT>
+  __device__ __forceinline__ bool begin(const AttnParams &p, int items_per_seq,
+                                        long long (&warp_sum)[NT / 32], Place &place) {
+    long long total = 0;
+    if (!find_place<NT>(
+            p, KT, items_per_seq,
+            [&](long long n) {
+              total = n;
+              run = max(quotient(n + gridDim.x - 1, gridDim.x), (long long)kMinTiles);
+              return run * blockIdx.x;
+            },
+            warp_sum, place))
+      return false;
+    pos = run * blockIdx.x;
+    end = min(pos + run, total);
+    s = place.seq;
+    len = place.len;
+    nt = item_tiles(len, KT);
+    x = (int)quotient(pos - place.first, nt);  // item of the sequence
+    tile0 = (int)(pos - place.first - (long long)x * nt);
+    return true;
+  }
+  // Tiles of the current item in this block.
+  __device__ __forceinline__ int tiles() const {
+    return (int)min((long long)(nt - tile0), end - pos);
+  }
+  // Names the join of a cut item, if this is the first block that starts inside it.
+  __device__ __forceinline__ void list_join(const AttnParams &p, int items_per_seq) const {
+    const long long a = pos - tile0, before = pos - run;
+    int4 cut = make_int4(-1, 0, 0, 0);
+    if (tile0 > 0 && before <= a)
+      cut = make_int4(s * items_per_seq + x, (int)quotient(a, run),
+                      (int)quotient(a + nt - 1, run), a == before ? 0 : 1);
+    p.cut[blockIdx.x] = cut;
+  }
+  template <int KT>
+  __device__ __forceinline__ void next(const AttnParams &p, int items_per_seq, int n) {
+    pos += n;
+    tile0 = 0;
+    if (++x == items_per_seq && pos < end) {
+      x = 0;
+      len = seq_len(p, ++s, false);
+      nt = item_tiles(len, KT);
+    }
+  }
+};
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnParams p) {
   using T = typename C::In;
@@ -543,27 +640,13 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
   const T *kc = static_cast<const T *>(p.k), *vc = static_cast<const T *>(p.v);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  long long run = 0, total = 0;  // tiles of a block, of all items
-  const bool any = find_place<NT>(
-      p, KT, items_per_seq,
-      [&](long long n) {
-        total = n;
-        run = max(quotient(n + gridDim.x - 1, gridDim.x), (long long)kMinTiles);
-        return run * blockIdx.x;
-      },
-      warp_sum, place);
-  if (!any) {
+  Walk w;
+  if (!w.begin<KT, NT>(p, items_per_seq, warp_sum, place)) {
     if (tid == 0) p.cut[blockIdx.x].x = -1;
     return;
   }
-  long long pos = run * blockIdx.x;
-  const long long end = min(pos + run, total);
-  int s = place.seq, len = place.len, nt = item_tiles(len, KT);
-  int x = (int)quotient(pos - place.first, nt);  // item of the sequence
-  int tile0 = (int)(pos - place.first - (long long)x * nt);
-
-  for (int seg = 0; pos < end; ++seg) {
-    const int n = (int)min((long long)(nt - tile0), end - pos);  // tiles of this item here
+  for (int seg = 0; w.pos < w.end; ++seg) {
+    const int n = w.tiles(), s = w.s, x = w.x, len = w.len, tile0 = w.tile0;
     const int kvh = p.row_blocks.div(x), r0 = (x - kvh * (int)p.row_blocks.d) * ROWS;
     const long long head = (long long)kvh * p.head_stride;
     const int32_t *table = p.table + (long long)s * p.max_pages;
@@ -626,16 +709,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
     for (int i = 0; i < S - 1; ++i) load_tile(i);
     int next_page = page[S];
 
-    if (seg == 0 && tid == NT - 1) {
-      // the first block that starts inside an item has it joined
-      const long long a = pos - tile0, before = pos - run;
-      const bool joins = tile0 > 0 && before <= a;
-      int4 cut = make_int4(-1, 0, 0, 0);
-      if (joins)
-        cut = make_int4(s * items_per_seq + x, (int)quotient(a, run),
-                        (int)quotient(a + nt - 1, run), a == before ? 0 : 1);
-      p.cut[blockIdx.x] = cut;
-    }
+    if (seg == 0 && tid == NT - 1) w.list_join(p, items_per_seq);
 
     int lim[sizeof(Tile::m) / sizeof(float)];
     Tile::limits(
@@ -664,50 +738,329 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
     acc.flush(so, sml);
     __syncthreads();
 
-    const bool whole = n == nt;
+    const bool whole = n == w.nt;
     const long long slot = (long long)blockIdx.x * 2 + (seg > 0);
-#pragma unroll 1
-    for (int e = tid; e < ROWS * (D / 4); e += NT) {
-      const int r = e / (D / 4), c = e % (D / 4) * 4;
-      float mm = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < WK; ++w) mm = fmaxf(mm, sml[w * ROWS + r].x);
-      const float ref = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f;
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < WK; ++w) {
-        const float2 ml = sml[w * ROWS + r];
-        const float f = exp2_ftz(ml.x - ref);
-        const float4 v = *reinterpret_cast<const float4 *>(so + (w * ROWS + r) * D + c);
-        ll += f * ml.y;
-        sum.x = fmaf(f, v.x, sum.x);
-        sum.y = fmaf(f, v.y, sum.y);
-        sum.z = fmaf(f, v.z, sum.z);
-        sum.w = fmaf(f, v.w, sum.w);
-      }
-      const long long row = rows[r];
-      if (row < 0) continue;
-      if (whole) {
-        // a row without keys has ll = 0 and sum = 0: its output is 0
-        const float inv = 1.f / (ll == 0.f ? 1.f : ll);
-        store4(static_cast<T *>(p.out) + row * D + c,
-               make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
-      } else {
-        *reinterpret_cast<float4 *>(p.part_o + (slot * ROWS + r) * D + c) = sum;
-        if (c == 0) p.part_ml[slot * ROWS + r] = make_float2(mm, ll);
-      }
-    }
+    finish_item<C>(p, so, D, sml, rows, whole, slot);
     __syncthreads();  // before the next item's copies reuse the tiles
 
-    pos += n;
-    tile0 = 0;
-    if (++x == items_per_seq && pos < end) {
-      x = 0;
-      len = seq_len(p, ++s, false);
-      nt = item_tiles(len, KT);
+    w.next<KT>(p, items_per_seq, n);
+  }
+}
+
+// ---- many rows (bf16): products on tcgen05, sums in tensor memory --------------
+//
+// From 17 rows the warp-level instruction leaves each scheduler two warps that
+// wait on one another's latencies. Here the 128 rows of the tensor-core
+// instruction are COPIES copies of up to 128 / COPIES rows: copy c takes the
+// c-th part of a tile's 64 keys, with a reference and sums of its own, as a
+// warp's key group does above. So every lane of four warps has one row and
+// 64 / COPIES keys, and a row's maximum and sum need no other lane.
+//
+// Warp 0 loads keys by TMA, a box of a page's tokens and 64 columns at a time,
+// into 128-byte-swizzled units of 64 keys (K and V in turn); warps 1-3 bring
+// q, and clear what the last page holds beyond the length from the last unit
+// of V; warps 4-7 turn scores into probabilities; warp 8 issues: S(i+1) =
+// Q K^T while the probabilities of tile i are made, then O += P V. The sums
+// stay in tensor memory; they are rescaled only when a row's maximum passes
+// its reference by more than 2^8, which keeps every probability below 2^8 and
+// the rescaling rare.
+template <int D_, int COPIES_>
+struct TcCfg {
+  using In = __nv_bfloat16;
+  static constexpr bool kTensorMemory = true;
+  static constexpr int D = D_, COPIES = COPIES_, KT = 64;
+  static constexpr int ROWS = 128 / COPIES, WK = COPIES, KC = KT / COPIES;
+  static constexpr int THREADS = 288;
+  static constexpr int UNIT = KT * D * 2, UNITS = D == 256 ? 4 : 8;
+  static constexpr int P_BYTES = 128 * 128, Q_BYTES = 128 * D * 2;
+  static constexpr int PITCH = D + 4;  // of the sums on their way out
+  static constexpr int SMEM = UNITS * UNIT + P_BYTES + Q_BYTES + 1024;
+  static constexpr int TCOLS = D == 256 ? 512 : 256;  // sums, then two tiles of scores
+  static constexpr int PER_SM = D == 64 && COPIES == 4 ? 2 : 1;
+  static_assert(128 * PITCH * 4 <= UNITS * UNIT + P_BYTES + Q_BYTES, "the sums fit");
+};
+
+constexpr float kMaxGrowth = 8.f;  // log2 of a probability's bound
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, C::PER_SM)
+    attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv, int box) {
+  using T = __nv_bfloat16;
+  constexpr int D = C::D, KT = C::KT, ROWS = C::ROWS, NT = C::THREADS, U = C::UNITS, KC = C::KC;
+  constexpr int CH = D / 8;  // 16-byte chunks of a row
+  extern __shared__ unsigned char raw[];
+  unsigned char *sm =
+      reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[U], empty[U], s_full[2], s_empty[2], p_full, o_done, q_full, patched;
+  __shared__ long long rows[ROWS], warp_sum[NT / 32];
+  __shared__ Place place;
+  __shared__ float2 sml[128];
+  __shared__ uint32_t tm_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t units_s = smem_u32(sm), p_s = units_s + U * C::UNIT, q_s = p_s + C::P_BYTES;
+  const int items_per_seq = p.H_kv * p.row_blocks.d;
+  if (tid == 0) {
+    for (int i = 0; i < U; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_empty[i], 4);
+    }
+    mbar_init(&p_full, 4);
+    mbar_init(&o_done, 1);
+    mbar_init(&q_full, 3);
+    mbar_init(&patched, 3);
+    fence_mbar_init();
+    prefetch_tmap(&mk);
+    prefetch_tmap(&mv);
+  }
+  // a copy's probabilities of the other copies' keys are zero, for good
+  for (int e = tid; e < C::P_BYTES / 16; e += NT)
+    *reinterpret_cast<uint4 *>(sm + U * C::UNIT + e * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  // tensor memory after the kernel before, and the next kernel after that (as
+  // in gemm_fp8.cu): of two kernels on an SM the earlier never waits for the later
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 8) {
+    tmem_alloc(&tm_s, C::TCOLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tm = tm_s, tm_score = tm + D;
+
+  Walk w;
+  const bool any = w.begin<KT, NT>(p, items_per_seq, warp_sum, place);
+  if (!any && tid == 0) p.cut[blockIdx.x].x = -1;
+  int tb = 0, patches = 0;  // tiles and cleared units of the items before
+  for (int seg = 0; any && w.pos < w.end; ++seg) {
+    const int n = w.tiles(), s = w.s, len = w.len, tile0 = w.tile0;
+    const int kvh = p.row_blocks.div(w.x), r0 = (w.x - kvh * (int)p.row_blocks.d) * ROWS;
+    // the item's last tile is here, and ends inside a unit
+    const int patch_from = len - (tile0 + n - 1) * KT;
+    const bool patch = patch_from < KT;
+    if (tid < ROWS) rows[tid] = out_row(p, s, kvh, r0 + tid);
+    if (seg == 0 && tid == NT - 1) w.list_join(p, items_per_seq);
+    __syncthreads();
+    bool ok = true;
+    if (warp == 0) {
+      // lane: one box of a unit; boxes of `box` tokens, D / 64 of them side by side
+      const int32_t *table = p.table + (long long)s * p.max_pages;
+      const int j = lane / (D / 64), c = lane % (D / 64);  // box row, 64 columns
+      const bool mine = j * box < KT;
+      auto page_of = [&](int i) -> int {
+        const int key = (tile0 + i) * KT + j * box;
+        return mine && i < n && key < len ? table[p.page_size.div(key)] : -1;
+      };
+      int page = page_of(0);
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        const int key = (tile0 + i) * KT + j * box, next = page_of(i + 1);
+        bool live = mine && key < len;
+        if (live && (page < 0 || page >= p.n_pages)) {
+          set_error(p.err, kDevBadPage);
+          live = false;
+        }
+        const int in_page = key - p.page_size.div(key) * (int)p.page_size.d;
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, live)) * box * 128;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int u = 2 * (tb + i) + v, slot = u % U;
+          ok = ok && mbar_wait(&empty[slot], (u / U + 1) & 1, p.err, kSiteAttnTile);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+          __syncwarp();
+          if (live)
+            tma_load_4d(sm + slot * C::UNIT + c * (KT * 128) + j * box * 128, v ? &mv : &mk, c * 64,
+                        kvh, in_page, page, &full[slot]);
+        }
+        page = next;
+      }
+    } else if (warp < 4) {
+      const int t96 = tid - 32;
+#pragma unroll 4
+      for (int e = t96; e < 128 * CH; e += 96) {
+        const int r = e / CH, c = e % CH;
+        const long long row = rows[r % ROWS];
+        cp_async16(q_s + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                   static_cast<const T *>(p.q) + (row < 0 ? 0 : row) * D + c * 8, row >= 0);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full);
+      if (patch) {
+        const int u = 2 * (tb + n - 1) + 1, slot = u % U;
+        ok = mbar_wait(&full[slot], (u / U) & 1, p.err, kSiteAttnTile);
+        ok = __all_sync(0xffffffffu, ok);
+        const int from = max(patch_from, 0);
+        if (ok)
+          for (int e = t96; e < (KT - from) * CH; e += 96) {
+            const int row = from + e / CH, c = e % CH;
+            *reinterpret_cast<uint4 *>(sm + slot * C::UNIT + (c >> 3) * (KT * 128) + row * 128 +
+                                       ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&patched);
+      }
+    } else if (warp == 8) {
+      auto sums = [&](int i) {  // O (+)= P V of tile i
+        const int t = tb + i, u = 2 * t + 1, slot = u % U;
+        ok = ok && mbar_wait_both(&p_full, t & 1, &full[slot], (u / U) & 1, p.err, kSiteAttnSum);
+        if (patch && i == n - 1) ok = ok && mbar_wait(&patched, patches & 1, p.err, kSiteAttnTile);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < KT / 16; ++ks)
+          umma_bf16_elect(tm, sdesc_kmajor(p_s + ks * 32),
+                          sdesc_mnmajor(units_s + slot * C::UNIT + ks * 2048, KT * 128),
+                          idesc_bf16_f32(128, D, false, true), i > 0 || ks > 0);
+        umma_commit_elect(&empty[slot]);
+        umma_commit_elect(&o_done);
+      };
+      ok = mbar_wait(&q_full, seg & 1, p.err, kSiteAttnTile);
+      ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        const int t = tb + i, b = t & 1, u = 2 * t, slot = u % U;
+        ok = mbar_wait_both(&s_empty[b], ((t >> 1) + 1) & 1, &full[slot], (u / U) & 1, p.err,
+                            kSiteAttnScore);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          umma_bf16_elect(tm_score + b * KT,
+                          sdesc_kmajor(q_s + (ks >> 2) * (128 * 128) + (ks & 3) * 32),
+                          sdesc_kmajor(units_s + slot * C::UNIT + (ks >> 2) * (KT * 128) +
+                                       (ks & 3) * 32),
+                          idesc_bf16_f32(128, KT, false, false), ks > 0);
+        umma_commit_elect(&empty[slot]);
+        umma_commit_elect(&s_full[b]);
+        if (i > 0) sums(i - 1);
+      }
+      if (ok) sums(n - 1);
+    } else {
+      const int R = (warp - 4) * 32 + lane, r = R % ROWS, part = R / ROWS * KC;
+      const uint32_t lanes = (uint32_t)((warp - 4) * 32) << 16;
+      const int row = r0 + r;
+      const int lim = row < p.T * (int)p.G.d ? len - p.T + p.G.div(row) + 1 : 0;
+      float ref = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        const int t = tb + i, b = t & 1;
+        ok = mbar_wait(&s_full[b], (t >> 1) & 1, p.err, kSiteAttnScore);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        float x[KC];
+        if constexpr (KC == 16) {
+          tmem_ld16(tm_score + lanes + b * KT + part, x);
+        } else {
+#pragma unroll
+          for (int c = 0; c < KC; c += 32) {
+            float part32[32];
+            tmem_ld32(tm_score + lanes + b * KT + part + c, part32);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[c + j] = part32[j];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[b]);
+        const int key0 = (tile0 + i) * KT + part;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+          x[j] = key0 + j < lim ? x[j] * p.scale_log2 : -INFINITY;
+          mx = fmaxf(mx, x[j]);
+        }
+        const bool grow = mx > ref + kMaxGrowth;
+        const float next = grow ? mx : ref;
+        const float alpha = grow ? exp2_ftz(ref - next) : 1.f;
+        ref = next;
+        l *= alpha;
+        // the tile before has left P, and its product is in the sums
+        if (i > 0) ok = mbar_wait(&o_done, (t - 1) & 1, p.err, kSiteAttnSum);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (i > 0 && __any_sync(0xffffffffu, grow)) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(tm + lanes + c, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] *= alpha;
+            tmem_st32(tm + lanes + c, o);
+          }
+          tmem_wait_st();
+        }
+        const float base = ref == -INFINITY ? 0.f : ref;
+        unsigned char *prow = sm + U * C::UNIT + R * 128;
+#pragma unroll
+        for (int j = 0; j < KC; j += 8) {
+          uint32_t q[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = exp2_ftz(x[j + 2 * k] - base), e = exp2_ftz(x[j + 2 * k + 1] - base);
+            l += a + e;
+            q[k] = bf16x2(a, e);
+          }
+          *reinterpret_cast<uint4 *>(prow + ((((part + j) >> 3) ^ (R & 7)) << 4)) =
+              make_uint4(q[0], q[1], q[2], q[3]);
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full);
+      }
+      if (ok) ok = mbar_wait(&o_done, (tb + n - 1) & 1, p.err, kSiteAttnSum);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        // all copies and products of the item are done: the sums take their place
+        tc_fence_after();
+        float *so = reinterpret_cast<float *>(sm) + R * C::PITCH;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tm + lanes + c, o);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4 *>(so + c + j) =
+                make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+        }
+        sml[R] = make_float2(ref, l);
+        tc_fence_before();
+      }
+    }
+    if (__syncthreads_or(!ok)) break;
+    finish_item<C>(p, reinterpret_cast<const float *>(sm), C::PITCH, sml, rows, n == w.nt,
+                   (long long)blockIdx.x * 2 + (seg > 0));
+    fence_proxy_async();  // the sums' place is loaded by TMA next
+    __syncthreads();
+    tb += n;
+    patches += patch;
+    w.next<KT>(p, items_per_seq, n);
+    if (C::COPIES > 1 && 128 * C::PITCH * 4 > U * C::UNIT && w.pos < w.end) {
+      // the sums have overwritten P's zeros
+      for (int e = tid; e < C::P_BYTES / 16; e += NT)
+        *reinterpret_cast<uint4 *>(sm + U * C::UNIT + e * 16) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async();
     }
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tm, C::TCOLS);
 }
 
 // Joins the cut items: block (i, r) row r of the item that the main kernel's
@@ -761,13 +1114,26 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnParams p) 
 
 // ---- host side ------------------------------------------------------------------
 
+// Tokens of a page in one TMA box (whole 8-row groups of a unit), 0 when the
+// pages do not cut a unit of 64 keys evenly.
+int box_of(const KvLayout &c) {
+  const int ps = c.page_size;
+  if (!c.bf16 || c.n_pages == 0 || ps % 8) return 0;
+  return ps % 64 == 0 ? 64 : 64 % ps == 0 ? ps : 0;
+}
+
 // Calls f with the configuration of a head size, type and number of rows (T
 // x G of an item): the smallest block of rows that holds them all, or the
 // largest there is (each block of rows reads the keys again).
 template <typename T, int D, class F>
-auto with_rows(int rows, F f) {
+auto with_rows(int rows, int box, F f) {
   if constexpr (sizeof(T) == 2) {
     if (rows <= 16) return f(Cfg<T, D, 1>{});
+    if (box) {
+      if (rows <= 32) return f(TcCfg<D, 4>{});
+      if (rows <= 64) return f(TcCfg<D, 2>{});
+      return f(TcCfg<D, 1>{});
+    }
     if (rows <= 32) return f(Cfg<T, D, 2>{});
     return f(Cfg<T, D, 4>{});
   } else {
@@ -779,14 +1145,30 @@ auto with_rows(int rows, F f) {
   }
 }
 template <typename T, class F>
-auto with_d(int D, int rows, F f) {
-  if (D == 64) return with_rows<T, 64>(rows, f);
-  if (D == 128) return with_rows<T, 128>(rows, f);
-  return with_rows<T, 256>(rows, f);
+auto with_d(int D, int rows, int box, F f) {
+  if (D == 64) return with_rows<T, 64>(rows, box, f);
+  if (D == 128) return with_rows<T, 128>(rows, box, f);
+  return with_rows<T, 256>(rows, box, f);
 }
 template <class F>
 auto with_cfg(const KvLayout &c, int rows, F f) {
-  return c.bf16 ? with_d<__nv_bfloat16>(c.D, rows, f) : with_d<float>(c.D, rows, f);
+  const int box = box_of(c);
+  return c.bf16 ? with_d<__nv_bfloat16>(c.D, rows, box, f) : with_d<float>(c.D, rows, box, f);
+}
+
+// A cache as (D, H_kv, page_size, n_pages); boxes of 64 columns x `box` tokens
+// of one head and page, 128-byte swizzle.
+bool map_cache(CUtensorMap *m, const void *base, const KvLayout &c, int box) {
+  const cuuint64_t dims[4] = {(cuuint64_t)c.D, (cuuint64_t)c.H_kv, (cuuint64_t)c.page_size,
+                              (cuuint64_t)c.n_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)c.head_stride * 2, (cuuint64_t)c.token_stride * 2,
+                                 (cuuint64_t)c.page_stride * 2};
+  const cuuint32_t b[4] = {64, 1, (cuuint32_t)box, 1}, es[4] = {1, 1, 1, 1};
+  return encode_fn() &&
+         encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims,
+                     strides, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr int kSms = 152;
@@ -803,12 +1185,24 @@ int grid_of(const KvLayout &c, int n_seqs, int max_pages, int row_blocks) {
 }
 
 template <class C>
-cudaError_t launch_cfg(const AttnParams &p, int grid, cudaStream_t stream) {
-  static_assert(C::SMEM + 4 * C::KT * 8 + 8 * C::ROWS + 128 <= 227 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::SMEM);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(attn_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, p);
+cudaError_t launch_cfg(const AttnParams &p, const KvLayout &c, int grid, cudaStream_t stream) {
+  cudaError_t e;
+  if constexpr (C::kTensorMemory) {
+    static_assert(C::SMEM + 4 * 1024 <= 227 * 1024, "shared memory");
+    const int box = box_of(c);
+    CUtensorMap mk, mv;
+    if (!map_cache(&mk, p.k, c, box) || !map_cache(&mv, p.v, c, box)) return cudaErrorInvalidValue;
+    e = cudaFuncSetAttribute(attn_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attn_tc_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, p, mk, mv,
+                   box);
+  } else {
+    static_assert(C::SMEM + 4 * C::KT * 8 + 8 * C::ROWS + 128 <= 227 * 1024, "shared memory");
+    e = cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(attn_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, p);
+  }
   if (e != cudaSuccess || grid == 1) return e;
   const int rows = p.row_blocks.d > 1 ? C::ROWS : p.T * (int)p.G.d;
   return launch_pdl(join_kernel<typename C::In, C::D, C::ROWS>, dim3(grid, rows),
@@ -851,7 +1245,7 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream) {
     ws += up256((size_t)grid * 16);
     p.part_ml = reinterpret_cast<float2 *>(ws);
     p.part_o = reinterpret_cast<float *>(ws + up256((size_t)grid * 2 * C::ROWS * 8));
-    return launch_cfg<C>(p, grid, stream);
+    return launch_cfg<C>(p, c, grid, stream);
   });
 }
 

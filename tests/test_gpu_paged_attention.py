@@ -137,6 +137,35 @@ def test_lengths_cut_between_blocks(gdn, dtype, H, T, lens):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [8, 16, 24, 32, 64, 128, 192])
+@pytest.mark.parametrize("layout", ["dense", "heads_first", "k_and_v_in_one"])
+def test_many_rows_pages_and_layouts(gdn, D, page, layout):
+    # 24, 56 and 104 rows for each kv head
+    for H, H_kv, T in ((12, 2, 4), (14, 2, 8), (13, 1, 8)):
+        c = Case(gdn, [3, 700, 64, 256, 0, 100, 1, 1025], T, H, H_kv, D, page, torch.bfloat16,
+                 layout=layout, seed=page + T)
+        c.check(c.run())
+
+
+def test_many_rows_growing_scores(gdn):
+    # keys that grow along the sequence: every tile raises the maximum, far
+    # beyond what the sums' reference leaves untouched
+    c = Case(gdn, [1500, 640, 130], 4, 16, 2, 128, 16, torch.bfloat16, seed=11, scale=0.05)
+    for s, (k, v) in enumerate(c.keys):
+        n = k.shape[0]
+        k *= torch.linspace(0.1, 6.0, n, device="cuda")[:, None, None].bfloat16()
+        j = torch.arange(n, device="cuda")
+        c.k[c.table[s, j // 16].long(), j % 16] = k
+    out = c.run()
+    for s in range(3):
+        for t in range(4):
+            w, a = c.want(s, t)
+            # scores of up to six times the other tests' size, and their rounding
+            tol = 6 * 5e-5 * a + 2.0 ** -8 * (a + w.abs())
+            assert bool(((out[s * 4 + t].double() - w).abs() <= tol).all())
+
+
 def test_many_short_sequences(gdn):
     g = torch.Generator()
     g.manual_seed(3)
