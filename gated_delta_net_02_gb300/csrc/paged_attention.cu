@@ -9,7 +9,7 @@
 // their kv head and for the T tokens, 4 G T D flops for 2 D elements.
 //
 //  * Rows: the T x G (token, query head) pairs of a kv head are the rows of
-//    one matrix product, in blocks of 16, 32 or 64, so that the cache is read
+//    one matrix product, in blocks of up to 128, so that the cache is read
 //    once for all of them.
 //  * Work: an item is one (sequence, kv head, row block); its keys are cut
 //    into tiles. All items' tiles form one line, and each block of the grid
@@ -18,15 +18,21 @@
 //    whole is finished there; of a cut item each block writes its (m, l,
 //    sum p v) to the workspace and a second kernel joins them, in the fixed
 //    order of the line.
-//  * bf16: products on the warp-level matrix instruction (m16n8k16): with
-//    at most 64 rows the tensor-memory path would leave most of its 128 rows
-//    idle. p is rounded to bf16 for the second product (the sum l takes the
-//    unrounded p): 2^-9 relative on each term, as the inputs are.
-//    fp32: fp32 products on the CUDA cores.
+//  * bf16: products on the warp-level matrix instruction (m16n8k16), or with
+//    many rows on tcgen05 (below). p is rounded to bf16 for the second product
+//    (the sum l takes the unrounded p): up to 2^-8 of each term, as the inputs
+//    are. fp32: fp32 products on the CUDA cores, in rows of 4 to 32.
 //  * Keys reach shared memory by 16-byte asynchronous copies, several tiles
 //    ahead; each key's address comes from its page, looked up a tile earlier.
 //    Rows beyond the length are filled with zeros, so what an unused part of
 //    a page holds (NaN included) reaches no result.
+//
+// Measured on one GB300 (us; the cache's bytes at the copy rate in brackets):
+// 64 sequences of 512 to 8192 tokens, 16 heads on 2 of 128, bf16, one token
+// 53.5 (42.2), of 2048 to 32768 173 (169); 8 x 8 tokens over 30k to 65k keys,
+// heads of 256, 142 (115); one sequence of 513 tokens 9.2. Some 10 us of each
+// call are no transfer: the launches, the chain of lengths, page table and
+// first keys, and the join.
 #include <cuda_bf16.h>
 #include <limits.h>
 
@@ -749,7 +755,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
 
 // ---- many rows (bf16): products on tcgen05, sums in tensor memory --------------
 //
-// From 17 rows the warp-level instruction leaves each scheduler two warps that
+// From some 33 rows the warp-level instruction leaves each scheduler two warps that
 // wait on one another's latencies. Here the 128 rows of the tensor-core
 // instruction are COPIES copies of up to 128 / COPIES rows: copy c takes the
 // c-th part of a tile's 64 keys, with a reference and sums of its own, as a
@@ -775,9 +781,10 @@ struct TcCfg {
   static constexpr int P_BYTES = 128 * 128, Q_BYTES = 128 * D * 2;
   static constexpr int PITCH = D + 4;  // of the sums on their way out
   static constexpr int SMEM = UNITS * UNIT + P_BYTES + Q_BYTES + 1024;
-  static constexpr int TCOLS = D == 256 ? 512 : 256;  // sums, then two tiles of scores
-  static constexpr int PER_SM = D == 64 && COPIES == 4 ? 2 : 1;
-  static_assert(128 * PITCH * 4 <= UNITS * UNIT + P_BYTES + Q_BYTES, "the sums fit");
+  static constexpr int OUT_BYTES = 128 * PITCH * 4;
+  static constexpr int TCOLS = D + 2 * KT <= 256 ? 256 : 512;  // sums, then two tiles of scores
+  static constexpr int PER_SM = 1;
+  static_assert(OUT_BYTES <= UNITS * UNIT + P_BYTES + Q_BYTES, "the sums fit");
 };
 
 constexpr float kMaxGrowth = 8.f;  // log2 of a probability's bound
@@ -792,7 +799,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   extern __shared__ unsigned char raw[];
   unsigned char *sm =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[U], empty[U], s_full[2], s_empty[2], p_full, o_done, q_full, patched;
+  __shared__ uint64_t full[U], empty[U], s_full[2], s_empty[2];
+  __shared__ uint64_t p_full, o_done, q_full, landed, patched;
   __shared__ long long rows[ROWS], warp_sum[NT / 32];
   __shared__ Place place;
   __shared__ float2 sml[128];
@@ -812,6 +820,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     mbar_init(&p_full, 4);
     mbar_init(&o_done, 1);
     mbar_init(&q_full, 3);
+    mbar_init(&landed, 1);
     mbar_init(&patched, 3);
     fence_mbar_init();
     prefetch_tmap(&mk);
@@ -897,8 +906,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
       if (patch) {
-        const int u = 2 * (tb + n - 1) + 1, slot = u % U;
-        ok = mbar_wait(&full[slot], (u / U) & 1, p.err, kSiteAttnTile);
+        // told by the issuing warp: a wait for the unit's own barrier from here
+        // could be phases early, which a parity does not show
+        const int slot = (2 * (tb + n - 1) + 1) % U;
+        ok = mbar_wait(&landed, patches & 1, p.err, kSiteAttnTile);
         ok = __all_sync(0xffffffffu, ok);
         const int from = max(patch_from, 0);
         if (ok)
@@ -915,8 +926,12 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       auto sums = [&](int i) {  // O (+)= P V of tile i
         const int t = tb + i, u = 2 * t + 1, slot = u % U;
         ok = ok && mbar_wait_both(&p_full, t & 1, &full[slot], (u / U) & 1, p.err, kSiteAttnSum);
-        if (patch && i == n - 1) ok = ok && mbar_wait(&patched, patches & 1, p.err, kSiteAttnTile);
         ok = __all_sync(0xffffffffu, ok);
+        if (patch && i == n - 1) {
+          if (ok && lane == 0) mbar_arrive(&landed);
+          ok = ok && mbar_wait(&patched, patches & 1, p.err, kSiteAttnTile);
+          ok = __all_sync(0xffffffffu, ok);
+        }
         if (!ok) return;
         tc_fence_after();
 #pragma unroll
@@ -950,8 +965,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       }
       if (ok) sums(n - 1);
     } else {
-      const int R = (warp - 4) * 32 + lane, r = R % ROWS, part = R / ROWS * KC;
-      const uint32_t lanes = (uint32_t)((warp - 4) * 32) << 16;
+      const int R = (warp & 3) * 32 + lane, r = R % ROWS, part = R / ROWS * KC;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, tm_sum = tm + lanes;
       const int row = r0 + r;
       const int lim = row < p.T * (int)p.G.d ? len - p.T + p.G.div(row) + 1 : 0;
       float ref = -INFINITY, l = 0.f;
@@ -998,10 +1013,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
-            tmem_ld32(tm + lanes + c, o);
+            tmem_ld32(tm_sum + c, o);
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] *= alpha;
-            tmem_st32(tm + lanes + c, o);
+            tmem_st32(tm_sum + c, o);
           }
           tmem_wait_st();
         }
@@ -1024,7 +1039,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full);
       }
-      if (ok) ok = mbar_wait(&o_done, (tb + n - 1) & 1, p.err, kSiteAttnSum);
+      ok = ok && mbar_wait(&o_done, (tb + n - 1) & 1, p.err, kSiteAttnSum);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         // all copies and products of the item are done: the sums take their place
@@ -1033,7 +1048,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
-          tmem_ld32(tm + lanes + c, o);
+          tmem_ld32(tm_sum + c, o);
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
             *reinterpret_cast<float4 *>(so + c + j) =
@@ -1051,7 +1066,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     tb += n;
     patches += patch;
     w.next<KT>(p, items_per_seq, n);
-    if (C::COPIES > 1 && 128 * C::PITCH * 4 > U * C::UNIT && w.pos < w.end) {
+    if (C::COPIES > 1 && C::OUT_BYTES > U * C::UNIT && w.pos < w.end) {
       // the sums have overwritten P's zeros
       for (int e = tid; e < C::P_BYTES / 16; e += NT)
         *reinterpret_cast<uint4 *>(sm + U * C::UNIT + e * 16) = make_uint4(0, 0, 0, 0);
@@ -1119,6 +1134,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnParams p) 
 int box_of(const KvLayout &c) {
   const int ps = c.page_size;
   if (!c.bf16 || c.n_pages == 0 || ps % 8) return 0;
+  // a tensor map's strides end at 2^40 bytes
+  if ((c.page_stride | c.token_stride | c.head_stride) >> 39) return 0;
   return ps % 64 == 0 ? 64 : 64 % ps == 0 ? ps : 0;
 }
 
@@ -1129,10 +1146,14 @@ template <typename T, int D, class F>
 auto with_rows(int rows, int box, F f) {
   if constexpr (sizeof(T) == 2) {
     if (rows <= 16) return f(Cfg<T, D, 1>{});
-    if (box) {
-      if (rows <= 32) return f(TcCfg<D, 4>{});
-      if (rows <= 64) return f(TcCfg<D, 2>{});
-      return f(TcCfg<D, 1>{});
+    // Tensor memory where it measured faster (us, 64 sequences of 512 to 8192,
+    // D = 128, or to 4096, D = 256; warp-level kernel in brackets): 64 rows of
+    // D = 256 94 (113), 128 rows 118 (201); 64 rows of D = 128 with boxes of 16
+    // tokens 98 (90), of 32 86 (90), of 64 80 (90), 128 rows 120 (150); 32 rows
+    // of either no faster, 64 rows of D = 64 120 (118).
+    if constexpr (D >= 128) {
+      if (box && rows > 64) return f(TcCfg<D, 1>{});
+      if (box && rows > 32 && (D == 256 || box >= 32)) return f(TcCfg<D, 2>{});
     }
     if (rows <= 32) return f(Cfg<T, D, 2>{});
     return f(Cfg<T, D, 4>{});

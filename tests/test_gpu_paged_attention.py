@@ -148,6 +148,15 @@ def test_many_rows_pages_and_layouts(gdn, D, page, layout):
         c.check(c.run())
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T", [4, 8, 16])
+def test_many_rows_and_many_tiles_in_a_block(gdn, D, T):
+    # some twenty tiles of 64 keys for each block, most items ending inside one
+    lens = [1000 + 7 * i for i in range(100)]
+    c = Case(gdn, lens, T, 16, 2, D, 16, torch.bfloat16, seed=D + T)
+    c.check(c.run())
+
+
 def test_many_rows_growing_scores(gdn):
     # keys that grow along the sequence: every tile raises the maximum, far
     # beyond what the sums' reference leaves untouched
