@@ -165,29 +165,33 @@ def _addr(x):
     """Device address of a tensor argument (or a raw integer address). The C
     ABI takes packed row-major buffers, so a strided view is refused here
     rather than read as if it were packed."""
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    if not x.is_contiguous():
+    if x is None or x.__class__ is int:   # the common cases first: this runs for
+        return x                          # every buffer of every call
+    try:
+        packed = x.is_contiguous()
+    except AttributeError:
+        if isinstance(x, int):            # an int of another class
+            return int(x)
+        raise
+    if not packed:
         raise ValueError("gdn: tensor arguments must be contiguous (packed row-major)")
     return x.data_ptr()
 
 
-def _rows_addr(x, stride, width):
-    """Device address of rows [n][heads][D] that lie `stride` elements apart
-    (0 = dense): a column range of a wider matrix is such a view."""
-    if x is None or isinstance(x, int):
+def _rows_addr(x, n, stride, width, D):
+    """Device address of n rows [heads][D] that lie `stride` elements apart
+    (0 = dense, `width`): a column range of a wider matrix is such a view."""
+    if x is None or x.__class__ is int:
         return x
     st = x.stride()
-    if x.shape[0] > 1 and st[0] != (stride or width) or st[2] != 1 or st[1] != x.shape[2]:
+    if st[2] != 1 or st[1] != D and width != D or n > 1 and st[0] != (stride or width):
         raise ValueError("gdn: rows must be packed, and apart by the shape's stride")
     return x.data_ptr()
 
 
 def _cache_addr(x, cache):
     """Device address of a cache tensor; a strided one must say so in `cache`."""
-    if x is None or isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
     if not (cache.token_stride or x.is_contiguous()):
         raise ValueError("gdn: a strided cache needs its strides in gdn_kv_cache")
@@ -200,9 +204,7 @@ def _check(status):
 
 
 def _stream(stream):
-    if stream is None:
-        return None
-    if isinstance(stream, int):
+    if stream is None or stream.__class__ is int:
         return stream
     return stream.cuda_stream  # torch.cuda.Stream
 
@@ -309,11 +311,12 @@ def gdn_rope_append(shape: gdn_rope_shape, cache: gdn_kv_cache, q, k, v, positio
                     slots, q_out, k_cache, v_cache, stream=None) -> None:
     """q, k and v may be column ranges of one wider matrix (the shape's
     strides); k_cache and v_cache have the layout of `cache`."""
-    kv = cache.H_kv * cache.D
+    n, D = shape.n_tokens, cache.D
+    kv = cache.H_kv * D
     _check(lib.gdn_rope_append(
         ctypes.byref(shape), ctypes.byref(cache),
-        _rows_addr(q, shape.q_stride, shape.H * cache.D), _rows_addr(k, shape.k_stride, kv),
-        _rows_addr(v, shape.v_stride, kv), _addr(positions), _addr(inv_freq), _addr(slots),
+        _rows_addr(q, n, shape.q_stride, shape.H * D, D), _rows_addr(k, n, shape.k_stride, kv, D),
+        _rows_addr(v, n, shape.v_stride, kv, D), _addr(positions), _addr(inv_freq), _addr(slots),
         _addr(q_out), _cache_addr(k_cache, cache), _cache_addr(v_cache, cache),
         _stream(stream)))
 

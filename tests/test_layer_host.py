@@ -199,3 +199,17 @@ def test_gemm_of_nothing(gdn):
     gemm(gdn, dict(M=0), a=0)
     gemm(gdn, dict(N=0), b=0)
     assert gdn.lib.gdn_gemm_fp8(None, *[0] * 6) == gdn.GDN_ERR_INVALID_ARG
+
+
+def test_binding_refuses_views_that_do_not_match_their_shape(gdn):
+    import torch
+    qkv = torch.zeros(5, 8 * 128)
+    q = qkv[:, :512].unflatten(1, (4, 128))
+    out = torch.zeros(5, 4, 128)
+    for stride, view in ((0, q), (1024, out), (1024, q.transpose(1, 2))):
+        with pytest.raises(ValueError, match="rows must be packed"):
+            rope(gdn, dict(q_stride=stride), q=view)
+    with pytest.raises(ValueError, match="contiguous"):
+        rope(gdn, q_out=qkv[:, ::2])
+    with pytest.raises(ValueError, match="needs its strides"):
+        rope(gdn, k_cache=torch.zeros(10, 2, 16, 128).transpose(1, 2))
