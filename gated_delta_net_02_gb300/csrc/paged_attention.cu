@@ -30,9 +30,9 @@
 // Measured on one GB300 (us; the cache's bytes at the copy rate in brackets):
 // 64 sequences of 512 to 8192 tokens, 16 heads on 2 of 128, bf16, one token
 // 53.5 (42.2), of 2048 to 32768 173 (169); 8 x 8 tokens over 30k to 65k keys,
-// heads of 256, 142 (115); one sequence of 513 tokens 9.2. Some 10 us of each
-// call are no transfer: the launches, the chain of lengths, page table and
-// first keys, and the join.
+// heads of 256, 142 (115); one sequence of 513 tokens 5.9. Some 10 us of a
+// long call are no transfer: the launches, the chain of lengths, page table
+// and first keys, and the join.
 #include <cuda_bf16.h>
 #include <limits.h>
 
@@ -247,13 +247,16 @@ struct TileBf16 {
   uint32_t qf[QREG ? D / 16 : 1][4];
   uint32_t q_addr;
 
-  __device__ __forceinline__ void start(uint32_t q_s) {
-    const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % C::WM;
-    const int row = wm * 16 + (lane & 15);
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     m[0] = m[1] = -INFINITY;
     l[0] = l[1] = 0.f;
+  }
+  __device__ __forceinline__ void start(uint32_t q_s) {
+    const int lane = threadIdx.x & 31, wm = (threadIdx.x >> 5) % C::WM;
+    const int row = wm * 16 + (lane & 15);
+    clear();
     q_addr = q_s;
     if constexpr (QREG) {
 #pragma unroll
@@ -399,6 +402,9 @@ struct TileF32 {
 
   __device__ __forceinline__ void start(uint32_t q_s) {
     q_addr = q_s;
+    clear();
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       m[r] = -INFINITY;
@@ -623,8 +629,12 @@ struct Walk {
   }
 };
 
-template <class C>
-__global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnParams p) {
+// SHORT: no cache is long enough to be worth the line of tiles. A cluster of
+// `split` blocks has one item, its tiles dealt out evenly, and joins it through
+// distributed shared memory in rank order: one launch, no workspace.
+template <class C, bool SHORT>
+__global__ void __launch_bounds__(C::THREADS, C::PER_SM)
+    attn_kernel(const AttnParams p, int split) {
   using T = typename C::In;
   using Tile = typename TileOf<C>::type;
   constexpr int D = C::D, KT = C::KT, ROWS = C::ROWS, WK = C::WK, S = C::STAGES;
@@ -647,11 +657,21 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   Walk w;
-  if (!w.begin<KT, NT>(p, items_per_seq, warp_sum, place)) {
+  const int rank = SHORT ? (int)(blockIdx.x % split) : 0;
+  if constexpr (SHORT) {
+    const int item = blockIdx.x / split;
+    w.s = item / items_per_seq;
+    w.x = item - w.s * items_per_seq;
+    w.len = seq_len(p, w.s, w.x == 0 && rank == 0);
+    w.nt = item_tiles(w.len, KT);
+    w.tile0 = rank * w.nt / split;
+    w.pos = 0;
+    w.end = (rank + 1) * w.nt / split - w.tile0;  // may be none
+  } else if (!w.begin<KT, NT>(p, items_per_seq, warp_sum, place)) {
     if (tid == 0) p.cut[blockIdx.x].x = -1;
     return;
   }
-  for (int seg = 0; w.pos < w.end; ++seg) {
+  for (int seg = 0; w.pos < w.end || (SHORT && seg == 0); ++seg) {
     const int n = w.tiles(), s = w.s, x = w.x, len = w.len, tile0 = w.tile0;
     const int kvh = p.row_blocks.div(x), r0 = (x - kvh * (int)p.row_blocks.d) * ROWS;
     const long long head = (long long)kvh * p.head_stride;
@@ -715,7 +735,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
     for (int i = 0; i < S - 1; ++i) load_tile(i);
     int next_page = page[S];
 
-    if (seg == 0 && tid == NT - 1) w.list_join(p, items_per_seq);
+    if (!SHORT && seg == 0 && tid == NT - 1) w.list_join(p, items_per_seq);
 
     int lim[sizeof(Tile::m) / sizeof(float)];
     Tile::limits(
@@ -726,6 +746,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
         },
         lim);
     Tile acc;
+    if (SHORT && n == 0) acc.clear();
     for (int i = 0; i < n; ++i) {
       cp_async_wait<S - 2>();
       __syncthreads();
@@ -744,9 +765,44 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM) attn_kernel(const AttnP
     acc.flush(so, sml);
     __syncthreads();
 
-    const bool whole = n == w.nt;
-    const long long slot = (long long)blockIdx.x * 2 + (seg > 0);
-    finish_item<C>(p, so, D, sml, rows, whole, slot);
+    if (SHORT && split > 1) {
+      // this block's piece of the item, behind its key groups' sums
+      float *piece = so + WK * ROWS * D;
+      float2 *piece_ml = reinterpret_cast<float2 *>(piece + ROWS * D);
+      AttnParams local = p;
+      local.part_o = piece;
+      local.part_ml = piece_ml;
+      finish_item<C>(local, so, D, sml, rows, false, 0);
+      cluster_sync();
+#pragma unroll 1
+      for (int e = rank * NT + tid; e < ROWS * (D / 4); e += split * NT) {
+        const int r = e / (D / 4), c = e % (D / 4) * 4;
+        if (rows[r] < 0) continue;
+        const uint32_t at_ml = smem_u32(piece_ml + r), at = smem_u32(piece + r * D + c);
+        float mm = -INFINITY, ll = 0.f;
+        for (int k = 0; k < split; ++k) mm = fmaxf(mm, ld_cluster_f2(at_ml, k).x);
+        const float ref = mm == -INFINITY ? 0.f : mm;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < split; ++k) {
+          const float2 ml = ld_cluster_f2(at_ml, k);
+          const float4 v = ld_cluster_f4(at, k);
+          const float f = exp2_ftz(ml.x - ref);
+          ll += f * ml.y;
+          sum.x = fmaf(f, v.x, sum.x);
+          sum.y = fmaf(f, v.y, sum.y);
+          sum.z = fmaf(f, v.z, sum.z);
+          sum.w = fmaf(f, v.w, sum.w);
+        }
+        const float inv = 1.f / (ll == 0.f ? 1.f : ll);
+        store4(static_cast<T *>(p.out) + rows[r] * D + c,
+               make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
+      }
+      cluster_sync();  // no block leaves while its piece is read
+      return;
+    }
+    finish_item<C>(p, so, D, sml, rows, n == w.nt, (long long)blockIdx.x * 2 + (seg > 0));
+    if (SHORT) return;
     __syncthreads();  // before the next item's copies reuse the tiles
 
     w.next<KT>(p, items_per_seq, n);
@@ -1205,6 +1261,23 @@ int grid_of(const KvLayout &c, int n_seqs, int max_pages, int row_blocks) {
   return (int)most;
 }
 
+// Blocks for each item when the longest possible sequence is short enough to
+// need no line of tiles (0: it is not). Many items of up to 16 tiles take a
+// block each, and the GPU's own scheduling evens them out (256 sequences of 1
+// to 1000 tokens, 8 kv heads of 64: 50 us, 77 as a line, where a block's items
+// follow one another with a gap at each). Few items are split over a cluster,
+// a few tiles a block (one sequence of 513 tokens 5.9 us, 9.2 as a line).
+template <class C>
+int short_split(const KvLayout &c, const AttnParams &p) {
+  const long long tiles = ((long long)p.max_pages * c.page_size + C::KT - 1) / C::KT;
+  const long long items = (long long)p.n_seqs * c.H_kv * p.row_blocks.d;
+  const long long most = (long long)C::PER_SM * kSms;
+  if (tiles <= 2 || items * 2 > most) return tiles <= 16 ? 1 : 0;
+  int split = 2;
+  while (split < 8 && split * 2 < tiles && items * split * 2 <= most) split *= 2;
+  return tiles <= 4 * split ? split : 0;
+}
+
 template <class C>
 cudaError_t launch_cfg(const AttnParams &p, const KvLayout &c, int grid, cudaStream_t stream) {
   cudaError_t e;
@@ -1220,9 +1293,20 @@ cudaError_t launch_cfg(const AttnParams &p, const KvLayout &c, int grid, cudaStr
                    box);
   } else {
     static_assert(C::SMEM + 4 * C::KT * 8 + 8 * C::ROWS + 128 <= 227 * 1024, "shared memory");
-    e = cudaFuncSetAttribute(attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static_assert((C::WK + 1) * C::ROWS * C::D * 4 + C::ROWS * 8 <= C::SMEM, "a piece fits");
+    const int split = short_split<C>(c, p);
+    if (split) {
+      e = cudaFuncSetAttribute(attn_kernel<C, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               C::SMEM);
+      if (e != cudaSuccess) return e;
+      const unsigned items = (unsigned)(p.n_seqs * p.H_kv * (int)p.row_blocks.d);
+      return launch_pdl_cluster(split, attn_kernel<C, true>, dim3(items * split), dim3(C::THREADS),
+                                C::SMEM, stream, p, split);
+    }
+    e = cudaFuncSetAttribute(attn_kernel<C, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_kernel<C>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, p);
+    e = launch_pdl(attn_kernel<C, false>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, p, 1);
   }
   if (e != cudaSuccess || grid == 1) return e;
   const int rows = p.row_blocks.d > 1 ? C::ROWS : p.T * (int)p.G.d;
