@@ -357,6 +357,7 @@ struct LargeCfg {
   static constexpr int HALF = 128 * kBlockK, STAGE = 2 * HALF;
   static constexpr int STAGES = 4, BOXES = 2;
   static constexpr int BOX = 32 * 128;  // output box of a warp: 32 rows of 128 bytes
+  static_assert(32 * 33 * 4 <= BOXES * BOX, "32 rows of 32 sums and a pad");
   static constexpr int SMEM = STAGES * STAGE + 8 * BOXES * BOX + 1024;
   static constexpr int THREADS = 384;  // four warps of roles, eight of epilogue
 };
@@ -388,6 +389,29 @@ __device__ __forceinline__ void store_boxes(unsigned char *box, int lane, const 
     if (lane == 0) {
       tma_store_2d(&mo, n0 + i * COLS, m0, at);
       bulk_commit();
+    }
+  }
+}
+
+// The same for rows that do not start on 16 bytes: transposed through shared
+// memory 32 columns at a time, so that a store's lanes write one run of a row.
+__device__ __forceinline__ void store_rows(const GemmParams &p, float *buf, int lane, int n0,
+                                           int m0, const float (&acc)[128]) {
+#pragma unroll
+  for (int c0 = 0; c0 < 128; c0 += 32) {
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 32; ++c) buf[lane * 33 + c] = acc[c0 + c];
+    __syncwarp();
+    const int n = n0 + c0 + lane;
+    if (n >= p.N) continue;
+    const int rows = min(32, p.M - m0);
+    long long at = (long long)m0 * p.N + n;
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r, at += p.N) {
+      const float v = buf[r * 33 + lane];
+      if (p.bf16_out) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
+      else static_cast<float *>(p.out)[at] = v;
     }
   }
 }
@@ -562,21 +586,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
       }
       if (!ok) break;
       const int m0 = t % m_tiles * C::TM + rank * 128 + (warp & 3) * 32;
-      const int n0 = t / m_tiles * C::TN + half * 128, m = m0 + lane;
+      const int n0 = t / m_tiles * C::TN + half * 128;
       if (boxes) {
         // through shared memory in swizzled boxes of 32 rows x 128 bytes, which
         // bulk copies take to the output while the next tile begins (stores
         // from registers, 32 rows at a time, took a sixth of the whole call)
         if (p.bf16_out) store_boxes<true>(box, lane, mo, n0, m0, acc);
         else store_boxes<false>(box, lane, mo, n0, m0, acc);
-      } else if (m < p.M) {
-        const long long at = (long long)m * p.N + n0;
-        const bool vec = (p.N & 3) == 0;
-#pragma unroll
-        for (int j = 0; j < 128; j += 4)
-          if (n0 + j < p.N)
-            store_out4(p, at + j, make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]),
-                       p.N - n0 - j, vec);
+      } else {
+        store_rows(p, reinterpret_cast<float *>(box), lane, n0, m0, acc);
       }
     }
     if (boxes && lane == 0) bulk_wait_all();
