@@ -47,22 +47,6 @@ namespace {
 constexpr int kJoinThreads = 128;
 constexpr int kMinTiles = 2;  // shortest run of tiles worth a block of its own
 
-// Division by a number fixed at launch: n / d for 0 <= n < 2^31 as one high
-// product and a shift (Granlund and Montgomery 1994: mul = floor(2^32 (2^s -
-// d) / d) + 1 with s = ceil(log2 d), q = (mulhi(mul, n) + n) >> s).
-struct FastDiv {
-  uint32_t mul, shift, d;
-  FastDiv() = default;
-  explicit FastDiv(uint32_t div) : d(div) {
-    shift = 0;
-    while ((1ull << shift) < d) ++shift;
-    mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
-  }
-  __device__ __forceinline__ int div(int n) const {
-    return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift);
-  }
-};
-
 struct AttnParams {
   const void *q, *k, *v;
   void *out;
