@@ -1258,7 +1258,11 @@ int short_split(const KvLayout &c, const AttnParams &p) {
   const long long most = (long long)C::PER_SM * kSms;
   if (tiles <= 2 || items * 2 > most) return tiles <= 16 ? 1 : 0;
   int split = 2;
-  while (split < 8 && split * 2 < tiles && items * split * 2 <= most) split *= 2;
+  // Not more clusters of 8 than find room at once where an SM holds one block:
+  // 14 items of 900 tokens, D 256, take 8.5 us by 8 and 10.9 by 4, 18 items
+  // 16.4 and 10.9. Where it holds more, all do (72 items, D 64: 6.9 and 7.7).
+  const int widest = C::PER_SM > 1 || items <= 14 ? 8 : 4;
+  while (split < widest && split * 2 < tiles && items * split * 2 <= most) split *= 2;
   return tiles <= 4 * split ? split : 0;
 }
 
