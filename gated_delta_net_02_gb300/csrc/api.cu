@@ -10,9 +10,9 @@
 #include <vector>
 
 #include "api_util.h"
-#include "common.cuh"
 #include "gdn.h"
 #include "kernels.h"
+#include "layer.cuh"
 
 namespace {
 

@@ -44,7 +44,6 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "tensor_map.h"
 #include "umma.cuh"
 
 namespace gdn {
@@ -1613,6 +1612,26 @@ __global__ void __launch_bounds__(SCAN_THREADS, 1)
 
 namespace gdn {
 namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                         cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  });
+  return fn;
+}
 
 // bf16 [Ntok][H][D] viewed as (D, H, Ntok); 64 x 1 x 64 boxes, 128-byte swizzle
 bool map_tokens(CUtensorMap *m, const void *base, int ntok, int H, int D) {

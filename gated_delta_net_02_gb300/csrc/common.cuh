@@ -16,8 +16,6 @@ enum DevErr : int {
   kDevBadSeqlens = 2,  // cu_seqlens is not a valid offset table
   kDevOverlap = 3,     // a state_in pointer points into the slot buffer
   kDevGateRange = 4,   // a chunk's cumulative log-gate leaves [-80, 80] (chunked path)
-  kDevBadSlot = 5,     // a slot index beyond the key-value cache
-  kDevBadPage = 6,     // a page table entry or a length beyond the key-value cache
 };
 
 // Where a bounded wait ran out: bits 8..15 of a timeout error word. The host
@@ -36,15 +34,6 @@ enum WaitSite : int {
   kSiteScanStage = 52,    // chunk scan, MMA issuer: a stage's copies
   kSiteScanS0 = 53,       // chunk scan, MMA issuer: the state operand
   kSiteScanD = 54,        // chunk scan, MMA issuer: the D tile
-  kSiteAttnTile = 57,     // attention: a tile of keys copied or used
-  kSiteAttnScore = 58,    // attention: scores formed or taken
-  kSiteAttnSum = 59,      // attention: probabilities taken into the sums
-  kSiteNormRow = 55,      // RMS norm: a group of rows
-  kSiteRopeRow = 56,      // rotary positions: a token's rows
-  kSiteGemmEmpty = 61,    // e4m3 product, producer: a stage released by its products
-  kSiteGemmStage = 62,    // e4m3 product, MMA issuer: a stage's copies
-  kSiteGemmAcc = 63,      // e4m3 product: a tensor-memory buffer filled or taken
-  kSiteGemmScale = 64,    // e4m3 product: a scale vector filled or taken
 };
 
 // Largest |cumulative log-gate| inside one chunk that the chunked kernels
@@ -120,18 +109,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
   return mbar_wait_n(bar, parity, err, site, kMaxPolls);
 }
 
-// Waits for two phases at once: a poll takes some 150 cycles even of a phase
-// that has completed, and the two polls of a round overlap.
-__device__ __forceinline__ bool mbar_wait_both(uint64_t *bar0, uint32_t parity0, uint64_t *bar1,
-                                               uint32_t parity1, int *err, int site) {
-  for (uint32_t i = 0; i < kMaxPolls; ++i) {
-    const bool a = mbar_try_wait(bar0, parity0), b = mbar_try_wait(bar1, parity1);
-    if (a && b) return true;
-  }
-  set_error(err, kDevTimeout | (site << 8));
-  return false;
-}
-
 // Orders this thread's generic-proxy shared-memory accesses before later
 // async-proxy accesses (TMA copies and stores, tcgen05.mma operands).
 __device__ __forceinline__ void fence_proxy_async() {
@@ -143,58 +120,20 @@ __device__ __forceinline__ void fence_proxy_async() {
 // scheduled once every block of the previous kernel in the stream has
 // executed griddepcontrol.launch_dependents; it must execute
 // griddepcontrol.wait before touching memory that kernel may write.
-// cluster: blocks of a cluster along x (1: none).
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl_cluster(int cluster, void (*kernel)(KArgs...), dim3 grid, dim3 block,
-                                      size_t smem, cudaStream_t stream, Args &&...args) {
+inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                              cudaStream_t stream, Args &&...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                              cudaStream_t stream, Args &&...args) {
-  return launch_pdl_cluster(1, kernel, grid, block, smem, stream, static_cast<Args &&>(args)...);
-}
-
-// ---- thread-block clusters ----------------------------------------------------
-
-// Every thread of every block of the cluster, warps converged.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                   : "memory");
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t local, uint32_t rank) {
-  float4 v;
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(remote)
-               : "memory");
-  return v;
-}
-
-__device__ __forceinline__ float2 ld_cluster_f2(uint32_t local, uint32_t rank) {
-  float2 v;
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
-               : "=f"(v.x), "=f"(v.y)
-               : "r"(remote)
-               : "memory");
-  return v;
 }
 
 // ---- bulk copies (TMA, non-tensor form) ------------------------------------
@@ -237,22 +176,6 @@ __device__ __forceinline__ void st_f4(float *p, float4 v) {
                "f"(v.y), "f"(v.z), "f"(v.w)
                : "memory");
 }
-
-// Division by a number fixed at launch: n / d for 0 <= n < 2^31 as one high
-// product and a shift (Granlund and Montgomery 1994: mul = floor(2^32 (2^s -
-// d) / d) + 1 with s = ceil(log2 d), q = (mulhi(mul, n) + n) >> s).
-struct FastDiv {
-  uint32_t mul, shift, d;
-  FastDiv() = default;
-  explicit FastDiv(uint32_t div) : d(div) {
-    shift = 0;
-    while ((1ull << shift) < d) ++shift;
-    mul = (uint32_t)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
-  }
-  __device__ __forceinline__ int div(int n) const {
-    return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift);
-  }
-};
 
 template <typename T>
 __device__ __forceinline__ float to_f32(T x);

@@ -34,10 +34,9 @@
 //    about as long again as the product.
 #include <cuda_bf16.h>
 
-#include "common.cuh"
 #include "kernels.h"
+#include "layer.cuh"
 #include "tensor_map.h"
-#include "umma.cuh"
 
 namespace gdn {
 namespace {

@@ -21,8 +21,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
-#include "common.cuh"
 #include "kernels.h"
+#include "layer.cuh"
 
 namespace gdn {
 namespace {

@@ -36,10 +36,9 @@
 #include <cuda_bf16.h>
 #include <limits.h>
 
-#include "common.cuh"
 #include "kernels.h"
+#include "layer.cuh"
 #include "tensor_map.h"
-#include "umma.cuh"
 
 namespace gdn {
 namespace {

@@ -18,9 +18,8 @@
 // about 2^-24 turns at any position.
 #include <cuda_bf16.h>
 
-#include "common.cuh"
 #include "kernels.h"
-#include "umma.cuh"
+#include "layer.cuh"
 
 namespace gdn {
 namespace {
