@@ -29,10 +29,10 @@
 //
 // Measured on one GB300 (us; the cache's bytes at the copy rate in brackets):
 // 64 sequences of 512 to 8192 tokens, 16 heads on 2 of 128, bf16, one token
-// 53.5 (42.2), of 2048 to 32768 173 (169); 8 x 8 tokens over 30k to 65k keys,
-// heads of 256, 142 (115); one sequence of 513 tokens 5.9. Some 10 us of a
-// long call are no transfer: the launches, the chain of lengths, page table
-// and first keys, and the join.
+// 52.6 (42.2), of 2048 to 32768 173 (169); 8 x 8 tokens over 30k to 65k keys,
+// heads of 256, 135 (115); one sequence of 513 tokens 5.9, of 60000 22.8 (9.1).
+// Some 10 us of a long call are no transfer: the launches, the chain of
+// lengths, page table and first keys, and the join (4 us of the 52.6).
 #include <cuda_bf16.h>
 #include <limits.h>
 
@@ -43,7 +43,6 @@
 namespace gdn {
 namespace {
 
-constexpr int kJoinThreads = 128;
 constexpr int kMinTiles = 2;  // shortest run of tiles worth a block of its own
 
 struct AttnParams {
@@ -52,7 +51,10 @@ struct AttnParams {
   const int32_t *table, *lens;
   float *part_o;    // [2 grid][rows][D] unnormalised sums of cut items
   float2 *part_ml;  // [2 grid][rows]
-  int4 *cut;        // [grid] joins: x = item (-1: none), y, z = first and last block
+  int4 *cut;        // [joins] x = item (-1: none), y = its first piece, z = its tiles
+                    // beyond that block's, w = tiles of a block
+  int joins;        // items, listed by item, or the grid, by block: the fewer
+  bool by_item;
   long long page_stride, token_stride, head_stride;
   FastDiv page_size, G, row_blocks;
   int n_seqs, T, H, H_kv, n_pages, max_pages, grouped;
@@ -591,14 +593,17 @@ struct Walk {
   __device__ __forceinline__ int tiles() const {
     return (int)min((long long)(nt - tile0), end - pos);
   }
-  // Names the join of a cut item, if this is the first block that starts inside it.
-  __device__ __forceinline__ void list_join(const AttnParams &p, int items_per_seq) const {
-    const long long a = pos - tile0, before = pos - run;
+  // Lists whether the current item, which starts here, has to be joined, and
+  // from which blocks: by item where items are few, else by block (of a
+  // block's items only the last can go on elsewhere).
+  __device__ __forceinline__ void list_join(const AttnParams &p, int items_per_seq, int n) const {
+    if (p.by_item ? tile0 != 0 : pos + n < end) return;
+    const int item = s * items_per_seq + x;
     int4 cut = make_int4(-1, 0, 0, 0);
-    if (tile0 > 0 && before <= a)
-      cut = make_int4(s * items_per_seq + x, (int)quotient(a, run),
-                      (int)quotient(a + nt - 1, run), a == before ? 0 : 1);
-    p.cut[blockIdx.x] = cut;
+    if (tile0 == 0 && n < nt)
+      cut = make_int4(item, 2 * blockIdx.x + (pos == run * blockIdx.x ? 0 : 1), nt - n,
+                      (int)min(run, (long long)INT_MAX));
+    p.cut[p.by_item ? item : (int)blockIdx.x] = cut;
   }
   template <int KT>
   __device__ __forceinline__ void next(const AttnParams &p, int items_per_seq, int n) {
@@ -651,7 +656,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     w.pos = 0;
     w.end = (rank + 1) * w.nt / split - w.tile0;  // may be none
   } else if (!w.begin<KT, NT>(p, items_per_seq, warp_sum, place)) {
-    if (tid == 0) p.cut[blockIdx.x].x = -1;
+    if (tid == 0 && !p.by_item) p.cut[blockIdx.x].x = -1;
     return;
   }
   for (int seg = 0; w.pos < w.end || (SHORT && seg == 0); ++seg) {
@@ -718,7 +723,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     for (int i = 0; i < S - 1; ++i) load_tile(i);
     int next_page = page[S];
 
-    if (!SHORT && seg == 0 && tid == NT - 1) w.list_join(p, items_per_seq);
+    if (!SHORT && tid == NT - 1) w.list_join(p, items_per_seq, n);
 
     int lim[sizeof(Tile::m) / sizeof(float)];
     Tile::limits(
@@ -884,7 +889,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 
   Walk w;
   const bool any = w.begin<KT, NT>(p, items_per_seq, warp_sum, place);
-  if (!any && tid == 0) p.cut[blockIdx.x].x = -1;
+  if (!any && tid == 0 && !p.by_item) p.cut[blockIdx.x].x = -1;
   int tb = 0, patches = 0;  // tiles and cleared units of the items before
   for (int seg = 0; any && w.pos < w.end; ++seg) {
     const int n = w.tiles(), s = w.s, len = w.len, tile0 = w.tile0;
@@ -893,7 +898,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     const int patch_from = len - (tile0 + n - 1) * KT;
     const bool patch = patch_from < KT;
     if (tid < ROWS) rows[tid] = out_row(p, s, kvh, r0 + tid);
-    if (seg == 0 && tid == NT - 1) w.list_join(p, items_per_seq);
+    if (tid == NT - 1) w.list_join(p, items_per_seq, n);
     __syncthreads();
     bool ok = true;
     if (warp == 0) {
@@ -1117,53 +1122,73 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   if (warp == 8) tmem_dealloc(tm, C::TCOLS);
 }
 
-// Joins the cut items: block (i, r) row r of the item that the main kernel's
-// block i listed. The warps take the pieces in turn, a lane D / 32 columns.
-template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttnParams p) {
+// Joins the cut items: block (i, r) row r of the item listed at i. The W warps
+// take the pieces in turn, a lane D / 64 pairs of columns.
+template <typename T, int D, int ROWS, int W>
+__global__ void __launch_bounds__(32 * W) join_kernel(const AttnParams p, int grid) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int VL = D / 32;
+  constexpr int VL = D / 64;  // float2 of a lane
   const int4 cut = p.cut[blockIdx.x];
-  if (cut.x < 0) return;
-  const int r = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // a main kernel that gave up (error word) may have left the list unwritten
+  if (cut.x < 0 || cut.x >= p.n_seqs * p.H_kv * (int)p.row_blocks.d || cut.y < 0 || cut.z <= 0 ||
+      cut.w <= 0)
+    return;
+  const int first = cut.y >> 1, np = (cut.z - 1) / cut.w + 2;  // blocks of the item
+  if (first + (long long)np > grid) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.y;
   const int per_seq = p.H_kv * (int)p.row_blocks.d, s = cut.x / per_seq, x = cut.x - s * per_seq;
   const int kvh = p.row_blocks.div(x), rb = x - kvh * (int)p.row_blocks.d;
   const long long row = out_row(p, s, kvh, rb * ROWS + r);
   if (row < 0) return;
-  const int np = cut.z - cut.y + 1;
   // the item is the first block's last item (its only one if it starts there),
   // and the first of all later blocks
-  auto slot = [&](int i) { return 2LL * (cut.y + i) + (i == 0 && cut.w); };
+  auto slot = [&](int i) { return i == 0 ? (long long)cut.y : 2LL * (first + i); };
   float mm = -INFINITY;
   for (int i = lane; i < np; i += 32) mm = fmaxf(mm, p.part_ml[slot(i) * ROWS + r].x);
 #pragma unroll
   for (int off = 16; off; off >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, off));
   const float ref = mm == -INFINITY ? 0.f : mm;
-  float sum[VL], ll = 0.f;
+  float2 sum[VL];
+  float ll = 0.f;
 #pragma unroll
-  for (int j = 0; j < VL; ++j) sum[j] = 0.f;
+  for (int j = 0; j < VL; ++j) sum[j] = make_float2(0.f, 0.f);
 #pragma unroll 4
-  for (int i = warp; i < np; i += 4) {
+  for (int i = warp; i < np; i += W) {
     const float2 ml = p.part_ml[slot(i) * ROWS + r];
     const float f = exp2_ftz(ml.x - ref);
     ll += f * ml.y;
-    const float *o = p.part_o + (slot(i) * ROWS + r) * D;
+    const float2 *o = reinterpret_cast<const float2 *>(p.part_o + (slot(i) * ROWS + r) * D);
 #pragma unroll
-    for (int j = 0; j < VL; ++j) sum[j] = fmaf(f, o[j * 32 + lane], sum[j]);
+    for (int j = 0; j < VL; ++j) {
+      const float2 v = o[j * 32 + lane];
+      sum[j].x = fmaf(f, v.x, sum[j].x);
+      sum[j].y = fmaf(f, v.y, sum[j].y);
+    }
   }
-  __shared__ float so[4][D], sl[4];
+  __shared__ float2 so[W][D / 2];
+  __shared__ float sl[W];
 #pragma unroll
   for (int j = 0; j < VL; ++j) so[warp][j * 32 + lane] = sum[j];
   if (lane == 0) sl[warp] = ll;
   __syncthreads();
-  const float l4 = sl[0] + sl[1] + sl[2] + sl[3], inv = 1.f / (l4 == 0.f ? 1.f : l4);
-  for (int c = threadIdx.x; c < D; c += kJoinThreads) {
-    const float v = (so[0][c] + so[1][c] + so[2][c] + so[3][c]) * inv;
-    T *out = static_cast<T *>(p.out) + row * D + c;
-    if constexpr (sizeof(T) == 2) *out = __float2bfloat16_rn(v);
-    else *out = v;
+  const int c = threadIdx.x;
+  if (c >= D / 2) return;
+  float l = 0.f;
+  float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    l += sl[k];
+    v.x += so[k][c].x;
+    v.y += so[k][c].y;
   }
+  const float inv = 1.f / (l == 0.f ? 1.f : l);
+  T *out = static_cast<T *>(p.out) + row * D + 2 * c;
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint32_t *>(out) = bf16x2(v.x * inv, v.y * inv);
+  else
+    *reinterpret_cast<float2 *>(out) = make_float2(v.x * inv, v.y * inv);
 }
 
 // ---- host side ------------------------------------------------------------------
@@ -1297,8 +1322,15 @@ cudaError_t launch_cfg(const AttnParams &p, const KvLayout &c, int grid, cudaStr
   }
   if (e != cudaSuccess || grid == 1) return e;
   const int rows = p.row_blocks.d > 1 ? C::ROWS : p.T * (int)p.G.d;
-  return launch_pdl(join_kernel<typename C::In, C::D, C::ROWS>, dim3(grid, rows),
-                    dim3(kJoinThreads), 0, stream, p);
+  const long long items = (long long)p.n_seqs * p.H_kv * p.row_blocks.d;
+  auto join = [&](auto kernel, int warps) {
+    return launch_pdl(kernel, dim3(p.joins, rows), dim3(32 * warps), 0, stream, p, grid);
+  };
+  // pieces of an item that 4 warps would take in many rounds (one sequence of
+  // 60000 tokens, 2 kv heads, 152 pieces: 22.8 us with 16 warps, 27.9 with 4;
+  // 8 sequences of 20000, 19 pieces: 35.6 and 34.8)
+  if (grid > 32 * items) return join(join_kernel<typename C::In, C::D, C::ROWS, 16>, 16);
+  return join(join_kernel<typename C::In, C::D, C::ROWS, 4>, 4);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -1332,6 +1364,14 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream) {
     using C = decltype(cfg);
     p.row_blocks = FastDiv((rows + C::ROWS - 1) / C::ROWS);
     const int grid = grid_of<C>(c, a.n_seqs, a.max_pages, (int)p.row_blocks.d);
+    const long long items = (long long)a.n_seqs * c.H_kv * p.row_blocks.d;
+    // By block, a join's empty places are left again after one read, and its
+    // others lie evenly on the SMs (64 sequences of 512 to 8192, one row block
+    // of 8: 52.6 us, 53.7 by item), until they are more than the GPU holds at
+    // once (8 sequences of 30k to 65k, 64 rows: 144 us, 137.7 by item).
+    const long long by_block = (long long)grid * (p.row_blocks.d > 1 ? C::ROWS : rows);
+    p.by_item = items <= grid && by_block > 16 * kSms;
+    p.joins = p.by_item ? (int)items : grid;
     unsigned char *ws = static_cast<unsigned char *>(a.workspace);
     p.cut = reinterpret_cast<int4 *>(ws);
     ws += up256((size_t)grid * 16);
