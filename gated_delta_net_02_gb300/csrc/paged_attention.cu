@@ -29,8 +29,8 @@
 //
 // Measured on one GB300 (us; the cache's bytes at the copy rate in brackets):
 // 64 sequences of 512 to 8192 tokens, 16 heads on 2 of 128, bf16, one token
-// 52.6 (42.2), of 2048 to 32768 173 (169); 8 x 8 tokens over 30k to 65k keys,
-// heads of 256, 135 (115); one sequence of 513 tokens 5.9, of 60000 22.8 (9.1).
+// 53.0 (42.2), of 2048 to 32768 173 (169); 8 x 8 tokens over 30k to 65k keys,
+// heads of 256, 137 (115); one sequence of 513 tokens 5.9, of 60000 22.8 (9.1).
 // Some 10 us of a long call are no transfer: the launches, the chain of
 // lengths, page table and first keys, and the join (4 us of the 52.6).
 #include <cuda_bf16.h>
@@ -106,7 +106,8 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 
 // Tile geometry. bf16: WM warps along the rows, 16 rows each; the other warps
-// share out the tile's keys. fp32: WM rows of each warp, all warps on all keys.
+// share out the tile's keys. fp32: four warps along the rows, WM rows each; the
+// other warps share out the keys, and a warp's lanes a key's columns.
 template <typename T, int D_, int WM_>
 struct Cfg {
   using In = T;
@@ -116,10 +117,12 @@ struct Cfg {
   static constexpr int ROWS = kBf16 ? 16 * WM : 4 * WM;
   // Two warps for each of an SM's schedulers: two blocks of four, or one of
   // eight where the tiles leave room for one block only and a warp has at
-  // least 16 keys of its own.
-  static constexpr int WARPS = kBf16 && D == 256 && WM > 1 ? 8 : 4;
+  // least 16 keys of its own. fp32: eight from heads of 128 on (us, eight and
+  // four: 16 sequences of 5000, 4 rows of 256, 137 and 168; 32 rows of 128 197
+  // and 223; 16 sequences of 10000, 16 rows of 64, 133 and 119).
+  static constexpr int WARPS = (kBf16 ? D == 256 && WM > 1 : D > 64) ? 8 : 4;
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr int WK = kBf16 ? WARPS / WM : 1;  // key groups with their own m, l and sum
+  static constexpr int WK = kBf16 ? WARPS / WM : WARPS / 4;  // key groups with their own m, l and sum
   static constexpr int KT = kBf16 ? 64 : 32;     // keys of a tile
   static constexpr int ROW_BYTES = D * (int)sizeof(T);
   static constexpr int CH = ROW_BYTES / 16;      // 16-byte chunks of a row
@@ -381,10 +384,14 @@ __device__ __forceinline__ void fma2(float &x, float &y, float a, float b, float
 template <class C>
 struct TileF32 {
   static constexpr int D = C::D, VL = D / 32, R = C::WM;
+  static constexpr int KEYS = C::KT / C::WK, PARTS = C::WK;
+  static_assert(KEYS * PARTS == 32, "a lane for each key and part of the columns");
   float o[R][VL];
   float m[R], l[R];
   uint32_t q_addr;
 
+  static __device__ __forceinline__ int row_group() { return threadIdx.x >> 5 & 3; }
+  static __device__ __forceinline__ int key_group() { return threadIdx.x >> 7; }
   __device__ __forceinline__ void start(uint32_t q_s) {
     q_addr = q_s;
     clear();
@@ -423,17 +430,18 @@ struct TileF32 {
   template <class F>
   static __device__ __forceinline__ void limits(F limit_of, int (&lim)[R]) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) lim[r] = limit_of((threadIdx.x >> 5) * R + r);
+    for (int r = 0; r < R; ++r) lim[r] = limit_of(row_group() * R + r);
   }
   __device__ __forceinline__ void tile(uint32_t k_s, uint32_t v_s, int key0, const int (&lim)[R],
                                        float scale_log2, float *p_s) {
-    const int lane = threadIdx.x & 31, row0 = (threadIdx.x >> 5) * R;
+    const int lane = threadIdx.x & 31, row0 = row_group() * R;
+    const int key = key_group() * KEYS + lane % KEYS, part = lane / KEYS;
     float s[R], s2[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) s[r] = s2[r] = 0.f;
 #pragma unroll(R > 4 ? 2 : 4)
-    for (int c = 0; c < C::CH; ++c) {
-      const float4 k = lds4(k_s + chunk_at<C>(lane, c));
+    for (int c = part; c < C::CH; c += PARTS) {
+      const float4 k = lds4(k_s + chunk_at<C>(key, c));
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const float4 q = lds4(q_addr + chunk_at<C>(row0 + r, c));
@@ -444,21 +452,25 @@ struct TileF32 {
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float x = key0 + lane < lim[r] ? (s[r] + s2[r]) * scale_log2 : -INFINITY;
+      float dot = s[r] + s2[r];
+#pragma unroll
+      for (int off = 16; off >= KEYS; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+      const float x = key0 + key < lim[r] ? dot * scale_log2 : -INFINITY;
       float mx = x;
 #pragma unroll
-      for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      for (int off = KEYS / 2; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float mn = fmaxf(m[r], mx), ref = mn == -INFINITY ? 0.f : mn;
       const float alpha = exp2_ftz(m[r] - ref), e = exp2_ftz(x - ref);
       m[r] = mn;
       l[r] = l[r] * alpha + e;  // this lane's keys; summed over the lanes at the end
-      p_s[(row0 + r) * C::KT + lane] = e;
+      if (part == 0) p_s[(row0 + r) * C::KT + key] = e;
 #pragma unroll
       for (int i = 0; i < VL; ++i) o[r][i] *= alpha;
     }
     __syncwarp();
 #pragma unroll(R > 4 ? 2 : 4)
-    for (int j = 0; j < C::KT; j += 2) {
+    for (int jk = 0; jk < KEYS; jk += 2) {
+      const int j = key_group() * KEYS + jk;
       float2 pj[R];
 #pragma unroll
       for (int r = 0; r < R; ++r)
@@ -477,12 +489,12 @@ struct TileF32 {
     }
   }
   __device__ __forceinline__ void flush(float *so, float2 *sml) {
-    const int lane = threadIdx.x & 31, row0 = (threadIdx.x >> 5) * R;
+    const int lane = threadIdx.x & 31, row0 = key_group() * C::ROWS + row_group() * R;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       float t = l[r];
 #pragma unroll
-      for (int off = 16; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+      for (int off = KEYS / 2; off; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
       if (lane == 0) sml[row0 + r] = make_float2(m[r], t);
 #pragma unroll
       for (int i = 0; i < VL; ++i) {
@@ -1368,7 +1380,7 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream) {
     // By block, a join's empty places are left again after one read, and its
     // others lie evenly on the SMs (64 sequences of 512 to 8192, one row block
     // of 8: 52.6 us, 53.7 by item), until they are more than the GPU holds at
-    // once (8 sequences of 30k to 65k, 64 rows: 144 us, 137.7 by item).
+    // once (8 sequences of 30k to 65k, 64 rows: 144 us, 137.5 by item).
     const long long by_block = (long long)grid * (p.row_blocks.d > 1 ? C::ROWS : rows);
     p.by_item = items <= grid && by_block > 16 * kSms;
     p.joins = p.by_item ? (int)items : grid;
