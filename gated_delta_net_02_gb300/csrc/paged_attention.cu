@@ -21,7 +21,7 @@
 //  * bf16: products on the warp-level matrix instruction (m16n8k16), or with
 //    many rows on tcgen05 (below). p is rounded to bf16 for the second product
 //    (the sum l takes the unrounded p): up to 2^-8 of each term, as the inputs
-//    are. fp32: fp32 products on the CUDA cores, in rows of 4 to 32.
+//    are. fp32: fp32 products on the CUDA cores, in blocks of 4 to 32 rows.
 //  * Keys reach shared memory by 16-byte asynchronous copies, several tiles
 //    ahead; each key's address comes from its page, looked up a tile earlier.
 //    Rows beyond the length are filled with zeros, so what an unused part of
@@ -117,26 +117,30 @@ struct Cfg {
   static constexpr int ROWS = kBf16 ? 16 * WM : 4 * WM;
   // Two warps for each of an SM's schedulers: two blocks of four, or one of
   // eight where the tiles leave room for one block only and a warp has at
-  // least 16 keys of its own. fp32: eight from heads of 128 on (us, eight and
-  // four: 16 sequences of 5000, 4 rows of 256, 137 and 168; 32 rows of 128 197
-  // and 223; 16 sequences of 10000, 16 rows of 64, 133 and 119).
-  static constexpr int WARPS = (kBf16 ? D == 256 && WM > 1 : D > 64) ? 8 : 4;
+  // least 16 keys of its own. fp32: eight from heads of 128 or 32 rows on (us,
+  // eight and four: 16 sequences of 5000, 4 rows of 256, 137 and 168; of 10000,
+  // 4 rows of 128 125 and 128, of 64 71.5 and 73, but 16 rows of 64 133 and 119).
+  static constexpr int WARPS = (kBf16 ? D == 256 && WM > 1 : D > 64 || WM > 4) ? 8 : 4;
   static constexpr int THREADS = 32 * WARPS;
-  static constexpr int WK = kBf16 ? WARPS / WM : WARPS / 4;  // key groups with their own m, l and sum
+  // fp32 from 16 rows on: warps of 8 rows (TileF32Wide)
+  static constexpr bool kWide = !kBf16 && ROWS >= 16;
+  static constexpr int WK = WARPS / (kBf16 ? WM : kWide ? ROWS / 8 : 4);  // key groups with their own m, l and sum
   static constexpr int KT = kBf16 ? 64 : 32;     // keys of a tile
   static constexpr int ROW_BYTES = D * (int)sizeof(T);
   static constexpr int CH = ROW_BYTES / 16;      // 16-byte chunks of a row
   static constexpr int TILE = KT * ROW_BYTES;    // K or V
   static constexpr int STAGES = 3;
   static constexpr int Q_BYTES = ROWS * ROW_BYTES;
-  static constexpr int P_BYTES = kBf16 ? 0 : ROWS * KT * 4;
+  static constexpr int P_PITCH = KT + (kWide ? 4 : 0);
+  static constexpr int P_BYTES = kBf16 ? 0 : ROWS * P_PITCH * 4;
   // q fragments stay in registers up to D = 128: q then only passes through
   // the last stage's place before that stage is first used
   static constexpr bool QREG = kBf16 && D <= 128;
   static constexpr int SMEM = STAGES * 2 * TILE + (QREG ? 0 : Q_BYTES) + P_BYTES;
   // blocks of an SM: what its shared memory holds, up to four of them
   static constexpr int FIT = 224 * 1024 / (SMEM + 4 * 1024);
-  static constexpr int PER_SM = FIT > 4 ? 4 : FIT < 1 ? 1 : FIT;
+  static constexpr int MOST = kWide && WARPS == 8 ? 2 : 4;  // 128 registers a thread
+  static constexpr int PER_SM = FIT > MOST ? MOST : FIT < 1 ? 1 : FIT;
   static_assert(!QREG || Q_BYTES <= 2 * TILE, "q fits a stage");
   static_assert(WK * ROWS * D * 4 <= STAGES * 2 * TILE, "the join reuses the tiles");
 };
@@ -385,7 +389,7 @@ template <class C>
 struct TileF32 {
   static constexpr int D = C::D, VL = D / 32, R = C::WM;
   static constexpr int KEYS = C::KT / C::WK, PARTS = C::WK;
-  static_assert(KEYS * PARTS == 32, "a lane for each key and part of the columns");
+  static_assert(C::kWide || KEYS * PARTS == 32, "a lane for each key and part of the columns");
   float o[R][VL];
   float m[R], l[R];
   uint32_t q_addr;
@@ -505,9 +509,164 @@ struct TileF32 {
   }
 };
 
+// fp32, 16 rows or more. With four rows a warp the shared memory is the
+// limit: a read of 512 bytes of K serves 4 x 4 products a lane. Here a warp
+// has 8 rows, and a lane the products of all 8 with KL keys over an eighth of
+// the columns: 8 parts (lane bits 1 to 3) x 4 key lanes (bits 0 and 4).
+// Neighbours read the same q, which lets the hardware take half a warp's
+// 16-byte reads at once (with the key lanes in bits 3 and 4 a read of q took
+// four turns, not two), and keys 4 apart, which the swizzle places in other
+// banks. The parts' sums fold into one row a lane (half of the rows given away
+// at each step), so that a row's maximum, exponentials and sum are one lane's
+// work and two shuffles. 18 sequences of 357 to 1821 tokens, 40 rows of 256 on
+// 8 kv heads 242 us (27 TFLOP/s, of some 80; 323 with four rows a warp), 16
+// sequences of 5000, 32 rows of 128 144 us (197). Both loops are unrolled
+// whole: 280 us otherwise, each read waited for by two warps a scheduler.
+template <class C>
+struct TileF32Wide {
+  static constexpr int D = C::D, VL = D / 32, R = 8, RG = C::ROWS / R;
+  static constexpr int KEYS = C::KT / C::WK, KL = KEYS / 4;
+  using Narrow = TileF32<C>;
+  float o[R][VL];
+  float m[1], l[1];  // of row part(); l of this lane's keys
+  uint32_t q_addr;
+
+  static __device__ __forceinline__ int part() { return threadIdx.x >> 1 & 7; }
+  static __device__ __forceinline__ int row_group() { return (threadIdx.x >> 5) % RG; }
+  static __device__ __forceinline__ int key_group() { return (threadIdx.x >> 5) / RG; }
+  __device__ __forceinline__ void start(uint32_t q_s) {
+    q_addr = q_s;
+    clear();
+  }
+  __device__ __forceinline__ void clear() {
+    m[0] = -INFINITY;
+    l[0] = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < VL; ++i) o[r][i] = 0.f;
+  }
+  template <class F>
+  static __device__ __forceinline__ void limits(F limit_of, int (&lim)[1]) {
+    lim[0] = limit_of(row_group() * R + part());
+  }
+  __device__ __forceinline__ void tile(uint32_t k_s, uint32_t v_s, int key0, const int (&lim)[1],
+                                       float scale_log2, float *p_s) {
+    const int lane = threadIdx.x & 31, part = this->part(), row0 = row_group() * R;
+    const int key = key_group() * KEYS + (lane & 1) * 4 + (lane >> 4);
+    auto step = [](int j) { return j / 2 * 8 + j % 2 * 2; };  // to the lane's j-th key
+    float v[R][KL], v2[R][KL];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < KL; ++j) v[r][j] = v2[r][j] = 0.f;
+#pragma unroll
+    for (int c0 = 0; c0 < C::CH; c0 += 8) {
+      const int c = c0 + part;
+      float4 k[KL];
+#pragma unroll
+      for (int j = 0; j < KL; ++j) k[j] = Narrow::lds4(k_s + chunk_at<C>(key + step(j), c));
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float4 q = Narrow::lds4(q_addr + chunk_at<C>(row0 + r, c));
+#pragma unroll
+        for (int j = 0; j < KL; ++j) {
+          fma2(v[r][j], v2[r][j], q.x, q.y, k[j].x, k[j].y);
+          fma2(v[r][j], v2[r][j], q.z, q.w, k[j].z, k[j].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < KL; ++j) v[r][j] += v2[r][j];
+#pragma unroll
+    for (int off = 4; off; off >>= 1) {
+#pragma unroll
+      for (int r = 0; r < off; ++r)
+#pragma unroll
+        for (int j = 0; j < KL; ++j) {
+          const bool up = part & off;
+          const float give = up ? v[r][j] : v[r + off][j], keep = up ? v[r + off][j] : v[r][j];
+          v[r][j] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * off);
+        }
+    }
+    // now v[0] is row `part`
+    float mx = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < KL; ++j) {
+      v[0][j] = key0 + key + step(j) < lim[0] ? v[0][j] * scale_log2 : -INFINITY;
+      mx = fmaxf(mx, v[0][j]);
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    const float mn = fmaxf(m[0], mx), ref = mn == -INFINITY ? 0.f : mn;
+    const float alpha = exp2_ftz(m[0] - ref);
+    m[0] = mn;
+    l[0] *= alpha;
+#pragma unroll
+    for (int j = 0; j < KL; ++j) {
+      const float e = exp2_ftz(v[0][j] - ref);
+      l[0] += e;
+      p_s[(row0 + part) * C::P_PITCH + key + step(j)] = e;
+    }
+    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float f = __shfl_sync(0xffffffffu, alpha, 2 * r);
+#pragma unroll
+        for (int i = 0; i < VL; ++i) o[r][i] *= f;
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int jk = 0; jk < KEYS; jk += 4) {
+      const int j = key_group() * KEYS + jk;
+      float4 pj[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        pj[r] = *reinterpret_cast<const float4 *>(p_s + (row0 + r) * C::P_PITCH + j);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        float x[VL];
+        Narrow::lds_v(v_s, j + jj, x);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float e = jj == 0 ? pj[r].x : jj == 1 ? pj[r].y : jj == 2 ? pj[r].z : pj[r].w;
+#pragma unroll
+          for (int i = 0; i < VL; i += 2) fma2(o[r][i], o[r][i + 1], x[i], x[i + 1], e, e);
+        }
+      }
+    }
+    __syncwarp();  // p_s is read before the next tile's takes its place
+  }
+  __device__ __forceinline__ void flush(float *so, float2 *sml) {
+    const int lane = threadIdx.x & 31, row0 = key_group() * C::ROWS + row_group() * R;
+    float t = l[0];
+    t += __shfl_xor_sync(0xffffffffu, t, 1);
+    t += __shfl_xor_sync(0xffffffffu, t, 16);
+    if ((lane & 17) == 0) sml[row0 + part()] = make_float2(m[0], t);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int i = 0; i < VL; ++i) {
+        const int col = VL == 2 ? lane * 2 + i : (i / 4) * 128 + lane * 4 + (i & 3);
+        so[(row0 + r) * D + col] = o[r][i];
+      }
+  }
+};
+
+template <class C, bool WIDE>
+struct TileF32Of {
+  using type = TileF32<C>;
+};
+template <class C>
+struct TileF32Of<C, true> {
+  using type = TileF32Wide<C>;
+};
 template <class C>
 struct TileOf {
-  using type = TileF32<C>;
+  using type = typename TileF32Of<C, C::kWide>::type;
 };
 template <int D, int WM>
 struct TileOf<Cfg<__nv_bfloat16, D, WM>> {
