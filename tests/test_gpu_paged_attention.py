@@ -268,3 +268,12 @@ def test_a_cache_beyond_32_bits_of_elements(gdn):
     c.k, c.v = k, v
     c.table.copy_(torch.tensor([ids], dtype=torch.int32))
     c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("H,H_kv,T", [(8, 1, 1), (16, 2, 2), (16, 2, 8)])
+@pytest.mark.parametrize("lens", [[20000], [15000, 0, 1, 6001, 130]])
+def test_items_of_many_blocks(gdn, dtype, D, H, H_kv, T, lens):
+    c = Case(gdn, lens, T, H, H_kv, D, 16, dtype, seed=H + T + D)
+    c.check(c.run())

@@ -197,3 +197,15 @@ def test_on_another_stream(gdn):
     b = run(gdn, 70, 4, 2, 128, 128, (64,), False, False, 16, torch.bfloat16, seed=4,
             stream=torch.cuda.Stream())
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,H,H_kv,D,rot,sec,neighbours,layout", [
+    (1217, 2, 1, 64, 64, (32,), False, "dense"), (5003, 4, 1, 64, 64, (20, 12), True, "heads_first"),
+    (5003, 6, 2, 128, 90, (45,), False, "k_and_v_in_one"), (4999, 1, 1, 256, 256, (128,), True, "dense"),
+    (7001, 3, 1, 64, 2, (1,), False, "dense"), (4864, 2, 2, 64, 0, (0,), False, "heads_first")])
+def test_many_short_rows(gdn, dtype, n, H, H_kv, D, rot, sec, neighbours, layout):
+    slots = torch.randperm(n, device="cuda")
+    slots[::7] = -1
+    run(gdn, n, H, H_kv, D, rot, sec, False, neighbours, 16, dtype, layout=layout, seed=n,
+        slots=slots)
