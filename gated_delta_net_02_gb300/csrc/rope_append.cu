@@ -413,9 +413,11 @@ cudaError_t launch_d(const RopeParams &p, cudaStream_t stream) {
   const int smem = (int)row * kStages * tpb + 4 * tpb * (p.rot / 2) * 4;
   const int unit = !whole ? p.rot / 2 : p.neighbours ? p.rot / VE : p.rot / 2 / VE;
   auto kernel = whole ? rope_rows_kernel<T, true> : rope_rows_kernel<T, false>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 47 * 1024) {  // less needs no leave, and the call costs the host time
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
   const int by_smem = kRowsSmem / (smem + 2048), per_sm = by_smem < kRowBlocks ? by_smem : kRowBlocks;
   const int most = kSms * (per_sm < 1 ? 1 : per_sm), groups = (p.n_tokens + tpb - 1) / tpb;
   return launch_pdl(kernel, dim3(groups < most ? groups : most), dim3(kThreads), smem, stream, p,
