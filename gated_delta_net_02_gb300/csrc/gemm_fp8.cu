@@ -140,8 +140,10 @@ struct SmallCfg {
   static constexpr int GROUPS = NT >= 64 ? 2 : 1;  // of four epilogue warps, each on its columns
   static constexpr int COLS = NT / GROUPS;
   static constexpr int THREADS = 128 + 128 * GROUPS;
-  static constexpr int SMEM = STAGES * STAGE + 1024;
   static constexpr int BUFS = 4, TCOLS = BUFS * NT;  // tensor-memory buffers
+  // The square tiles take all columns: 8 KB that nothing uses keep a block of
+  // any other form off their SM (see tmem_never_waits_crosswise).
+  static constexpr int SMEM = STAGES * STAGE + 1024 + (TOKENS ? 8 * 1024 : 0);
   // The sums on their way out: [NT][128], or [128][NT + 4] so that a lane's
   // 16-byte stores of its own row and the reads along rows meet no conflict.
   static constexpr int PITCH = TOKENS ? NT + 4 : 128;
@@ -185,8 +187,9 @@ __global__ void __launch_bounds__(SmallCfg<NT, TOKENS>::THREADS)
     prefetch_tmap(&ma);
   }
   // Tensor memory only once the kernel before has completed, and the next
-  // kernel only once this one has its own: of two kernels on one SM that both
-  // allocate, the earlier never waits for the later.
+  // kernel only once this one has its own: of two kernels of one stream on one
+  // SM that both allocate, the earlier never waits for the later. Of kernels of
+  // different streams see tmem_never_waits_crosswise.
   // The first tiles of B start for the L2 while the kernel before still runs:
   // a hint, which changes nothing if that kernel writes them.
   if (tid == 0)
@@ -359,7 +362,38 @@ struct LargeCfg {
   static_assert(32 * 33 * 4 <= BOXES * BOX, "32 rows of 32 sums and a pad");
   static constexpr int SMEM = STAGES * STAGE + 8 * BOXES * BOX + 1024;
   static constexpr int THREADS = 384;  // four warps of roles, eight of epilogue
+  static constexpr int TCOLS = 512;
 };
+
+// Kernels of different streams that hold tensor memory while they wait for
+// other blocks of their cluster. A block waits in its allocation, without a
+// limit, until the columns are free; were two such kernels to share SMs that
+// lack columns for both, each could hold the columns that a block of the
+// other's cluster waits for. So of any two forms, either their blocks do not
+// fit one SM together (228 KB, 1 KB of it reserved for each block; static
+// shared memory is left out, which errs towards fitting) or their columns do.
+// Three blocks of any forms do not fit. The attention and the chunk kernels
+// allocate too, but none of them waits for another block while it holds what a
+// block of these could wait for: chunk_prep's and the attention's blocks end by
+// themselves, and a chunk scan fills an SM alone.
+constexpr int kSmSmem = 228 * 1024, kBlockReserve = 1024, kTmemCols = 512;
+template <class A, class B>
+constexpr bool tmem_never_waits_crosswise() {
+  return A::SMEM + B::SMEM + 2 * kBlockReserve > kSmSmem || A::TCOLS + B::TCOLS <= kTmemCols;
+}
+template <class A, class... Rest>
+constexpr bool tmem_all_pairs() {
+  if constexpr (sizeof...(Rest) == 0) {
+    return tmem_never_waits_crosswise<A, A>();
+  } else {
+    return tmem_never_waits_crosswise<A, A>() && (tmem_never_waits_crosswise<A, Rest>() && ...) &&
+           tmem_all_pairs<Rest...>();
+  }
+}
+static_assert(tmem_all_pairs<SmallCfg<16, false>, SmallCfg<32, false>, SmallCfg<64, false>,
+                             SmallCfg<128, true>, LargeCfg>(),
+              "two kernels' clusters could wait for each other's tensor memory");
+static_assert(3 * (SmallCfg<16, false>::SMEM + kBlockReserve) > kSmSmem, "three blocks on an SM");
 
 // The warp's 32 rows x 128 columns of acc, lane = row, in boxes of 128 bytes.
 template <bool BF16>
@@ -446,12 +480,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
     prefetch_tmap(&mb);
     prefetch_tmap(&ma);
   }
-  // Tensor memory only once the kernel before has completed, and the next
-  // kernel only once this one has its own: of two kernels on one SM that both
-  // allocate, the earlier never waits for the later.
+  // Tensor memory as in gemm_small_kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();
-  if (warp == 2) tmem_alloc_pair(&tm_s, 512);
+  if (warp == 2) tmem_alloc_pair(&tm_s, C::TCOLS);
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both blocks' barriers stand
@@ -602,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
   __syncthreads();
   cluster_sync();  // nothing of the pair arrives in a block that has left
   tc_fence_after();
-  if (warp == 2) tmem_dealloc_pair(tm, 512);
+  if (warp == 2) tmem_dealloc_pair(tm, C::TCOLS);
 }
 
 // ---- host side ------------------------------------------------------------------
