@@ -47,6 +47,8 @@ constexpr int kRingSmem = 216 * 1024;  // of an SM, for all its blocks
 constexpr int kRingThreads = 256;
 // blocks of an SM, which its registers and shared memory are shared out to
 constexpr int ring_blocks(int nv) { return nv == 1 ? 4 : nv == 2 ? 2 : 1; }
+// and the most that a block's ring may take of the latter
+constexpr int ring_bytes(int nv) { return kRingSmem / ring_blocks(nv) - 1024; }
 
 __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
   const uint4 u = *reinterpret_cast<const uint4 *>(p);
@@ -473,7 +475,7 @@ cudaError_t launch_t(const NormParams &p, cudaStream_t stream) {
     const uint32_t half = (uint32_t)d.rpc * p.cols * (uint32_t)sizeof(T);
     const uint32_t stage = half * (p.residual ? 2 : 1);
     const int grid = kSms * ring_blocks(d.nv);
-    int stages = (int)((kRingSmem / ring_blocks(d.nv) - 1024) / stage);
+    int stages = (int)(ring_bytes(d.nv) / stage);
     if (stages > kMaxStages) stages = kMaxStages;
     // below two rows a block the ring has nothing to run ahead for
     if (stages >= 2 && d.nv <= 4 && groups >= 2 * grid) {
@@ -481,8 +483,10 @@ cudaError_t launch_t(const NormParams &p, cudaStream_t stream) {
                     : d.nv == 2 ? norm_ring_kernel<T, 2>
                                 : norm_ring_kernel<T, 4>;
       const size_t smem = (size_t)stages * stage;
-      cudaError_t e =
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      // The attribute is the process's: always the most that any call needs,
+      // or another thread's call could lower it between here and the launch.
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           ring_bytes(d.nv));
       if (e != cudaSuccess) return e;
       const bool wide = ((reinterpret_cast<uintptr_t>(p.residual_out) |
                           reinterpret_cast<uintptr_t>(p.out)) & 31) == 0;

@@ -413,9 +413,12 @@ cudaError_t launch_d(const RopeParams &p, cudaStream_t stream) {
   const int smem = (int)row * kStages * tpb + 4 * tpb * (p.rot / 2) * 4;
   const int unit = !whole ? p.rot / 2 : p.neighbours ? p.rot / VE : p.rot / 2 / VE;
   auto kernel = whole ? rope_rows_kernel<T, true> : rope_rows_kernel<T, false>;
-  if (smem > 47 * 1024) {  // less needs no leave, and the call costs the host time
+  // Less needs no leave, and the call costs the host time. The attribute is the
+  // process's: always the most that any call needs, or another thread's call
+  // could lower it between here and the launch.
+  if (smem > 47 * 1024) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
     if (e != cudaSuccess) return e;
   }
   const int by_smem = kRowsSmem / (smem + 2048), per_sm = by_smem < kRowBlocks ? by_smem : kRowBlocks;
