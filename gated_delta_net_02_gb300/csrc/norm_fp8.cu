@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks(NV))
   __shared__ float red[2][16];
   const int rpc = blockDim.x / tr, t = threadIdx.x % tr, sub = threadIdx.x / tr;
   const int warp = threadIdx.x >> 5, wr = tr >> 5, nvec = p.cols >> 4, nblk = (p.cols + 127) >> 7;
-  const int groups = (p.rows + rpc - 1) / rpc;
+  const int groups = (p.rows - 1) / rpc + 1;
   const T *x = static_cast<const T *>(p.x), *r = static_cast<const T *>(p.residual);
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
@@ -494,7 +494,7 @@ cudaError_t launch_t(const NormParams &p, cudaStream_t stream) {
   };
   if (p.cols % 16 == 0) {
     const Split d(p.cols / 16, kRingThreads, kRingThreads);
-    const int groups = (p.rows + d.rpc - 1) / d.rpc;
+    const int groups = (p.rows - 1) / d.rpc + 1;
     const uint32_t half = (uint32_t)d.rpc * p.cols * (uint32_t)sizeof(T);
     const uint32_t stage = half * (p.residual ? 2 : 1);
     const int grid = kSms * ring_blocks(d.nv);
@@ -518,7 +518,7 @@ cudaError_t launch_t(const NormParams &p, cudaStream_t stream) {
     }
   }
   const Split d(nvec, 512, 256);
-  const int nv = d.nv, tr = d.tr, groups = (p.rows + d.rpc - 1) / d.rpc;
+  const int nv = d.nv, tr = d.tr, groups = (p.rows - 1) / d.rpc + 1;
   const dim3 block(d.tr * d.rpc);
   switch (nv) {
     case 1: return launch_pdl(norm_rows_kernel<T, 1>, dim3(groups), block, 0, stream, p, tr);
