@@ -89,6 +89,36 @@ gdn_status kv_layout(const char *fn, const gdn_kv_cache *cache, gdn::KvLayout *l
   return GDN_OK;
 }
 
+// Whether rows of two buffers with the layout `l` share elements, the second
+// `delta` elements behind the first: a difference of places
+//   dp * page_stride + dt * token_stride + dh * head_stride
+// comes within D of it. kv_layout has seen to it that each level steps over
+// all of the level below, so at each level, largest stride first, only the two
+// counts around what is left can come that near.
+bool rows_collide(const gdn::KvLayout &l, long long delta) {
+  struct { long long stride, n; } lv[3] = {
+      {l.page_stride, l.n_pages}, {l.token_stride, l.page_size}, {l.head_stride, l.H_kv}};
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (lv[j].stride < lv[j + 1].stride) {
+        const auto t = lv[j];
+        lv[j] = lv[j + 1];
+        lv[j + 1] = t;
+      }
+  for (int pick = 0; pick < 8; ++pick) {
+    long long left = delta;
+    for (int i = 0; i < 3; ++i) {
+      if (lv[i].n <= 1) continue;
+      long long c = left / lv[i].stride - (left % lv[i].stride < 0) + (pick >> i & 1);
+      const long long most = lv[i].n - 1;
+      c = c > most ? most : c < -most ? -most : c;
+      left -= c * lv[i].stride;
+    }
+    if (left > -l.D && left < l.D) return true;
+  }
+  return false;
+}
+
 // Checks the sizes of an attention call; cache layout as kv_layout.
 gdn_status attn_shape(const char *fn, const gdn_attn_shape *shape, const gdn_kv_cache *cache,
                       gdn::KvLayout *l, size_t *cache_bytes) {
@@ -280,9 +310,13 @@ gdn_status gdn_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cach
       if ((st = check_apart(fn, outs[i], b)) != GDN_OK) return st;
   }
   // one buffer may hold both caches interleaved (strides twice as long), so
-  // the two are compared only where they would be the same rows
+  // the two are compared row by row
   if (k_cache == v_cache)
     return fail(GDN_ERR_INVALID_ARG, "%s: k_cache and v_cache are the same", fn);
+  if (ranges_overlap(k_cache, cache_bytes, v_cache, cache_bytes) &&
+      rows_collide(a.cache, (static_cast<const char *>(v_cache) -
+                             static_cast<const char *>(k_cache)) / (long long)e))
+    return fail(GDN_ERR_INVALID_ARG, "%s: rows of k_cache and v_cache overlap", fn);
   for (int i = 1; i < 3; ++i)
     if ((st = check_apart(fn, outs[0], outs[i])) != GDN_OK) return st;
   if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;

@@ -1,0 +1,45 @@
+"""What the binding and the C entry points of the attention layer accept and
+refuse beside the cases of test_layer_host.py (no GPU needed)."""
+import pytest
+
+from test_layer_host import FAKE, STEP, refused, rope
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    from gated_delta_net_02_gb300 import build
+    build.build()
+    from gated_delta_net_02_gb300 import gdn as mod
+    return mod
+
+
+def test_rows_of_the_two_caches_stay_apart(gdn):
+    import random
+    rng = random.Random(5)
+    seen = set()
+    for _ in range(400):
+        n, p, H, D = rng.randint(1, 3), rng.randint(1, 3), rng.randint(1, 3), 64
+        # levels in any order, each over all of the one below, with gaps at times
+        counts, strides, span = {"p": n, "t": p, "h": H}, {}, D
+        for level in rng.sample("pth", 3):
+            strides[level] = span + rng.choice([0, 0, 4, 64, 128, 200])
+            span += (counts[level] - 1) * strides[level]
+        s = [strides[x] for x in "pth"]
+        delta = 4 * rng.randint(1, span // 4 + 2) * rng.choice([1, -1])
+        k = FAKE + 7 * STEP
+        rows = {i * s[0] + j * s[1] + h * s[2] for i in range(n) for j in range(p) for h in range(H)}
+        meet = any(abs(a + delta - b) < D for a in rows for b in rows)
+        # q_out lies on the k cache: what is refused next where the caches are apart
+        st, msg = refused(gdn, lambda: rope(
+            gdn, dict(rot_dim=64, section=(16, 8, 8)),
+            dict(n_pages=n, page_size=p, H_kv=H, D=D, dtype=gdn.GDN_F32, page_stride=s[0],
+                 token_stride=s[1], head_stride=s[2]),
+            k_cache=k, v_cache=k + 4 * delta, q_out=k))
+        word = "rows of k_cache and v_cache overlap" if meet else "q_out overlaps k_cache"
+        assert st == gdn.GDN_ERR_INVALID_ARG and word in msg, (s, (n, p, H), delta)
+        seen.add((meet, abs(delta) < span))
+    assert {(True, True), (False, True), (False, False)} <= seen
+    # one dense layout inside the other
+    for off in (16, 256, 4096, 40960 * 2 - 16):
+        st, msg = refused(gdn, lambda: rope(gdn, k_cache=k, v_cache=k + off))
+        assert "rows of k_cache and v_cache overlap" in msg
