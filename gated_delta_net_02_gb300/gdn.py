@@ -193,9 +193,33 @@ def _cache_addr(x, cache):
     """Device address of a cache tensor; a strided one must say so in `cache`."""
     if x is None or x.__class__ is int:
         return x
-    if not (cache.token_stride or x.is_contiguous()):
-        raise ValueError("gdn: a strided cache needs its strides in gdn_kv_cache")
+    if not cache.token_stride:
+        if not x.is_contiguous():
+            raise ValueError("gdn: a strided cache needs its strides in gdn_kv_cache")
+    elif (x.stride() != (cache.page_stride, cache.token_stride, cache.head_stride, 1)
+          and not _cache_matches(x, cache)):
+        raise ValueError("gdn: the cache's strides are not those in gdn_kv_cache")
     return x.data_ptr()
+
+
+def _cache_matches(x, cache):
+    """Whether tensor x, in another form than [n_pages, page_size, H_kv, D],
+    has the elements that `cache` names: its dimensions in another order, or
+    pages and tokens in one. A packed tensor is memory from its start on."""
+    levels = [(stride, n) for stride, n in (
+        (cache.page_stride, cache.n_pages), (cache.token_stride, cache.page_size),
+        (cache.head_stride, cache.H_kv), (1, cache.D)) if n > 1]
+    if x.is_contiguous():
+        held = x.untyped_storage().nbytes() // x.element_size() - x.storage_offset()
+        return cache.n_pages == 0 or sum(stride * (n - 1) for stride, n in levels) < held
+    dims = {stride: n for stride, n in zip(x.stride(), x.shape) if n > 1 and stride > 0}
+    last = dict.fromkeys(dims, 0)      # index of the cache's last element
+    for stride, n in levels:
+        along = max((d for d in dims if stride % d == 0), default=None)
+        if along is None:
+            return False
+        last[along] += (n - 1) * (stride // along)
+    return all(last[d] < n for d, n in dims.items())
 
 
 def _check(status):

@@ -1,8 +1,9 @@
 """What the binding and the C entry points of the attention layer accept and
 refuse beside the cases of test_layer_host.py (no GPU needed)."""
 import pytest
+import torch
 
-from test_layer_host import FAKE, STEP, refused, rope
+from test_layer_host import FAKE, STEP, kv, refused, rope
 
 
 @pytest.fixture(scope="module")
@@ -11,6 +12,47 @@ def gdn():
     build.build()
     from gated_delta_net_02_gb300 import gdn as mod
     return mod
+
+
+def strided(gdn, n_pages, page, H_kv, D, strides):
+    return kv(gdn, n_pages=n_pages, page_size=page, H_kv=H_kv, D=D, dtype=gdn.GDN_F32,
+              page_stride=strides[0], token_stride=strides[1], head_stride=strides[2])
+
+
+def test_strided_caches_that_match_their_struct(gdn):
+    n, p, H, D = 10, 16, 2, 64
+    both = torch.zeros(n, 2, p, H, D)
+    heads = torch.zeros(n, H, p, D)
+    slots = torch.zeros(n * p, 2, H, D)
+    packed = torch.zeros(n, p, H, D)
+    wide, first = (2 * p * H * D, H * D, D), (H * p * D, D, p * D)
+    for x, size, strides in (
+            (both[:, 0], (n, p, H), wide), (both[:, 1], (n, p, H), wide),
+            (both, (n, p, H), wide), (both[3:, 0], (n - 3, p, H), wide),
+            (both[:, 0, :, 1:], (n, p, 1), wide),
+            (heads.transpose(1, 2), (n, p, H), first), (heads, (n, p, H), first),
+            (heads[:, :, ::2].transpose(1, 2), (n, p // 2, H), (H * p * D, 2 * D, p * D)),
+            (slots[:, 1], (n, p, H), (2 * p * H * D, 2 * H * D, D)),
+            (packed, (n, p, H), (p * H * D, H * D, D)),
+            (packed.view(-1), (n, p, H), (p * H * D, H * D, D)),
+            (torch.zeros(n, p, 2 * H * D)[..., :H * D], (n, p, H), (2 * p * H * D, 2 * H * D, D))):
+        assert gdn._cache_addr(x, strided(gdn, *size, D, strides)) == x.data_ptr()
+
+
+def test_strided_caches_that_do_not_match_are_refused(gdn):
+    n, p, H, D = 10, 16, 2, 64
+    both = torch.zeros(n, 2, p, H, D)
+    heads = torch.zeros(n, H, p, D).transpose(1, 2)
+    wide = (2 * p * H * D, H * D, D)
+    for x, pages, strides in (
+            (both[:, 0], n, (p * H * D, H * D, D)),        # as if k stood alone
+            (both[:, 0], n, (2 * p * H * D, D, p * D)),    # as if heads came first
+            (heads, n, (H * p * D, H * D, D)),             # as if tokens came first
+            (heads, n, (H * p * D, D, 2 * p * D)),
+            (both, n + 1, wide),                           # a page more than there are
+            (torch.zeros(n, p, H, D), n, wide)):           # beyond the tensor's memory
+        with pytest.raises(ValueError, match="the cache's strides"):
+            gdn._cache_addr(x, strided(gdn, pages, p, H, D, strides))
 
 
 def test_rows_of_the_two_caches_stay_apart(gdn):
