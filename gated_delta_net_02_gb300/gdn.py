@@ -183,6 +183,8 @@ def _rows_addr(x, n, stride, width, D):
     (0 = dense, `width`): a column range of a wider matrix is such a view."""
     if x is None or x.__class__ is int:
         return x
+    if isinstance(x, int):
+        return int(x)
     st = x.stride()
     if st[2] != 1 or st[1] != D and width != D or n > 1 and st[0] != (stride or width):
         raise ValueError("gdn: rows must be packed, and apart by the shape's stride")
@@ -193,6 +195,8 @@ def _cache_addr(x, cache):
     """Device address of a cache tensor; a strided one must say so in `cache`."""
     if x is None or x.__class__ is int:
         return x
+    if isinstance(x, int):
+        return int(x)
     if not cache.token_stride:
         if not x.is_contiguous():
             raise ValueError("gdn: a strided cache needs its strides in gdn_kv_cache")
@@ -230,6 +234,8 @@ def _check(status):
 def _stream(stream):
     if stream is None or stream.__class__ is int:
         return stream
+    if isinstance(stream, int):
+        return int(stream)
     return stream.cuda_stream  # torch.cuda.Stream
 
 

@@ -14,6 +14,19 @@ def gdn():
     return mod
 
 
+class Address(int):
+    """An int of another class, as an enum's member or a wrapped handle is."""
+
+
+def test_ints_of_another_class_are_addresses_and_streams(gdn):
+    assert gdn._stream(Address(7)) == 7 and type(gdn._stream(Address(7))) is int
+    shape = gdn.gdn_norm_shape(0, 256, gdn.GDN_BF16, 1, 1e-6, 0.0)
+    gdn.gdn_rmsnorm_fp8(shape, *[Address(FAKE)] * 7, Address(0))
+    # the refusal shows that the call itself was reached with these addresses
+    st, msg = refused(gdn, lambda: rope(gdn, q=Address(FAKE), k_cache=Address(FAKE + 8 * STEP)))
+    assert st == gdn.GDN_ERR_INVALID_ARG and "are the same" in msg
+
+
 def strided(gdn, n_pages, page, H_kv, D, strides):
     return kv(gdn, n_pages=n_pages, page_size=page, H_kv=H_kv, D=D, dtype=gdn.GDN_F32,
               page_stride=strides[0], token_stride=strides[1], head_stride=strides[2])
