@@ -186,7 +186,8 @@ def _rows_addr(x, n, stride, width, D):
     if isinstance(x, int):
         return int(x)
     st = x.stride()
-    if st[2] != 1 or st[1] != D and width != D or n > 1 and st[0] != (stride or width):
+    if (len(st) != 3 or st[2] != 1 or st[1] != D and width != D
+            or n > 1 and st[0] != (stride or width)):
         raise ValueError("gdn: rows must be packed, and apart by the shape's stride")
     return x.data_ptr()
 

@@ -27,6 +27,12 @@ def test_ints_of_another_class_are_addresses_and_streams(gdn):
     assert st == gdn.GDN_ERR_INVALID_ARG and "are the same" in msg
 
 
+def test_rows_of_another_rank_are_refused(gdn):
+    for x in (torch.zeros(5, 4 * 128), torch.zeros(5 * 4 * 128), torch.zeros(1, 5, 4, 128)):
+        with pytest.raises(ValueError, match="rows must be packed"):
+            rope(gdn, q=x)
+
+
 def strided(gdn, n_pages, page, H_kv, D, strides):
     return kv(gdn, n_pages=n_pages, page_size=page, H_kv=H_kv, D=D, dtype=gdn.GDN_F32,
               page_stride=strides[0], token_stride=strides[1], head_stride=strides[2])
