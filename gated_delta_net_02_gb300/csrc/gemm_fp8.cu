@@ -208,8 +208,9 @@ __global__ void __launch_bounds__(SmallCfg<NT, TOKENS>::THREADS)
   float acc[C::COLS];
   const int col0 = warp < 4 ? 0 : (warp - 4) / 4 * C::COLS;  // the epilogue warp's columns
   if (warp == 0) {
-    if (lane == 0)
-      for (int i = 0; i < nk; ++i) {
+    if (lane == 0) {
+      int i = 0;
+      for (; i < nk; ++i) {
         const int s = i % S;
         if (i >= S && !mbar_wait(&empty[s], (i / S - 1) & 1, p.err, kSiteGemmEmpty)) break;
         unsigned char *st = sm + s * C::STAGE;
@@ -217,8 +218,11 @@ __global__ void __launch_bounds__(SmallCfg<NT, TOKENS>::THREADS)
         tma_load_2d(TOKENS ? st + C::A_BYTES : st, &mb, (kb0 + i) * kBlockK, n0, &full[s]);
         tma_load_2d(TOKENS ? st : st + C::A_BYTES, &ma, (kb0 + i) * kBlockK, m0, &full[s]);
       }
+      for (int j = max(i - S, 0); j < i; ++j) mbar_drain(&full[j % S], (j / S) & 1);
+    }
   } else if (warp == 1) {
-    for (int i = 0; i < nk; ++i) {
+    int i = 0;
+    for (; i < nk; ++i) {
       const int s = i % S, b = i % NB;
       // a buffer never used yet counts as the phase before the first: given back
       const bool ok = mbar_wait_both(&bars.tempty[b], (i / NB + 1) & 1, &full[s], (i / S) & 1,
@@ -229,6 +233,7 @@ __global__ void __launch_bounds__(SmallCfg<NT, TOKENS>::THREADS)
       umma_e4m3_k128(tm + b * NT, sdesc_kmajor(st), sdesc_kmajor(st + C::A_BYTES),
                      idesc_e4m3_f32(128, NT), smem_u32(&empty[s]), smem_u32(&bars.tfull[b]));
     }
+    if (i > 0) mbar_drain(&empty[(i - 1) % S], ((i - 1) / S) & 1);
   } else if (warp == 2 && !TOKENS) {
     // Scales of the tile's rows of A times that of its block of B, a group of
     // stages at a time; the next group's loads are under way while this one
@@ -514,6 +519,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
             tma_load_2d_pair(st + C::HALF, &mb, kb * kBlockK, n0, bar);
           }
         }
+        // a stage's barrier counts the copies of both blocks, and neither leaves
+        // before the other
+        if (rank == 0)
+          for (int j = max(i - S, 0); j < i; ++j) mbar_drain(&full[j % S], (j / S) & 1);
       }
     } else if (warp == 1) {
       if (rank == 0) {
@@ -532,6 +541,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(LargeCfg::THREADS, 1
                                 idesc_e4m3_f32(C::TM, C::TN), smem_u32(&empty[s]),
                                 smem_u32(&bars.tfull[b]));
           }
+        if (i > 0) mbar_drain(&empty[(i - 1) % S], ((i - 1) / S) & 1);
       }
     } else if (warp == 2) {
       // scales of the block's rows of A and of the tile's two blocks of B, a

@@ -58,6 +58,15 @@ __device__ __forceinline__ bool mbar_wait_both(uint64_t *bar0, uint32_t parity0,
   return false;
 }
 
+// Wait of a block that is about to leave for its own copies and products in
+// flight, so that none lands in what the next block holds. They are long over
+// unless a wait before gave up; then this one, shorter, gives up in silence.
+constexpr uint32_t kDrainPolls = 1u << 22;
+__device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kDrainPolls; ++i)
+    if (mbar_try_wait(bar, parity)) return;
+}
+
 // ---- launches -------------------------------------------------------------
 
 // launch_pdl with blocks in clusters along x (1: none).

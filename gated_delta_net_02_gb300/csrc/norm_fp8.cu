@@ -383,7 +383,17 @@ __global__ void __launch_bounds__(kRingThreads, ring_blocks(NV))
 #pragma unroll
     for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     if ((threadIdx.x & 31) == 0) red[it & 1][warp] = sum;
-    if (__syncthreads_or(!ok)) break;
+    if (__syncthreads_or(!ok)) {
+      if (threadIdx.x == 0)  // the stages loaded ahead
+        for (int i = 0; i < stages && g < groups; ++i, g += gridDim.x) {
+          mbar_drain(&full[s], phase);
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+      break;
+    }
     if (threadIdx.x == 0) load(g + stages * gridDim.x, s);
     float rstd = 1.f;
     if (p.normalize)

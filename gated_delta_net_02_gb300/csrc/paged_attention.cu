@@ -1062,6 +1062,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   const bool any = w.begin<KT, NT>(p, items_per_seq, warp_sum, place);
   if (!any && tid == 0 && !p.by_item) p.cut[blockIdx.x].x = -1;
   int tb = 0, patches = 0;  // tiles and cleared units of the items before
+  int loaded = 0, used = 0;  // units that warp 0 has loaded, and warp 8 given back last, plus one
+  bool gave_up = false;
   for (int seg = 0; any && w.pos < w.end; ++seg) {
     const int n = w.tiles(), s = w.s, len = w.len, tile0 = w.tile0;
     const int kvh = p.row_blocks.div(w.x), r0 = (w.x - kvh * (int)p.row_blocks.d) * ROWS;
@@ -1100,6 +1102,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
           __syncwarp();
+          loaded = u + 1;
           if (live)
             tma_load_4d(sm + slot * C::UNIT + c * (KT * 128) + j * box * 128, v ? &mv : &mk, c * 64,
                         kvh, in_page, page, &full[slot]);
@@ -1156,6 +1159,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
                           idesc_bf16_f32(128, D, false, true), i > 0 || ks > 0);
         umma_commit_elect(&empty[slot]);
         umma_commit_elect(&o_done);
+        used = u + 1;
       };
       ok = mbar_wait(&q_full, seg & 1, p.err, kSiteAttnTile);
       ok = __all_sync(0xffffffffu, ok);
@@ -1176,6 +1180,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
                           idesc_bf16_f32(128, KT, false, false), ks > 0);
         umma_commit_elect(&empty[slot]);
         umma_commit_elect(&s_full[b]);
+        used = u + 1;
         if (i > 0) sums(i - 1);
       }
       if (ok) sums(n - 1);
@@ -1273,7 +1278,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         tc_fence_before();
       }
     }
-    if (__syncthreads_or(!ok)) break;
+    gave_up = __syncthreads_or(!ok);
+    if (gave_up) break;
     finish_item<C>(p, reinterpret_cast<const float *>(sm), C::PITCH, sml, rows, n == w.nt,
                    (long long)blockIdx.x * 2 + (seg > 0));
     fence_proxy_async();  // the sums' place is loaded by TMA next
@@ -1287,6 +1293,11 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         *reinterpret_cast<uint4 *>(sm + U * C::UNIT + e * 16) = make_uint4(0, 0, 0, 0);
       fence_proxy_async();
     }
+  }
+  if (gave_up) {  // otherwise every item's copies and products have been waited for
+    if (warp == 0)
+      for (int u = max(loaded - U, 0); u < loaded; ++u) mbar_drain(&full[u % U], (u / U) & 1);
+    if (warp == 8 && used > 0) mbar_drain(&empty[(used - 1) % U], ((used - 1) / U) & 1);
   }
   tc_fence_before();
   __syncthreads();

@@ -319,7 +319,12 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks)
     const long long next_slot = slot_of(it + 1);
     angles(it);
     const bool ok = mbar_wait(&full[s], (it / kStages) & 1, p.err, kSiteRopeRow);
-    if (__syncthreads_or(!ok)) break;
+    if (__syncthreads_or(!ok)) {
+      if (tid == 0)  // the stages loaded ahead
+        for (int i = it; i < it + kStages - 1 && group_of(i) < groups; ++i)
+          mbar_drain(&full[i % kStages], (i / kStages) & 1);
+      break;
+    }
     const float *cs0 = trig + (it & 1) * 2 * tpb * half, *sn0 = cs0 + tpb * half;
     unsigned char *st = smem + s * stage;
     if constexpr (WHOLE) {
