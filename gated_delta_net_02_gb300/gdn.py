@@ -183,9 +183,12 @@ def _rows_addr(x, n, stride, width, D):
     (0 = dense, `width`): a column range of a wider matrix is such a view."""
     if x is None or x.__class__ is int:
         return x
-    if isinstance(x, int):
-        return int(x)
-    st = x.stride()
+    try:
+        st = x.stride()
+    except AttributeError:
+        if isinstance(x, int):
+            return int(x)
+        raise
     if (len(st) != 3 or st[2] != 1 or st[1] != D and width != D
             or n > 1 and st[0] != (stride or width)):
         raise ValueError("gdn: rows must be packed, and apart by the shape's stride")
@@ -196,15 +199,19 @@ def _cache_addr(x, cache):
     """Device address of a cache tensor; a strided one must say so in `cache`."""
     if x is None or x.__class__ is int:
         return x
-    if isinstance(x, int):
-        return int(x)
+    try:
+        address = x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):
+            return int(x)
+        raise
     if not cache.token_stride:
         if not x.is_contiguous():
             raise ValueError("gdn: a strided cache needs its strides in gdn_kv_cache")
     elif (x.stride() != (cache.page_stride, cache.token_stride, cache.head_stride, 1)
           and not _cache_matches(x, cache)):
         raise ValueError("gdn: the cache's strides are not those in gdn_kv_cache")
-    return x.data_ptr()
+    return address
 
 
 def _cache_matches(x, cache):
@@ -235,9 +242,12 @@ def _check(status):
 def _stream(stream):
     if stream is None or stream.__class__ is int:
         return stream
-    if isinstance(stream, int):
-        return int(stream)
-    return stream.cuda_stream  # torch.cuda.Stream
+    try:
+        return stream.cuda_stream  # torch.cuda.Stream
+    except AttributeError:
+        if isinstance(stream, int):
+            return int(stream)
+        raise
 
 
 def gdn_version() -> str:
