@@ -999,6 +999,7 @@ struct TcCfg {
   static constexpr int OUT_BYTES = 128 * PITCH * 4;
   static constexpr int TCOLS = D + 2 * KT <= 256 ? 256 : 512;  // sums, then two tiles of scores
   static constexpr int PER_SM = 1;
+  static_assert(KC % 32 == 0, "a lane reads its keys' scores 32 at a time");
   static_assert(OUT_BYTES <= UNITS * UNIT + P_BYTES + Q_BYTES, "the sums fit");
 };
 
@@ -1058,7 +1059,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tm = tm_s, tm_score = tm + D;
 
-  Walk w;
+  Walk w{};
   const bool any = w.begin<KT, NT>(p, items_per_seq, warp_sum, place);
   if (!any && tid == 0 && !p.by_item) p.cut[blockIdx.x].x = -1;
   int tb = 0, patches = 0;  // tiles and cleared units of the items before
@@ -1198,16 +1199,12 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         if (!ok) break;
         tc_fence_after();
         float x[KC];
-        if constexpr (KC == 16) {
-          tmem_ld16(tm_score + lanes + b * KT + part, x);
-        } else {
 #pragma unroll
-          for (int c = 0; c < KC; c += 32) {
-            float part32[32];
-            tmem_ld32(tm_score + lanes + b * KT + part + c, part32);
+        for (int c = 0; c < KC; c += 32) {
+          float part32[32];
+          tmem_ld32(tm_score + lanes + b * KT + part + c, part32);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[c + j] = part32[j];
-          }
+          for (int j = 0; j < 32; ++j) x[c + j] = part32[j];
         }
         tc_fence_before();
         __syncwarp();
