@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+from test_gpu_paged_attention import Case
+
 pytestmark = pytest.mark.gpu
 
 
@@ -26,3 +28,20 @@ def test_norm_of_the_most_rows(gdn):
     del x
     torch.cuda.empty_cache()
     assert low == high == 2
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("page", [16, 64])
+def test_strides_that_no_second_element_uses(gdn, D, page):
+    # of a level with one element (one kv head, one page) any stride is legal
+    c = Case(gdn, [page - 3], 8, 13, 1, D, page, torch.bfloat16, seed=page + D)
+    n = c.k.shape[0]
+    for head_stride in (8, D, 1 << 20):
+        c.cache = gdn.gdn_kv_cache(n, page, 1, D, gdn.GDN_BF16, page * D, D, head_stride)
+        c.check(c.run())
+    own = int(c.table[0, 0])
+    c.k, c.v = c.k[own:own + 1].clone(), c.v[own:own + 1].clone()
+    c.table[0, 0] = 0
+    for page_stride in (8, page * D, 1 << 40):
+        c.cache = gdn.gdn_kv_cache(1, page, 1, D, gdn.GDN_BF16, page_stride, D, 8)
+        c.check(c.run())
