@@ -20,13 +20,13 @@
 //    rows of A its 16 to 64 columns, so that no tensor-core row idles. Bound
 //    by the read of B: k is split over a cluster of up to 8 blocks, which add
 //    their sums through distributed shared memory in rank order. 64 x 2560 x
-//    2048 6.0 us, 16 x 8192 x 4096 7.3 us (4.6 TB/s).
+//    2048 6.0 us, 16 x 8192 x 4096 7.4 us (4.6 TB/s).
 //  * at most one 128 x 128 tile for each SM: rows of A as the instruction's
 //    rows (a row's scale is then a lane's own, not a read for each column);
-//    split and joined alike. 256 x 4096 x 4096 10.3 us, 512 x 4096 x 4096
-//    13.5 us (17.7 us as 256 x 256 tiles).
+//    split and joined alike. 256 x 4096 x 4096 10.2 us, 512 x 4096 x 4096
+//    13.4 us (17.7 us as 256 x 256 tiles).
 //  * more: 256 x 256 tiles of a pair of blocks (cta_group::2), persistent.
-//    8192 x 8192 x 4096 198 us (2770 TFLOP/s), 1024 x 4096 x 4096 17.2 us. It
+//    8192 x 8192 x 4096 196 us (2800 TFLOP/s), 1024 x 4096 x 4096 17.7 us. It
 //    should be bound by the tensor cores: its instructions alone take 123 us,
 //    with the stages' loads and barriers 163. Two tensor-memory buffers are
 //    all there is, and a block's product cannot start before the buffer of

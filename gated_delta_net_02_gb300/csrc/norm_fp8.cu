@@ -16,7 +16,7 @@
 // Measured on one GB300: 64 x 2048 bf16 with residual 1.9 us; 34739 x 4096
 // 178 us (5.6 TB/s of its own bytes, of 6.8 copied).
 // What is left there: 57 rows a block and their first loads after the
-// previous kernel, and some 350 instructions a warp and row (half of the
+// previous kernel, and some 360 instructions a warp and row (half of the
 // issue slots).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>

@@ -30,7 +30,8 @@
 // Measured on one GB300 (us; the cache's bytes at the copy rate in brackets):
 // 64 sequences of 512 to 8192 tokens, 16 heads on 2 of 128, bf16, one token
 // 53.0 (42.2), of 2048 to 32768 173 (169); 8 x 8 tokens over 30k to 65k keys,
-// heads of 256, 137 (115); one sequence of 513 tokens 5.9, of 60000 22.8 (9.1).
+// heads of 256, 137 (115); one sequence of 513 tokens 5.9 (in a page table
+// that ends with it; 10.2 in a wide one, see short_split), of 60000 22.8 (9.1).
 // Some 10 us of a long call are no transfer: the launches, the chain of
 // lengths, page table and first keys, and the join (4 us of the 52.6).
 #include <cuda_bf16.h>
@@ -1389,11 +1390,12 @@ template <typename T, int D, class F>
 auto with_rows(int rows, int box, F f) {
   if constexpr (sizeof(T) == 2) {
     if (rows <= 16) return f(Cfg<T, D, 1>{});
-    // Tensor memory where it measured faster (us, 64 sequences of 512 to 8192,
-    // D = 128, or to 4096, D = 256; warp-level kernel in brackets): 64 rows of
-    // D = 256 94 (113), 128 rows 118 (201); 64 rows of D = 128 with boxes of 16
-    // tokens 98 (90), of 32 86 (90), of 64 80 (90), 128 rows 120 (150); 32 rows
-    // of either no faster, 64 rows of D = 64 120 (118).
+    // Tensor memory where it measured faster or even (us, 64 sequences of 512 to
+    // 8192, D = 128, or to 4096, D = 256, boxes of 16, 32 and 64 tokens;
+    // warp-level kernel in brackets): 64 rows of D = 256 91, 86, 84 (110), 128
+    // rows 112, 107, 105 (196); 64 rows of D = 128 96, 82, 77 (80), 128 rows 114,
+    // 101, 97 (146). 32 rows of D = 128 91, 77, 72 (60), of D = 256 84, 78, 76
+    // (80); 64 rows of D = 64 were even.
     if constexpr (D >= 128) {
       if (box && rows > 64) return f(TcCfg<D, 1>{});
       if (box && rows > 32 && (D == 256 || box >= 32)) return f(TcCfg<D, 2>{});
@@ -1449,7 +1451,9 @@ int grid_of(const KvLayout &c, int n_seqs, int max_pages, int row_blocks) {
 }
 
 // Blocks for each item when the longest possible sequence is short enough to
-// need no line of tiles (0: it is not). Many items of up to 16 tiles take a
+// need no line of tiles (0: it is not). The page table's width decides, since
+// the lengths are known on the device only: one sequence of 513 tokens takes 5.9
+// us in a table of 33 or 64 pages of 16 and 10.2 in one of 512 or 8192. Many items of up to 16 tiles take a
 // block each, and the GPU's own scheduling evens them out (256 sequences of 1
 // to 1000 tokens, 8 kv heads of 64: 50 us, 77 as a line, where a block's items
 // follow one another with a gap at each). Few items are split over a cluster,

@@ -15,7 +15,9 @@
 // passes some thousand radians (2^-24 of it). The product is formed in turns,
 // as the fp32 product plus its exact error (fused multiply-add), so that the
 // whole turns drop out exactly and what is left of the angle has an error of
-// about 2^-24 turns at any position.
+// about 2^-24 turns for positions up to 2^24 and inverse frequencies up to 1;
+// beyond, the rounding of position * (the frequency's low part) outgrows that,
+// to some 2^-21 turns at 2^31.
 #include <cuda_bf16.h>
 
 #include "kernels.h"

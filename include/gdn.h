@@ -304,7 +304,8 @@ gdn_status gdn_checkpoint_select(int n_keep, int L, int n_slots, int ckpt_every,
  *                                          normalize = 0: y = h)
  *   scale[b] = max(max |y| over columns [128 b, 128 b + 128) / 448, 2^-100)
  *   fp8      = y / scale[b], rounded to e4m3 (to nearest even, saturating)
- * so y is about fp8 * scale. NaNs take no part in the maximum and stay NaN.
+ * so y is about fp8 * scale; each of the two quotients is rounded once to fp32.
+ * NaNs take no part in the maximum and stay NaN.
  */
 typedef struct {
   int rows, cols;      /* rows >= 0, cols >= 1 */
@@ -382,12 +383,13 @@ typedef enum { GDN_ROPE_AXES_SECTIONED = 0, GDN_ROPE_AXES_INTERLEAVED = 1 } gdn_
  * head turns by the angle positions[axis(i)][t] * inv_freq[i]:
  *   (a, b) -> (a cos - b sin, a sin + b cos)
  * and the other elements pass unchanged. The angle is reduced to one turn
- * beyond fp32 (error below 2e-6 for positions up to 2^24, in proportion to
- * the position beyond), so long positions lose nothing. The rotated q goes to q_out; the rotated k and v go to slot
- * slots[t] of the cache (page slot / page_size, token slot % page_size).
+ * beyond fp32 (inv_freq up to 1: error below 2e-6 for positions up to 2^24, in
+ * proportion to the position beyond), so long positions lose nothing. The
+ * rotated q goes to q_out; the rotated k and v go to slot slots[t] of the cache
+ * (page slot / page_size, token slot % page_size).
  * A negative slot (padding) writes no cache entry; one beyond the cache is
  * skipped and reported as GDN_ERR_DEVICE_ARG by gdn_check_device_error. Of
- * two tokens with one slot, either may stay.
+ * two tokens with one slot, each element that stays may be either's.
  */
 typedef struct {
   int n_tokens;             /* >= 0 */
@@ -408,7 +410,8 @@ typedef struct {
  * inv_freq   device fp32 [rot_dim / 2]
  * slots      device int64 [n_tokens]
  * q_out      device [n_tokens][H][D]; overlaps no other buffer
- * k_cache, v_cache  device buffers of the layout `cache`
+ * k_cache, v_cache  device buffers of the layout `cache`; no row of one shares
+ *            bytes with a row of the other (k and v may alternate in one buffer)
  */
 gdn_status gdn_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cache, const void *q,
                            const void *k, const void *v, const int32_t *positions,
@@ -440,6 +443,10 @@ typedef struct {
   gdn_qk_map kv_map; /* query head -> kv head */
 } gdn_attn_shape;
 
+/* max_pages is also what the call's kernel is chosen by (the lengths are known
+ * on the device only): with a table much wider than the longest sequence a short
+ * batch takes the form for long ones, which starts some 4 us later. */
+
 /* Bytes of device workspace gdn_paged_attention needs (at most 64 MiB); 0 for
  * arguments that it refuses. Depends on the shapes alone, not on lens. */
 size_t gdn_paged_attention_workspace_size(const gdn_attn_shape *shape, const gdn_kv_cache *cache);
@@ -452,7 +459,7 @@ size_t gdn_paged_attention_workspace_size(const gdn_attn_shape *shape, const gdn
  * lens        device int32 [n_seqs], 0 <= lens[s] <= max_pages * page_size
  *             and at most 2^30 (a longer one is cut to that, a negative one
  *             is 0)
- * out         device [n_seqs*T][H][D]
+ * out         device [n_seqs*T][H][D]; overlaps no other buffer
  * workspace   device buffer of at least gdn_paged_attention_workspace_size
  *             bytes, 256-byte aligned; its contents on entry do not matter.
  *             Calls that can overlap on the GPU need one each.
