@@ -2,6 +2,8 @@
 // in include/gdn.h): argument validation and dispatch to their kernels.
 #include <cuda_runtime.h>
 
+#include <limits.h>
+
 #include <cmath>
 
 #include "api_util.h"
@@ -152,6 +154,9 @@ gdn_status gdn_rmsnorm_fp8(const gdn_norm_shape *shape, const void *x, const voi
   const gdn_norm_shape &s = *shape;
   if (s.rows < 0 || s.cols < 1)
     return fail(GDN_ERR_INVALID_ARG, "%s: rows=%d cols=%d", fn, s.rows, s.cols);
+  // column indexes step by up to 256 in 32 bits
+  if (s.cols > INT_MAX - 1023)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: cols=%d is above 2^31 - 1024", fn, s.cols);
   if (!dtype_ok(s.dtype)) return fail(GDN_ERR_INVALID_ARG, "%s: dtype %d", fn, (int)s.dtype);
   if (s.normalize != 0 && s.normalize != 1)
     return fail(GDN_ERR_INVALID_ARG, "%s: normalize %d", fn, s.normalize);

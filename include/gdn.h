@@ -308,7 +308,7 @@ gdn_status gdn_checkpoint_select(int n_keep, int L, int n_slots, int ckpt_every,
  * NaNs take no part in the maximum and stay NaN.
  */
 typedef struct {
-  int rows, cols;      /* rows >= 0, cols >= 1 */
+  int rows, cols;      /* rows >= 0, 1 <= cols <= 2^31 - 1024 */
   gdn_dtype dtype;     /* of x, residual, weight, residual_out and out */
   int normalize;       /* 1: as above; 0: y = h (a plain quantiser) */
   float eps;           /* finite, >= 0 */

@@ -3,7 +3,7 @@ refuse beside the cases of test_layer_host.py (no GPU needed)."""
 import pytest
 import torch
 
-from test_layer_host import FAKE, STEP, kv, refused, rope
+from test_layer_host import FAKE, STEP, kv, norm, refused, rope
 
 
 @pytest.fixture(scope="module")
@@ -104,3 +104,9 @@ def test_rows_of_the_two_caches_stay_apart(gdn):
     for off in (16, 256, 4096, 40960 * 2 - 16):
         st, msg = refused(gdn, lambda: rope(gdn, k_cache=k, v_cache=k + off))
         assert "rows of k_cache and v_cache overlap" in msg
+
+
+def test_norm_refuses_columns_that_its_indexes_cannot_step_over(gdn):
+    for cols in (2 ** 31 - 1, 2 ** 31 - 1023):
+        st, msg = refused(gdn, lambda: norm(gdn, dict(rows=1, cols=cols)))
+        assert st == gdn.GDN_ERR_UNSUPPORTED and "above 2^31 - 1024" in msg
