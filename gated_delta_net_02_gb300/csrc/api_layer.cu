@@ -142,6 +142,103 @@ gdn_status attn_shape(const char *fn, const gdn_attn_shape *shape, const gdn_kv_
   return GDN_OK;
 }
 
+// Checks a call that rotates and appends, and fills its arguments (n_tokens = 0:
+// nothing to do). The norm's weights may be NULL.
+gdn_status rope_args(const char *fn, const gdn_rope_shape *shape, const gdn_kv_cache *cache,
+                     const void *q, const void *k, const void *v, const void *q_weight,
+                     const void *k_weight, const int32_t *positions, const float *inv_freq,
+                     const int64_t *slots, void *q_out, void *k_cache, void *v_cache,
+                     gdn::RopeArgs &a) {
+  if (!shape) return fail(GDN_ERR_INVALID_ARG, "%s: shape is NULL", fn);
+  const gdn_rope_shape &s = *shape;
+  size_t cache_bytes = 0;
+  gdn_status st = kv_layout(fn, cache, &a.cache, &cache_bytes);
+  if (st != GDN_OK) return st;
+  const int D = a.cache.D, H_kv = a.cache.H_kv;
+  if (s.n_tokens < 0 || s.H < 1)
+    return fail(GDN_ERR_INVALID_ARG, "%s: n_tokens=%d H=%d", fn, s.n_tokens, s.H);
+  if (s.H > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "%s: H=%d is above 2^20", fn, s.H);
+  if (s.rot_dim < 0 || s.rot_dim > D || (s.rot_dim & 1))
+    return fail(GDN_ERR_INVALID_ARG, "%s: rot_dim=%d (need even, 0 to D=%d)", fn, s.rot_dim, D);
+  if (s.pairs != GDN_ROPE_HALVES && s.pairs != GDN_ROPE_NEIGHBOURS)
+    return fail(GDN_ERR_INVALID_ARG, "%s: pairs %d", fn, (int)s.pairs);
+  if (s.axes != GDN_ROPE_AXES_SECTIONED && s.axes != GDN_ROPE_AXES_INTERLEAVED)
+    return fail(GDN_ERR_INVALID_ARG, "%s: axes %d", fn, (int)s.axes);
+  if (s.n_axes < 1 || s.n_axes > 4)
+    return fail(GDN_ERR_INVALID_ARG, "%s: n_axes=%d (need 1 to 4)", fn, s.n_axes);
+  const int half = s.rot_dim / 2;
+  int left = half;
+  for (int i = 0; i < s.n_axes; ++i) {
+    if (s.section[i] < 0 || s.section[i] > left)
+      return fail(GDN_ERR_INVALID_ARG, "%s: the sections do not sum to rot_dim / 2 = %d", fn, half);
+    // taking turns, axis i > 0 has the frequencies i, i + n_axes, ... below half
+    if (s.axes == GDN_ROPE_AXES_INTERLEAVED && i > 0 &&
+        s.section[i] > (half - i + s.n_axes - 1) / s.n_axes)
+      return fail(GDN_ERR_INVALID_ARG, "%s: section[%d]=%d is more than the axis's turns", fn, i,
+                  s.section[i]);
+    left -= s.section[i];
+  }
+  if (left)
+    return fail(GDN_ERR_INVALID_ARG, "%s: the sections do not sum to rot_dim / 2 = %d", fn, half);
+  const long long m = a.cache.bf16 ? 8 : 4;
+  const long long dense[3] = {(long long)s.H * D, (long long)H_kv * D, (long long)H_kv * D};
+  long long stride[3] = {s.q_stride, s.k_stride, s.v_stride};
+  const char *names[3] = {"q_stride", "k_stride", "v_stride"};
+  for (int i = 0; i < 3; ++i) {
+    if (stride[i] == 0) stride[i] = dense[i];
+    if (stride[i] < dense[i] || stride[i] % m || stride[i] > (1LL << 28))
+      return fail(GDN_ERR_INVALID_ARG,
+                  "%s: %s=%lld (need a multiple of 16 bytes from %lld to 2^28)", fn, names[i],
+                  stride[i], dense[i]);
+  }
+  a.n_tokens = s.n_tokens;
+  if (s.n_tokens == 0) return GDN_OK;
+  const size_t e = a.cache.bf16 ? 2 : 4, n = (size_t)s.n_tokens;
+  const Buf in[] = {{"q", q, e * ((n - 1) * (size_t)stride[0] + (size_t)dense[0])},
+                    {"k", k, e * ((n - 1) * (size_t)stride[1] + (size_t)dense[1])},
+                    {"v", v, e * ((n - 1) * (size_t)stride[2] + (size_t)dense[2])},
+                    {"positions", positions, 4 * n * s.n_axes},
+                    {"slots", slots, 8 * n},
+                    {"inv_freq", inv_freq, 4 * (size_t)half},
+                    {"q_weight", q_weight, e * (size_t)D},
+                    {"k_weight", k_weight, e * (size_t)D}};
+  const Buf outs[] = {{"q_out", q_out, e * n * (size_t)dense[0]},
+                      {"k_cache", k_cache, cache_bytes},
+                      {"v_cache", v_cache, cache_bytes}};
+  for (const Buf &b : in) {
+    const bool optional = &b == &in[5] ? half == 0 : &b > &in[5];
+    if (!b.p && !optional)
+      return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, b.name);
+    if ((st = check_aligned(fn, b)) != GDN_OK) return st;
+  }
+  for (int i = 0; i < 3; ++i) {
+    if (!outs[i].p) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, outs[i].name);
+    if ((st = check_aligned(fn, outs[i])) != GDN_OK) return st;
+    for (const Buf &b : in)
+      if ((st = check_apart(fn, outs[i], b)) != GDN_OK) return st;
+  }
+  // one buffer may hold both caches interleaved (strides twice as long), so
+  // the two are compared row by row
+  if (k_cache == v_cache)
+    return fail(GDN_ERR_INVALID_ARG, "%s: k_cache and v_cache are the same", fn);
+  if (ranges_overlap(k_cache, cache_bytes, v_cache, cache_bytes) &&
+      rows_collide(a.cache, (static_cast<const char *>(v_cache) -
+                             static_cast<const char *>(k_cache)) / (long long)e))
+    return fail(GDN_ERR_INVALID_ARG, "%s: rows of k_cache and v_cache overlap", fn);
+  for (int i = 1; i < 3; ++i)
+    if ((st = check_apart(fn, outs[0], outs[i])) != GDN_OK) return st;
+  if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;
+  a.q = q; a.k = k; a.v = v;
+  a.q_stride = stride[0]; a.k_stride = stride[1]; a.v_stride = stride[2];
+  a.positions = positions; a.inv_freq = inv_freq; a.slots = slots;
+  a.q_out = q_out; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.H = s.H; a.rot_dim = s.rot_dim; a.n_axes = s.n_axes;
+  for (int i = 0; i < 4; ++i) a.section[i] = i < s.n_axes ? s.section[i] : 0;
+  a.neighbours = s.pairs == GDN_ROPE_NEIGHBOURS;
+  a.interleaved = s.axes == GDN_ROPE_AXES_INTERLEAVED;
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -248,93 +345,34 @@ gdn_status gdn_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cach
                            const void *k, const void *v, const int32_t *positions,
                            const float *inv_freq, const int64_t *slots, void *q_out,
                            void *k_cache, void *v_cache, gdn_stream_t stream) {
-  const char *fn = "gdn_rope_append";
-  if (!shape) return fail(GDN_ERR_INVALID_ARG, "%s: shape is NULL", fn);
-  const gdn_rope_shape &s = *shape;
   gdn::RopeArgs a{};
-  size_t cache_bytes = 0;
-  gdn_status st = kv_layout(fn, cache, &a.cache, &cache_bytes);
-  if (st != GDN_OK) return st;
-  const int D = a.cache.D, H_kv = a.cache.H_kv;
-  if (s.n_tokens < 0 || s.H < 1)
-    return fail(GDN_ERR_INVALID_ARG, "%s: n_tokens=%d H=%d", fn, s.n_tokens, s.H);
-  if (s.H > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "%s: H=%d is above 2^20", fn, s.H);
-  if (s.rot_dim < 0 || s.rot_dim > D || (s.rot_dim & 1))
-    return fail(GDN_ERR_INVALID_ARG, "%s: rot_dim=%d (need even, 0 to D=%d)", fn, s.rot_dim, D);
-  if (s.pairs != GDN_ROPE_HALVES && s.pairs != GDN_ROPE_NEIGHBOURS)
-    return fail(GDN_ERR_INVALID_ARG, "%s: pairs %d", fn, (int)s.pairs);
-  if (s.axes != GDN_ROPE_AXES_SECTIONED && s.axes != GDN_ROPE_AXES_INTERLEAVED)
-    return fail(GDN_ERR_INVALID_ARG, "%s: axes %d", fn, (int)s.axes);
-  if (s.n_axes < 1 || s.n_axes > 4)
-    return fail(GDN_ERR_INVALID_ARG, "%s: n_axes=%d (need 1 to 4)", fn, s.n_axes);
-  const int half = s.rot_dim / 2;
-  int left = half;
-  for (int i = 0; i < s.n_axes; ++i) {
-    if (s.section[i] < 0 || s.section[i] > left)
-      return fail(GDN_ERR_INVALID_ARG, "%s: the sections do not sum to rot_dim / 2 = %d", fn, half);
-    // taking turns, axis i > 0 has the frequencies i, i + n_axes, ... below half
-    if (s.axes == GDN_ROPE_AXES_INTERLEAVED && i > 0 &&
-        s.section[i] > (half - i + s.n_axes - 1) / s.n_axes)
-      return fail(GDN_ERR_INVALID_ARG, "%s: section[%d]=%d is more than the axis's turns", fn, i,
-                  s.section[i]);
-    left -= s.section[i];
-  }
-  if (left)
-    return fail(GDN_ERR_INVALID_ARG, "%s: the sections do not sum to rot_dim / 2 = %d", fn, half);
-  const long long m = a.cache.bf16 ? 8 : 4;
-  const long long dense[3] = {(long long)s.H * D, (long long)H_kv * D, (long long)H_kv * D};
-  long long stride[3] = {s.q_stride, s.k_stride, s.v_stride};
-  const char *names[3] = {"q_stride", "k_stride", "v_stride"};
-  for (int i = 0; i < 3; ++i) {
-    if (stride[i] == 0) stride[i] = dense[i];
-    if (stride[i] < dense[i] || stride[i] % m || stride[i] > (1LL << 28))
-      return fail(GDN_ERR_INVALID_ARG,
-                  "%s: %s=%lld (need a multiple of 16 bytes from %lld to 2^28)", fn, names[i],
-                  stride[i], dense[i]);
-  }
-  if (s.n_tokens == 0) return GDN_OK;
-  const size_t e = a.cache.bf16 ? 2 : 4, n = (size_t)s.n_tokens;
-  const Buf in[] = {{"q", q, e * ((n - 1) * (size_t)stride[0] + (size_t)dense[0])},
-                    {"k", k, e * ((n - 1) * (size_t)stride[1] + (size_t)dense[1])},
-                    {"v", v, e * ((n - 1) * (size_t)stride[2] + (size_t)dense[2])},
-                    {"positions", positions, 4 * n * s.n_axes},
-                    {"slots", slots, 8 * n},
-                    {"inv_freq", inv_freq, 4 * (size_t)half}};
-  const Buf outs[] = {{"q_out", q_out, e * n * (size_t)dense[0]},
-                      {"k_cache", k_cache, cache_bytes},
-                      {"v_cache", v_cache, cache_bytes}};
-  for (const Buf &b : in) {
-    if (!b.p && !(b.p == inv_freq && half == 0))
-      return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, b.name);
-    if ((st = check_aligned(fn, b)) != GDN_OK) return st;
-  }
-  for (int i = 0; i < 3; ++i) {
-    if (!outs[i].p) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, outs[i].name);
-    if ((st = check_aligned(fn, outs[i])) != GDN_OK) return st;
-    for (const Buf &b : in)
-      if ((st = check_apart(fn, outs[i], b)) != GDN_OK) return st;
-  }
-  // one buffer may hold both caches interleaved (strides twice as long), so
-  // the two are compared row by row
-  if (k_cache == v_cache)
-    return fail(GDN_ERR_INVALID_ARG, "%s: k_cache and v_cache are the same", fn);
-  if (ranges_overlap(k_cache, cache_bytes, v_cache, cache_bytes) &&
-      rows_collide(a.cache, (static_cast<const char *>(v_cache) -
-                             static_cast<const char *>(k_cache)) / (long long)e))
-    return fail(GDN_ERR_INVALID_ARG, "%s: rows of k_cache and v_cache overlap", fn);
-  for (int i = 1; i < 3; ++i)
-    if ((st = check_apart(fn, outs[0], outs[i])) != GDN_OK) return st;
-  if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;
-  a.q = q; a.k = k; a.v = v;
-  a.q_stride = stride[0]; a.k_stride = stride[1]; a.v_stride = stride[2];
-  a.positions = positions; a.inv_freq = inv_freq; a.slots = slots;
-  a.q_out = q_out; a.k_cache = k_cache; a.v_cache = v_cache;
-  a.n_tokens = s.n_tokens; a.H = s.H; a.rot_dim = s.rot_dim; a.n_axes = s.n_axes;
-  for (int i = 0; i < 4; ++i) a.section[i] = i < s.n_axes ? s.section[i] : 0;
-  a.neighbours = s.pairs == GDN_ROPE_NEIGHBOURS;
-  a.interleaved = s.axes == GDN_ROPE_AXES_INTERLEAVED;
+  const gdn_status st = rope_args("gdn_rope_append", shape, cache, q, k, v, nullptr, nullptr,
+                                  positions, inv_freq, slots, q_out, k_cache, v_cache, a);
+  if (st != GDN_OK || a.n_tokens == 0) return st;
   return check_launch(gdn::launch_rope_append(a, reinterpret_cast<cudaStream_t>(stream)),
                       "gdn_rope_append launch");
+}
+
+gdn_status gdn_qknorm_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cache,
+                                  const gdn_qk_norm *norm, const void *q, const void *k,
+                                  const void *v, const void *q_weight, const void *k_weight,
+                                  const int32_t *positions, const float *inv_freq,
+                                  const int64_t *slots, void *q_out, void *k_cache,
+                                  void *v_cache, gdn_stream_t stream) {
+  const char *fn = "gdn_qknorm_rope_append";
+  if (!norm) return fail(GDN_ERR_INVALID_ARG, "%s: norm is NULL", fn);
+  if (!std::isfinite(norm->eps) || norm->eps < 0.f)
+    return fail(GDN_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
+  if (!std::isfinite(norm->weight_offset))
+    return fail(GDN_ERR_INVALID_ARG, "%s: weight_offset is not finite", fn);
+  gdn::QkNormArgs a{};
+  const gdn_status st = rope_args(fn, shape, cache, q, k, v, q_weight, k_weight, positions,
+                                  inv_freq, slots, q_out, k_cache, v_cache, a.rope);
+  if (st != GDN_OK || a.rope.n_tokens == 0) return st;
+  a.q_weight = q_weight; a.k_weight = k_weight;
+  a.eps = norm->eps; a.weight_offset = norm->weight_offset;
+  return check_launch(gdn::launch_qknorm_rope(a, reinterpret_cast<cudaStream_t>(stream)),
+                      "gdn_qknorm_rope_append launch");
 }
 
 size_t gdn_paged_attention_workspace_size(const gdn_attn_shape *shape, const gdn_kv_cache *cache) {

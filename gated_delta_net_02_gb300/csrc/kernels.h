@@ -125,6 +125,14 @@ struct RopeArgs {
 };
 cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t stream);
 
+// The same with an RMS norm of each q and k head first; see qknorm_rope.cu.
+struct QkNormArgs {
+  RopeArgs rope;
+  const void *q_weight, *k_weight;         // [D] or NULL
+  float eps, weight_offset;
+};
+cudaError_t launch_qknorm_rope(const QkNormArgs &a, cudaStream_t stream);
+
 // Attention over a paged cache; see paged_attention.cu.
 struct AttnArgs {
   KvLayout cache;

@@ -86,6 +86,10 @@ class gdn_rope_shape(ctypes.Structure):
                 ("v_stride", ctypes.c_longlong)]
 
 
+class gdn_qk_norm(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("weight_offset", ctypes.c_float)]
+
+
 class gdn_attn_shape(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int), ("T", ctypes.c_int), ("H", ctypes.c_int),
                 ("max_pages", ctypes.c_int), ("scale", ctypes.c_float),
@@ -134,6 +138,10 @@ lib.gdn_gemm_fp8.argtypes = [ctypes.POINTER(gdn_gemm_shape), _vp, _vp, _vp, _vp,
 lib.gdn_rope_append.restype = _st
 lib.gdn_rope_append.argtypes = [ctypes.POINTER(gdn_rope_shape), ctypes.POINTER(gdn_kv_cache),
                                 _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+lib.gdn_qknorm_rope_append.restype = _st
+lib.gdn_qknorm_rope_append.argtypes = [
+    ctypes.POINTER(gdn_rope_shape), ctypes.POINTER(gdn_kv_cache), ctypes.POINTER(gdn_qk_norm),
+    _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
 lib.gdn_paged_attention_workspace_size.restype = ctypes.c_size_t
 lib.gdn_paged_attention_workspace_size.argtypes = [ctypes.POINTER(gdn_attn_shape),
                                                    ctypes.POINTER(gdn_kv_cache)]
@@ -360,6 +368,21 @@ def gdn_rope_append(shape: gdn_rope_shape, cache: gdn_kv_cache, q, k, v, positio
         _rows_addr(v, n, shape.v_stride, kv, D), _addr(positions), _addr(inv_freq), _addr(slots),
         _addr(q_out), _cache_addr(k_cache, cache), _cache_addr(v_cache, cache),
         _stream(stream)))
+
+
+def gdn_qknorm_rope_append(shape: gdn_rope_shape, cache: gdn_kv_cache, norm: gdn_qk_norm, q, k, v,
+                           q_weight, k_weight, positions, inv_freq, slots, q_out, k_cache, v_cache,
+                           stream=None) -> None:
+    """gdn_rope_append with an RMS norm of every q and k head before the
+    rotation; q_weight and k_weight may be None."""
+    n, D = shape.n_tokens, cache.D
+    kv = cache.H_kv * D
+    _check(lib.gdn_qknorm_rope_append(
+        ctypes.byref(shape), ctypes.byref(cache), ctypes.byref(norm),
+        _rows_addr(q, n, shape.q_stride, shape.H * D, D), _rows_addr(k, n, shape.k_stride, kv, D),
+        _rows_addr(v, n, shape.v_stride, kv, D), _addr(q_weight), _addr(k_weight),
+        _addr(positions), _addr(inv_freq), _addr(slots), _addr(q_out),
+        _cache_addr(k_cache, cache), _cache_addr(v_cache, cache), _stream(stream)))
 
 
 def gdn_paged_attention_workspace_size(shape: gdn_attn_shape, cache: gdn_kv_cache) -> int:

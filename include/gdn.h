@@ -419,6 +419,31 @@ gdn_status gdn_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cach
                            void *k_cache, void *v_cache, gdn_stream_t stream);
 
 /*
+ * gdn_rope_append for models that norm every q and k head before the
+ * rotation. Per token and head (all arithmetic and sums in fp32, one rounding
+ * at the end):
+ *   y = x / sqrt(mean(x^2) + eps) * (weight_offset + weight)
+ * over the head's D elements; the first rot_dim elements of y are then
+ * rotated, the others are written as they are. v is copied.
+ */
+typedef struct {
+  float eps;           /* finite, >= 0 */
+  float weight_offset; /* 0, or 1 for weights stored around zero */
+} gdn_qk_norm;
+
+/*
+ * q_weight, k_weight  device [D], dtype of the cache, for all q and all k
+ *            heads; each may be NULL (without that factor)
+ * The other arguments are those of gdn_rope_append.
+ */
+gdn_status gdn_qknorm_rope_append(const gdn_rope_shape *shape, const gdn_kv_cache *cache,
+                                  const gdn_qk_norm *norm, const void *q, const void *k,
+                                  const void *v, const void *q_weight, const void *k_weight,
+                                  const int32_t *positions, const float *inv_freq,
+                                  const int64_t *slots, void *q_out, void *k_cache,
+                                  void *v_cache, gdn_stream_t stream);
+
+/*
  * Attention of the last T tokens of each sequence over its pages (T = 1:
  * decode; T = draft_max + 1: verify). Sequence s has lens[s] tokens in the
  * cache, the new ones included; its token j is at page

@@ -1,0 +1,57 @@
+"""Refusals of the entry points that verify a tree of drafts, all made before
+the device is touched (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from test_layer_host import BAD_CACHES, FAKE, STEP, gdn, kv, refused  # noqa: F401
+
+
+def qknorm(gdn, shape=None, cache=None, eps=1e-6, offset=0.0, **kw):
+    sh = dict(n_tokens=5, H=4, rot_dim=128, pairs=0, n_axes=3, section=(32, 16, 16), axes=0,
+              q_stride=0, k_stride=0, v_stride=0)
+    sh.update(shape or {})
+    sh["section"] = (ctypes.c_int * 4)(*sh["section"])
+    p = {n: FAKE + i * STEP for i, n in enumerate(
+        ("q", "k", "v", "q_weight", "k_weight", "positions", "inv_freq", "slots", "q_out",
+         "k_cache", "v_cache"))}
+    p.update(kw)
+    gdn.gdn_qknorm_rope_append(
+        gdn.gdn_rope_shape(*(sh[f[0]] for f in gdn.gdn_rope_shape._fields_)),
+        kv(gdn, **(cache or {})), gdn.gdn_qk_norm(eps, offset), *p.values())
+
+
+@pytest.mark.parametrize("cache,status", BAD_CACHES)
+def test_qknorm_refuses_caches(gdn, cache, status):
+    st, msg = refused(gdn, lambda: qknorm(gdn, cache=cache))
+    assert st == status and "gdn_qknorm_rope_append" in msg
+
+
+@pytest.mark.parametrize("args", [
+    dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(offset=float("nan")),
+    dict(shape=dict(n_tokens=-1)), dict(shape=dict(H=0)), dict(shape=dict(rot_dim=130)),
+    dict(shape=dict(section=(32, 16, 15))), dict(shape=dict(q_stride=512 - 8))])
+def test_qknorm_refuses_shapes(gdn, args):
+    st, msg = refused(gdn, lambda: qknorm(gdn, **args))
+    assert st == gdn.GDN_ERR_INVALID_ARG and "gdn_qknorm_rope_append" in msg
+
+
+@pytest.mark.parametrize("ptrs,word", [
+    (dict(q=0), "q is NULL"), (dict(inv_freq=0), "inv_freq is NULL"),
+    (dict(q_weight=FAKE + 3 * STEP + 8), "q_weight is not 16-byte"),
+    (dict(k_weight=FAKE + 4 * STEP + 2), "k_weight is not 16-byte"),
+    (dict(q_out=FAKE + 3 * STEP), "q_out overlaps q_weight"),
+    (dict(k_cache=FAKE + 4 * STEP), "k_cache overlaps k_weight"),
+    (dict(v_cache=FAKE + 9 * STEP), "are the same")])
+def test_qknorm_refuses_buffers(gdn, ptrs, word):
+    st, msg = refused(gdn, lambda: qknorm(gdn, **ptrs))
+    assert st == gdn.GDN_ERR_INVALID_ARG and word in msg
+
+
+def test_qknorm_of_no_tokens_and_null_structs(gdn):
+    qknorm(gdn, dict(n_tokens=0), q=0)
+    qknorm(gdn, dict(n_tokens=0), q_weight=0, k_weight=0)
+    null = gdn.lib.gdn_qknorm_rope_append
+    shape, norm = ctypes.byref(gdn.gdn_rope_shape()), ctypes.byref(gdn.gdn_qk_norm())
+    for args in ((None, None, norm), (shape, None, norm), (shape, None, None)):
+        assert null(*args, *[0] * 12) == gdn.GDN_ERR_INVALID_ARG
