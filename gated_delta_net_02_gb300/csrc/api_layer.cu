@@ -14,27 +14,6 @@ using namespace gdn::api;
 
 namespace {
 
-struct Buf {
-  const char *name;
-  const void *p;
-  size_t bytes;
-};
-
-gdn_status check_aligned(const char *fn, const Buf &b) {
-  if (!aligned16(b.p))
-    return fail(GDN_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, b.name);
-  return GDN_OK;
-}
-
-// GDN_ERR_INVALID_ARG if `out` shares bytes with `b` (either may be NULL).
-gdn_status check_apart(const char *fn, const Buf &out, const Buf &b) {
-  if (out.p && b.p && ranges_overlap(out.p, out.bytes, b.p, b.bytes))
-    return fail(GDN_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, out.name, b.name);
-  return GDN_OK;
-}
-
-bool dtype_ok(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
-
 // Checks a cache layout and resolves its strides; *bytes is the extent of
 // each of its two buffers.
 gdn_status kv_layout(const char *fn, const gdn_kv_cache *cache, gdn::KvLayout *l, size_t *bytes) {

@@ -26,5 +26,26 @@ inline bool ranges_overlap(const void *a, size_t na, const void *b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+struct Buf {
+  const char *name;
+  const void *p;
+  size_t bytes;
+};
+
+inline gdn_status check_aligned(const char *fn, const Buf &b) {
+  if (!aligned16(b.p))
+    return fail(GDN_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, b.name);
+  return GDN_OK;
+}
+
+// GDN_ERR_INVALID_ARG if `out` shares bytes with `b` (either may be NULL).
+inline gdn_status check_apart(const char *fn, const Buf &out, const Buf &b) {
+  if (out.p && b.p && ranges_overlap(out.p, out.bytes, b.p, b.bytes))
+    return fail(GDN_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, out.name, b.name);
+  return GDN_OK;
+}
+
+inline bool dtype_ok(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
+
 }  // namespace api
 }  // namespace gdn

@@ -148,4 +148,18 @@ struct AttnArgs {
 size_t attn_workspace_size(const KvLayout &c, int n_seqs, int T, int H, int max_pages);
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream);
 
+// One token of each row of logits; see sample.cu.
+struct SampleArgs {
+  const void *logits;           // rows of `vocab`, `stride` elements apart
+  long long stride;
+  const float *temperature, *top_p, *min_p;  // [rows] or NULL
+  const int32_t *top_k;                      // [rows] or NULL
+  const float *uniform;                      // [rows]
+  int32_t *tokens;                           // [rows]
+  float *probs;                              // [rows] or NULL
+  int rows, vocab;
+  bool bf16;
+};
+cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
+
 }  // namespace gdn

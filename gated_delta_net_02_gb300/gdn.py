@@ -96,6 +96,12 @@ class gdn_attn_shape(ctypes.Structure):
                 ("kv_map", ctypes.c_int)]
 
 
+class gdn_sample_shape(ctypes.Structure):
+    # row_stride = 0 (the default) means rows of vocab elements, packed
+    _fields_ = [("rows", ctypes.c_int), ("vocab", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("row_stride", ctypes.c_longlong)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"libgdn.so is not built ({LIB_PATH}); run "
                       "gated_delta_net_02_gb300/build.py or __graft_entry__.build()")
@@ -149,6 +155,9 @@ lib.gdn_paged_attention.restype = _st
 lib.gdn_paged_attention.argtypes = [ctypes.POINTER(gdn_attn_shape),
                                     ctypes.POINTER(gdn_kv_cache), _vp, _vp, _vp, _vp, _vp, _vp,
                                     _vp, ctypes.c_size_t, _vp]
+lib.gdn_sample.restype = _st
+lib.gdn_sample.argtypes = [ctypes.POINTER(gdn_sample_shape), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                           _vp, _vp]
 lib.gdn_seq_table_create.restype = _st
 lib.gdn_seq_table_create.argtypes = [_i, _i, ctypes.POINTER(_vp)]
 lib.gdn_seq_table_destroy.restype = None
@@ -397,6 +406,32 @@ def gdn_paged_attention(shape: gdn_attn_shape, cache: gdn_kv_cache, q, k_cache, 
         ctypes.byref(shape), ctypes.byref(cache), _addr(q), _cache_addr(k_cache, cache),
         _cache_addr(v_cache, cache), _addr(page_table), _addr(lens), _addr(out),
         _addr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def _matrix_addr(x, rows, cols, stride):
+    """Device address of `rows` rows of `cols` elements, `stride` apart (0 = packed)."""
+    if x is None or x.__class__ is int:
+        return x
+    try:
+        st = x.stride()
+    except AttributeError:
+        if isinstance(x, int):
+            return int(x)
+        raise
+    if st[-1] != 1 and cols > 1 or rows > 1 and (
+            not x.is_contiguous() if not stride or stride == cols else st[:-1] != (stride,)):
+        raise ValueError("gdn: rows must be packed, and apart by the shape's stride")
+    return x.data_ptr()
+
+
+def gdn_sample(shape: gdn_sample_shape, logits, temperature, top_k, top_p, min_p, uniform, tokens,
+               probs=None, stream=None) -> None:
+    """One token of each row of logits from given random numbers; temperature,
+    top_k, top_p, min_p and probs may be None."""
+    _check(lib.gdn_sample(
+        ctypes.byref(shape), _matrix_addr(logits, shape.rows, shape.vocab, shape.row_stride),
+        _addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p), _addr(uniform),
+        _addr(tokens), _addr(probs), _stream(stream)))
 
 
 def gdn_check_device_error(stream=None) -> None:

@@ -498,6 +498,49 @@ gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const gdn_kv_cache *
                                void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * One token of each row of logits (a decode step's sequences, or every
+ * drafted token that a verify step scored), from a random number that the
+ * caller gives. Per row, with its own settings:
+ *   w[i]  = exp((x[i] - max x) / temperature)
+ *   order = by logit, largest first, equal ones by index, lowest first
+ *   kept  = the first n of that order, n the least of
+ *             top_k;
+ *             the fewest whose mass (sum of w) is at least top_p times that of
+ *             the first top_k;
+ *             those with w[i] >= min_p;
+ *           but one at least
+ *   token = the first kept index, counting up, whose running mass is above
+ *           uniform * (mass of all kept)
+ *   prob  = w[token] / (mass of all kept)
+ * temperature <= 0 (or NaN) takes the first token of the order (prob 1). A
+ * NaN logit counts as -infinity. Tokens at +infinity have weight 1 and all
+ * others 0. A row with nothing above -infinity gives token -1, prob 0.
+ * top_k <= 0, top_p >= 1, min_p <= 0 or NaN: no such limit.
+ * Weights and masses are whole numbers of 2^-44 of the largest weight (a
+ * weight is off by some 2^-40; below 2^-45 it is 0), so the result is the same
+ * bits every time and its place between two tokens is that of 64-bit sums.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int rows;             /* >= 0, at most 2^24 */
+  int vocab;            /* 1 .. 2^18 */
+  gdn_dtype dtype;      /* of the logits */
+  long long row_stride; /* elements between rows, any from vocab on; 0 = vocab */
+} gdn_sample_shape;
+
+/*
+ * logits       device [rows] rows of [vocab], row_stride apart
+ * temperature, top_p, min_p  device fp32 [rows]; top_k device int32 [rows];
+ *              each may be NULL (temperature 1; no limit)
+ * uniform      device fp32 [rows], 0 <= uniform < 1 (outside: the first or
+ *              the last kept token; NaN: the first)
+ * tokens       device int32 [rows]
+ * probs        device fp32 [rows], or NULL
+ */
+gdn_status gdn_sample(const gdn_sample_shape *shape, const void *logits, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p,
+                      const float *uniform, int32_t *tokens, float *probs, gdn_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Rollback bookkeeping: a host-side table with one entry per sequence (the
  * recurrent memory's per-sequence record of which stored state is live,
  * "llama-memory-recurrent: clear rs_idx in clear", koboldcpp commits, tag

@@ -55,3 +55,46 @@ def test_qknorm_of_no_tokens_and_null_structs(gdn):
     shape, norm = ctypes.byref(gdn.gdn_rope_shape()), ctypes.byref(gdn.gdn_qk_norm())
     for args in ((None, None, norm), (shape, None, norm), (shape, None, None)):
         assert null(*args, *[0] * 12) == gdn.GDN_ERR_INVALID_ARG
+
+
+def sample(gdn, shape=None, **kw):
+    sh = dict(rows=4, vocab=1000, dtype=gdn.GDN_BF16, row_stride=0)
+    sh.update(shape or {})
+    p = {n: FAKE + i * STEP for i, n in enumerate(
+        ("logits", "temperature", "top_k", "top_p", "min_p", "uniform", "tokens", "probs"))}
+    p.update(kw)
+    gdn.gdn_sample(gdn.gdn_sample_shape(*(sh[f[0]] for f in gdn.gdn_sample_shape._fields_)),
+                   *p.values())
+
+
+@pytest.mark.parametrize("shape,status", [
+    (dict(rows=-1), 1), (dict(vocab=0), 1), (dict(dtype=2), 1), (dict(row_stride=999), 1),
+    (dict(row_stride=-1000), 1), (dict(vocab=(1 << 18) + 1), 2), (dict(rows=(1 << 24) + 1), 2),
+    (dict(row_stride=(1 << 32) + 1), 2)])
+def test_sample_refuses_shapes(gdn, shape, status):
+    st, msg = refused(gdn, lambda: sample(gdn, shape))
+    assert st == status and "gdn_sample" in msg
+
+
+@pytest.mark.parametrize("ptrs,word", [
+    (dict(logits=0), "logits is NULL"), (dict(uniform=0), "uniform is NULL"),
+    (dict(tokens=0), "tokens is NULL"), (dict(logits=FAKE + 2), "logits is not 16-byte"),
+    (dict(top_k=FAKE + 2 * STEP + 4), "top_k is not 16-byte"),
+    (dict(probs=FAKE + 7 * STEP + 8), "probs is not 16-byte"), (dict(tokens=FAKE), "tokens overlaps"),
+    (dict(probs=FAKE + 6 * STEP), "overlaps"), (dict(probs=FAKE + 5 * STEP), "probs overlaps uniform")])
+def test_sample_refuses_buffers(gdn, ptrs, word):
+    st, msg = refused(gdn, lambda: sample(gdn, **ptrs))
+    assert st == gdn.GDN_ERR_INVALID_ARG and word in msg
+
+
+def test_sample_of_no_rows(gdn):
+    sample(gdn, dict(rows=0), logits=0, tokens=0, uniform=0)
+    assert gdn.lib.gdn_sample(None, *[0] * 9) == gdn.GDN_ERR_INVALID_ARG
+
+
+def test_sample_binding_refuses_views_that_do_not_match_their_shape(gdn):
+    import torch
+    base = torch.zeros(4, 1008, dtype=torch.bfloat16)
+    for stride, view in ((0, base[:, :1000]), (1009, base[:, :1000]), (1008, base.t()[:1000].t()[:, ::2])):
+        with pytest.raises(ValueError, match="rows must be packed"):
+            sample(gdn, dict(row_stride=stride), logits=view)
