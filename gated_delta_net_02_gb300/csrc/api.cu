@@ -20,8 +20,6 @@ thread_local char g_msg[512];
 
 gdn_status ok() { return GDN_OK; }
 
-bool head_size_ok(int d) { return d == 64 || d == 128; }
-
 }  // namespace
 
 // One error word per device; kernels receive its device address.
@@ -84,16 +82,6 @@ extern "C" {
 const char *gdn_last_error(void) { return g_msg; }
 
 const char *gdn_version(void) { return "libgdn 0.2.0 (sm_103a)"; }
-
-// Resolves the grouped-query fields: H_qk = 0 means H; H_qk must divide H.
-static gdn_status qk_heads(const char *fn, int H, int H_qk, int qk_map, int *hq) {
-  *hq = H_qk == 0 ? H : H_qk;
-  if (*hq <= 0 || *hq > H || H % *hq != 0)
-    return fail(GDN_ERR_INVALID_ARG, "%s: H_qk=%d must divide H=%d", fn, H_qk, H);
-  if (qk_map != GDN_QK_TILED && qk_map != GDN_QK_GROUPED)
-    return fail(GDN_ERR_INVALID_ARG, "%s: qk_map %d", fn, qk_map);
-  return GDN_OK;
-}
 
 // True when the device can dereference p: device or managed memory, or
 // page-locked host memory mapped into the device's address space at the same
@@ -515,6 +503,9 @@ gdn_status gdn_decode_device_error(int word) {
     case gdn::kDevBadSlot:
       return fail(GDN_ERR_DEVICE_ARG, "a slot index is beyond the cache's pages (that token's "
                                       "k and v were not written)");
+    case gdn::kDevBadTree:
+      return fail(GDN_ERR_DEVICE_ARG,
+                  "device: a tree's words, its number of nodes or a leaf name no tree");
     case gdn::kDevBadPage:
       return fail(GDN_ERR_DEVICE_ARG, "a page table entry is not a page of the cache, or a "
                                       "sequence is longer than its page table");

@@ -45,6 +45,18 @@ inline gdn_status check_apart(const char *fn, const Buf &out, const Buf &b) {
   return GDN_OK;
 }
 
+inline bool head_size_ok(int d) { return d == 64 || d == 128; }
+
+// Resolves the grouped-query fields: H_qk = 0 means H; H_qk must divide H.
+inline gdn_status qk_heads(const char *fn, int H, int H_qk, int qk_map, int *hq) {
+  *hq = H_qk == 0 ? H : H_qk;
+  if (*hq <= 0 || *hq > H || H % *hq != 0)
+    return fail(GDN_ERR_INVALID_ARG, "%s: H_qk=%d must divide H=%d", fn, H_qk, H);
+  if (qk_map != GDN_QK_TILED && qk_map != GDN_QK_GROUPED)
+    return fail(GDN_ERR_INVALID_ARG, "%s: qk_map %d", fn, qk_map);
+  return GDN_OK;
+}
+
 inline bool dtype_ok(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16; }
 
 }  // namespace api

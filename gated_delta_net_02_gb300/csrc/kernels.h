@@ -148,6 +148,24 @@ struct AttnArgs {
 size_t attn_workspace_size(const KvLayout &c, int n_seqs, int T, int H, int max_pages);
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream);
 
+// The delta rule along a tree of drafted tokens; see tree_delta.cu.
+struct TreeDeltaArgs {
+  const void *q, *k, *v;             // as RecurrentArgs, T tokens of each sequence
+  const float *g, *beta;
+  const float *const *state_in;      // device [n_seqs], NULL = zero
+  const int32_t *n_nodes;            // device [n_seqs] or NULL
+  const unsigned long long *tree;    // device [n_seqs][T]
+  const int32_t *leaf;               // commit: device [n_seqs]
+  float *out, *updates;              // [n_seqs*T][H][Dv]; commit: updates is read
+  float *state_out;                  // commit: [n_seqs][H][Dk][Dv]
+  int n_seqs, T, H, Hqk, Dk, Dv;
+  bool qk_grouped, kda, bf16;
+  float scale;
+  int *err;
+};
+cudaError_t launch_tree_forward(const TreeDeltaArgs &a, cudaStream_t stream);
+cudaError_t launch_tree_commit(const TreeDeltaArgs &a, cudaStream_t stream);
+
 // One token of each row of logits; see sample.cu.
 struct SampleArgs {
   const void *logits;           // rows of `vocab`, `stride` elements apart

@@ -15,6 +15,7 @@ namespace gdn {
 enum LayerDevErr : int {
   kDevBadSlot = 5,  // a slot index beyond the key-value cache
   kDevBadPage = 6,  // a page table entry or a length beyond the key-value cache
+  kDevBadTree = 7,  // a tree's words, number of nodes or leaf name no tree
 };
 
 // Wait sites (bits 8..15 of a timeout), after those of the delta-rule kernels.

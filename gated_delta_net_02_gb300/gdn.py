@@ -155,6 +155,12 @@ lib.gdn_paged_attention.restype = _st
 lib.gdn_paged_attention.argtypes = [ctypes.POINTER(gdn_attn_shape),
                                     ctypes.POINTER(gdn_kv_cache), _vp, _vp, _vp, _vp, _vp, _vp,
                                     _vp, ctypes.c_size_t, _vp]
+lib.gdn_tree_forward.restype = _st
+lib.gdn_tree_forward.argtypes = [ctypes.POINTER(gdn_shape), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _vp, _vp, _i, _vp]
+lib.gdn_tree_commit.restype = _st
+lib.gdn_tree_commit.argtypes = [ctypes.POINTER(gdn_shape), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i,
+                                _vp]
 lib.gdn_sample.restype = _st
 lib.gdn_sample.argtypes = [ctypes.POINTER(gdn_sample_shape), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                            _vp, _vp]
@@ -406,6 +412,23 @@ def gdn_paged_attention(shape: gdn_attn_shape, cache: gdn_kv_cache, q, k_cache, 
         ctypes.byref(shape), ctypes.byref(cache), _addr(q), _cache_addr(k_cache, cache),
         _cache_addr(v_cache, cache), _addr(page_table), _addr(lens), _addr(out),
         _addr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def gdn_tree_forward(shape: gdn_shape, q, k, v, g, beta, state_in, n_nodes, tree, out, updates,
+                     mode, stream=None) -> None:
+    """The delta rule along every branch of a tree of drafted tokens; `tree`:
+    an int64 (or uint64) tensor of the words, n_nodes may be None."""
+    _check(lib.gdn_tree_forward(ctypes.byref(shape), _addr(q), _addr(k), _addr(v), _addr(g),
+                                _addr(beta), _addr(state_in), _addr(n_nodes), _addr(tree),
+                                _addr(out), _addr(updates), _MODES[mode], _stream(stream)))
+
+
+def gdn_tree_commit(shape: gdn_shape, k, g, updates, state_in, tree, leaf, state_out, mode,
+                    stream=None) -> None:
+    """The state after node leaf[s] of each sequence, from gdn_tree_forward's updates."""
+    _check(lib.gdn_tree_commit(ctypes.byref(shape), _addr(k), _addr(g), _addr(updates),
+                               _addr(state_in), _addr(tree), _addr(leaf), _addr(state_out),
+                               _MODES[mode], _stream(stream)))
 
 
 def _matrix_addr(x, rows, cols, stride):

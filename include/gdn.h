@@ -498,6 +498,61 @@ gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const gdn_kv_cache *
                                void *workspace, size_t workspace_bytes, gdn_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Trees of drafted tokens. A verify step may score several continuations of a
+ * sequence at once: its T tokens are the nodes of a tree (of several, if
+ * several follow the last accepted token), numbered so that a node comes
+ * after its parent. The tree of sequence s is T words of 64 bits:
+ *   bit j of tree[s][t]: node j is an ancestor of node t, or t itself
+ * so T is at most 64. n_nodes[s] (0 .. T) says how many of the T nodes the
+ * sequence has; rows of the others are padding. n_nodes = NULL: all have T.
+ *
+ * The gated delta rule along every branch: with S_p the state after node t's
+ * parent (state_in for a node without one), node t has
+ *   S = decay(S_p), d = beta (v - S^T k), S <- S + k d^T, o = scale S^T q
+ * (decay as gdn_forward). No state is written: o and d follow from state_in,
+ * the keys of the ancestors and their d, and gdn_tree_commit forms the one
+ * state that is wanted from the d once a branch is accepted. All products and
+ * sums are as exact as fp32 ones, for bf16 inputs too; any gate is computed,
+ * -inf included.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * shape       as gdn_forward, T = nodes of each sequence, at most 64
+ * q, k, v, g, beta, state_in  as gdn_forward (token s*T+t is node t)
+ * n_nodes     device int32 [n_seqs], or NULL
+ * tree        device uint64 [n_seqs][T]; words of padding are not read
+ * out         device fp32 [n_seqs*T][H][D_v]: o
+ * updates     device fp32 [n_seqs*T][H][D_v]: d
+ * Padding rows of out and updates are 0; their inputs are not used. n_nodes
+ * outside 0 .. T, or words that are no tree (bit t missing in word t, a later
+ * node's bit, an ancestor whose own ancestors differ) are reported as
+ * GDN_ERR_DEVICE_ARG by gdn_check_device_error, and that sequence's rows are
+ * not written. out and updates overlap each other and the inputs nowhere, nor any
+ * state_in[s] (not checked).
+ */
+gdn_status gdn_tree_forward(const gdn_shape *shape, const void *q, const void *k, const void *v,
+                            const float *g, const float *beta, const float *const *state_in,
+                            const int32_t *n_nodes, const uint64_t *tree, float *out,
+                            float *updates, gdn_mode mode, gdn_stream_t stream);
+
+/*
+ * The state after node leaf[s] of each sequence, from the same k, g, state_in
+ * and tree as gdn_tree_forward's and the updates that it wrote:
+ *   S = state_in, then for each ancestor of the leaf and the leaf in turn
+ *   S = decay(S) + k d^T
+ * leaf        device int32 [n_seqs]; -1: no node, the state is state_in
+ * state_out   device fp32 [n_seqs][H][D_k][D_v]. state_in[s] may be the place
+ *             of sequence s in it (in place); any other overlap is reported as
+ *             GDN_ERR_DEVICE_ARG and that sequence's state is not written.
+ * A leaf outside -1 .. T-1, or whose word lacks its own bit or has a later
+ * node's, is reported likewise. The scale of `shape` is not used.
+ */
+gdn_status gdn_tree_commit(const gdn_shape *shape, const void *k, const float *g,
+                           const float *updates, const float *const *state_in,
+                           const uint64_t *tree, const int32_t *leaf, float *state_out,
+                           gdn_mode mode, gdn_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * One token of each row of logits (a decode step's sequences, or every
  * drafted token that a verify step scored), from a random number that the
  * caller gives. Per row, with its own settings:

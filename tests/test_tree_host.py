@@ -98,3 +98,55 @@ def test_sample_binding_refuses_views_that_do_not_match_their_shape(gdn):
     for stride, view in ((0, base[:, :1000]), (1009, base[:, :1000]), (1008, base.t()[:1000].t()[:, ::2])):
         with pytest.raises(ValueError, match="rows must be packed"):
             sample(gdn, dict(row_stride=stride), logits=view)
+
+
+def delta(gdn, call, shape=None, mode="gda", **kw):
+    sh = dict(n_seqs=3, T=8, H=4, D_k=128, D_v=128, in_dtype=gdn.GDN_BF16, scale=0.0, H_qk=2,
+              qk_map=0)
+    sh.update(shape or {})
+    names = {"forward": ("q", "k", "v", "g", "beta", "state_in", "n_nodes", "tree", "out", "updates"),
+             "commit": ("k", "g", "updates", "state_in", "tree", "leaf", "state_out")}[call]
+    p = {n: FAKE + i * STEP for i, n in enumerate(names)}
+    p.update(kw)
+    f = gdn.gdn_tree_forward if call == "forward" else gdn.gdn_tree_commit
+    f(gdn.gdn_shape(*(sh[f[0]] for f in gdn.gdn_shape._fields_)), *p.values(), mode)
+
+
+@pytest.mark.parametrize("call", ["forward", "commit"])
+@pytest.mark.parametrize("shape,status", [
+    (dict(n_seqs=-1), 1), (dict(T=-1), 1), (dict(H=0), 1), (dict(D_k=0), 1), (dict(D_v=-1), 1),
+    (dict(in_dtype=2), 1), (dict(scale=float("nan")), 1), (dict(H_qk=3), 1), (dict(qk_map=2), 1),
+    (dict(D_k=256), 2), (dict(D_v=32), 2), (dict(T=65), 2), (dict(n_seqs=1 << 23), 2)])
+def test_tree_calls_refuse_shapes(gdn, call, shape, status):
+    st, msg = refused(gdn, lambda: delta(gdn, call, shape))
+    assert st == status and "gdn_tree_" + call in msg
+
+
+@pytest.mark.parametrize("call,ptrs,word", [
+    ("forward", dict(q=0), "q is NULL"), ("forward", dict(tree=0), "tree is NULL"),
+    ("forward", dict(updates=0), "updates is NULL"), ("forward", dict(state_in=0), "state_in is NULL"),
+    ("forward", dict(n_nodes=FAKE + 6 * STEP + 4), "n_nodes is not 16-byte"),
+    ("forward", dict(out=FAKE + 2 * STEP), "out overlaps v"),
+    ("forward", dict(out=FAKE + 6 * STEP), "out overlaps n_nodes"),
+    ("forward", dict(updates=FAKE + 8 * STEP + 16), "updates overlaps out"),
+    ("commit", dict(leaf=0), "leaf is NULL"), ("commit", dict(g=FAKE + STEP + 8), "g is not 16-byte"),
+    ("commit", dict(state_out=0), "state_out is NULL"),
+    ("commit", dict(state_out=FAKE + 2 * STEP), "state_out overlaps updates")])
+def test_tree_calls_refuse_buffers(gdn, call, ptrs, word):
+    st, msg = refused(gdn, lambda: delta(gdn, call, **ptrs))
+    assert st == gdn.GDN_ERR_INVALID_ARG and word in msg
+
+
+def test_tree_calls_of_nothing(gdn):
+    for call in ("forward", "commit"):
+        for shape in (dict(n_seqs=0), dict(T=0)):
+            delta(gdn, call, shape, k=0, tree=0)
+    assert gdn.lib.gdn_tree_forward(None, *[0] * 12) == gdn.GDN_ERR_INVALID_ARG
+    assert gdn.lib.gdn_tree_commit(None, *[0] * 9) == gdn.GDN_ERR_INVALID_ARG
+    with pytest.raises(KeyError):
+        delta(gdn, "forward", mode="other")
+
+
+def test_device_error_of_a_bad_tree(gdn):
+    st, msg = gdn.gdn_decode_device_error(7)
+    assert st == gdn.GDN_ERR_DEVICE_ARG and "tree" in msg
