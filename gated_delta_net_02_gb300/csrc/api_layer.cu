@@ -218,6 +218,62 @@ gdn_status rope_args(const char *fn, const gdn_rope_shape *shape, const gdn_kv_c
   return GDN_OK;
 }
 
+// Checks an attention call and fills its arguments (n_seqs or T 0: nothing to
+// do). `size` is its kernels' workspace.
+gdn_status attn_args(const char *fn, const gdn_attn_shape *shape, const gdn_kv_cache *cache,
+                     const void *q, const void *k_cache, const void *v_cache,
+                     const int32_t *page_table, const int32_t *lens, void *out, void *workspace,
+                     size_t workspace_bytes,
+                     size_t (*size)(const gdn::KvLayout &, int, int, int, int), gdn::AttnArgs &a) {
+  size_t cache_bytes = 0;
+  gdn_status st = attn_shape(fn, shape, cache, &a.cache, &cache_bytes);
+  if (st != GDN_OK) return st;
+  const gdn_attn_shape &s = *shape;
+  a.n_seqs = s.n_seqs; a.T = s.T;
+  if (s.n_seqs == 0 || s.T == 0) return GDN_OK;
+  const size_t e = a.cache.bf16 ? 2 : 4, rows = (size_t)s.n_seqs * s.T * s.H;
+  const size_t need = size(a.cache, s.n_seqs, s.T, s.H, s.max_pages);
+  const Buf in[] = {{"q", q, e * rows * a.cache.D},
+                    {"k_cache", k_cache, cache_bytes},
+                    {"v_cache", v_cache, cache_bytes},
+                    {"page_table", page_table, 4 * (size_t)s.n_seqs * s.max_pages},
+                    {"lens", lens, 4 * (size_t)s.n_seqs}};
+  const Buf outs[] = {{"out", out, e * rows * a.cache.D}, {"workspace", workspace, need}};
+  for (const Buf &b : in) {
+    // no pages: every sequence is empty, and nothing of them is read
+    if (!b.p && !(b.bytes == 0 && &b != &in[0]))
+      return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, b.name);
+    if ((st = check_aligned(fn, b)) != GDN_OK) return st;
+  }
+  for (const Buf &o : outs) {
+    if (!o.p) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, o.name);
+    if ((st = check_aligned(fn, o)) != GDN_OK) return st;
+    for (const Buf &b : in)
+      if ((st = check_apart(fn, o, b)) != GDN_OK) return st;
+  }
+  if ((st = check_apart(fn, outs[0], outs[1])) != GDN_OK) return st;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(GDN_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+  if (workspace_bytes < need)
+    return fail(GDN_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes,
+                need);
+  if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;
+  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.table = page_table; a.lens = lens; a.out = out; a.workspace = workspace;
+  a.H = s.H; a.max_pages = s.max_pages;
+  a.grouped = s.kv_map == GDN_QK_GROUPED;
+  a.scale = s.scale != 0.f ? s.scale : 1.0f / std::sqrt((float)a.cache.D);
+  return GDN_OK;
+}
+
+constexpr int kMostNodes = 64;  // bits of a tree's word
+
+gdn_status tree_shape(const char *fn, const gdn_attn_shape *shape) {
+  if (shape->T > kMostNodes)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: T=%d nodes (at most %d)", fn, shape->T, kMostNodes);
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -367,47 +423,50 @@ gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const gdn_kv_cache *
                                const void *q, const void *k_cache, const void *v_cache,
                                const int32_t *page_table, const int32_t *lens, void *out,
                                void *workspace, size_t workspace_bytes, gdn_stream_t stream) {
-  const char *fn = "gdn_paged_attention";
   gdn::AttnArgs a{};
-  size_t cache_bytes = 0;
-  gdn_status st = attn_shape(fn, shape, cache, &a.cache, &cache_bytes);
-  if (st != GDN_OK) return st;
-  const gdn_attn_shape &s = *shape;
-  if (s.n_seqs == 0 || s.T == 0) return GDN_OK;
-  const size_t e = a.cache.bf16 ? 2 : 4, rows = (size_t)s.n_seqs * s.T * s.H;
-  const size_t need = gdn::attn_workspace_size(a.cache, s.n_seqs, s.T, s.H, s.max_pages);
-  const Buf in[] = {{"q", q, e * rows * a.cache.D},
-                    {"k_cache", k_cache, cache_bytes},
-                    {"v_cache", v_cache, cache_bytes},
-                    {"page_table", page_table, 4 * (size_t)s.n_seqs * s.max_pages},
-                    {"lens", lens, 4 * (size_t)s.n_seqs}};
-  const Buf outs[] = {{"out", out, e * rows * a.cache.D}, {"workspace", workspace, need}};
-  for (const Buf &b : in) {
-    // no pages: every sequence is empty, and nothing of them is read
-    if (!b.p && !(b.bytes == 0 && &b != &in[0]))
-      return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, b.name);
-    if ((st = check_aligned(fn, b)) != GDN_OK) return st;
-  }
-  for (const Buf &o : outs) {
-    if (!o.p) return fail(GDN_ERR_INVALID_ARG, "%s: %s is NULL", fn, o.name);
-    if ((st = check_aligned(fn, o)) != GDN_OK) return st;
-    for (const Buf &b : in)
-      if ((st = check_apart(fn, o, b)) != GDN_OK) return st;
-  }
-  if ((st = check_apart(fn, outs[0], outs[1])) != GDN_OK) return st;
-  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-    return fail(GDN_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
-  if (workspace_bytes < need)
-    return fail(GDN_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes,
-                need);
-  if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;
-  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
-  a.table = page_table; a.lens = lens; a.out = out; a.workspace = workspace;
-  a.n_seqs = s.n_seqs; a.T = s.T; a.H = s.H; a.max_pages = s.max_pages;
-  a.grouped = s.kv_map == GDN_QK_GROUPED;
-  a.scale = s.scale != 0.f ? s.scale : 1.0f / std::sqrt((float)a.cache.D);
+  const gdn_status st =
+      attn_args("gdn_paged_attention", shape, cache, q, k_cache, v_cache, page_table, lens, out,
+                workspace, workspace_bytes, gdn::attn_workspace_size, a);
+  if (st != GDN_OK || a.n_seqs == 0 || a.T == 0) return st;
   return check_launch(gdn::launch_paged_attention(a, reinterpret_cast<cudaStream_t>(stream)),
                       "gdn_paged_attention launch");
+}
+
+size_t gdn_tree_attention_workspace_size(const gdn_attn_shape *shape, const gdn_kv_cache *cache) {
+  const char *fn = "gdn_tree_attention_workspace_size";
+  gdn::KvLayout l;
+  size_t cache_bytes = 0;
+  if (attn_shape(fn, shape, cache, &l, &cache_bytes) != GDN_OK) return 0;
+  if (tree_shape(fn, shape) != GDN_OK || shape->n_seqs == 0 || shape->T == 0) return 0;
+  return gdn::tree_attn_workspace_size(l, shape->n_seqs, shape->T, shape->H, shape->max_pages);
+}
+
+gdn_status gdn_tree_attention(const gdn_attn_shape *shape, const gdn_kv_cache *cache,
+                              const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *page_table, const int32_t *lens,
+                              const int32_t *n_nodes, const uint64_t *tree, void *out,
+                              void *workspace, size_t workspace_bytes, gdn_stream_t stream) {
+  const char *fn = "gdn_tree_attention";
+  gdn::AttnArgs a{};
+  gdn_status st;
+  if (shape && (st = tree_shape(fn, shape)) != GDN_OK) return st;
+  st = attn_args(fn, shape, cache, q, k_cache, v_cache, page_table, lens, out, workspace,
+                 workspace_bytes, gdn::tree_attn_workspace_size, a);
+  if (st != GDN_OK || a.n_seqs == 0 || a.T == 0) return st;
+  const size_t n = (size_t)a.n_seqs, e = a.cache.bf16 ? 2 : 4;
+  const Buf in[] = {{"tree", tree, 8 * n * a.T}, {"n_nodes", n_nodes, 4 * n}};
+  const Buf outs[] = {{"out", out, e * n * a.T * a.H * a.cache.D},
+                      {"workspace", workspace, workspace_bytes}};
+  if (!tree) return fail(GDN_ERR_INVALID_ARG, "%s: tree is NULL", fn);
+  for (const Buf &b : in) {
+    if ((st = check_aligned(fn, b)) != GDN_OK) return st;
+    for (const Buf &o : outs)
+      if ((st = check_apart(fn, o, b)) != GDN_OK) return st;
+  }
+  a.tree = reinterpret_cast<const unsigned long long *>(tree);
+  a.n_nodes = n_nodes;
+  return check_launch(gdn::launch_tree_attention(a, reinterpret_cast<cudaStream_t>(stream)),
+                      "gdn_tree_attention launch");
 }
 
 }  // extern "C"

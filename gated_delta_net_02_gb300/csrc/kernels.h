@@ -144,9 +144,14 @@ struct AttnArgs {
   bool grouped;                 // query head h reads kv head h / (H / H_kv), else h % H_kv
   float scale;
   int *err;
+  // trees only
+  const int32_t *n_nodes = nullptr;         // [n_seqs] or NULL
+  const unsigned long long *tree = nullptr; // [n_seqs][T]
 };
 size_t attn_workspace_size(const KvLayout &c, int n_seqs, int T, int H, int max_pages);
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream);
+size_t tree_attn_workspace_size(const KvLayout &c, int n_seqs, int T, int H, int max_pages);
+cudaError_t launch_tree_attention(const AttnArgs &a, cudaStream_t stream);
 
 // The delta rule along a tree of drafted tokens; see tree_delta.cu.
 struct TreeDeltaArgs {

@@ -155,6 +155,12 @@ lib.gdn_paged_attention.restype = _st
 lib.gdn_paged_attention.argtypes = [ctypes.POINTER(gdn_attn_shape),
                                     ctypes.POINTER(gdn_kv_cache), _vp, _vp, _vp, _vp, _vp, _vp,
                                     _vp, ctypes.c_size_t, _vp]
+lib.gdn_tree_attention_workspace_size.restype = ctypes.c_size_t
+lib.gdn_tree_attention_workspace_size.argtypes = lib.gdn_paged_attention_workspace_size.argtypes
+lib.gdn_tree_attention.restype = _st
+lib.gdn_tree_attention.argtypes = [ctypes.POINTER(gdn_attn_shape), ctypes.POINTER(gdn_kv_cache),
+                                   _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                                   _vp]
 lib.gdn_tree_forward.restype = _st
 lib.gdn_tree_forward.argtypes = [ctypes.POINTER(gdn_shape), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                  _vp, _vp, _i, _vp]
@@ -412,6 +418,21 @@ def gdn_paged_attention(shape: gdn_attn_shape, cache: gdn_kv_cache, q, k_cache, 
         ctypes.byref(shape), ctypes.byref(cache), _addr(q), _cache_addr(k_cache, cache),
         _cache_addr(v_cache, cache), _addr(page_table), _addr(lens), _addr(out),
         _addr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def gdn_tree_attention_workspace_size(shape: gdn_attn_shape, cache: gdn_kv_cache) -> int:
+    return int(lib.gdn_tree_attention_workspace_size(ctypes.byref(shape), ctypes.byref(cache)))
+
+
+def gdn_tree_attention(shape: gdn_attn_shape, cache: gdn_kv_cache, q, k_cache, v_cache, page_table,
+                       lens, n_nodes, tree, out, workspace, workspace_bytes: int,
+                       stream=None) -> None:
+    """Attention of a tree of drafted tokens of each sequence over its pages;
+    `tree`: an int64 (or uint64) tensor of the words, n_nodes may be None."""
+    _check(lib.gdn_tree_attention(
+        ctypes.byref(shape), ctypes.byref(cache), _addr(q), _cache_addr(k_cache, cache),
+        _cache_addr(v_cache, cache), _addr(page_table), _addr(lens), _addr(n_nodes), _addr(tree),
+        _addr(out), _addr(workspace), int(workspace_bytes), _stream(stream)))
 
 
 def gdn_tree_forward(shape: gdn_shape, q, k, v, g, beta, state_in, n_nodes, tree, out, updates,

@@ -505,7 +505,38 @@ gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const gdn_kv_cache *
  *   bit j of tree[s][t]: node j is an ancestor of node t, or t itself
  * so T is at most 64. n_nodes[s] (0 .. T) says how many of the T nodes the
  * sequence has; rows of the others are padding. n_nodes = NULL: all have T.
- *
+ * ---------------------------------------------------------------------- */
+
+/* Bytes of device workspace gdn_tree_attention needs (at most 64 MiB); 0 for
+ * arguments that it refuses. Depends on the shapes alone. */
+size_t gdn_tree_attention_workspace_size(const gdn_attn_shape *shape, const gdn_kv_cache *cache);
+
+/*
+ * Attention of the nodes over the sequence's pages. The sequence has lens[s]
+ * tokens in the cache, its m = n_nodes[s] nodes being the last of them (node j is
+ * token lens[s] - m + j: appended by gdn_rope_append or gdn_qknorm_rope_append
+ * with the positions that the nodes' depths give). Node t sees all tokens
+ * before the nodes, and those nodes that its word names:
+ *   out = sum_j softmax_j(scale q . k_j) v_j
+ * Any words are taken, a node without its own bit among them; a row that sees
+ * no key is 0, as are the rows of padding, whose q and words are not used.
+ * Bits from m on are ignored. With lens[s] < m the first m - lens[s] nodes have
+ * no key. Statistics, sums and the use of a NaN or infinity
+ * in v of one of the nodes (it reaches all rows of its sequence) are as in
+ * gdn_paged_attention, and so are all arguments but
+ * n_nodes     device int32 [n_seqs] (0 .. T), or NULL
+ * tree        device uint64 [n_seqs][T]
+ * shape->T    nodes of each sequence, at most 64
+ * n_nodes out of range is cut to it and reported as GDN_ERR_DEVICE_ARG by
+ * gdn_check_device_error.
+ */
+gdn_status gdn_tree_attention(const gdn_attn_shape *shape, const gdn_kv_cache *cache,
+                              const void *q, const void *k_cache, const void *v_cache,
+                              const int32_t *page_table, const int32_t *lens,
+                              const int32_t *n_nodes, const uint64_t *tree, void *out,
+                              void *workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/*
  * The gated delta rule along every branch: with S_p the state after node t's
  * parent (state_in for a node without one), node t has
  *   S = decay(S_p), d = beta (v - S^T k), S <- S + k d^T, o = scale S^T q
@@ -514,9 +545,6 @@ gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const gdn_kv_cache *
  * state that is wanted from the d once a branch is accepted. All products and
  * sums are as exact as fp32 ones, for bf16 inputs too; any gate is computed,
  * -inf included.
- * ---------------------------------------------------------------------- */
-
-/*
  * shape       as gdn_forward, T = nodes of each sequence, at most 64
  * q, k, v, g, beta, state_in  as gdn_forward (token s*T+t is node t)
  * n_nodes     device int32 [n_seqs], or NULL
@@ -528,7 +556,8 @@ gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const gdn_kv_cache *
  * node's bit, an ancestor whose own ancestors differ) are reported as
  * GDN_ERR_DEVICE_ARG by gdn_check_device_error, and that sequence's rows are
  * not written. out and updates overlap each other and the inputs nowhere, nor any
- * state_in[s] (not checked).
+ * state_in[s] (not checked). With n_seqs = 0 or T = 0 this call and the next
+ * do nothing.
  */
 gdn_status gdn_tree_forward(const gdn_shape *shape, const void *q, const void *k, const void *v,
                             const float *g, const float *beta, const float *const *state_in,

@@ -150,3 +150,47 @@ def test_tree_calls_of_nothing(gdn):
 def test_device_error_of_a_bad_tree(gdn):
     st, msg = gdn.gdn_decode_device_error(7)
     assert st == gdn.GDN_ERR_DEVICE_ARG and "tree" in msg
+
+
+def tree_attend(gdn, shape=None, cache=None, nbytes=1 << 23, **kw):
+    sh = dict(n_seqs=3, T=2, H=8, max_pages=4, scale=0.0, kv_map=1)
+    sh.update(shape or {})
+    p = {n: FAKE + i * STEP for i, n in enumerate(
+        ("q", "k_cache", "v_cache", "page_table", "lens", "n_nodes", "tree", "out", "workspace"))}
+    p.update(kw)
+    gdn.gdn_tree_attention(gdn.gdn_attn_shape(*(sh[f[0]] for f in gdn.gdn_attn_shape._fields_)),
+                           kv(gdn, **(cache or {})), *p.values(), nbytes)
+
+
+@pytest.mark.parametrize("cache,status", BAD_CACHES)
+def test_tree_attention_refuses_caches(gdn, cache, status):
+    st, msg = refused(gdn, lambda: tree_attend(gdn, cache=cache))
+    assert st == status and "gdn_tree_attention" in msg
+    assert gdn.gdn_tree_attention_workspace_size(gdn.gdn_attn_shape(3, 2, 8, 4, 0.0, 1),
+                                                 kv(gdn, **cache)) == 0
+
+
+@pytest.mark.parametrize("shape,status", [
+    (dict(n_seqs=-1), 1), (dict(T=-1), 1), (dict(H=0), 1), (dict(H=3), 1), (dict(max_pages=-1), 1),
+    (dict(kv_map=2), 1), (dict(scale=float("inf")), 1), (dict(n_seqs=1 << 28), 2), (dict(T=65), 2)])
+def test_tree_attention_refuses_shapes(gdn, shape, status):
+    st, msg = refused(gdn, lambda: tree_attend(gdn, shape))
+    assert st == status and "gdn_tree_attention" in msg
+
+
+@pytest.mark.parametrize("ptrs,word", [
+    (dict(q=0), "q is NULL"), (dict(tree=0), "tree is NULL"), (dict(workspace=0), "workspace is"),
+    (dict(tree=FAKE + 6 * STEP + 8), "tree is not 16-byte"),
+    (dict(n_nodes=FAKE + 5 * STEP + 4), "n_nodes is not 16-byte"),
+    (dict(out=FAKE + 6 * STEP), "out overlaps tree"), (dict(out=FAKE + 5 * STEP), "out overlaps n_nodes"),
+    (dict(workspace=FAKE + 6 * STEP), "workspace overlaps tree"), (dict(nbytes=1000), "needed")])
+def test_tree_attention_refuses_buffers(gdn, ptrs, word):
+    st, msg = refused(gdn, lambda: tree_attend(gdn, **ptrs))
+    assert st == gdn.GDN_ERR_INVALID_ARG and word in msg
+
+
+def test_tree_attention_of_nothing(gdn):
+    tree_attend(gdn, dict(n_seqs=0), q=0)
+    tree_attend(gdn, dict(T=0), tree=0)
+    assert gdn.lib.gdn_tree_attention(None, None, *[0] * 11) == gdn.GDN_ERR_INVALID_ARG
+    assert gdn.gdn_tree_attention_workspace_size(gdn.gdn_attn_shape(3, 65, 8, 4, 0.0, 1), kv(gdn)) == 0
