@@ -257,7 +257,6 @@ gdn_status attn_args(const char *fn, const gdn_attn_shape *shape, const gdn_kv_c
   if (workspace_bytes < need)
     return fail(GDN_ERR_INVALID_ARG, "%s: workspace %zu bytes < %zu needed", fn, workspace_bytes,
                 need);
-  if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
   a.table = page_table; a.lens = lens; a.out = out; a.workspace = workspace;
   a.H = s.H; a.max_pages = s.max_pages;
@@ -424,10 +423,11 @@ gdn_status gdn_paged_attention(const gdn_attn_shape *shape, const gdn_kv_cache *
                                const int32_t *page_table, const int32_t *lens, void *out,
                                void *workspace, size_t workspace_bytes, gdn_stream_t stream) {
   gdn::AttnArgs a{};
-  const gdn_status st =
+  gdn_status st =
       attn_args("gdn_paged_attention", shape, cache, q, k_cache, v_cache, page_table, lens, out,
                 workspace, workspace_bytes, gdn::attn_workspace_size, a);
   if (st != GDN_OK || a.n_seqs == 0 || a.T == 0) return st;
+  if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;
   return check_launch(gdn::launch_paged_attention(a, reinterpret_cast<cudaStream_t>(stream)),
                       "gdn_paged_attention launch");
 }
@@ -463,6 +463,7 @@ gdn_status gdn_tree_attention(const gdn_attn_shape *shape, const gdn_kv_cache *c
     for (const Buf &o : outs)
       if ((st = check_apart(fn, o, b)) != GDN_OK) return st;
   }
+  if ((st = device_err_ptr(&a.err)) != GDN_OK) return st;
   a.tree = reinterpret_cast<const unsigned long long *>(tree);
   a.n_nodes = n_nodes;
   return check_launch(gdn::launch_tree_attention(a, reinterpret_cast<cudaStream_t>(stream)),
