@@ -8,18 +8,20 @@
 // Bound by HBM: a row is read once; a cluster of up to 8 blocks holds it in
 // shared memory and makes all further passes there.
 //  * Masses decide between tokens by whole numbers: a weight is an integer in
-//    units of 2^-44 of the largest (an error of about one unit of 2^-40, of
-//    fp32 pairs and a table of 2^(-i/256)), so a sum has the same value in any
-//    order, and with it the token. Tokens below 2^-45 of the largest have
-//    mass 0.
+//    units of 2^-44 of (about) the largest, so a sum has the same value in any
+//    order, and with it the token. Logits lie on a grid of 2^-8 to 2^-7 octaves of
+//    weight; a weight is the product of two table entries for its grid point and
+//    a polynomial for the rest, in 32-bit mantissas: some 2^-30 of itself off.
+//    Tokens below 2^-45 of the largest have mass 0.
 //  * The order is never made. The last kept value is found by histograms:
-//    16 bins an octave of weight first, then the bin's values by their ordered
+//    16 grid points a bin first, then the bin's values by their ordered
 //    bits, 1024 bins at a time, until a bin is one value. Of the tokens with
 //    that value the lowest indexes are kept.
-//  * The top-p mass needs weights of the whole row. The first histogram adds 12
-//    bits of each (32-bit atomics), which bounds the masses well enough to leave
-//    some neighbouring bins; their masses and all before them are then added
-//    exactly.
+//  * The first histogram of masses adds a weight as three numbers of 16 bits,
+//    by 32-bit atomics that are skipped where they are 0, as the upper ones
+//    mostly are; one 64-bit addition to shared memory is a loop.
+//  * A bin is looked for in sums of 32 bins first, then in those 32: blocks read
+//    one another's shared memory slowly (all bins by all blocks took 6 us).
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -32,11 +34,12 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMostBlocks = 8;       // of a cluster
 constexpr int kBins = 1024;          // of a histogram; two of each thread
 constexpr int kSms = 152;
-constexpr int kOne = 44;             // log2 of the largest weight
-constexpr float kOctaves = 45.f;     // weights below 2^-45 are 0
-constexpr int kGroups = 32;          // pieces of a warp's share with a mass of their own
+constexpr float kOctaves = 44.9f;     // further down, weights are 0
+constexpr int kGroups = 16;          // pieces of a warp's share with a mass of their own
+constexpr int kFine = 64, kCoarse = 184;  // table entries: 45 octaves x 256 points, by 64
 
 struct SampleParams {
   const void *logits;
@@ -48,33 +51,14 @@ struct SampleParams {
   int rows, vocab;
 };
 
-// 2^(40 - i / 256), rounded.
-struct PowTable {
-  u64 v[256];
-  constexpr PowTable() : v() {
-    for (int i = 0; i < 256; ++i) {
-      const double x = -0.69314718055994530942 * i / 256;
-      double term = 1, sum = 1;
-      for (int n = 1; n < 30; ++n) {
-        term *= x / n;
-        sum += term;
-      }
-      v[i] = (u64)(sum * 1099511627776.0 + 0.5);
-    }
-  }
-};
-__device__ constexpr PowTable kPow{};
-
-// A float's bits in the order of the values, +0 and -0 the same (canon()).
+// A float's bits in the order of the values, +0 and -0 the same.
 __device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t b = __float_as_uint(x);
+  const uint32_t b = __float_as_uint(x + 0.f);
   return b ^ ((int)b < 0 ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k ^ ((int)k < 0 ? 0x80000000u : 0xffffffffu));
 }
-// NaN counts as -inf, -0 as +0.
-__device__ __forceinline__ float canon(float x) { return x == x ? x + 0.f : -INFINITY; }
 
 __device__ __forceinline__ u64 ld_cluster_u64(const void *local, uint32_t rank) {
   u64 v;
@@ -105,44 +89,59 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {  // inclusive
   return v;
 }
 
-// Weights of a row. y = log2(1 / weight), as the sum of two floats.
-struct Scale {
-  float top, c_hi, c_lo;  // log2(e) / temperature
-  // the high part of y: the same for equal logits, and never smaller for a
-  // smaller one
-  __device__ __forceinline__ float y_of(float x) const {
-    if (top == INFINITY) return x == top ? 0.f : INFINITY;
-    return (top - x) * c_hi;
+// The row's grid of logits. Its step is the power of two that makes 2^-8 to 2^-7
+// octaves; point j lies j steps below the largest logit's.
+struct Grid {
+  // A coarse entry: 2^(-64 j steps) as mantissa, and the factors that take a
+  // product of mantissas to units of 2^-44: 2^(12 - n) above, 2^(44 - n) below 2^32.
+  struct Coarse {
+    uint32_t mantissa, above, below, pad;
+  };
+  float from;      // logits less this, 0 or the largest: exact (Sterbenz) where it is not 0
+  float low;       // the lowest logit with any weight
+  float magic;     // 1.5 x 2^23 steps: adding it leaves the point in the low bits
+  int top;         // bits of the largest logit's sum
+  float ln_step;   // logits to natural logarithms of weight
+  const Coarse *coarse;
+  const uint32_t *fine;
+
+  // The point of x >= low: the same for equal logits, never smaller for a smaller one.
+  __device__ __forceinline__ int point(float x) const {
+    return top - __float_as_int(__fadd_rd(x - from, magic));
   }
-  // The weight, y < kOctaves being its high part.
-  __device__ __forceinline__ u64 weight(float x, float y, const u64 *table) const {
-    float lo = 0.f;
-    if (top != INFINITY) {
-      const float s = top - x;  // and what s is short of top - x (Knuth's two-sum)
-      const float b = s - top;
-      const float e = (top - (s - b)) + (-x - b);
-      lo = fmaf(s, c_hi, -y) + fmaf(s, c_lo, e * c_hi);
-    }
-    // y = i / 256 + r, 0 <= r < 1 / 256
-    const float t = __fadd_rd(y * 256.f, 8388608.f);
-    const int i = __float_as_int(t) & 0x7fffff;
-    const float r = fmaf(t - 8388608.f, -1.f / 256, y);
-    // 1 - 2^-(r + lo) = z + (rest): z = r ln 2 with its error
-    const float ln2 = 0.693147182464599609375f, ln2_lo = -1.904654299957767e-9f;
-    const float z = r * ln2;
-    const float rr = r + lo;
-    const float q = rr * rr * (0.24022651f - rr * (0.055504109f - rr * 0.0096181291f));
-    const float rest = fmaf(r, ln2, -z) + fmaf(r, ln2_lo, fmaf(lo, ln2, -q));
-    const uint32_t u = (uint32_t)(int)__float2uint_rn(z * 1099511627776.f) +
-                       (uint32_t)__float2int_rn(rest * 1099511627776.f);
-    const u64 p = table[i & 255];
-    const uint32_t p32 = p >> 40 ? 0xffffffffu : (uint32_t)(p >> 8);
-    const int n = i >> 8;
-    // r + lo below 0 is a weight just above the table's (|lo| ln 2 < 1e-5)
-    const u64 w = z < 1e-4f && (int)u < 0 ? p + __umulhi(p32, 0u - u) : p - __umulhi(p32, u);
-    return ((w << 4) + ((1ull << n) >> 1)) >> n;
+  // The weight of x >= low, and its point.
+  __device__ __forceinline__ u64 weight(float x, int &j) const {
+    const float d = x - from, sum = __fadd_rd(d, magic);
+    j = top - __float_as_int(sum);
+    const float t = (d - (sum - magic)) * ln_step;  // 0 <= t < 2^-7.5, from an exact rest
+    const Coarse c = coarse[j >> 6];
+    const uint32_t m = __umulhi(c.mantissa, fine[j & 63]);
+    // e^t - 1
+    const float e = fmaf(t * t, fmaf(t, 1.f / 6, 0.5f), t);
+    const uint32_t v = m + __umulhi(m, __float2uint_rn(e * 4294967296.f));
+    return (u64)v * c.above + (((u64)v * c.below + 0x80000000u) >> 32);
+  }
+  __device__ __forceinline__ u64 weight(float x) const {
+    int j;
+    return weight(x, j);
   }
 };
+
+// Positive numbers below 1 as 64-bit fractions and powers of two: value
+// fraction 2^-64 2^-shift, the fraction's top bit set.
+struct Small {
+  u64 fraction;
+  int shift;
+};
+__device__ __forceinline__ Small operator*(Small a, Small b) {
+  u64 f = __umul64hi(a.fraction, b.fraction);
+  int n = a.shift + b.shift;
+  if (!(f >> 63)) {
+    f <<= 1;
+    ++n;
+  }
+  return Small{f, n};
+}
 
 template <typename T>
 struct Vec {
@@ -174,19 +173,32 @@ struct Vec {
 };
 
 struct Shared {
-  u64 table[256];
-  u64 mass[2][kBins];      // two histograms in turn, so that one is cleared
-  uint32_t count[2][kBins];  // while the other is read by the cluster
-  u64 part[2];             // this block's sums of two passes
+  Grid::Coarse coarse[kCoarse];
+  uint32_t fine[kFine];
+  // two histograms in turn, so that one is cleared while the other is read: the
+  // tokens of a bin, and their mass in three parts (in `wide` and `more`) or as one
+  // number, with the bin's largest key in `more`
+  struct Histogram {
+    alignas(16) union {
+      u64 mass[kBins];
+      uint32_t part[2][kBins];
+    } wide;
+    uint32_t count[kBins], more[kBins];
+  } hist[2];
+  u64 group[2][32];        // sums of 32 bins
+  Small power[14];         // 2^(-2^k steps)
   u64 warp_part[kWarps], warp_part2[kWarps];
   u64 seg_mass[kWarps][kGroups];
   uint32_t seg_ties[kWarps][kGroups];
-  u64 warp_mass[kWarps];
-  uint32_t warp_ties[kWarps];
-  float top;
+  alignas(16) u64 warp_mass[kWarps];
+  u64 warp_kept[kWarps];
+  alignas(16) uint32_t warp_ties[kWarps];
+  float top, step, ln_step;
+  float depth;             // logits from the largest to weight 0
+  double min_drop;         // temperature * log(min_p)
   float warp_top[kWarps];
-  int found[4];
-  u64 found64[4];
+  int found;
+  u64 before, there, goal, total;
 };
 
 // A row's share of one block, and the passes over it.
@@ -198,64 +210,44 @@ struct Share {
   int v0, v1;        // this warp's vectors, counted from `row`
   uint4 *own;        // this warp's place in shared memory
 
-  __device__ __forceinline__ Vec<T> fetch(int v) const {
+  // A vector of the row's ends: what is not of the row is -inf.
+  __device__ __forceinline__ Vec<T> fetch_end(int v) const {
     const T *p = row + (long long)v * VE;
     const int e0 = v * VE - before;  // index of the first element
-    if (e0 >= 0 && e0 + VE <= cols) {
-      Vec<T> x(__ldg(reinterpret_cast<const uint4 *>(p)));
-#pragma unroll
-      for (int i = 0; i < VE; ++i) x.v[i] = canon(x.v[i]);
-      return x;
-    }
     Vec<T> x(make_uint4(0, 0, 0, 0));
 #pragma unroll
     for (int i = 0; i < VE; ++i)
-      x.v[i] = e0 + i >= 0 && e0 + i < cols ? canon(to_f32(p[i])) : -INFINITY;
+      x.v[i] = e0 + i >= 0 && e0 + i < cols ? to_f32(p[i]) : -INFINITY;
     return x;
+  }
+  // The share to shared memory: whole vectors by asynchronous copies, all of
+  // them under way at once; each lane's are those that it reads later.
+  __device__ __forceinline__ void load() const {
+    const uint4 *p = reinterpret_cast<const uint4 *>(row);
+    const int lane = threadIdx.x & 31;
+    const int f0 = max(v0, before ? 1 : 0), f1 = min(v1, (before + cols) / VE);
+    for (int v = v0 + lane; v < v1; v += 32) {
+      if (v >= f0 && v < f1)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(own + (v - v0))),
+                     "l"(p + v)
+                     : "memory");
+      else
+        own[v - v0] = fetch_end(v).pack();
+    }
   }
   __device__ __forceinline__ Vec<T> get(int v) const { return Vec<T>(own[v - v0]); }
   template <class F>
+  __device__ __forceinline__ void each_vector(F f) const {
+    for (int v = v0 + (threadIdx.x & 31); v < v1; v += 32) f(get(v));
+  }
+  template <class F>
   __device__ __forceinline__ void each(F f) const {
-    for (int v = v0 + (threadIdx.x & 31); v < v1; v += 32) {
-      const Vec<T> x = get(v);
+    each_vector([&](const Vec<T> &x) {
 #pragma unroll
       for (int i = 0; i < VE; ++i) f(x.v[i]);
-    }
+    });
   }
 };
-
-// Sum of `mine` over the block's threads into part[i], for the cluster to read
-// behind its next barrier.
-__device__ __forceinline__ void block_part(Shared &sh, int i, u64 mine) {
-  mine = warp_sum(mine);
-  if ((threadIdx.x & 31) == 0) sh.warp_part[threadIdx.x >> 5] = mine;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    u64 sum = 0;
-    for (int w = 0; w < kWarps; ++w) sum += sh.warp_part[w];
-    sh.part[i] = sum;
-  }
-}
-
-// Block-wide inclusive scan of two numbers of each thread: the sums before the
-// thread's own in *a and *b.
-__device__ __forceinline__ void block_scan(Shared &sh, u64 &a, u64 &b) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const u64 sa = warp_scan(a), sb = warp_scan(b);
-  __syncthreads();
-  if (lane == 31) {
-    sh.warp_part[warp] = sa;
-    sh.warp_part2[warp] = sb;
-  }
-  __syncthreads();
-  u64 ba = 0, bb = 0;
-  for (int w = 0; w < warp; ++w) {
-    ba += sh.warp_part[w];
-    bb += sh.warp_part2[w];
-  }
-  a = ba + sa - a;
-  b = bb + sb - b;
-}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -269,11 +261,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % blocks;
   const long long r = blockIdx.x / blocks;
-  for (int i = tid; i < kBins; i += kThreads) {
-    sh.mass[0][i] = sh.mass[1][i] = 0;
-    sh.count[0][i] = sh.count[1][i] = 0;
-  }
-  if (tid < 256) sh.table[tid] = kPow.v[tid];
+  auto clear = [&](int b) {
+    for (int i = tid; i < (int)sizeof(sh.hist[b]) / 16; i += kThreads)
+      reinterpret_cast<uint4 *>(&sh.hist[b])[i] = make_uint4(0, 0, 0, 0);
+  };
+  clear(0);
+  clear(1);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   Share<T> share;
@@ -293,14 +286,59 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float u = p.uniform[r];
 
   // ---- the row arrives; its maximum
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int v = share.v0 + lane; v < share.v1; v += 32) {
-    const Vec<T> x = share.fetch(v);
+  share.load();
+  // 64-bit floating point is two operations a cycle of an SM, and slow to
+  // return: where it is needed, one thread does it.
+  if (tid == 0) {
+    // octaves of weight for each unit of logit, log2(e) / temperature, as the sum
+    // of two floats; steps stay inside fp32's range
+    const float t = fminf(fmaxf(temperature, 1e-30f), 3e33f);
+    const float c = 1.442695041f / t;
+    const float c_lo = (fmaf(-c, t, 1.442695041f) + 1.925963033e-8f) / t;
+    const int e = (__float_as_int(c) >> 23) - 127;
+    sh.step = __int_as_float((127 - 8 - e) << 23);
+    sh.ln_step = c * 0.693147181f;
+    sh.depth = kOctaves / c;
+    // octaves of a step (2^-8 to 2^-7), then x = their natural logarithm's size, in
+    // units of 2^-64; 2^-step = e^-x by its series
+    const u64 octaves = ((u64)(__float_as_int(c) & 0x7fffff | 0x800000) << 33) +
+                        (u64)(long long)(c_lo * sh.step * 18446744073709551616.f);
+    const u64 x = __umul64hi(octaves, 0xb17217f7d1cf79acull);
+    u64 sum = ~0ull / 720;
 #pragma unroll
-    for (int i = 0; i < VE; ++i) top = fmaxf(top, x.v[i]);
-    share.own[v - share.v0] = x.pack();
+    for (int n = 5; n >= 1; --n) {
+      u64 inverse = ~0ull;  // 1 / n!
+      for (int i = 2; i <= n; ++i) inverse /= i;
+      sum = inverse - __umul64hi(x, sum);
+    }
+    Small power{0ull - __umul64hi(x, sum), 0};
+    for (int k = 0; k < 14; ++k) {
+      sh.power[k] = power;
+      power = power * power;
+    }
   }
+  if (tid == kThreads - 1 && min_p > 0.f)
+    sh.min_drop = (double)fminf(temperature, 3e33f) * log((double)min_p);
+  __syncthreads();
+  if (tid < kCoarse + kFine) {
+    const int i = tid < kCoarse ? tid * kFine : tid - kCoarse;
+    Small m{~0ull, 0};
+#pragma unroll
+    for (int k = 0; k < 14; ++k)
+      if (i >> k & 1) m = m * sh.power[k];
+    // as a mantissa of up to 2^32 and 2^-n
+    const int n = m.shift;
+    const uint32_t mantissa = (uint32_t)(m.fraction >> 32);
+    if (tid < kCoarse)
+      // 0.99: room for what the polynomial adds
+      sh.coarse[tid] = Grid::Coarse{__umulhi(mantissa, 4252017623u), n <= 12 ? 1u << (12 - n) : 0u,
+                                    n > 12 && n <= 44 ? 1u << (44 - n) : 0u, 0u};
+    else
+      sh.fine[tid - kCoarse] = mantissa >> n;  // n = 0 or 1
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  float top = -INFINITY;
+  share.each([&](float x) { top = fmaxf(top, x); });
 #pragma unroll
   for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
   if (lane == 0) sh.warp_top[warp] = top;
@@ -310,10 +348,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     sh.top = top;
   }
   cluster_sync();
-  for (int k = 0; k < blocks; ++k) {
-    const float other = __uint_as_float(ld_cluster_u32(&sh.top, k));
-    top = k == 0 ? other : fmaxf(top, other);
-  }
+  top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < kMostBlocks; ++k)
+    if (k < blocks) top = fmaxf(top, __uint_as_float(ld_cluster_u32(&sh.top, k)));
   if (top == -INFINITY) {  // nothing to choose from
     if (rank == 0 && tid == 0) {
       p.tokens[r] = -1;
@@ -322,219 +360,217 @@ __global__ void __launch_bounds__(kThreads, 2)
     cluster_sync();
     return;
   }
-  Scale sc;
+  if (top == INFINITY) {  // tokens at infinity share all of the mass
+    for (int v = share.v0 + lane; v < share.v1; v += 32) {
+      Vec<T> x = share.get(v);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) x.v[i] = x.v[i] == INFINITY ? 0.f : -INFINITY;
+      share.own[v - share.v0] = x.pack();
+    }
+    top = 0.f;
+  }
+  Grid grid;
   {
-    sc.top = top;
-    const double c = temperature > 0.f ? fmin(1.4426950408889634074 / (double)temperature, 1e30) : 0.;
-    sc.c_hi = (float)c;
-    sc.c_lo = (float)(c - (double)sc.c_hi);
+    // far from 0, fp32 has no room for the grid beside the logit's own size;
+    // less the largest, all that have weight are exact
+    grid.from = fabsf(top) > 32.f * sh.depth ? top : 0.f;
+    grid.magic = 12582912.f * sh.step;
+    grid.low = top - sh.depth;
+    grid.top = __float_as_int(__fadd_rd(top - grid.from, grid.magic));
+    grid.ln_step = sh.ln_step;
+    grid.coarse = sh.coarse;
+    grid.fine = sh.fine;
   }
 
-  // What is kept: keys above `cut`, and the first `ties` tokens at it.
-  uint32_t cut = 0;
+  // What is kept: logits above `cut`, and the first `ties` tokens at it.
+  float cut = -INFINITY;
   u64 ties = 0;
   int buf = 0;  // histogram in use
-  // A pass's barrier. Whoever is behind it has read the histogram before,
-  // which is cleared for the pass after (block_scan's barriers come between).
-  auto pass_done = [&] {
+  auto bin_of = [&](float x) { return grid.point(x) >> 4; };
+
+  // The end of a pass that filled a histogram: value(bin) is what is looked for
+  // in it. Whoever is behind the cluster's barrier has read the histogram
+  // before, which is cleared for the pass after.
+  auto pass_done = [&](auto value) {
+    __syncthreads();
+    u64 sum = value(sh.hist[buf], 2 * tid) + value(sh.hist[buf], 2 * tid + 1);
+#pragma unroll
+    for (int off = 8; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if ((lane & 15) == 0) sh.group[buf][tid >> 4] = sum;
     cluster_sync();
-    for (int i = tid; i < kBins; i += kThreads) {
-      sh.mass[buf ^ 1][i] = 0;
-      sh.count[buf ^ 1][i] = 0;
+    clear(buf ^ 1);
+  };
+  // Finds the bin where the running value, `have` before the first, first reaches
+  // want(sum of all): one warp, first in the groups of 32 bins, then in one. far(k, bin)
+  // reads block k's. Leaves sh.found (-1: none), sh.before it, and sh.goal = want.
+  auto search = [&](u64 have, auto want_of, auto far) {
+    if (warp == 0) {
+      u64 x = 0;
+#pragma unroll
+      for (int k = 0; k < kMostBlocks; ++k)
+        if (k < blocks) x += ld_cluster_u64(&sh.group[buf][lane], k);
+      u64 end = have + warp_scan(x);
+      const u64 total = __shfl_sync(0xffffffffu, end, 31);
+      const u64 want = want_of(total);
+      uint32_t at = __ballot_sync(0xffffffffu, end - x < want && want <= end);
+      int found = -1;
+      u64 before = 0;
+      if (at) {
+        const int g = __ffs(at) - 1;
+        before = __shfl_sync(0xffffffffu, end - x, g);
+        x = 0;
+#pragma unroll
+        for (int k = 0; k < kMostBlocks; ++k)
+          if (k < blocks) x += far(k, g * 32 + lane);
+        end = before + warp_scan(x);
+        at = __ballot_sync(0xffffffffu, end - x < want && want <= end);
+        const int i = __ffs(at) - 1;
+        before = __shfl_sync(0xffffffffu, end - x, i & 31);
+        found = g * 32 + i;
+      }
+      if (lane == 0) {
+        sh.found = found;
+        sh.before = before;
+        sh.goal = want;
+        sh.total = total;
+      }
     }
+    __syncthreads();
   };
-  auto bin_of = [&](float y) {  // 16 an octave
-    return (__float_as_int(__fadd_rd(y * 16.f, 8388608.f)) & 0x7fffff);
+  auto count_in = [](const Shared::Histogram &h, int i) -> u64 { return h.count[i]; };
+  auto mass_in = [](const Shared::Histogram &h, int i) -> u64 { return h.wide.mass[i]; };
+  auto parts_in = [](const Shared::Histogram &h, int i) -> u64 {
+    return h.more[i] + ((u64)h.wide.part[0][i] << 16) + ((u64)h.wide.part[1][i] << 32);
   };
-  // A key range that holds every value of bins b0 .. b1, by a margin.
-  auto range_of = [&](int b0, int b1, uint32_t &khi, uint32_t &klo) {
-    if (sc.top == INFINITY || sc.c_hi == 0.f) {
-      khi = key_of(top);
-      klo = sc.top == INFINITY ? khi : 0;
-    } else {
-      const float near = b0 / 16.f / sc.c_hi, far = (b1 + 1) / 16.f / sc.c_hi;
-      const float margin = 1e-5f * (fabsf(top) + far);
-      const float hi = top - near + margin, lo = top - far - margin;
-      khi = min(key_of(canon(hi)), key_of(top));
-      klo = lo > -INFINITY ? key_of(canon(lo)) : 0;
-    }
-    khi >>= kLow;
-    klo >>= kLow;
+  auto far_count = [&](int k, int i) -> u64 { return ld_cluster_u32(&sh.hist[buf].count[i], k); };
+  auto far_mass = [&](int k, int i) { return ld_cluster_u64(&sh.hist[buf].wide.mass[i], k); };
+  auto far_parts = [&](int k, int i) {
+    return ld_cluster_u32(&sh.hist[buf].more[i], k) +
+           ((u64)ld_cluster_u32(&sh.hist[buf].wide.part[0][i], k) << 16) +
+           ((u64)ld_cluster_u32(&sh.hist[buf].wide.part[1][i], k) << 32);
   };
-  auto merged = [&](int i, u64 &count, u64 &mass) {
-    count = mass = 0;
-    for (int k = 0; k < blocks; ++k) {
-      count += ld_cluster_u32(&sh.count[buf][i], k);
-      mass += ld_cluster_u64(&sh.mass[buf][i], k);
-    }
-  };
+
   // The value at which the order's running count (BY_MASS: mass) first reaches
-  // `want`, among the values above key `above` whose first bin is b0 .. b1;
-  // `have` = what comes before those bins. Result in cut (its key); have then
-  // is what comes before that value, and *there the tokens with it.
-  auto refine = [&](bool by_mass, u64 want, uint32_t above, int b0, int b1, u64 have, u64 &there) {
-    uint32_t khi, klo;
-    range_of(b0, b1, khi, klo);
+  // `want`, among the logits above `above` in bin `bin`; `have` = what comes
+  // before that bin. Leaves the value in cut, what comes before it in sh.before
+  // and the tokens with it in sh.there.
+  auto refine = [&](bool by_mass, u64 want, float above, int bin, u64 have) {
+    // a range that holds every value of the bin, by a margin of some roundings
+    const int edge = grid.top - __float_as_int(grid.magic) - 16 * bin;  // its first point, in steps
+    const float lo = fmaxf(of_key(key_of((edge - 15) * sh.step + grid.from) - 8), grid.low);
+    const float hi = fminf(of_key(key_of((edge + 1) * sh.step + grid.from) + 8), top);
+    uint32_t khi = key_of(hi) >> kLow, klo = key_of(lo) >> kLow;
     for (;;) {
       int shift = 0;
       while ((khi - klo) >> shift >= (uint32_t)kBins) ++shift;
       share.each([&](float x) {
-        const float y = sc.y_of(x);
-        const uint32_t key = key_of(x), k = key >> kLow;
-        if (!(y < kOctaves) || key <= above || k > khi || k < klo) return;
-        const int b = bin_of(y);
-        if (b < b0 || b > b1) return;
+        if (!(x >= lo) || !(x <= hi)) return;
+        const uint32_t k = key_of(x) >> kLow;
+        if (bin_of(x) != bin || !(x > above) || k > khi || k < klo) return;
         const int i = (int)((khi - k) >> shift);
-        atomicAdd(&sh.count[buf][i], 1u);
-        if (by_mass) atomicAdd(&sh.mass[buf][i], sc.weight(x, y, sh.table));
+        atomicAdd(&sh.hist[buf].count[i], 1u);
+        atomicMax(&sh.hist[buf].more[i], k);
+        if (by_mass) atomicAdd(&sh.hist[buf].wide.mass[i], grid.weight(x));
       });
-      pass_done();
-      u64 n[2], m[2];
-      merged(2 * tid, n[0], m[0]);
-      merged(2 * tid + 1, n[1], m[1]);
-      u64 nb = n[0] + n[1], mb = m[0] + m[1];
-      block_scan(sh, nb, mb);
-      u64 at = have + (by_mass ? mb : nb);
+      if (by_mass) {
+        pass_done(mass_in);
+        search(have, [&](u64) { return want; }, far_mass);
+      } else {
+        pass_done(count_in);
+        search(have, [&](u64) { return want; }, far_count);
+      }
+      const int i = sh.found;
+      have = sh.before;
+      // the bin's tokens, and their largest key
+      uint32_t there = 0, key = 0;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const u64 step = by_mass ? m[j] : n[j];
-        if (at < want && want <= at + step) {
-          sh.found[0] = 2 * tid + j;
-          sh.found64[0] = at;
-          sh.found64[1] = n[j];
+      for (int k = 0; k < kMostBlocks; ++k)
+        if (k < blocks) {
+          there += ld_cluster_u32(&sh.hist[buf].count[i], k);
+          key = max(key, ld_cluster_u32(&sh.hist[buf].more[i], k));
         }
-        at += step;
-      }
-      __syncthreads();
-      const int i = sh.found[0];
-      have = sh.found64[0];
-      there = sh.found64[1];
-      __syncthreads();
       buf ^= 1;
-      const uint32_t first = khi - ((uint32_t)i << shift);
-      if (shift == 0) {
-        cut = first << kLow;
-        if constexpr (kLow > 0) cut |= (int)cut < 0 ? 0u : 0xffffu;
-        return have;
+      if (shift == 0 || there == 1) {  // one value
+        key <<= kLow;
+        if constexpr (kLow > 0) key |= (int)key < 0 ? 0u : 0xffffu;
+        cut = of_key(key);
+        if (tid == 0) sh.there = there;
+        __syncthreads();
+        return;
       }
+      __syncthreads();
+      khi -= (uint32_t)i << shift;
       const uint32_t span = (1u << shift) - 1;
-      klo = first - klo > span ? first - span : klo;
-      khi = first;
+      klo = khi - klo > span ? khi - span : klo;
     }
   };
 
   const bool greedy = !(temperature > 0.f) || min_p > 1.f;
   if (greedy) {
-    cut = key_of(top);
+    cut = top;
     ties = 1;
   } else {
     if (top_k > 0 && top_k < p.vocab) {
       share.each([&](float x) {
-        const float y = sc.y_of(x);
-        if (y < kOctaves) atomicAdd(&sh.count[buf][bin_of(y)], 1u);
+        if (x >= grid.low) atomicAdd(&sh.hist[buf].count[bin_of(x)], 1u);
       });
-      pass_done();
-      u64 n[2], m[2], none = 0;
-      merged(2 * tid, n[0], m[0]);
-      merged(2 * tid + 1, n[1], m[1]);
-      u64 before = n[0] + n[1];
-      if (tid == 0) sh.found[0] = -1;
-      block_scan(sh, before, none);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (before < (u64)top_k && (u64)top_k <= before + n[j]) {
-          sh.found[0] = 2 * tid + j;
-          sh.found64[0] = before;
-        }
-        before += n[j];
-      }
-      __syncthreads();
-      const int b = sh.found[0];
-      const u64 have = sh.found64[0];
+      pass_done(count_in);
+      search(0, [&](u64) { return (u64)top_k; }, far_count);
+      const int bin = sh.found;
+      const u64 have = sh.before;
       __syncthreads();
       buf ^= 1;
-      if (b >= 0) {  // else fewer tokens than top_k have any mass
-        u64 there;
-        ties = (u64)top_k - refine(false, (u64)top_k, 0, b, b, have, there);
+      if (bin >= 0) {  // else fewer tokens than top_k have any mass
+        refine(false, (u64)top_k, cut, bin, have);
+        ties = (u64)top_k - sh.before;
       }
     }
     if (top_p < 1.f) {
-      const uint32_t above = cut;
-      u64 sum = 0;
-      share.each([&](float x) {
-        const float y = sc.y_of(x);
-        if (!(y < kOctaves) || key_of(x) <= above) return;
-        const u64 w = sc.weight(x, y, sh.table);
-        sum += w;
-        const int b = bin_of(y);
-        // 12 bits below the octave's largest
-        atomicAdd(reinterpret_cast<uint32_t *>(&sh.mass[buf][b]), (uint32_t)(w >> 1 << (b >> 4) >> 31));
-        atomicAdd(&sh.count[buf][b], 1u);
+      const float above = cut, low = fmaxf(grid.low, of_key(key_of(above) + 1));
+      share.each_vector([&](const Vec<T> &x) {
+        u64 w[VE];
+        int j[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) w[i] = grid.weight(fmaxf(x.v[i], grid.low), j[i]);
+        auto &h = sh.hist[buf];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          if (!(x.v[i] >= low)) continue;
+          const int b = j[i] >> 4;
+          atomicAdd(&h.more[b], (uint32_t)w[i] & 0xffff);
+          const uint32_t up = (uint32_t)(w[i] >> 16);
+          if (up) {
+            atomicAdd(&h.wide.part[0][b], up & 0xffff);
+            if (up >> 16) atomicAdd(&h.wide.part[1][b], up >> 16);
+          }
+        }
       });
-      block_part(sh, 0, sum);
-      pass_done();
-      u64 total = 0;
-      for (int k = 0; k < blocks; ++k) total += ld_cluster_u64(&sh.part[0], k);
-      u64 tie_weight = 0;
-      if (ties > 0) {
-        const float x = of_key(cut);
-        tie_weight = sc.weight(x, sc.y_of(x), sh.table);
-      }
-      const double goal = ceil((double)top_p * (double)(total + ties * tie_weight));
-      const u64 want = goal < 1. ? 1 : (u64)goal;
-      // the running mass of a bin's end, from below and above
-      u64 n[2], m[2], lo[2], hi[2];
-      merged(2 * tid, n[0], m[0]);
-      merged(2 * tid + 1, n[1], m[1]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int octave = (2 * tid + j) >> 4;
-        const u64 at_least = (m[j] << 32) >> octave, at_most = ((m[j] + n[j]) << 32) >> octave;
-        lo[j] = at_least > n[j] ? at_least - n[j] : 0;
-        hi[j] = n[j] ? at_most + n[j] + 1 : 0;
-      }
-      u64 before_lo = lo[0] + lo[1], before_hi = hi[0] + hi[1];
-      if (tid == 0) {
-        sh.found[0] = kBins - 1;
-        sh.found[1] = kBins - 1;
-      }
-      block_scan(sh, before_lo, before_hi);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (before_hi < want && want <= before_hi + hi[j]) sh.found[0] = 2 * tid + j;
-        if (before_lo < want && want <= before_lo + lo[j]) sh.found[1] = 2 * tid + j;
-        before_hi += hi[j];
-        before_lo += lo[j];
-      }
-      __syncthreads();
-      const int b0 = sh.found[0], b1 = sh.found[1];
+      pass_done(parts_in);
+      const u64 tie_weight = ties > 0 ? grid.weight(cut) : 0;
+      search(0, [&](u64 total) {
+        const double goal = ceil((double)top_p * (double)(total + ties * tie_weight));
+        return goal < 1. ? (u64)1 : (u64)goal;
+      }, far_parts);
+      const u64 want = sh.goal, have = sh.before, total = sh.total;
+      const int bin = sh.found;
       __syncthreads();
       buf ^= 1;
-      if (want > total) {  // among the last of the top k
-        ties = tie_weight ? min(ties, (want - total + tie_weight - 1) / tie_weight) : ties;
-      } else {
-        // what comes before the bins, exactly
-        sum = 0;
-        share.each([&](float x) {
-          const float y = sc.y_of(x);
-          if (y < kOctaves && key_of(x) > above && bin_of(y) < b0) sum += sc.weight(x, y, sh.table);
-        });
-        block_part(sh, 1, sum);
-        cluster_sync();
-        u64 have = 0, there;
-        for (int k = 0; k < blocks; ++k) have += ld_cluster_u64(&sh.part[1], k);
-        have = refine(true, want, above, b0, b1, have, there);
-        const float x = of_key(cut);
-        const u64 w = sc.weight(x, sc.y_of(x), sh.table);
-        ties = w ? min(there, (want - have + w - 1) / w) : there;
+      u64 least = want - total, each = tie_weight, most = ties;  // beyond the last of the top k
+      if (bin >= 0) {
+        refine(true, want, above, bin, have);
+        least = want - sh.before;
+        each = grid.weight(cut);
+        most = sh.there;
       }
+      ties = each ? min(most, (least + each - 1) / each) : most;
     }
-    if (min_p > 0.f && sc.top != INFINITY) {
+    if (min_p > 0.f) {
       // the smallest logit that is not below the bound
-      const float x = __double2float_ru((double)top + (double)temperature * log((double)min_p));
-      uint32_t k = min(key_of(canon(x)), key_of(top));
-      if (k > cut) {  // all of that value: what is below it goes
-        cut = k - 1;
+      if (tid == 0) sh.found = __float_as_int(__double2float_ru((double)top + sh.min_drop));
+      __syncthreads();
+      const float least = fminf(__int_as_float(sh.found), top);
+      if (least > cut) {  // all of that value: what is below it goes
+        cut = of_key(key_of(least) - 1);
         ties = 0;
       }
     }
@@ -544,23 +580,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int chunks = (warp_vecs + 31) / 32, per = (chunks + kGroups - 1) / kGroups;
   u64 cut_weight = 0;
   if (ties > 0) {
-    const float x = of_key(cut);
-    const float y = sc.y_of(x);
-    if (greedy) cut_weight = 1ull << kOne;
-    else if (y < kOctaves) cut_weight = sc.weight(x, y, sh.table);
+    if (greedy) cut_weight = 1;
+    else if (cut >= grid.low) cut_weight = grid.weight(cut);
   }
+  auto weight_of = [&](float x) -> u64 {
+    return x > cut && x >= grid.low ? grid.weight(x) : 0;
+  };
+  // a vector's mass above the cut, and its tokens at it
   auto mass_of = [&](const Vec<T> &x, bool live, u64 &mass, uint32_t &at_cut) {
     mass = 0;
     at_cut = 0;
     if (!live) return;
 #pragma unroll
     for (int i = 0; i < VE; ++i) {
-      const uint32_t key = key_of(x.v[i]);
-      at_cut += ties > 0 && key == cut;
-      if (key <= cut) continue;
-      const float y = sc.y_of(x.v[i]);
-      if (y < kOctaves) mass += sc.weight(x.v[i], y, sh.table);
+      at_cut += x.v[i] == cut;
+      if (x.v[i] > cut) mass += weight_of(x.v[i]);
     }
+    if (ties == 0) at_cut = 0;
   };
   u64 warp_total = 0;
   uint32_t warp_at_cut = 0;
@@ -576,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       mass += m;
       n += at;
     }
-    if (g * per < chunks) {
+    if (__any_sync(0xffffffffu, (uint32_t)mass | (uint32_t)(mass >> 32) | n)) {
       mass = warp_sum(mass);
       n = __reduce_add_sync(0xffffffffu, n);
     }
@@ -592,46 +628,63 @@ __global__ void __launch_bounds__(kThreads, 2)
     sh.warp_ties[warp] = warp_at_cut;
   }
   cluster_sync();
-  // every warp scans all warps' masses, 32 at a time
-  u64 run = 0, total = 0, seen = 0;
-  u64 my_before = 0, my_mass = 0, my_seen = 0;
-  for (int w0 = 0; w0 < blocks * kWarps; w0 += 32) {
-    const int w = w0 + lane;
-    u64 m = 0, n = 0;
-    if (w < blocks * kWarps) {
-      m = ld_cluster_u64(&sh.warp_mass[w % kWarps], w / kWarps);
-      n = ld_cluster_u32(&sh.warp_ties[w % kWarps], w / kWarps);
+  // one warp scans all warps' masses, four of each lane, and leaves its block's
+  if (warp == 0) {
+    static_assert(kMostBlocks * kWarps == 4 * 32, "four of each lane");
+    const int from = lane / (kWarps / 4), w = lane % (kWarps / 4) * 4;
+    u64 m[4] = {0, 0, 0, 0}, n[4] = {0, 0, 0, 0}, m_sum = 0, n_sum = 0;
+    if (from < blocks) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m[i] = ld_cluster_u64(&sh.warp_mass[w + i], from);
+        n[i] = ld_cluster_u32(&sh.warp_ties[w + i], from);
+      }
     }
-    const u64 n_scan = warp_scan(n), n_before = seen + n_scan - n;
-    const u64 kept = n_before < ties ? min(n, ties - n_before) : 0;
-    m += kept * cut_weight;
-    const u64 m_scan = warp_scan(m);
-    const int me = rank * kWarps + warp - w0;
-    if (me >= 0 && me < 32) {
-      my_before = __shfl_sync(0xffffffffu, run + m_scan - m, me);
-      my_mass = __shfl_sync(0xffffffffu, m, me);
-      my_seen = __shfl_sync(0xffffffffu, n_before, me);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n_sum += n[i];
+    u64 seen = warp_scan(n_sum) - n_sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u64 seen_i = seen;
+      m[i] += (seen < ties ? min(n[i], ties - seen) : 0) * cut_weight;
+      m_sum += m[i];
+      seen += n[i];
+      n[i] = seen_i;
     }
-    run += __shfl_sync(0xffffffffu, m_scan, 31);
-    seen += __shfl_sync(0xffffffffu, n_scan, 31);
+    u64 run = warp_scan(m_sum) - m_sum;
+    if (from == rank) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sh.warp_part[w + i] = run;
+        sh.warp_part2[w + i] = n[i];
+        sh.warp_kept[w + i] = m[i];
+        run += m[i];
+      }
+      run -= m_sum;
+    }
+    const u64 total = __shfl_sync(0xffffffffu, run + m_sum, 31);
+    if (lane == 0) {
+      // the first token whose running mass is above u * total
+      u64 x = 0;
+      if (u > 0.f) {
+        const double at = (double)u * (double)total;
+        x = at < (double)total ? min((u64)at, total - 1) : total - 1;
+      }
+      sh.goal = x;
+      sh.total = total;
+    }
   }
-  total = run;
-  // the first token whose running mass is above u * total
-  u64 goal = 0;
-  if (u > 0.f) {
-    const double x = (double)u * (double)total;
-    goal = x < (double)total ? (u64)x : total - 1;
-    if (goal >= total) goal = total - 1;
-  }
+  __syncthreads();
+  const u64 total = sh.total, goal = sh.goal, my_before = sh.warp_part[warp],
+            my_seen = sh.warp_part2[warp], my_mass = sh.warp_kept[warp];
   if (my_before <= goal && goal < my_before + my_mass) {
     // the piece, then its vectors in order
-    u64 m = sh.seg_mass[warp][lane], n = sh.seg_ties[warp][lane];
+    u64 m = lane < kGroups ? sh.seg_mass[warp][lane] : 0, n = lane < kGroups ? sh.seg_ties[warp][lane] : 0;
     const u64 n_before = my_seen + warp_scan(n) - n;
     m += (n_before < ties ? min(n, ties - n_before) : 0) * cut_weight;
     const u64 end = my_before + warp_scan(m);
     const int g = __ffs(__ballot_sync(0xffffffffu, end > goal)) - 1;
-    run = __shfl_sync(0xffffffffu, end - m, g);
-    seen = __shfl_sync(0xffffffffu, n_before, g);
+    u64 run = __shfl_sync(0xffffffffu, end - m, g), seen = __shfl_sync(0xffffffffu, n_before, g);
     for (int c = g * per; c < min((g + 1) * per, chunks); ++c) {
       const int v = share.v0 + c * 32 + lane;
       const bool live = v < share.v1;
@@ -646,14 +699,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (mine) {
         u64 at_mass = run + m_scan - m;
         for (int i = 0; i < VE; ++i) {
-          const uint32_t key = key_of(x.v[i]);
-          u64 w = 0;
-          if (key > cut) {
-            const float y = sc.y_of(x.v[i]);
-            if (y < kOctaves) w = sc.weight(x.v[i], y, sh.table);
-          } else if (ties > 0 && key == cut && rank_of++ < ties) {
-            w = cut_weight;
-          }
+          u64 w = weight_of(x.v[i]);
+          if (x.v[i] == cut && rank_of++ < ties) w = cut_weight;
           if (at_mass <= goal && goal < at_mass + w) {
             p.tokens[r] = v * VE + i - share.before;
             if (p.probs) p.probs[r] = (float)((double)w / (double)total);
@@ -671,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // Bytes of a row's share in shared memory: two blocks on an SM up to the first;
 // the second is what 8 blocks need of the longest rows (2^18 fp32).
-constexpr int kShareTwo = 72 * 1024, kShareMost = 136 * 1024;
+constexpr int kShareTwo = 75200, kShareMost = 136 * 1024;
+static_assert(2 * (kShareTwo + sizeof(Shared) + 1024) <= 228 * 1024, "two blocks");
 static_assert(((1 << 18) * 4 / 16 + 8 * kWarps) / (8 * kWarps) * kWarps * 16 <= kShareMost, "fits");
 
 template <typename T>
@@ -681,7 +729,7 @@ cudaError_t launch_t(const SampleParams &p, cudaStream_t stream) {
   int blocks = 1;
   auto share = [&] { return (vecs + blocks * kWarps - 1) / (blocks * kWarps); };
   auto bytes = [&] { return share() * kWarps * 16; };
-  while (blocks < 8 && (bytes() > kShareTwo ||
+  while (blocks < kMostBlocks && (bytes() > kShareTwo ||
                         ((long long)p.rows * blocks * 2 <= kSms && bytes() > 8 * 1024)))
     blocks *= 2;
   // above what needs no leave; always the most, since the attribute is the process's
