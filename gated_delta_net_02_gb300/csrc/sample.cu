@@ -15,7 +15,7 @@
 //    Tokens below 2^-45 of the largest have mass 0.
 //  * The order is never made. The last kept value is found by histograms:
 //    16 grid points a bin first, then the bin's values by their ordered
-//    bits, 1024 bins at a time, until a bin is one value. Of the tokens with
+//    bits, 512 bins at a time, until a bin is one value. Of the tokens with
 //    that value the lowest indexes are kept.
 //  * The first histogram of masses adds a weight as three numbers of 16 bits,
 //    by 32-bit atomics that are skipped where they are 0, as the upper ones
@@ -35,7 +35,7 @@ using u64 = unsigned long long;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostBlocks = 8;       // of a cluster
-constexpr int kBins = 1024;          // of a histogram; two of each thread
+constexpr int kBins = 768, kFineBins = 512;  // of the first histograms and of a bin's
 constexpr int kSms = 152;
 constexpr float kOctaves = 44.9f;     // further down, weights are 0
 constexpr int kGroups = 16;          // pieces of a warp's share with a mass of their own
@@ -175,25 +175,25 @@ struct Vec {
 struct Shared {
   Grid::Coarse coarse[kCoarse];
   uint32_t fine[kFine];
-  // two histograms in turn, so that one is cleared while the other is read: the
-  // tokens of a bin, and their mass in three parts (in `wide` and `more`) or as one
-  // number, with the bin's largest key in `more`
-  struct Histogram {
-    alignas(16) union {
-      u64 mass[kBins];
-      uint32_t part[2][kBins];
-    } wide;
-    uint32_t count[kBins], more[kBins];
-  } hist[2];
+  // two histograms in turn, so that one is cleared while the other is read
+  union Histogram {
+    uint32_t part[3][kBins];  // of the grid's bins: a number in parts of 16 bits
+    struct {                  // of one bin's values: mass, tokens, largest key
+      u64 mass[kFineBins];
+      uint32_t count[kFineBins], most[kFineBins];
+    } fine;
+  };
+  alignas(16) Histogram hist[2];
   u64 group[2][32];        // sums of 32 bins
   Small power[14];         // 2^(-2^k steps)
+  float queue[kWarps][64];
   u64 warp_part[kWarps], warp_part2[kWarps];
   u64 seg_mass[kWarps][kGroups];
   uint32_t seg_ties[kWarps][kGroups];
   alignas(16) u64 warp_mass[kWarps];
   u64 warp_kept[kWarps];
   alignas(16) uint32_t warp_ties[kWarps];
-  float top, step, ln_step;
+  float top, step, ln_step, least;
   float depth;             // logits from the largest to weight 0
   double min_drop;         // temperature * log(min_p)
   float warp_top[kWarps];
@@ -209,6 +209,7 @@ struct Share {
   int before, cols;  // elements before the row's start, and after it begins
   int v0, v1;        // this warp's vectors, counted from `row`
   uint4 *own;        // this warp's place in shared memory
+  float *queue;      // and its queue of 64
 
   // A vector of the row's ends: what is not of the row is -inf.
   __device__ __forceinline__ Vec<T> fetch_end(int v) const {
@@ -237,15 +238,59 @@ struct Share {
   }
   __device__ __forceinline__ Vec<T> get(int v) const { return Vec<T>(own[v - v0]); }
   template <class F>
-  __device__ __forceinline__ void each_vector(F f) const {
-    for (int v = v0 + (threadIdx.x & 31); v < v1; v += 32) f(get(v));
-  }
-  template <class F>
   __device__ __forceinline__ void each(F f) const {
-    each_vector([&](const Vec<T> &x) {
+    for (int v = v0 + (threadIdx.x & 31); v < v1; v += 32) {
+      const Vec<T> x = get(v);
 #pragma unroll
       for (int i = 0; i < VE; ++i) f(x.v[i]);
-    });
+    }
+  }
+  // f(x) for the logits lo <= x <= hi of the warp's chunks c0 .. c1 of 32 vectors;
+  // every lane of the warp takes part. Where they are few, a lane would wait for
+  // another's f at each of its own logits: they are queued, and 32 of them
+  // done at once.
+  template <class F>
+  __device__ __forceinline__ void each_between(float lo, float hi, int c0, int c1, F f) const {
+    const int lane = threadIdx.x & 31;
+    int n = 0;  // in the queue
+    for (int c = c0; c < c1; ++c) {
+      const int v = v0 + c * 32 + lane;
+      Vec<T> x(make_uint4(0, 0, 0, 0));
+      if (v < v1) x = get(v);
+      bool in[VE];
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        in[i] = v < v1 && x.v[i] >= lo && x.v[i] <= hi;
+        mine += in[i];
+      }
+      const uint32_t some = __ballot_sync(0xffffffffu, mine);
+      if (!some) continue;
+      if (__reduce_add_sync(0xffffffffu, mine) >= 16 * VE) {
+#pragma unroll
+        for (int i = 0; i < VE; ++i)
+          if (in[i]) f(x.v[i]);
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const uint32_t m = __ballot_sync(0xffffffffu, in[i]);
+        if (!m) continue;
+        if (in[i]) queue[n + __popc(m & ((1u << lane) - 1))] = x.v[i];
+        n += __popc(m);
+        if (n >= 32) {
+          __syncwarp();
+          const float first = queue[lane], rest = queue[32 + lane];
+          __syncwarp();
+          n -= 32;
+          if (lane < n) queue[lane] = rest;
+          f(first);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane < n) f(queue[lane]);
+    __syncwarp();
   }
 };
 
@@ -279,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     share.v0 = min((rank * kWarps + warp) * warp_vecs, vecs);
     share.v1 = min(share.v0 + warp_vecs, vecs);
     share.own = reinterpret_cast<uint4 *>(smem) + warp * warp_vecs;
+    share.queue = sh.queue[warp];
   }
   const float temperature = p.temperature ? p.temperature[r] : 1.f;
   const float top_p = p.top_p ? p.top_p[r] : 1.f, min_p = p.min_p ? p.min_p[r] : 0.f;
@@ -382,18 +428,24 @@ __global__ void __launch_bounds__(kThreads, 2)
     grid.fine = sh.fine;
   }
 
+  // the smallest logit that is not below min_p's bound
+  if (tid == kThreads - 1 && min_p > 0.f)
+    sh.least = fminf(__double2float_ru((double)top + sh.min_drop), top);
+
   // What is kept: logits above `cut`, and the first `ties` tokens at it.
   float cut = -INFINITY;
   u64 ties = 0;
   int buf = 0;  // histogram in use
   auto bin_of = [&](float x) { return grid.point(x) >> 4; };
+  const int chunks = (share.v1 - share.v0 + 31) / 32;  // of 32 vectors
 
   // The end of a pass that filled a histogram: value(bin) is what is looked for
   // in it. Whoever is behind the cluster's barrier has read the histogram
   // before, which is cleared for the pass after.
-  auto pass_done = [&](auto value) {
+  auto pass_done = [&](int bins, auto value) {
     __syncthreads();
-    u64 sum = value(sh.hist[buf], 2 * tid) + value(sh.hist[buf], 2 * tid + 1);
+    u64 sum = 0;
+    if (2 * tid < bins) sum = value(sh.hist[buf], 2 * tid) + value(sh.hist[buf], 2 * tid + 1);
 #pragma unroll
     for (int off = 8; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     if ((lane & 15) == 0) sh.group[buf][tid >> 4] = sum;
@@ -437,46 +489,48 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncthreads();
   };
-  auto count_in = [](const Shared::Histogram &h, int i) -> u64 { return h.count[i]; };
-  auto mass_in = [](const Shared::Histogram &h, int i) -> u64 { return h.wide.mass[i]; };
+  auto count_in = [](const Shared::Histogram &h, int i) -> u64 { return h.fine.count[i]; };
+  auto mass_in = [](const Shared::Histogram &h, int i) -> u64 { return h.fine.mass[i]; };
+  auto low_in = [](const Shared::Histogram &h, int i) -> u64 { return h.part[0][i]; };
   auto parts_in = [](const Shared::Histogram &h, int i) -> u64 {
-    return h.more[i] + ((u64)h.wide.part[0][i] << 16) + ((u64)h.wide.part[1][i] << 32);
+    return h.part[0][i] + ((u64)h.part[1][i] << 16) + ((u64)h.part[2][i] << 32);
   };
-  auto far_count = [&](int k, int i) -> u64 { return ld_cluster_u32(&sh.hist[buf].count[i], k); };
-  auto far_mass = [&](int k, int i) { return ld_cluster_u64(&sh.hist[buf].wide.mass[i], k); };
+  auto far_count = [&](int k, int i) -> u64 { return ld_cluster_u32(&sh.hist[buf].fine.count[i], k); };
+  auto far_mass = [&](int k, int i) { return ld_cluster_u64(&sh.hist[buf].fine.mass[i], k); };
+  auto far_low = [&](int k, int i) -> u64 { return ld_cluster_u32(&sh.hist[buf].part[0][i], k); };
   auto far_parts = [&](int k, int i) {
-    return ld_cluster_u32(&sh.hist[buf].more[i], k) +
-           ((u64)ld_cluster_u32(&sh.hist[buf].wide.part[0][i], k) << 16) +
-           ((u64)ld_cluster_u32(&sh.hist[buf].wide.part[1][i], k) << 32);
+    return ld_cluster_u32(&sh.hist[buf].part[0][i], k) +
+           ((u64)ld_cluster_u32(&sh.hist[buf].part[1][i], k) << 16) +
+           ((u64)ld_cluster_u32(&sh.hist[buf].part[2][i], k) << 32);
   };
 
   // The value at which the order's running count (BY_MASS: mass) first reaches
-  // `want`, among the logits above `above` in bin `bin`; `have` = what comes
+  // `want`, among the logits from `low` on in bin `bin`; `have` = what comes
   // before that bin. Leaves the value in cut, what comes before it in sh.before
   // and the tokens with it in sh.there.
-  auto refine = [&](bool by_mass, u64 want, float above, int bin, u64 have) {
+  auto refine = [&](bool by_mass, u64 want, float low, int bin, u64 have) {
     // a range that holds every value of the bin, by a margin of some roundings
     const int edge = grid.top - __float_as_int(grid.magic) - 16 * bin;  // its first point, in steps
-    const float lo = fmaxf(of_key(key_of((edge - 15) * sh.step + grid.from) - 8), grid.low);
+    const float lo = fmaxf(of_key(key_of((edge - 15) * sh.step + grid.from) - 8), low);
     const float hi = fminf(of_key(key_of((edge + 1) * sh.step + grid.from) + 8), top);
     uint32_t khi = key_of(hi) >> kLow, klo = key_of(lo) >> kLow;
     for (;;) {
       int shift = 0;
-      while ((khi - klo) >> shift >= (uint32_t)kBins) ++shift;
-      share.each([&](float x) {
-        if (!(x >= lo) || !(x <= hi)) return;
+      while ((khi - klo) >> shift >= (uint32_t)kFineBins) ++shift;
+      share.each_between(lo, hi, 0, chunks, [&](float x) {
         const uint32_t k = key_of(x) >> kLow;
-        if (bin_of(x) != bin || !(x > above) || k > khi || k < klo) return;
+        if (bin_of(x) != bin || k > khi || k < klo) return;
         const int i = (int)((khi - k) >> shift);
-        atomicAdd(&sh.hist[buf].count[i], 1u);
-        atomicMax(&sh.hist[buf].more[i], k);
-        if (by_mass) atomicAdd(&sh.hist[buf].wide.mass[i], grid.weight(x));
+        auto &h = sh.hist[buf].fine;
+        atomicAdd(&h.count[i], 1u);
+        atomicMax(&h.most[i], k);
+        if (by_mass) atomicAdd(&h.mass[i], grid.weight(x));
       });
       if (by_mass) {
-        pass_done(mass_in);
+        pass_done(kFineBins, mass_in);
         search(have, [&](u64) { return want; }, far_mass);
       } else {
-        pass_done(count_in);
+        pass_done(kFineBins, count_in);
         search(have, [&](u64) { return want; }, far_count);
       }
       const int i = sh.found;
@@ -486,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int k = 0; k < kMostBlocks; ++k)
         if (k < blocks) {
-          there += ld_cluster_u32(&sh.hist[buf].count[i], k);
-          key = max(key, ld_cluster_u32(&sh.hist[buf].more[i], k));
+          there += ld_cluster_u32(&sh.hist[buf].fine.count[i], k);
+          key = max(key, ld_cluster_u32(&sh.hist[buf].fine.most[i], k));
         }
       buf ^= 1;
       if (shift == 0 || there == 1) {  // one value
@@ -512,40 +566,34 @@ __global__ void __launch_bounds__(kThreads, 2)
   } else {
     if (top_k > 0 && top_k < p.vocab) {
       share.each([&](float x) {
-        if (x >= grid.low) atomicAdd(&sh.hist[buf].count[bin_of(x)], 1u);
+        if (x >= grid.low) atomicAdd(&sh.hist[buf].part[0][bin_of(x)], 1u);
       });
-      pass_done(count_in);
-      search(0, [&](u64) { return (u64)top_k; }, far_count);
+      pass_done(kBins, low_in);
+      search(0, [&](u64) { return (u64)top_k; }, far_low);
       const int bin = sh.found;
       const u64 have = sh.before;
       __syncthreads();
       buf ^= 1;
       if (bin >= 0) {  // else fewer tokens than top_k have any mass
-        refine(false, (u64)top_k, cut, bin, have);
+        refine(false, (u64)top_k, grid.low, bin, have);
         ties = (u64)top_k - sh.before;
       }
     }
     if (top_p < 1.f) {
-      const float above = cut, low = fmaxf(grid.low, of_key(key_of(above) + 1));
-      share.each_vector([&](const Vec<T> &x) {
-        u64 w[VE];
-        int j[VE];
-#pragma unroll
-        for (int i = 0; i < VE; ++i) w[i] = grid.weight(fmaxf(x.v[i], grid.low), j[i]);
-        auto &h = sh.hist[buf];
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          if (!(x.v[i] >= low)) continue;
-          const int b = j[i] >> 4;
-          atomicAdd(&h.more[b], (uint32_t)w[i] & 0xffff);
-          const uint32_t up = (uint32_t)(w[i] >> 16);
-          if (up) {
-            atomicAdd(&h.wide.part[0][b], up & 0xffff);
-            if (up >> 16) atomicAdd(&h.wide.part[1][b], up >> 16);
-          }
+      const float low = fmaxf(grid.low, of_key(key_of(cut) + 1));
+      share.each_between(low, top, 0, chunks, [&](float x) {
+        int j;
+        const u64 w = grid.weight(x, j);
+        auto &part = sh.hist[buf].part;
+        const int b = j >> 4;
+        atomicAdd(&part[0][b], (uint32_t)w & 0xffff);
+        const uint32_t up = (uint32_t)(w >> 16);
+        if (up) {
+          atomicAdd(&part[1][b], up & 0xffff);
+          if (up >> 16) atomicAdd(&part[2][b], up >> 16);
         }
       });
-      pass_done(parts_in);
+      pass_done(kBins, parts_in);
       const u64 tie_weight = ties > 0 ? grid.weight(cut) : 0;
       search(0, [&](u64 total) {
         const double goal = ceil((double)top_p * (double)(total + ties * tie_weight));
@@ -557,18 +605,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       buf ^= 1;
       u64 least = want - total, each = tie_weight, most = ties;  // beyond the last of the top k
       if (bin >= 0) {
-        refine(true, want, above, bin, have);
+        refine(true, want, low, bin, have);
         least = want - sh.before;
         each = grid.weight(cut);
         most = sh.there;
       }
-      ties = each ? min(most, (least + each - 1) / each) : most;
+      ties = most > 1 && each ? min(most, (least + each - 1) / each) : most;
     }
     if (min_p > 0.f) {
-      // the smallest logit that is not below the bound
-      if (tid == 0) sh.found = __float_as_int(__double2float_ru((double)top + sh.min_drop));
       __syncthreads();
-      const float least = fminf(__int_as_float(sh.found), top);
+      const float least = sh.least;
       if (least > cut) {  // all of that value: what is below it goes
         cut = of_key(key_of(least) - 1);
         ties = 0;
@@ -577,41 +623,24 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 
   // ---- the masses of the warps' shares, piece by piece
-  const int chunks = (warp_vecs + 31) / 32, per = (chunks + kGroups - 1) / kGroups;
+  const int per = (chunks + kGroups - 1) / kGroups;
   u64 cut_weight = 0;
   if (ties > 0) {
     if (greedy) cut_weight = 1;
     else if (cut >= grid.low) cut_weight = grid.weight(cut);
   }
-  auto weight_of = [&](float x) -> u64 {
-    return x > cut && x >= grid.low ? grid.weight(x) : 0;
-  };
-  // a vector's mass above the cut, and its tokens at it
-  auto mass_of = [&](const Vec<T> &x, bool live, u64 &mass, uint32_t &at_cut) {
-    mass = 0;
-    at_cut = 0;
-    if (!live) return;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      at_cut += x.v[i] == cut;
-      if (x.v[i] > cut) mass += weight_of(x.v[i]);
-    }
-    if (ties == 0) at_cut = 0;
-  };
+  // the lowest logit kept: tokens at the cut are counted
+  const float low = ties > 0 ? cut : fmaxf(grid.low, of_key(key_of(cut) + 1));
   u64 warp_total = 0;
   uint32_t warp_at_cut = 0;
   for (int g = 0; g < kGroups; ++g) {
     u64 mass = 0;
     uint32_t n = 0;
-    for (int c = g * per; c < min((g + 1) * per, chunks); ++c) {
-      const int v = share.v0 + c * 32 + lane;
-      const bool live = v < share.v1;
-      u64 m;
-      uint32_t at;
-      mass_of(share.get(live ? v : share.v0), live, m, at);
-      mass += m;
-      n += at;
-    }
+    if (g * per < chunks)
+      share.each_between(low, top, g * per, min((g + 1) * per, chunks), [&](float x) {
+        if (x == cut) ++n;
+        else if (x >= grid.low) mass += grid.weight(x);
+      });
     if (__any_sync(0xffffffffu, (uint32_t)mass | (uint32_t)(mass >> 32) | n)) {
       mass = warp_sum(mass);
       n = __reduce_add_sync(0xffffffffu, n);
@@ -687,30 +716,38 @@ __global__ void __launch_bounds__(kThreads, 2)
     u64 run = __shfl_sync(0xffffffffu, end - m, g), seen = __shfl_sync(0xffffffffu, n_before, g);
     for (int c = g * per; c < min((g + 1) * per, chunks); ++c) {
       const int v = share.v0 + c * 32 + lane;
-      const bool live = v < share.v1;
-      const Vec<T> x = share.get(live ? v : share.v0);
-      uint32_t at;
-      mass_of(x, live, m, at);
-      const u64 at_scan = warp_scan((u64)at);
-      u64 rank_of = seen + at_scan - at;  // ties before this lane's
-      m += (rank_of < ties ? min((u64)at, ties - rank_of) : 0) * cut_weight;
+      Vec<T> x(make_uint4(0, 0, 0, 0));
+      if (v < share.v1) x = share.get(v);
+      // the lane's masses, and its tokens at the cut
+      u64 w[VE];
+      m = n = 0;
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const bool at = ties > 0 && v < share.v1 && x.v[i] == cut;
+        const bool in = v < share.v1 && x.v[i] > cut && x.v[i] >= grid.low;
+        w[i] = in ? grid.weight(x.v[i]) : 0;
+        n += at;
+        m += w[i];
+      }
+      const u64 n_scan = warp_scan(n), n_from = seen + n_scan - n;  // ties before this lane's
+      m += (n_from < ties ? min(n, ties - n_from) : 0) * cut_weight;
       const u64 m_scan = warp_scan(m);
-      const bool mine = run + m_scan - m <= goal && goal < run + m_scan;
+      u64 at = run + m_scan - m, rank_of = n_from;
+      const bool mine = at <= goal && goal < at + m;
       if (mine) {
-        u64 at_mass = run + m_scan - m;
+#pragma unroll
         for (int i = 0; i < VE; ++i) {
-          u64 w = weight_of(x.v[i]);
-          if (x.v[i] == cut && rank_of++ < ties) w = cut_weight;
-          if (at_mass <= goal && goal < at_mass + w) {
+          if (ties > 0 && x.v[i] == cut && rank_of++ < ties) w[i] = cut_weight;
+          if (at <= goal && goal < at + w[i]) {
             p.tokens[r] = v * VE + i - share.before;
-            if (p.probs) p.probs[r] = (float)((double)w / (double)total);
+            if (p.probs) p.probs[r] = (float)((double)w[i] / (double)total);
           }
-          at_mass += w;
+          at += w[i];
         }
       }
       if (__any_sync(0xffffffffu, mine)) break;
       run += __shfl_sync(0xffffffffu, m_scan, 31);
-      seen += __shfl_sync(0xffffffffu, at_scan, 31);
+      seen += __shfl_sync(0xffffffffu, n_scan, 31);
     }
   }
   cluster_sync();  // no block leaves while its sums are read
@@ -718,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // Bytes of a row's share in shared memory: two blocks on an SM up to the first;
 // the second is what 8 blocks need of the longest rows (2^18 fp32).
-constexpr int kShareTwo = 75200, kShareMost = 136 * 1024;
+constexpr int kShareTwo = 80 * 1024, kShareMost = 136 * 1024;
 static_assert(2 * (kShareTwo + sizeof(Shared) + 1024) <= 228 * 1024, "two blocks");
 static_assert(((1 << 18) * 4 / 16 + 8 * kWarps) / (8 * kWarps) * kWarps * 16 <= kShareMost, "fits");
 
