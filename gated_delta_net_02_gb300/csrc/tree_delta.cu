@@ -38,152 +38,425 @@ __device__ __forceinline__ int qk_head(const TreeParams &p, int h) {
   return p.grouped ? h / (p.H / p.Hqk) : h % p.Hqk;
 }
 
-constexpr int kThreads = 128;
-constexpr int kCols = 64;  // columns of the state in a block
+// Loads of matrix fragments, and the products of 16 x 16 by 16 x 8 of a warp.
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 
-// Block: one sequence, head and 64 columns.
-template <typename T, int DK, int DV, bool KDA>
-__global__ void __launch_bounds__(kThreads) tree_forward_kernel(const TreeParams p) {
+// Two numbers as three bf16 parts each (8 bits of each number in turn: together
+// its 24), packed in pairs.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&part)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    part[i] = pack_bf16(x, y);
+    x -= __uint_as_float(part[i] << 16);
+    y -= __uint_as_float(part[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 u = reinterpret_cast<const float4 *>(p)[i];
+    v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
+  }
+}
+
+// Sizes of a block's shared memory, in bytes, for n nodes.
+template <typename T_, int DK_, int DV_, bool KDA_>
+struct Form {
+  using In = T_;
+  static constexpr int DK = DK_, DV = DV_;
+  static constexpr bool KDA = KDA_;
+  // rows of c k and c q: bf16 keys are their own operand, the scalar c is
+  // multiplied afterwards; otherwise three bf16 parts
+  static constexpr bool kPlain = sizeof(In) == 2 && !KDA;
+  static constexpr int PARTS = kPlain ? 1 : 3;
+  static constexpr int PITCH = DK * 2 + 16;  // of an operand's row: conflict-free ldmatrix
+  static constexpr int UP = DV + 4;          // of a row of sums, in floats
+  static constexpr int THREADS = DV * 2;     // a warp: 32 columns of one half of the rows
+  __host__ __device__ static constexpr int larger(int a, int b) { return a > b ? a : b; }
+  // queries follow the keys; tiles of 16 rows start at either
+  __host__ __device__ static constexpr int rows(int n) {
+    return larger((2 * n + 15) / 16 * 16, n + (n + 15) / 16 * 16);
+  }
+  __host__ __device__ static constexpr int operand(int n) { return rows(n) * PITCH; }
+  __host__ __device__ static constexpr int raw(int n) {  // keys, queries and decays
+    return kPlain ? 0 : 4 * n * DK * (KDA ? 3 : 2);
+  }
+  __host__ __device__ static constexpr int sums(int n) { return 4 * 2 * n * UP; }
+  // the sums take the place of the raw rows
+  __host__ __device__ static constexpr int smem(int n) {
+    return PARTS * operand(n) + larger(raw(n), sums(n)) + 4 * n * (n + 1);
+  }
+};
+
+// Block: one sequence and head.
+//  * What needs the tree alone comes first, while the state is on its way to
+//    L2: the products of keys along the paths (bf16 keys and one decay a head:
+//    all of them on the matrix instruction; else one path a warp, decays
+//    multiplied on the way), and the operands c k and c q.
+//  * Then S_0^T (c k), S_0^T (c q): a warp takes 32 columns and half of the
+//    rows of the state, straight from memory into fragments (a lane's 16 bytes
+//    are one row's columns of four products), and splits it into three bf16
+//    parts. Of products of parts all are kept whose size is above 2^-24.
+//  * d then goes from the root downwards, nodes of one depth together; a warp
+//    has 16 columns, which need no other warp.
+template <class F>
+__global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  constexpr int PER = DK / 32;             // elements of a lane
-  constexpr int GROUPS = kThreads / kCols; // threads of a column
-  extern __shared__ __align__(16) float sm[];
+  using T = typename F::In;
+  constexpr int DK = F::DK, DV = F::DV, THREADS = F::THREADS, WARPS = THREADS / 32, UP = F::UP;
+  constexpr bool KDA = F::KDA;
+  extern __shared__ __align__(16) unsigned char smem[];
   __shared__ u64 words[64];
-  __shared__ int depth[64], bad, most;
-  __shared__ float root[64], beta[64];
+  __shared__ float root[64], beta[64], alpha[64];
+  __shared__ int depth[64], order[64], level_end[65], bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int part = blockIdx.x % (DV / kCols), sh = blockIdx.x / (DV / kCols);
-  const int h = sh % p.H, s = sh / p.H, NT = p.T;
-  float *kf = sm, *qf = kf + NT * DK, *al = qf + NT * DK;
-  float *kc = KDA ? al + NT * DK : kf, *qc = KDA ? kc + NT * DK : qf;
-  float *ck = (KDA ? qc + NT * DK : al + NT), *cq = ck + NT * NT;
-  float *d = cq + NT * NT, *uq = d + NT * kCols;
+  const int h = blockIdx.x % p.H, s = blockIdx.x / p.H, NT = p.T;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  int nodes = p.n_nodes ? p.n_nodes[s] : NT;
-  if (tid == 0) bad = nodes < 0 || nodes > NT, most = 0;
-  nodes = min(max(nodes, 0), NT);
-  if (tid < nodes) words[tid] = p.tree[(long long)s * NT + tid];
-  __syncthreads();
+  const float *S = p.state_in[s];
+  if (S) S += (long long)h * DK * DV;
+  if (tid == 0 && S)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S), "n"(DK * DV * 4));
+  int n = p.n_nodes ? p.n_nodes[s] : NT;
+  if (tid == 0) bad = n < 0 || n > NT;
+  n = min(max(n, 0), NT);
   const long long t0 = (long long)s * NT;
-  if (tid < nodes) {
+  const int hq = qk_head(p, h);
+  const T *vt = static_cast<const T *>(p.v) + (t0 * p.H + h) * DV;  // node t: + t * H * DV
+  const long long v_step = (long long)p.H * DV;
+  if (tid < n) {
+    words[tid] = p.tree[t0 + tid];
+    beta[tid] = p.beta[(t0 + tid) * p.H + h];
+    if (!KDA) alpha[tid] = expf(p.g[(t0 + tid) * p.H + h]);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + tid * v_step));
+    if (DV * sizeof(T) > 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + tid * v_step + DV / 2));
+  }
+  const int op_bytes = F::operand(n);
+  unsigned char *const op = smem;  // [part][k rows, then q rows]
+  float *const raw_k = reinterpret_cast<float *>(smem + F::PARTS * op_bytes), *raw_q = raw_k + n * DK,
+               *const raw_a = raw_q + n * DK;
+  float *const uk = raw_k, *const uq = uk + n * UP;  // [n][UP]; uk becomes d
+  float *const ck = reinterpret_cast<float *>(smem + F::PARTS * op_bytes +
+                                              F::larger(F::raw(n), F::sums(n)));
+  float *const cq = ck + n * (n + 1) / 2;  // row t: [0, t], from t (t + 1) / 2 on
+  auto tri = [](int t) { return t * (t + 1) / 2; };
+
+  // keys and queries
+  constexpr int VE = 16 / (int)sizeof(T), VECS = DK / VE;
+  for (int e = tid; e < 2 * n * VECS; e += THREADS) {
+    const int r = e / VECS, c = e % VECS * VE, t = r < n ? r : r - n;
+    const T *src = static_cast<const T *>(r < n ? p.k : p.q) + ((t0 + t) * p.Hqk + hq) * DK + c;
+    const uint4 u = *reinterpret_cast<const uint4 *>(src);
+    if constexpr (F::kPlain) {
+      *reinterpret_cast<uint4 *>(op + r * F::PITCH + c * 2) = u;
+    } else {
+      float *dst = raw_k + r * DK + c;
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float2 *>(dst + 2 * i) = make_float2(
+              __uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+      } else {
+        *reinterpret_cast<uint4 *>(dst) = u;
+      }
+    }
+  }
+  if constexpr (KDA)
+    for (int e = tid; e < n * (DK / 4); e += THREADS) {
+      const int t = e / (DK / 4), c = e % (DK / 4) * 4;
+      const float4 g =
+          *reinterpret_cast<const float4 *>(p.g + ((t0 + t) * p.H + h) * DK + c);
+      *reinterpret_cast<float4 *>(raw_a + t * DK + c) =
+          make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
+    }
+  __syncthreads();
+
+  // the tree: its words have to be those of a tree; nodes in order of depth
+  if (tid < n) {
     const u64 w = words[tid], up = w & ~(1ull << tid);
     const int parent = up ? 63 - __clzll(up) : -1;
     if (!(w >> tid & 1) || parent >= tid || (parent >= 0 && words[parent] != up)) bad = 1;
     depth[tid] = __popcll(up);
-    atomicMax(&most, depth[tid]);
-    beta[tid] = p.beta[(t0 + tid) * p.H + h];
-    if (!KDA) al[tid] = expf(p.g[(t0 + tid) * p.H + h]);
-  }
-  const int hq = qk_head(p, h);
-  for (int e = tid; e < nodes * DK; e += kThreads) {
-    const int t = e / DK, i = e % DK;
-    const long long at = ((t0 + t) * p.Hqk + hq) * DK + i;
-    kf[e] = to_f32(static_cast<const T *>(p.k)[at]);
-    qf[e] = to_f32(static_cast<const T *>(p.q)[at]);
-    if (KDA) al[e] = expf(p.g[((t0 + t) * p.H + h) * DK + i]);
   }
   __syncthreads();
   if (bad) {
     if (tid == 0) set_error(p.err, kDevBadTree);
     return;
   }
-  // products of keys along each node's path, and the decay from the root
-  for (int t = warp; t < nodes; t += kThreads / 32) {
-    float kt[PER], qt[PER], w[PER];
-#pragma unroll
-    for (int m = 0; m < PER; ++m) {
-      kt[m] = kf[t * DK + m * 32 + lane];
-      qt[m] = qf[t * DK + m * 32 + lane];
-      w[m] = 1.f;
+  if (tid < n) {
+    int before = 0, shallower = 0;
+    for (int t = 0; t < n; ++t) {
+      shallower += depth[t] < depth[tid];
+      before += depth[t] < depth[tid] || (depth[t] == depth[tid] && t < tid);
     }
-    u64 left = words[t];
-    while (left) {
-      const int j = 63 - __clzll(left);
-      left &= ~(1ull << j);
-      float a = 0.f, b = 0.f;
+    order[before] = tid;
+    if (before == n - 1) level_end[depth[tid]] = n;
+    if (before == shallower && depth[tid] > 0) level_end[depth[tid] - 1] = before;
+  }
+  const int levels = n;  // an upper bound; a level ends at n at the latest
+
+  if constexpr (F::kPlain) {
+    // all products of keys (and queries) with keys
+    const uint32_t op_s = smem_u32(op);
+    const int mt = (2 * n + 15) / 16, nt = (n + 15) / 16;
+    for (int tile = warp; tile < mt * nt; tile += WARPS) {
+      const int m0 = tile / nt * 16, n0 = tile % nt * 16;
+      float g[2][4] = {};
 #pragma unroll
-      for (int m = 0; m < PER; ++m) {
-        const float x = w[m] * kf[j * DK + m * 32 + lane];
-        a = fmaf(kt[m], x, a);
-        b = fmaf(qt[m], x, b);
-        w[m] *= KDA ? al[j * DK + m * 32 + lane] : al[j];
+      for (int ks = 0; ks < DK / 16; ++ks) {
+        uint32_t a[4], b[4];
+        ldsm4(a, op_s + (m0 + (lane & 15)) * F::PITCH + (ks * 16 + (lane >> 4) * 8) * 2);
+        ldsm4(b, op_s + (n0 + (lane & 7) + ((lane >> 4) << 3)) * F::PITCH +
+                     (ks * 16 + ((lane >> 3) & 1) * 8) * 2);
+        mma16816(g[0], a, b[0], b[1]);
+        mma16816(g[1], a, b[2], b[3]);
       }
 #pragma unroll
-      for (int off = 16; off; off >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, off);
-        b += __shfl_xor_sync(0xffffffffu, b, off);
-      }
-      if (lane == 0) {
-        ck[t * NT + j] = a;
-        cq[t * NT + j] = b;
-      }
-    }
-    if (KDA) {
-#pragma unroll
-      for (int m = 0; m < PER; ++m) {
-        kc[t * DK + m * 32 + lane] = kt[m] * w[m];
-        qc[t * DK + m * 32 + lane] = qt[m] * w[m];
+      for (int x = 0; x < 8; ++x) {
+        const int r = m0 + (lane >> 2) + (x & 2) * 4, j = n0 + (x >> 2) * 8 + (lane & 3) * 2 + (x & 1);
+        const int t = r < n ? r : r - n;
+        if (r < 2 * n && j <= t) (r < n ? ck : cq)[tri(t) + j] = g[x >> 2][x & 3];
       }
     }
-    if (lane == 0) root[t] = KDA ? 1.f : w[0];
+    __syncthreads();
+    if (tid < n) {
+      float w = 1.f;
+      u64 left = words[tid];
+      while (left) {
+        const int j = 63 - __clzll(left);
+        left &= ~(1ull << j);
+        ck[tri(tid) + j] *= w;
+        cq[tri(tid) + j] *= w;
+        w *= alpha[j];
+      }
+      root[tid] = w;
+    }
+  } else {
+    // one path a warp: a lane has every 32nd 16 bytes of a row
+    constexpr int PER = DK / 32;
+    for (int t = warp; t < n; t += WARPS) {
+      float kt[PER], qt[PER], w[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        kt[i] = raw_k[t * DK + lane * PER + i];
+        qt[i] = raw_q[t * DK + lane * PER + i];
+        w[i] = 1.f;
+      }
+      u64 left = words[t];
+      while (left) {
+        // four ancestors at a time: eight sums, folded over the lanes
+        float sum[8];
+        int js[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int j = left ? 63 - __clzll(left) : -1;
+          js[x] = j;
+          float a = 0.f, b = 0.f;
+          if (j >= 0) {
+            left &= ~(1ull << j);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+              const float y = w[i] * raw_k[j * DK + lane * PER + i];
+              a = fmaf(kt[i], y, a);
+              b = fmaf(qt[i], y, b);
+              w[i] *= KDA ? raw_a[j * DK + lane * PER + i] : alpha[j];
+            }
+          }
+          sum[x] = a;
+          sum[4 + x] = b;
+        }
+#pragma unroll
+        for (int half = 4; half; half >>= 1) {
+#pragma unroll
+          for (int x = 0; x < half; ++x) {
+            const bool up = lane & half;
+            const float give = up ? sum[x] : sum[x + half], keep = up ? sum[x + half] : sum[x];
+            sum[x] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+          }
+        }
+        sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 8);
+        sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], 16);
+        // lane x has sum x
+        const int j = lane & 2 ? (lane & 1 ? js[3] : js[2]) : (lane & 1 ? js[1] : js[0]);
+        if (lane < 8 && j >= 0) (lane < 4 ? ck : cq)[tri(t) + j] = sum[0];
+      }
+      // the operands: c k and c q in parts
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < PER; i += 2) {
+          const float *y = x ? qt : kt;
+          uint32_t part[3];
+          split3(y[i] * w[i], y[i + 1] * w[i + 1], part);
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            *reinterpret_cast<uint32_t *>(op + k * op_bytes + (x * n + t) * F::PITCH +
+                                          (lane * PER + i) * 2) = part[k];
+        }
+      if (lane == 0) root[t] = 1.f;
+    }
   }
   __syncthreads();
-  // S_0^T of the keys and queries
-  const int c = tid % kCols, grp = tid / kCols, col = part * kCols + c;
-  const float *S = p.state_in[s];
-  if (S) S += (long long)h * DK * DV + col;
-  for (int base = grp * 4; base < nodes; base += 4 * GROUPS) {
-    float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
-    const int n = min(4, nodes - base);
+
+  // ---- S_0^T of the operands, 16 nodes at a time
+  constexpr int COLS = DV / 32, HALF = DK / 2, KS = HALF / 16;
+  const int col0 = warp % COLS * 32, half = warp / COLS;
+  const float *mine = S ? S + (long long)(half * HALF + (lane & 3) * 2) * DV + col0 + (lane >> 2) * 4
+                        : nullptr;
+  const uint32_t op_s = smem_u32(op);
+  const int tiles = n <= 8 ? 1 : 2;  // up to 8 nodes: keys and queries in one tile
+  for (int c0 = 0; c0 < n; c0 += 16) {
+    float acc[2][4][4] = {};
     if (S) {
-      for (int i = 0; i < DK; ++i) {
-        const float x = S[(long long)i * DV];
+      float4 x[2][4];
+      auto load = [&](int ks) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = base + (j < n ? j : 0);
-          a[j] = fmaf(x, kc[t * DK + i], a[j]);
-          b[j] = fmaf(x, qc[t * DK + i], b[j]);
+        for (int i = 0; i < 4; ++i)
+          x[ks & 1][i] = ld_stream_f4(mine + (long long)(ks * 16 + (i >> 1) * 8 + (i & 1)) * DV);
+      };
+      load(0);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if (ks + 1 < KS) load(ks + 1);
+        // column product i, k pair y: parts
+        uint32_t b[4][2][3];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const float4 &lo = x[ks & 1][2 * y], &hi = x[ks & 1][2 * y + 1];
+          split3(lo.x, hi.x, b[0][y]);
+          split3(lo.y, hi.y, b[1][y]);
+          split3(lo.z, hi.z, b[2][y]);
+          split3(lo.w, hi.w, b[3][y]);
+        }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (m >= tiles) break;
+          const uint32_t at = op_s + (c0 + m * n + (lane & 15)) * F::PITCH +
+                              (half * HALF + ks * 16 + (lane >> 4) * 8) * 2;
+#pragma unroll
+          for (int pa = 0; pa < F::PARTS; ++pa) {
+            uint32_t a[4];
+            ldsm4(a, at + pa * op_bytes);
+#pragma unroll
+            for (int pb = 0; pb < 3; ++pb) {
+              if (pa + pb > 2) continue;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma16816(acc[m][i], a, b[i][0][pb], b[i][1][pb]);
+            }
+          }
         }
       }
     }
-    for (int j = 0; j < n; ++j) {
-      d[(base + j) * kCols + c] = a[j] * root[base + j];
-      uq[(base + j) * kCols + c] = b[j] * root[base + j];
+    // a lane's 8 columns of rows lane / 4 and + 8: the halves of the state are added
+    // in turn
+#pragma unroll
+    for (int turn = 1; turn >= 0; --turn) {
+      if (half == turn) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          if (m >= tiles) break;
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int r = (lane >> 2) + 8 * y;
+            int t = c0 + r, is_q = m;
+            if (tiles == 1) {
+              is_q = r >= n;
+              t = is_q ? r - n : r;
+            }
+            if (t >= n || (tiles == 2 && r >= 16)) continue;
+            const int c = col0 + (lane & 3) * 8;
+            float *dst = (is_q ? uq : uk) + t * UP + c;
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              o[i] = acc[m][i][2 * y];
+              o[4 + i] = acc[m][i][2 * y + 1];
+            }
+            float4 *d4 = reinterpret_cast<float4 *>(dst);
+            if (turn == 0) {
+              const float w = root[t];
+              const float4 u0 = d4[0], u1 = d4[1];
+              o[0] = (o[0] + u0.x) * w; o[1] = (o[1] + u0.y) * w;
+              o[2] = (o[2] + u0.z) * w; o[3] = (o[3] + u0.w) * w;
+              o[4] = (o[4] + u1.x) * w; o[5] = (o[5] + u1.y) * w;
+              o[6] = (o[6] + u1.z) * w; o[7] = (o[7] + u1.w) * w;
+              if (!is_q) {
+                float v[8];
+                load8(vt + t * v_step + c, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = v[i] - o[i];
+              }
+            }
+            d4[0] = make_float4(o[0], o[1], o[2], o[3]);
+            d4[1] = make_float4(o[4], o[5], o[6], o[7]);
+          }
+        }
+      }
+      __syncthreads();
     }
   }
-  __syncthreads();
-  // d, one depth after the other
-  const T *v = static_cast<const T *>(p.v);
-  for (int level = 0; nodes > 0 && level <= most; ++level) {
-    for (int t = grp; t < nodes; t += GROUPS) {
-      if (depth[t] != level) continue;
-      float u = d[t * kCols + c];
-      u64 left = words[t] & ~(1ull << t);
-      while (left) {
-        const int j = __ffsll(left) - 1;
-        left &= left - 1;
-        u = fmaf(ck[t * NT + j], d[j * kCols + c], u);
-      }
-      d[t * kCols + c] = beta[t] * (to_f32(v[((t0 + t) * p.H + h) * DV + col]) - u);
+
+  // ---- d from the root downwards, then o; a warp's 16 columns, 8 nodes at a time
+  const int c = warp * 16 + (lane & 3) * 4, slot = lane >> 2;
+  auto along = [&](float4 x, const float *coef, u64 left, float sign) {
+    while (left) {
+      const int j = __ffsll(left) - 1;
+      left &= left - 1;
+      const float w = sign * coef[j];
+      const float4 d = *reinterpret_cast<const float4 *>(uk + j * UP + c);
+      x.x = fmaf(w, d.x, x.x);
+      x.y = fmaf(w, d.y, x.y);
+      x.z = fmaf(w, d.z, x.z);
+      x.w = fmaf(w, d.w, x.w);
     }
-    __syncthreads();
+    return x;
+  };
+  for (int level = 0, from = 0; level < levels && from < n; ++level) {
+    const int to = level_end[level];
+    for (int i = from + slot; i < to; i += 8) {
+      const int t = order[i];
+      float4 *at = reinterpret_cast<float4 *>(uk + t * UP + c);
+      const float4 x = along(*at, ck + tri(t), words[t] & ~(1ull << t), -1.f);
+      const float b = beta[t];
+      *at = make_float4(b * x.x, b * x.y, b * x.z, b * x.w);
+    }
+    __syncwarp();
+    from = to;
   }
-  for (int t = grp; t < NT; t += GROUPS) {
-    float o = 0.f, x = 0.f;
-    if (t < nodes) {
-      o = uq[t * kCols + c];
-      u64 left = words[t];
-      while (left) {
-        const int j = __ffsll(left) - 1;
-        left &= left - 1;
-        o = fmaf(cq[t * NT + j], d[j * kCols + c], o);
-      }
-      o *= p.scale;
-      x = d[t * kCols + c];
+  float *const out = p.out + (t0 * p.H + h) * DV + c, *const up = p.updates + (t0 * p.H + h) * DV + c;
+  for (int i = slot; i < NT; i += 8) {
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f), x = o;
+    int t = i;
+    if (i < n) {
+      t = order[i];
+      o = along(*reinterpret_cast<const float4 *>(uq + t * UP + c), cq + tri(t), words[t], 1.f);
+      o = make_float4(p.scale * o.x, p.scale * o.y, p.scale * o.z, p.scale * o.w);
+      x = *reinterpret_cast<const float4 *>(uk + t * UP + c);
     }
-    const long long at = ((t0 + t) * p.H + h) * DV + col;
-    p.out[at] = o;
-    p.updates[at] = x;
+    st_f4(out + t * v_step, o);
+    st_f4(up + t * v_step, x);
   }
 }
 
@@ -268,16 +541,14 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeP
   for (int r = 0; r < ROWS; ++r) st_f4(place + at + r * DV, st[r]);
 }
 
-template <typename T, int DK, int DV, bool KDA>
+template <class F>
 cudaError_t forward(const TreeParams &p, cudaStream_t stream) {
-  const int n = p.T;
-  const int smem = 4 * (n * DK * (KDA ? 5 : 2) + (KDA ? 0 : n) + 2 * n * n + 2 * n * kCols);
-  const cudaError_t e =
-      cudaFuncSetAttribute(tree_forward_kernel<T, DK, DV, KDA>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * 64 * (DK * 5 + 2 * 64 + 2 * kCols));
+  static_assert(F::smem(64) + 4096 <= 227 * 1024, "shared memory");
+  const cudaError_t e = cudaFuncSetAttribute(
+      tree_forward_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem(64));
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_forward_kernel<T, DK, DV, KDA>,
-                    dim3((unsigned)(p.n_seqs * p.H * (DV / kCols))), dim3(kThreads), smem, stream, p);
+  return launch_pdl(tree_forward_kernel<F>, dim3((unsigned)(p.n_seqs * p.H)), dim3(F::THREADS),
+                    F::smem(p.T), stream, p);
 }
 
 template <typename T, int DK, int DV, bool KDA>
@@ -292,13 +563,7 @@ cudaError_t commit(const TreeParams &p, cudaStream_t stream) {
                     smem, stream, p);
 }
 
-// Calls f with the configuration of a call's types, head sizes and gates.
-template <typename T, int DK, int DV, bool KDA_>
-struct Form {
-  using In = T;
-  static constexpr int Dk = DK, Dv = DV;
-  static constexpr bool KDA = KDA_;
-};
+// Calls f with the form of a call's types, head sizes and gates.
 template <typename T, int DK, int DV, class F>
 cudaError_t with_gate(bool kda, F f) {
   return kda ? f(Form<T, DK, DV, true>{}) : f(Form<T, DK, DV, false>{});
@@ -329,14 +594,14 @@ TreeParams tree_params(const TreeDeltaArgs &a) {
 cudaError_t launch_tree_forward(const TreeDeltaArgs &a, cudaStream_t stream) {
   return with_form(a, [&](auto f) {
     using F = decltype(f);
-    return forward<typename F::In, F::Dk, F::Dv, F::KDA>(tree_params(a), stream);
+    return forward<F>(tree_params(a), stream);
   });
 }
 
 cudaError_t launch_tree_commit(const TreeDeltaArgs &a, cudaStream_t stream) {
   return with_form(a, [&](auto f) {
     using F = decltype(f);
-    return commit<typename F::In, F::Dk, F::Dv, F::KDA>(tree_params(a), stream);
+    return commit<typename F::In, F::DK, F::DV, F::KDA>(tree_params(a), stream);
   });
 }
 
