@@ -81,6 +81,29 @@ __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
   }
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// N consecutive elements of shared memory as fp32.
+template <int N>
+__device__ __forceinline__ void get(const __nv_bfloat16 *p, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(p + i);
+    v[i] = __uint_as_float(u << 16);
+    v[i + 1] = __uint_as_float(u & 0xffff0000u);
+  }
+}
+template <int N>
+__device__ __forceinline__ void get(const float *p, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 u = *reinterpret_cast<const float2 *>(p + i);
+    v[i] = u.x;
+    v[i + 1] = u.y;
+  }
+}
+
 // Sizes of a block's shared memory, in bytes, for n nodes.
 template <typename T_, int DK_, int DV_, bool KDA_>
 struct Form {
@@ -101,7 +124,7 @@ struct Form {
   }
   __host__ __device__ static constexpr int operand(int n) { return rows(n) * PITCH; }
   __host__ __device__ static constexpr int raw(int n) {  // keys, queries and decays
-    return kPlain ? 0 : 4 * n * DK * (KDA ? 3 : 2);
+    return kPlain ? 0 : n * DK * (2 * (int)sizeof(In) + (KDA ? 4 : 0));
   }
   __host__ __device__ static constexpr int sums(int n) { return 4 * 2 * n * UP; }
   // the sums take the place of the raw rows
@@ -121,7 +144,9 @@ struct Form {
 //    parts. Of products of parts all are kept whose size is above 2^-24.
 //  * d then goes from the root downwards, nodes of one depth together; a warp
 //    has 16 columns, which need no other warp.
-template <class F>
+// TILES: of 16 rows of the operands taken at once; 1 (up to 8 nodes): keys and
+// queries in one.
+template <class F, int TILES>
 __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   using T = typename F::In;
@@ -131,65 +156,79 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   __shared__ u64 words[64];
   __shared__ float root[64], beta[64], alpha[64];
   __shared__ int depth[64], order[64], level_end[65], bad;
+  __shared__ alignas(4) unsigned char path[64][64];  // ancestors, the parent first
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % p.H, s = blockIdx.x / p.H, NT = p.T;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float *S = p.state_in[s];
-  if (S) S += (long long)h * DK * DV;
-  if (tid == 0 && S)
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S), "n"(DK * DV * 4));
-  int n = p.n_nodes ? p.n_nodes[s] : NT;
-  if (tid == 0) bad = n < 0 || n > NT;
-  n = min(max(n, 0), NT);
   const long long t0 = (long long)s * NT;
   const int hq = qk_head(p, h);
   const T *vt = static_cast<const T *>(p.v) + (t0 * p.H + h) * DV;  // node t: + t * H * DV
   const long long v_step = (long long)p.H * DV;
-  if (tid < n) {
-    words[tid] = p.tree[t0 + tid];
-    beta[tid] = p.beta[(t0 + tid) * p.H + h];
-    if (!KDA) alpha[tid] = expf(p.g[(t0 + tid) * p.H + h]);
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + tid * v_step));
-    if (DV * sizeof(T) > 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + tid * v_step + DV / 2));
-  }
-  const int op_bytes = F::operand(n);
+  const int op_bytes = F::operand(NT);
   unsigned char *const op = smem;  // [part][k rows, then q rows]
-  float *const raw_k = reinterpret_cast<float *>(smem + F::PARTS * op_bytes), *raw_q = raw_k + n * DK,
-               *const raw_a = raw_q + n * DK;
-  float *const uk = raw_k, *const uq = uk + n * UP;  // [n][UP]; uk becomes d
+  T *const raw_k = reinterpret_cast<T *>(smem + F::PARTS * op_bytes), *const raw_q = raw_k + NT * DK;
+  float *const raw_a = reinterpret_cast<float *>(raw_q + NT * DK);
+  float *const uk = reinterpret_cast<float *>(raw_k), *const uq = uk + NT * UP;  // uk becomes d
   float *const ck = reinterpret_cast<float *>(smem + F::PARTS * op_bytes +
-                                              F::larger(F::raw(n), F::sums(n)));
-  float *const cq = ck + n * (n + 1) / 2;  // row t: [0, t], from t (t + 1) / 2 on
+                                              F::larger(F::raw(NT), F::sums(NT)));
+  float *const cq = ck + NT * (NT + 1) / 2;  // row t: [0, t], from t (t + 1) / 2 on
   auto tri = [](int t) { return t * (t + 1) / 2; };
 
-  // keys and queries
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // keys, queries and gates on their way to shared memory (padding too: nothing
+  // reads it)
   constexpr int VE = 16 / (int)sizeof(T), VECS = DK / VE;
-  for (int e = tid; e < 2 * n * VECS; e += THREADS) {
-    const int r = e / VECS, c = e % VECS * VE, t = r < n ? r : r - n;
-    const T *src = static_cast<const T *>(r < n ? p.k : p.q) + ((t0 + t) * p.Hqk + hq) * DK + c;
-    const uint4 u = *reinterpret_cast<const uint4 *>(src);
-    if constexpr (F::kPlain) {
-      *reinterpret_cast<uint4 *>(op + r * F::PITCH + c * 2) = u;
-    } else {
-      float *dst = raw_k + r * DK + c;
-      if constexpr (sizeof(T) == 2) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<float2 *>(dst + 2 * i) = make_float2(
-              __uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-      } else {
-        *reinterpret_cast<uint4 *>(dst) = u;
-      }
-    }
+  for (int e = tid; e < 2 * NT * VECS; e += THREADS) {
+    const int r = e / VECS, c = e % VECS * VE, t = r < NT ? r : r - NT;
+    const T *src = static_cast<const T *>(r < NT ? p.k : p.q) + ((t0 + t) * p.Hqk + hq) * DK + c;
+    cp_async16(F::kPlain ? smem_u32(op + r * F::PITCH + c * 2) : smem_u32(raw_k + r * DK + c), src);
   }
   if constexpr (KDA)
-    for (int e = tid; e < n * (DK / 4); e += THREADS) {
+    for (int e = tid; e < NT * (DK / 4); e += THREADS) {
       const int t = e / (DK / 4), c = e % (DK / 4) * 4;
-      const float4 g =
-          *reinterpret_cast<const float4 *>(p.g + ((t0 + t) * p.H + h) * DK + c);
-      *reinterpret_cast<float4 *>(raw_a + t * DK + c) =
-          make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
+      cp_async16(smem_u32(raw_a + t * DK + c), p.g + ((t0 + t) * p.H + h) * DK + c);
+    }
+  const float *S = p.state_in[s];
+  int n = p.n_nodes ? p.n_nodes[s] : NT;
+  if (tid < NT) {
+    const u64 w = p.tree[t0 + tid];
+    const float b = p.beta[(t0 + tid) * p.H + h], g = KDA ? 0.f : p.g[(t0 + tid) * p.H + h];
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + tid * v_step));
+    if (DV * sizeof(T) > 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + tid * v_step + DV / 2));
+    if (DV * sizeof(T) > 256) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + tid * v_step + DV / 4));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(vt + tid * v_step + 3 * DV / 4));
+    }
+    words[tid] = w;
+    beta[tid] = b;
+    if (!KDA) alpha[tid] = expf(g);
+  }
+  if (tid == 0) bad = n < 0 || n > NT;
+  n = min(max(n, 0), NT);
+  // the state's first fragments to registers, the rest to L2
+  constexpr int COLS = DV / 32, HALF = DK / 2, KS = HALF / 16;
+  constexpr int AHEAD = TILES == 1 ? KS : 2;  // steps of the state in registers
+  const int col0 = warp % COLS * 32, half = warp / COLS;
+  if (S) S += (long long)h * DK * DV;
+  const float *mine = S ? S + (long long)(half * HALF + (lane & 3) * 2) * DV + col0 + (lane >> 2) * 4
+                        : nullptr;
+  float4 x[AHEAD][4];
+  auto load = [&](int ks) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      x[ks % AHEAD][i] = ld_stream_f4(mine + (long long)(ks * 16 + (i >> 1) * 8 + (i & 1)) * DV);
+  };
+  if (S) {
+#pragma unroll
+    for (int ks = 0; ks < AHEAD; ++ks) load(ks);
+    if (AHEAD < KS && tid == 0)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S), "n"(DK * DV * 4));
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (KDA)  // each thread what it has brought itself
+    for (int e = tid; e < NT * (DK / 4); e += THREADS) {
+      float4 *at = reinterpret_cast<float4 *>(raw_a) + e;
+      const float4 g = *at;
+      *at = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
     }
   __syncthreads();
 
@@ -199,6 +238,12 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
     const int parent = up ? 63 - __clzll(up) : -1;
     if (!(w >> tid & 1) || parent >= tid || (parent >= 0 && words[parent] != up)) bad = 1;
     depth[tid] = __popcll(up);
+    int l = 0;
+    for (u64 left = up; left; ++l) {
+      const int j = 63 - __clzll(left);
+      left &= ~(1ull << j);
+      path[tid][l] = (unsigned char)j;
+    }
   }
   __syncthreads();
   if (bad) {
@@ -215,12 +260,11 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
     if (before == n - 1) level_end[depth[tid]] = n;
     if (before == shallower && depth[tid] > 0) level_end[depth[tid] - 1] = before;
   }
-  const int levels = n;  // an upper bound; a level ends at n at the latest
 
   if constexpr (F::kPlain) {
     // all products of keys (and queries) with keys
     const uint32_t op_s = smem_u32(op);
-    const int mt = (2 * n + 15) / 16, nt = (n + 15) / 16;
+    const int mt = (2 * NT + 15) / 16, nt = (n + 15) / 16;
     for (int tile = warp; tile < mt * nt; tile += WARPS) {
       const int m0 = tile / nt * 16, n0 = tile % nt * 16;
       float g[2][4] = {};
@@ -236,17 +280,15 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         const int r = m0 + (lane >> 2) + (x & 2) * 4, j = n0 + (x >> 2) * 8 + (lane & 3) * 2 + (x & 1);
-        const int t = r < n ? r : r - n;
-        if (r < 2 * n && j <= t) (r < n ? ck : cq)[tri(t) + j] = g[x >> 2][x & 3];
+        const int t = r < NT ? r : r - NT;
+        if (t < n && j <= t) (r < NT ? ck : cq)[tri(t) + j] = g[x >> 2][x & 3];
       }
     }
     __syncthreads();
     if (tid < n) {
-      float w = 1.f;
-      u64 left = words[tid];
-      while (left) {
-        const int j = 63 - __clzll(left);
-        left &= ~(1ull << j);
+      float w = alpha[tid];
+      for (int l = 0; l < depth[tid]; ++l) {
+        const int j = path[tid][l];
         ck[tri(tid) + j] *= w;
         cq[tri(tid) + j] *= w;
         w *= alpha[j];
@@ -254,16 +296,14 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
       root[tid] = w;
     }
   } else {
-    // one path a warp: a lane has every 32nd 16 bytes of a row
+    // one path a warp
     constexpr int PER = DK / 32;
     for (int t = warp; t < n; t += WARPS) {
       float kt[PER], qt[PER], w[PER];
+      get(raw_k + t * DK + lane * PER, kt);
+      get(raw_q + t * DK + lane * PER, qt);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        kt[i] = raw_k[t * DK + lane * PER + i];
-        qt[i] = raw_q[t * DK + lane * PER + i];
-        w[i] = 1.f;
-      }
+      for (int i = 0; i < PER; ++i) w[i] = 1.f;
       u64 left = words[t];
       while (left) {
         // four ancestors at a time: eight sums, folded over the lanes
@@ -276,12 +316,15 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
           float a = 0.f, b = 0.f;
           if (j >= 0) {
             left &= ~(1ull << j);
+            float kj[PER], aj[PER];
+            get(raw_k + j * DK + lane * PER, kj);
+            if constexpr (KDA) get(raw_a + j * DK + lane * PER, aj);
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-              const float y = w[i] * raw_k[j * DK + lane * PER + i];
+              const float y = w[i] * kj[i];
               a = fmaf(kt[i], y, a);
               b = fmaf(qt[i], y, b);
-              w[i] *= KDA ? raw_a[j * DK + lane * PER + i] : alpha[j];
+              w[i] *= KDA ? aj[i] : alpha[j];
             }
           }
           sum[x] = a;
@@ -312,7 +355,7 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
           split3(y[i] * w[i], y[i + 1] * w[i + 1], part);
 #pragma unroll
           for (int k = 0; k < 3; ++k)
-            *reinterpret_cast<uint32_t *>(op + k * op_bytes + (x * n + t) * F::PITCH +
+            *reinterpret_cast<uint32_t *>(op + k * op_bytes + (x * NT + t) * F::PITCH +
                                           (lane * PER + i) * 2) = part[k];
         }
       if (lane == 0) root[t] = 1.f;
@@ -321,39 +364,30 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   __syncthreads();
 
   // ---- S_0^T of the operands, 16 nodes at a time
-  constexpr int COLS = DV / 32, HALF = DK / 2, KS = HALF / 16;
-  const int col0 = warp % COLS * 32, half = warp / COLS;
-  const float *mine = S ? S + (long long)(half * HALF + (lane & 3) * 2) * DV + col0 + (lane >> 2) * 4
-                        : nullptr;
   const uint32_t op_s = smem_u32(op);
-  const int tiles = n <= 8 ? 1 : 2;  // up to 8 nodes: keys and queries in one tile
   for (int c0 = 0; c0 < n; c0 += 16) {
-    float acc[2][4][4] = {};
+    float acc[TILES][4][4] = {};
     if (S) {
-      float4 x[2][4];
-      auto load = [&](int ks) {
+      if (c0 > 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          x[ks & 1][i] = ld_stream_f4(mine + (long long)(ks * 16 + (i >> 1) * 8 + (i & 1)) * DV);
-      };
-      load(0);
+        for (int ks = 0; ks < AHEAD; ++ks) load(ks);
+      }
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        if (ks + 1 < KS) load(ks + 1);
         // column product i, k pair y: parts
         uint32_t b[4][2][3];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float4 &lo = x[ks & 1][2 * y], &hi = x[ks & 1][2 * y + 1];
+          const float4 &lo = x[ks % AHEAD][2 * y], &hi = x[ks % AHEAD][2 * y + 1];
           split3(lo.x, hi.x, b[0][y]);
           split3(lo.y, hi.y, b[1][y]);
           split3(lo.z, hi.z, b[2][y]);
           split3(lo.w, hi.w, b[3][y]);
         }
+        if (ks + AHEAD < KS) load(ks + AHEAD);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (m >= tiles) break;
-          const uint32_t at = op_s + (c0 + m * n + (lane & 15)) * F::PITCH +
+        for (int m = 0; m < TILES; ++m) {
+          const uint32_t at = op_s + (c0 + m * NT + (lane & 15)) * F::PITCH +
                               (half * HALF + ks * 16 + (lane >> 4) * 8) * 2;
 #pragma unroll
           for (int pa = 0; pa < F::PARTS; ++pa) {
@@ -375,17 +409,16 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
     for (int turn = 1; turn >= 0; --turn) {
       if (half == turn) {
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          if (m >= tiles) break;
+        for (int m = 0; m < TILES; ++m) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const int r = (lane >> 2) + 8 * y;
             int t = c0 + r, is_q = m;
-            if (tiles == 1) {
-              is_q = r >= n;
-              t = is_q ? r - n : r;
+            if (TILES == 1) {
+              is_q = r >= NT;
+              t = is_q ? r - NT : r;
             }
-            if (t >= n || (tiles == 2 && r >= 16)) continue;
+            if (t >= n) continue;
             const int c = col0 + (lane & 3) * 8;
             float *dst = (is_q ? uq : uk) + t * UP + c;
             float o[8];
@@ -420,25 +453,30 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
 
   // ---- d from the root downwards, then o; a warp's 16 columns, 8 nodes at a time
   const int c = warp * 16 + (lane & 3) * 4, slot = lane >> 2;
-  auto along = [&](float4 x, const float *coef, u64 left, float sign) {
-    while (left) {
-      const int j = __ffsll(left) - 1;
-      left &= left - 1;
-      const float w = sign * coef[j];
-      const float4 d = *reinterpret_cast<const float4 *>(uk + j * UP + c);
-      x.x = fmaf(w, d.x, x.x);
-      x.y = fmaf(w, d.y, x.y);
-      x.z = fmaf(w, d.z, x.z);
-      x.w = fmaf(w, d.w, x.w);
+  // x + sign sum over the ancestors of t of coef[j] d_j
+  auto along = [&](float4 x, const float *coef, int t, int len, float sign) {
+    for (int l = 0; l < len; l += 4) {
+      const uint32_t js = *reinterpret_cast<const uint32_t *>(&path[t][l]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (l + i >= len) break;
+        const int j = js >> (8 * i) & 0xff;
+        const float w = sign * coef[j];
+        const float4 d = *reinterpret_cast<const float4 *>(uk + j * UP + c);
+        x.x = fmaf(w, d.x, x.x);
+        x.y = fmaf(w, d.y, x.y);
+        x.z = fmaf(w, d.z, x.z);
+        x.w = fmaf(w, d.w, x.w);
+      }
     }
     return x;
   };
-  for (int level = 0, from = 0; level < levels && from < n; ++level) {
+  for (int level = 0, from = 0; from < n; ++level) {
     const int to = level_end[level];
     for (int i = from + slot; i < to; i += 8) {
       const int t = order[i];
       float4 *at = reinterpret_cast<float4 *>(uk + t * UP + c);
-      const float4 x = along(*at, ck + tri(t), words[t] & ~(1ull << t), -1.f);
+      const float4 x = along(*at, ck + tri(t), t, level, -1.f);
       const float b = beta[t];
       *at = make_float4(b * x.x, b * x.y, b * x.z, b * x.w);
     }
@@ -451,9 +489,12 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
     int t = i;
     if (i < n) {
       t = order[i];
-      o = along(*reinterpret_cast<const float4 *>(uq + t * UP + c), cq + tri(t), words[t], 1.f);
-      o = make_float4(p.scale * o.x, p.scale * o.y, p.scale * o.z, p.scale * o.w);
       x = *reinterpret_cast<const float4 *>(uk + t * UP + c);
+      const float w = cq[tri(t) + t];
+      o = *reinterpret_cast<const float4 *>(uq + t * UP + c);
+      o = make_float4(fmaf(w, x.x, o.x), fmaf(w, x.y, o.y), fmaf(w, x.z, o.z), fmaf(w, x.w, o.w));
+      o = along(o, cq + tri(t), t, depth[t], 1.f);
+      o = make_float4(p.scale * o.x, p.scale * o.y, p.scale * o.z, p.scale * o.w);
     }
     st_f4(out + t * v_step, o);
     st_f4(up + t * v_step, x);
@@ -541,14 +582,18 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeP
   for (int r = 0; r < ROWS; ++r) st_f4(place + at + r * DV, st[r]);
 }
 
+template <class F, int TILES>
+cudaError_t forward_tiles(const TreeParams &p, cudaStream_t stream) {
+  static_assert(F::smem(64) + 8192 <= 227 * 1024, "shared memory");
+  const cudaError_t e = cudaFuncSetAttribute(
+      tree_forward_kernel<F, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem(64));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_forward_kernel<F, TILES>, dim3((unsigned)(p.n_seqs * p.H)),
+                    dim3(F::THREADS), F::smem(p.T), stream, p);
+}
 template <class F>
 cudaError_t forward(const TreeParams &p, cudaStream_t stream) {
-  static_assert(F::smem(64) + 4096 <= 227 * 1024, "shared memory");
-  const cudaError_t e = cudaFuncSetAttribute(
-      tree_forward_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::smem(64));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(tree_forward_kernel<F>, dim3((unsigned)(p.n_seqs * p.H)), dim3(F::THREADS),
-                    F::smem(p.T), stream, p);
+  return p.T <= 8 ? forward_tiles<F, 1>(p, stream) : forward_tiles<F, 2>(p, stream);
 }
 
 template <typename T, int DK, int DV, bool KDA>
