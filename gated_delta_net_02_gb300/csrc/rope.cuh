@@ -95,8 +95,8 @@ template <typename T>
 struct Vec16 {  // 16 bytes of T as fp32
   static constexpr int N = 16 / sizeof(T);
   float v[N];
-  __device__ __forceinline__ void load(const T *p) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+  __device__ __forceinline__ void load(const T *p) { unpack(*reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void unpack(uint4 u) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -13,6 +13,7 @@
 // Bound by HBM: the first state is read once (the token loop with a slot for
 // each node would write as many states as there are nodes).
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "kernels.h"
 #include "layer.cuh"
@@ -53,15 +54,47 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // Two numbers as three bf16 parts each (8 bits of each number in turn: together
 // its 24), packed in pairs.
-__device__ __forceinline__ void split3(float x, float y, uint32_t (&part)[3]) {
+__device__ __forceinline__ void split(float x, float y, uint32_t (&part)[3]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     part[i] = pack_bf16(x, y);
     x -= __uint_as_float(part[i] << 16);
     y -= __uint_as_float(part[i] & 0xffff0000u);
   }
+}
+// As two fp16 parts (11 bits in turn, in all 23 with the second's sign), of numbers
+// scaled to below 2^15: what the second cannot hold is below 2^-25.
+__device__ __forceinline__ void split(float x, float y, uint32_t (&part)[2]) {
+  const __half2 hi = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(hi);
+  const __half2 lo = __floats2half2_rn(x - f.x, y - f.y);
+  part[0] = *reinterpret_cast<const uint32_t *>(&hi);
+  part[1] = *reinterpret_cast<const uint32_t *>(&lo);
+}
+// The power of two that takes the largest of a warp's finite numbers (m: the
+// largest size of this lane's) to 8 .. 16; 1 for zeros.
+__device__ __forceinline__ float scale_of(float m) {
+#pragma unroll
+  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (m == 0.f) return 1.f;
+  return __int_as_float(min(254 + 3 - (__float_as_int(m) >> 23), 254) << 23);
+}
+__device__ __forceinline__ float finite(float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.f; }
+// 1 / s of a power of two, which may lie below the normal numbers.
+__device__ __forceinline__ float inverse(float s) {
+  const int e = __float_as_int(s) >> 23;
+  return e == 254 ? 0x1p-127f : __int_as_float((254 - e) << 23);
 }
 
 __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
@@ -84,6 +117,12 @@ __device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+template <int BYTES>
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "n"(BYTES));
+}
+constexpr int kBlocksAtOnce = 2 * 152;
+
 // N consecutive elements of shared memory as fp32.
 template <int N>
 __device__ __forceinline__ void get(const __nv_bfloat16 *p, float (&v)[N]) {
@@ -110,10 +149,11 @@ struct Form {
   using In = T_;
   static constexpr int DK = DK_, DV = DV_;
   static constexpr bool KDA = KDA_;
-  // rows of c k and c q: bf16 keys are their own operand, the scalar c is
-  // multiplied afterwards; otherwise three bf16 parts
+  // rows of c k and c q: bf16 keys are their own operand (the scalar c is
+  // multiplied afterwards), against three bf16 parts of the state; otherwise two fp16
+  // parts against two
   static constexpr bool kPlain = sizeof(In) == 2 && !KDA;
-  static constexpr int PARTS = kPlain ? 1 : 3;
+  static constexpr int PARTS = kPlain ? 1 : 2, STATE_PARTS = kPlain ? 3 : 2;
   static constexpr int PITCH = DK * 2 + 16;  // of an operand's row: conflict-free ldmatrix
   static constexpr int UP = DV + 4;          // of a row of sums, in floats
   static constexpr int THREADS = DV * 2;     // a warp: 32 columns of one half of the rows
@@ -140,8 +180,8 @@ struct Form {
 //    multiplied on the way), and the operands c k and c q.
 //  * Then S_0^T (c k), S_0^T (c q): a warp takes 32 columns and half of the
 //    rows of the state, straight from memory into fragments (a lane's 16 bytes
-//    are one row's columns of four products), and splits it into three bf16
-//    parts. Of products of parts all are kept whose size is above 2^-24.
+//    are one row's columns of four products), and splits it into parts that
+//    hold its 24 bits. Of products of parts all are kept whose size is above 2^-23.
 //  * d then goes from the root downwards, nodes of one depth together; a warp
 //    has 16 columns, which need no other warp.
 // TILES: of 16 rows of the operands taken at once; 1 (up to 8 nodes): keys and
@@ -154,7 +194,9 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   constexpr bool KDA = F::KDA;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ u64 words[64];
-  __shared__ float root[64], beta[64], alpha[64];
+  // what a node's sums with the state are multiplied by: bf16 keys by c, others by
+  // what undoes their rows' scales
+  __shared__ float root[2][64], beta[64], alpha[64];
   __shared__ int depth[64], order[64], level_end[65], bad;
   __shared__ alignas(4) unsigned char path[64][64];  // ancestors, the parent first
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -220,16 +262,15 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   if (S) {
 #pragma unroll
     for (int ks = 0; ks < AHEAD; ++ks) load(ks);
-    if (AHEAD < KS && tid == 0)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(S), "n"(DK * DV * 4));
+    if (AHEAD < KS && tid == 0) prefetch_l2<DK * DV * 4>(S);
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  if constexpr (KDA)  // each thread what it has brought itself
-    for (int e = tid; e < NT * (DK / 4); e += THREADS) {
-      float4 *at = reinterpret_cast<float4 *>(raw_a) + e;
-      const float4 g = *at;
-      *at = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
-    }
+  // and to L2 the state of a block that starts when this one ends: without it
+  // all blocks that run at a time load together and then compute together
+  if (tid == THREADS - 1 && blockIdx.x + kBlocksAtOnce < gridDim.x) {
+    const int b = blockIdx.x + kBlocksAtOnce;
+    const float *later = p.state_in[b / p.H];
+    if (later) prefetch_l2<DK * DV * 4>(later + (long long)(b % p.H) * DK * DV);
+  }
   __syncthreads();
 
   // the tree: its words have to be those of a tree; nodes in order of depth
@@ -248,6 +289,7 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   __syncthreads();
   if (bad) {
     if (tid == 0) set_error(p.err, kDevBadTree);
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
   if (tid < n) {
@@ -260,6 +302,14 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
     if (before == n - 1) level_end[depth[tid]] = n;
     if (before == shallower && depth[tid] > 0) level_end[depth[tid] - 1] = before;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (KDA)  // each thread what it has brought itself
+    for (int e = tid; e < NT * (DK / 4); e += THREADS) {
+      float4 *at = reinterpret_cast<float4 *>(raw_a) + e;
+      const float4 g = *at;
+      *at = make_float4(expf(g.x), expf(g.y), expf(g.z), expf(g.w));
+    }
+  __syncthreads();
 
   if constexpr (F::kPlain) {
     // all products of keys (and queries) with keys
@@ -267,33 +317,48 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
     const int mt = (2 * NT + 15) / 16, nt = (n + 15) / 16;
     for (int tile = warp; tile < mt * nt; tile += WARPS) {
       const int m0 = tile / nt * 16, n0 = tile % nt * 16;
-      float g[2][4] = {};
+      float g[4][4] = {};  // two chains of each half
 #pragma unroll
       for (int ks = 0; ks < DK / 16; ++ks) {
         uint32_t a[4], b[4];
         ldsm4(a, op_s + (m0 + (lane & 15)) * F::PITCH + (ks * 16 + (lane >> 4) * 8) * 2);
         ldsm4(b, op_s + (n0 + (lane & 7) + ((lane >> 4) << 3)) * F::PITCH +
                      (ks * 16 + ((lane >> 3) & 1) * 8) * 2);
-        mma16816(g[0], a, b[0], b[1]);
-        mma16816(g[1], a, b[2], b[3]);
+        mma16816(g[ks & 2], a, b[0], b[1]);
+        mma16816(g[(ks & 2) + 1], a, b[2], b[3]);
       }
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
         const int r = m0 + (lane >> 2) + (x & 2) * 4, j = n0 + (x >> 2) * 8 + (lane & 3) * 2 + (x & 1);
         const int t = r < NT ? r : r - NT;
-        if (t < n && j <= t) (r < NT ? ck : cq)[tri(t) + j] = g[x >> 2][x & 3];
+        if (t < n && j <= t) (r < NT ? ck : cq)[tri(t) + j] = g[x >> 2][x & 3] + g[2 + (x >> 2)][x & 3];
       }
     }
     __syncthreads();
     if (tid < n) {
       float w = alpha[tid];
-      for (int l = 0; l < depth[tid]; ++l) {
-        const int j = path[tid][l];
-        ck[tri(tid) + j] *= w;
-        cq[tri(tid) + j] *= w;
-        w *= alpha[j];
+      const int len = depth[tid];
+      float *const k_row = ck + tri(tid), *const q_row = cq + tri(tid);
+      for (int l = 0; l < len; l += 4) {
+        const uint32_t js = *reinterpret_cast<const uint32_t *>(&path[tid][l]);
+        float a[4], x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = l + i < len ? js >> (8 * i) & 0xff : tid;
+          a[i] = alpha[j];
+          x[i] = k_row[j];
+          y[i] = q_row[j];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (l + i >= len) break;
+          const int j = js >> (8 * i) & 0xff;
+          k_row[j] = x[i] * w;
+          q_row[j] = y[i] * w;
+          w *= a[i];
+        }
       }
-      root[tid] = w;
+      root[0][tid] = root[1][tid] = w;
     }
   } else {
     // one path a warp
@@ -347,18 +412,25 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
       }
       // the operands: c k and c q in parts
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x) {
+        float y[PER], m = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          y[i] = (x ? qt[i] : kt[i]) * w[i];
+          m = fmaxf(m, finite(y[i]));
+        }
+        const float scale = scale_of(m);
 #pragma unroll
         for (int i = 0; i < PER; i += 2) {
-          const float *y = x ? qt : kt;
-          uint32_t part[3];
-          split3(y[i] * w[i], y[i + 1] * w[i + 1], part);
+          uint32_t part[2];
+          split(y[i] * scale, y[i + 1] * scale, part);
 #pragma unroll
-          for (int k = 0; k < 3; ++k)
+          for (int k = 0; k < 2; ++k)
             *reinterpret_cast<uint32_t *>(op + k * op_bytes + (x * NT + t) * F::PITCH +
                                           (lane * PER + i) * 2) = part[k];
         }
-      if (lane == 0) root[t] = 1.f;
+        if (lane == 0) root[x][t] = inverse(scale);
+      }
     }
   }
   __syncthreads();
@@ -366,7 +438,7 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   // ---- S_0^T of the operands, 16 nodes at a time
   const uint32_t op_s = smem_u32(op);
   for (int c0 = 0; c0 < n; c0 += 16) {
-    float acc[TILES][4][4] = {};
+    float acc[TILES][4][4] = {}, scale = 1.f;
     if (S) {
       if (c0 > 0) {
 #pragma unroll
@@ -374,15 +446,46 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
       }
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
+        float4 (&xs)[4] = x[ks % AHEAD];
+        if constexpr (!F::kPlain) {
+          // numbers up to 2^15 after scaling; the scale follows the state's size
+          float m = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            m = fmaxf(fmaxf(m, fmaxf(fabsf(xs[i].x), fabsf(xs[i].y))),
+                      fmaxf(fabsf(xs[i].z), fabsf(xs[i].w)));
+          if (__any_sync(0xffffffffu, ks == 0 || !(m * scale < 32768.f))) {
+            m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              m = fmaxf(fmaxf(m, fmaxf(finite(xs[i].x), finite(xs[i].y))),
+                        fmaxf(finite(xs[i].z), finite(xs[i].w)));
+            const float next = scale_of(m);
+            if (ks == 0 || next < scale) {
+              const float f = ks == 0 ? 1.f : next * inverse(scale);
+              scale = next;
+#pragma unroll
+              for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) acc[t][i][y] *= f;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            xs[i].x *= scale; xs[i].y *= scale; xs[i].z *= scale; xs[i].w *= scale;
+          }
+        }
         // column product i, k pair y: parts
-        uint32_t b[4][2][3];
+        uint32_t b[4][2][F::STATE_PARTS];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float4 &lo = x[ks % AHEAD][2 * y], &hi = x[ks % AHEAD][2 * y + 1];
-          split3(lo.x, hi.x, b[0][y]);
-          split3(lo.y, hi.y, b[1][y]);
-          split3(lo.z, hi.z, b[2][y]);
-          split3(lo.w, hi.w, b[3][y]);
+          const float4 &lo = xs[2 * y], &hi = xs[2 * y + 1];
+          split(lo.x, hi.x, b[0][y]);
+          split(lo.y, hi.y, b[1][y]);
+          split(lo.z, hi.z, b[2][y]);
+          split(lo.w, hi.w, b[3][y]);
         }
         if (ks + AHEAD < KS) load(ks + AHEAD);
 #pragma unroll
@@ -394,15 +497,18 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
             uint32_t a[4];
             ldsm4(a, at + pa * op_bytes);
 #pragma unroll
-            for (int pb = 0; pb < 3; ++pb) {
-              if (pa + pb > 2) continue;
+            for (int pb = 0; pb < F::STATE_PARTS; ++pb) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma16816(acc[m][i], a, b[i][0][pb], b[i][1][pb]);
+              for (int i = 0; i < 4; ++i) {
+                if constexpr (F::kPlain) mma16816(acc[m][i], a, b[i][0][pb], b[i][1][pb]);
+                else if (pa + pb < 2) mma16816_f16(acc[m][i], a, b[i][0][pb], b[i][1][pb]);
+              }
             }
           }
         }
       }
     }
+    const float unscale = F::kPlain ? 1.f : inverse(scale);
     // a lane's 8 columns of rows lane / 4 and + 8: the halves of the state are added
     // in turn
 #pragma unroll
@@ -424,12 +530,12 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
             float o[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              o[i] = acc[m][i][2 * y];
-              o[4 + i] = acc[m][i][2 * y + 1];
+              o[i] = acc[m][i][2 * y] * unscale;
+              o[4 + i] = acc[m][i][2 * y + 1] * unscale;
             }
             float4 *d4 = reinterpret_cast<float4 *>(dst);
             if (turn == 0) {
-              const float w = root[t];
+              const float w = root[is_q][t];
               const float4 u0 = d4[0], u1 = d4[1];
               o[0] = (o[0] + u0.x) * w; o[1] = (o[1] + u0.y) * w;
               o[2] = (o[2] + u0.z) * w; o[3] = (o[3] + u0.w) * w;
@@ -457,16 +563,22 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   auto along = [&](float4 x, const float *coef, int t, int len, float sign) {
     for (int l = 0; l < len; l += 4) {
       const uint32_t js = *reinterpret_cast<const uint32_t *>(&path[t][l]);
+      // all four at once; beyond the path, the first again by 0
+      float w[4];
+      float4 d[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (l + i >= len) break;
-        const int j = js >> (8 * i) & 0xff;
-        const float w = sign * coef[j];
-        const float4 d = *reinterpret_cast<const float4 *>(uk + j * UP + c);
-        x.x = fmaf(w, d.x, x.x);
-        x.y = fmaf(w, d.y, x.y);
-        x.z = fmaf(w, d.z, x.z);
-        x.w = fmaf(w, d.w, x.w);
+        const int j = js >> (l + i < len ? 8 * i : 0) & 0xff;
+        w[i] = l + i < len ? sign * coef[j] : 0.f;
+        d[i] = *reinterpret_cast<const float4 *>(uk + j * UP + c);
+        if (i > 0 && l + i >= len) d[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x.x = fmaf(w[i], d[i].x, x.x);
+        x.y = fmaf(w[i], d[i].y, x.y);
+        x.z = fmaf(w[i], d[i].z, x.z);
+        x.w = fmaf(w[i], d[i].w, x.w);
       }
     }
     return x;
