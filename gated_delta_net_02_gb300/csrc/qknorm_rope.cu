@@ -12,7 +12,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of qknorm_kernel
 
 struct NormParams {
   const void *qw, *kw;
@@ -85,54 +85,79 @@ __global__ void __launch_bounds__(kThreads) qknorm_kernel(const RopeParams p, co
   }
 }
 
-// Persistent blocks; a token's rows pass through shared memory by bulk copies
-// both ways, a ring of kStages groups of tpb tokens, as in rope_append.cu. A
-// head's row is the work of D / (2 x 16 bytes) lanes, each with two vectors of 16
-// bytes that lie half a rotation apart (so that partners meet in one lane), in
-// registers from the sum of squares to the rotation.
+// Persistent warps, each on its own: a warp's tokens pass through its ring of
+// kStages groups of tpb tokens in shared memory, by bulk copies both ways, and no
+// warp waits for another (with a block on a token, as in rope_append.cu, its 18
+// heads of 256 made two unequal rounds between two barriers: 217 us on 34739
+// tokens). A head's row is the work of D / (2 x 16 bytes) lanes, each with two
+// vectors of 16 bytes that lie half a rotation apart (so that partners meet in one
+// lane), in registers from the sum of squares to the rotation.
 constexpr int kStages = 3;
-constexpr int kRowBlocks = 4;
-constexpr int kStageBytes = 16 * 1024;
+constexpr int kMostWarps = 16;
+constexpr int kStageBytes = 4 * 1024;  // of a group of tokens with short rows
 constexpr int kMostTokens = 8;
+constexpr int kMostAngles = 4;         // of a lane and group
 constexpr int kRowsSmem = 220 * 1024;
+
+// Two numbers to an instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, u, v;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\t"
+      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 w, u, v, w;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
 
 // How a rotation meets the vectors of a head: whole vectors of two halves, of
 // neighbouring pairs, or pairs of two halves that cut a vector.
 enum Meet { kHalves, kNeighbours, kCut };
 
 template <typename T, int D, Meet MEET>
-__global__ void __launch_bounds__(kThreads, kRowBlocks)
+__global__ void __launch_bounds__(32 * kMostWarps)
     qknorm_rows_kernel(const RopeParams p, const NormParams n, uint32_t q_bytes, uint32_t kv_bytes,
-                       int tpb, FastDiv by_heads) {
+                       int tpb, int warp_bytes, FastDiv by_q, FastDiv by_kv, FastDiv by_half) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int VE = 16 / (int)sizeof(T), LPR = D / VE / 2;  // lanes of a head's row
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint64_t full[kStages];
-  const int tid = threadIdx.x, half = p.rot >> 1;
+  extern __shared__ __align__(128) unsigned char smem_all[];
+  __shared__ uint64_t full_all[kMostWarps][kStages];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = p.rot >> 1;
+  uint64_t *const full = full_all[warp];
+  unsigned char *const smem = smem_all + (size_t)warp * warp_bytes;
   const uint32_t row = q_bytes + 2 * kv_bytes, stage = tpb * row;
-  // sines and cosines of two groups of tokens, [tpb][half] each
-  float *trig = reinterpret_cast<float *>(smem + kStages * stage);
-  if (tid == 0) {
+  // sines and cosines of a group of tokens, [tpb][half] each
+  float *const cs0 = reinterpret_cast<float *>(smem + kStages * stage), *const sn0 = cs0 + tpb * half;
+  if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
     fence_mbar_init();
   }
-  __syncthreads();
+  __syncwarp();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int groups = (p.n_tokens + tpb - 1) / tpb, heads = p.H + p.H_kv;
-  auto group_of = [&](int it) { return (long long)blockIdx.x + (long long)it * gridDim.x; };
+  const int groups = (p.n_tokens + tpb - 1) / tpb;
+  const long long first = (long long)warp * gridDim.x + blockIdx.x,
+                  step = (long long)gridDim.x * (blockDim.x >> 5);
+  auto group_of = [&](int it) { return first + it * step; };
   auto tokens_of = [&](long long g) {
     return g < groups ? min(tpb, p.n_tokens - (int)g * tpb) : 0;
   };
-  // a lane of warp 0 for each token of a group
+  // a lane for each token of a group
   auto load = [&](int it) {
     const long long g = group_of(it);
     const int nt = tokens_of(g), s = it % kStages;
     if (nt == 0) return;
-    if (tid == 0) mbar_arrive_expect_tx(&full[s], nt * row);
+    if (lane == 0) mbar_arrive_expect_tx(&full[s], nt * row);
     __syncwarp();
-    if (tid < nt) {
-      const long long tok = g * tpb + tid;
-      unsigned char *st = smem + s * stage + tid * row;
+    if (lane < nt) {
+      const long long tok = g * tpb + lane;
+      unsigned char *st = smem + s * stage + lane * row;
       bulk_g2s(st, static_cast<const T *>(p.q) + tok * p.q_stride, q_bytes, &full[s]);
       bulk_g2s(st + q_bytes, static_cast<const T *>(p.k) + tok * p.k_stride, kv_bytes, &full[s]);
       bulk_g2s(st + q_bytes + kv_bytes, static_cast<const T *>(p.v) + tok * p.v_stride, kv_bytes,
@@ -141,203 +166,221 @@ __global__ void __launch_bounds__(kThreads, kRowBlocks)
   };
   auto slot_of = [&](int it) -> long long {
     const long long g = group_of(it);
-    return tid < tokens_of(g) ? p.slots[g * tpb + tid] : -1;
+    return lane < tokens_of(g) ? p.slots[g * tpb + lane] : -1;
   };
-  long long slot = -1;
-  if (tid < 32) {
-    for (int it = 0; it < kStages - 1; ++it) load(it);
-    slot = slot_of(0);
-  }
+  for (int it = 0; it < kStages - 1; ++it) load(it);
+  long long slot = slot_of(0);
   // the lane's two vectors of a head, from these elements on
-  const int l = tid % LPR;
+  const int l = lane % LPR;
   int at_a = 2 * l * VE, at_b = at_a + VE;
   if (MEET == kHalves) {
     const int turning = half / VE;
     at_a = l < turning ? l * VE : p.rot + 2 * (l - turning) * VE;
     at_b = l < turning ? at_a + half : at_a + VE;
   }
-  // their weights, as they are stored
-  uint4 wq[2], wk[2];
+  // a vector's factors, as they are stored
+  auto weights = [&](const void *w, int at) {
+    return *reinterpret_cast<const uint4 *>(static_cast<const T *>(w) + at);
+  };
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  const uint4 wq[2] = {n.qw ? weights(n.qw, at_a) : none, n.qw ? weights(n.qw, at_b) : none};
+  const uint4 wk[2] = {n.kw ? weights(n.kw, at_a) : none, n.kw ? weights(n.kw, at_b) : none};
+  // A lane has the same pairs of the same tokens of each group: their axes and
+  // frequencies stay, their positions are read a group ahead.
+  float freq[kMostAngles];
+  int my_j[kMostAngles], my_axis[kMostAngles], pos[kMostAngles];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int at = i ? at_b : at_a;
-    if (n.qw) wq[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(n.qw) + at);
-    if (n.kw) wk[i] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(n.kw) + at);
+  for (int x = 0; x < kMostAngles; ++x) {
+    const int e = lane + 32 * x;
+    my_j[x] = tpb;
+    if (e < tpb * half) {
+      my_j[x] = by_half.div(e);
+      const int i = e - my_j[x] * half;
+      my_axis[x] = axis_of(p, i);
+      freq[x] = p.inv_freq[i];
+    }
   }
-  // A thread has one pair of one token of each group (tpb * half threads do):
-  // its axis and frequency stay, its position is read a group ahead.
-  const int my_j = half > 0 ? tid / half : tpb, my_i = tid - my_j * half;
-  const int32_t *my_pos = nullptr;
-  float freq = 0.f;
-  if (my_j < tpb) {
-    my_pos = p.positions + (long long)axis_of(p, my_i) * p.n_tokens + my_j;
-    freq = p.inv_freq[my_i];
-  }
-  auto position = [&](int it) -> int {
+  auto positions = [&](int it) {
     const long long g = group_of(it);
-    return my_j < tokens_of(g) ? my_pos[g * tpb] : 0;
+    const int nt = tokens_of(g);
+#pragma unroll
+    for (int x = 0; x < kMostAngles; ++x)
+      if (my_j[x] < nt)
+        pos[x] = p.positions[(long long)my_axis[x] * p.n_tokens + g * tpb + my_j[x]];
   };
-  int pos = position(0);
-  auto angles = [&](int it) {
-    float *cs = trig + (it & 1) * 2 * tpb * half, *sn = cs + tpb * half;
-    const int next = position(it + 1);
-    if (my_j < tpb) sincospif(2.f * reduced_turns(pos, freq), &sn[tid], &cs[tid]);
-    pos = next;
-  };
+  positions(0);
   int it = 0;
-  for (long long g = blockIdx.x; g < groups; g += gridDim.x, ++it) {
+  for (long long g = first; g < groups; g += step, ++it) {
     const int s = it % kStages, nt = tokens_of(g);
     const long long next_slot = slot_of(it + 1);
-    angles(it);
+#pragma unroll
+    for (int x = 0; x < kMostAngles; ++x)
+      if (my_j[x] < nt)
+        sincospif(2.f * reduced_turns(pos[x], freq[x]), &sn0[lane + 32 * x], &cs0[lane + 32 * x]);
+    positions(it + 1);
     const bool ok = mbar_wait(&full[s], (it / kStages) & 1, p.err, kSiteRopeRow);
-    if (__syncthreads_or(!ok)) {
-      if (tid == 0)  // the stages loaded ahead
+    if (!__all_sync(0xffffffffu, ok)) {
+      if (lane == 0)  // the stages loaded ahead
         for (int i = it; i < it + kStages - 1 && group_of(i) < groups; ++i)
           mbar_drain(&full[i % kStages], (i / kStages) & 1);
       break;
     }
-    const float *cs0 = trig + (it & 1) * 2 * tpb * half, *sn0 = cs0 + tpb * half;
     unsigned char *st = smem + s * stage;
-    const int rows = nt * heads;
-    // a warp's lanes stay together: the sums pass between them
-    for (int r0 = (tid & ~31) / LPR; r0 < rows; r0 += kThreads / LPR) {
-      const int r = r0 + (tid & 31) / LPR;
-      const bool live = r < rows;
-      const int j = by_heads.div(live ? r : 0), h = (live ? r : 0) - j * heads;
-      T *head = reinterpret_cast<T *>(st + j * row) + h * D;
-      Vec16<T> a, b;
-      a.load(head + at_a);
-      b.load(head + at_b);
-      float sum = 0.f;
+    // The rows of q (k) heads, h0 .. h0 + H of each token.
+    auto norm_rows = [&](int h0, int H, const FastDiv &by_H, const void *weight, const uint4 (&w)[2]) {
+      // offset + weight, for the lane's two vectors; 1 without a weight
+      float2 f[VE];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) sum = fmaf(a.v[i], a.v[i], fmaf(b.v[i], b.v[i], sum));
+      for (int x = 0; x < 2; ++x) {
+        Vec16<T> v;
+        v.unpack(w[x]);
+        const float base = weight ? n.offset : 1.f;
 #pragma unroll
-      for (int off = LPR / 2; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      const float inv = 1.f / sqrtf(sum * (1.f / D) + n.eps);
-      const bool is_q = h < p.H;
-      if (is_q ? n.qw != nullptr : n.kw != nullptr) {
-        Vec16<T> w;
-        const float base = n.offset * inv;
-        w.unpack(is_q ? wq[0] : wk[0]);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) a.v[i] *= fmaf(w.v[i], inv, base);
-        w.unpack(is_q ? wq[1] : wk[1]);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) b.v[i] *= fmaf(w.v[i], inv, base);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          a.v[i] *= inv;
-          b.v[i] *= inv;
-        }
+        for (int i = 0; i < VE; i += 2)
+          f[(x * VE + i) / 2] = make_float2(base + v.v[i], base + v.v[i + 1]);
       }
-      const float *cs = cs0 + j * half, *sn = sn0 + j * half;
-      if constexpr (MEET == kHalves) {
-        if (at_a < half) {
+      const int rows = nt * H;
+#pragma unroll 2
+      for (int r0 = 0; r0 < rows; r0 += 32 / LPR) {
+        const int r = r0 + lane / LPR;
+        const bool live = r < rows;
+        const int j = by_H.div(live ? r : 0), h = h0 + (live ? r : 0) - j * H;
+        T *head = reinterpret_cast<T *>(st + j * row) + h * D;
+        Vec16<T> a, b;
+        a.load(head + at_a);
+        b.load(head + at_b);
+        float2 y[VE];  // the two vectors' pairs
+#pragma unroll
+        for (int i = 0; i < VE; i += 2) {
+          y[i / 2] = make_float2(a.v[i], a.v[i + 1]);
+          y[(VE + i) / 2] = make_float2(b.v[i], b.v[i + 1]);
+        }
+        float2 squares = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) squares = fma2(y[i], y[i], squares);
+        float sum = squares.x + squares.y;
+#pragma unroll
+        for (int off = LPR / 2; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        const float inv = rsqrtf(fmaf(sum, 1.f / D, n.eps));
+#pragma unroll
+        for (int i = 0; i < VE; ++i) y[i] = mul2(y[i], mul2(f[i], make_float2(inv, inv)));
+        const float *cs = cs0 + j * half, *sn = sn0 + j * half;
+        if constexpr (MEET == kHalves) {
+          if (at_a < half) {
+#pragma unroll
+            for (int i = 0; i < VE; i += 2) {
+              const float2 c = *reinterpret_cast<const float2 *>(cs + at_a + i);
+              const float2 t = *reinterpret_cast<const float2 *>(sn + at_a + i);
+              const float2 u = y[i / 2], v = y[(VE + i) / 2];
+              y[i / 2] = fma2(make_float2(-v.x, -v.y), t, mul2(u, c));
+              y[(VE + i) / 2] = fma2(u, t, mul2(v, c));
+            }
+          }
+        } else if constexpr (MEET == kNeighbours) {
+          // a vector's pairs stand side by side, at_b behind at_a
+          const int pair0 = at_a >> 1;
 #pragma unroll
           for (int i = 0; i < VE; ++i) {
-            const float c = cs[at_a + i], t = sn[at_a + i], x = a.v[i] * c - b.v[i] * t;
-            b.v[i] = a.v[i] * t + b.v[i] * c;
-            a.v[i] = x;
+            if (pair0 + i >= half) break;
+            const float c = cs[pair0 + i], t = sn[pair0 + i];
+            y[i] = fma2(make_float2(-y[i].y, y[i].x), make_float2(t, t),
+                        mul2(y[i], make_float2(c, c)));
           }
         }
-      } else if constexpr (MEET == kNeighbours) {
-        auto turn = [&](Vec16<T> &x, int at) {
+        if constexpr (MEET != kCut) {
 #pragma unroll
           for (int i = 0; i < VE; i += 2) {
-            if (at + i >= p.rot) break;
-            const float c = cs[(at + i) >> 1], t = sn[(at + i) >> 1];
-            const float y = x.v[i] * c - x.v[i + 1] * t;
-            x.v[i + 1] = x.v[i] * t + x.v[i + 1] * c;
-            x.v[i] = y;
+            a.v[i] = y[i / 2].x;
+            a.v[i + 1] = y[i / 2].y;
+            b.v[i] = y[(VE + i) / 2].x;
+            b.v[i + 1] = y[(VE + i) / 2].y;
           }
-        };
-        turn(a, at_a);
-        turn(b, at_b);
-      }
-      if constexpr (MEET != kCut) {
-        if (live) {
-          a.store(head + at_a);
-          b.store(head + at_b);
-        }
-      } else {
-        // the partners lie in other lanes' vectors: read again, once the row's
-        // sum is known, and normed one by one
-        auto normed = [&](int d) {
-          const T *w = static_cast<const T *>(is_q ? n.qw : n.kw);
-          const float y = to_f32(head[d]) * inv;
-          return w ? y * (n.offset + to_f32(w[d])) : y;
-        };
-        __syncwarp();
-        if (live) {
-          for (int i = l; i < half; i += LPR) {
-            const float x = normed(i), y = normed(i + half), c = cs[i], t = sn[i];
-            head[i] = from_f32<T>(x * c - y * t);
-            head[i + half] = from_f32<T>(x * t + y * c);
+          if (live) {
+            a.store(head + at_a);
+            b.store(head + at_b);
           }
-          for (int d = p.rot + l; d < D; d += LPR) head[d] = from_f32<T>(normed(d));
+        } else {
+          // the partners lie in other lanes' vectors: read again, once the row's
+          // sum is known, and normed one by one
+          auto normed = [&](int d) {
+            const float x = to_f32(head[d]) * inv;
+            return weight ? x * (n.offset + to_f32(static_cast<const T *>(weight)[d])) : x;
+          };
+          __syncwarp();
+          if (live) {
+            for (int i = l; i < half; i += LPR) {
+              const float u = normed(i), v = normed(i + half), c = cs[i], t = sn[i];
+              head[i] = from_f32<T>(u * c - v * t);
+              head[i + half] = from_f32<T>(u * t + v * c);
+            }
+            for (int d = p.rot + l; d < D; d += LPR) head[d] = from_f32<T>(normed(d));
+          }
         }
       }
-    }
+    };
+    norm_rows(0, p.H, by_q, n.qw, wq);
+    norm_rows(p.H, p.H_kv, by_kv, n.kw, wk);
     fence_proxy_async();
-    __syncthreads();
-    if (tid < 32) {
-      if (tid < nt) {
-        const long long tok = g * tpb + tid;
-        const unsigned char *src = st + tid * row;
-        bulk_s2g(static_cast<T *>(p.q_out) + tok * p.H * D, src, q_bytes);
-        if (slot >= p.n_slots) {
-          set_error(p.err, kDevBadSlot);
-        } else if (slot >= 0) {
-          const long long at = slot_offset(p, slot);
-          T *kd = static_cast<T *>(p.k_cache) + at, *vd = static_cast<T *>(p.v_cache) + at;
-          // a slot's heads are one run of the cache unless its layout parts them
-          const int runs = p.head_stride == D ? 1 : p.H_kv;
-          const uint32_t bytes = kv_bytes / runs;
-          for (int r = 0; r < runs; ++r) {
-            bulk_s2g(kd + r * p.head_stride, src + q_bytes + r * bytes, bytes);
-            bulk_s2g(vd + r * p.head_stride, src + q_bytes + kv_bytes + r * bytes, bytes);
-          }
+    __syncwarp();
+    if (lane < nt) {
+      const long long tok = g * tpb + lane;
+      const unsigned char *src = st + lane * row;
+      bulk_s2g(static_cast<T *>(p.q_out) + tok * p.H * D, src, q_bytes);
+      if (slot >= p.n_slots) {
+        set_error(p.err, kDevBadSlot);
+      } else if (slot >= 0) {
+        const long long at = slot_offset(p, slot);
+        T *kd = static_cast<T *>(p.k_cache) + at, *vd = static_cast<T *>(p.v_cache) + at;
+        // a slot's heads are one run of the cache unless its layout parts them
+        const int runs = p.head_stride == D ? 1 : p.H_kv;
+        const uint32_t bytes = kv_bytes / runs;
+        for (int r = 0; r < runs; ++r) {
+          bulk_s2g(kd + r * p.head_stride, src + q_bytes + r * bytes, bytes);
+          bulk_s2g(vd + r * p.head_stride, src + q_bytes + kv_bytes + r * bytes, bytes);
         }
       }
-      bulk_commit();
-      slot = next_slot;
-      // the stage loaded next was stored from an iteration ago: all but the
-      // stores just issued have read theirs
-      bulk_wait_read_but1();
-      __syncwarp();
-      load(it + kStages - 1);
     }
+    bulk_commit();
+    slot = next_slot;
+    // the stage loaded next was stored from an iteration ago: all but the
+    // stores just issued have read theirs
+    bulk_wait_read_but1();
+    __syncwarp();
+    load(it + kStages - 1);
   }
-  if (tid < 32) bulk_wait_all();
+  bulk_wait_all();
 }
 
 template <typename T, int D>
 cudaError_t launch_d(const RopeParams &p, const NormParams &n, cudaStream_t stream) {
   constexpr int VE = 16 / (int)sizeof(T);
   const long long row = (long long)(p.H + 2 * p.H_kv) * D * (int)sizeof(T);
-  if (row * kStages + 4 * (p.rot / 2) * 4 > kRowsSmem)  // rows too long for the ring
+  const int half = p.rot / 2;
+  // a warp's ring and its angles; bulk copies want 16 bytes
+  auto bytes_of = [&](long long tpb) { return row * kStages * tpb + (8 * tpb * half + 15) / 16 * 16; };
+  if (bytes_of(1) > kRowsSmem)  // rows too long for the ring
     return launch_pdl(qknorm_kernel<T, D>, dim3(p.n_tokens), dim3(kThreads), 0, stream, p, n);
-  // tokens of a stage: a block each while there are blocks for them, and no
-  // more pairs in a group than threads
+  // tokens of a group: a warp each while there are warps for them
   int tpb = kStageBytes / row < kMostTokens ? (int)(kStageBytes / row) : kMostTokens;
-  while (tpb > 1 && (p.n_tokens < kRowBlocks * kSms * tpb || tpb * (p.rot / 2) > kThreads)) --tpb;
+  while (tpb > 1 && (p.n_tokens < kMostWarps * kSms * tpb || tpb * half > 32 * kMostAngles)) --tpb;
   if (tpb < 1) tpb = 1;
-  const int smem = (int)row * kStages * tpb + 4 * tpb * (p.rot / 2) * 4;
-  auto kernel = p.neighbours             ? qknorm_rows_kernel<T, D, kNeighbours>
-                : (p.rot / 2) % VE == 0 ? qknorm_rows_kernel<T, D, kHalves>
-                                         : qknorm_rows_kernel<T, D, kCut>;
+  const int warp_bytes = (int)bytes_of(tpb), groups = (p.n_tokens + tpb - 1) / tpb;
+  const int fit = kRowsSmem / warp_bytes, most = fit < kMostWarps ? fit : kMostWarps;
+  const int each = (groups + kSms - 1) / kSms, warps = each < most ? each : most;
+  const int blocks = (groups + warps - 1) / warps;
+  auto kernel = p.neighbours     ? qknorm_rows_kernel<T, D, kNeighbours>
+                : half % VE == 0 ? qknorm_rows_kernel<T, D, kHalves>
+                                 : qknorm_rows_kernel<T, D, kCut>;
   // as in rope_append.cu: less needs no leave, and the attribute is the process's
+  const int smem = warps * warp_bytes;
   if (smem > 47 * 1024) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
     if (e != cudaSuccess) return e;
   }
-  const int by_smem = kRowsSmem / (smem + 2048), per_sm = by_smem < kRowBlocks ? by_smem : kRowBlocks;
-  const int most = kSms * (per_sm < 1 ? 1 : per_sm), groups = (p.n_tokens + tpb - 1) / tpb;
-  return launch_pdl(kernel, dim3(groups < most ? groups : most), dim3(kThreads), smem, stream, p, n,
+  return launch_pdl(kernel, dim3(blocks < kSms ? blocks : kSms), dim3(32 * warps), smem, stream, p, n,
                     (uint32_t)(p.H * D * (int)sizeof(T)), (uint32_t)(p.H_kv * D * (int)sizeof(T)),
-                    tpb, FastDiv(p.H + p.H_kv));
+                    tpb, warp_bytes, FastDiv(p.H), FastDiv(p.H_kv), FastDiv(half > 0 ? half : 1));
 }
 
 template <typename T>
