@@ -12,89 +12,23 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;  // of qknorm_kernel
-
 struct NormParams {
   const void *qw, *kw;
   float eps, offset;
 };
 
-// Rows too long for the ring of qknorm_rows_kernel: one block a token, one warp a
-// head; partners of a pair are read again.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) qknorm_kernel(const RopeParams p, const NormParams n) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ float cs[D / 2], sn[D / 2];
-  __shared__ long long at_s;  // element offset of the slot, -1 = none
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, half = p.rot >> 1;
-  const long long tok = blockIdx.x;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int i = tid; i < half; i += kThreads) {
-    const int pos = p.positions[(long long)axis_of(p, i) * p.n_tokens + tok];
-    sincospif(2.f * reduced_turns(pos, p.inv_freq[i]), &sn[i], &cs[i]);
-  }
-  if (tid == 0) {
-    const long long slot = p.slots[tok];
-    at_s = -1;
-    if (slot >= p.n_slots) set_error(p.err, kDevBadSlot);
-    else if (slot >= 0) at_s = slot_offset(p, slot);
-  }
-  __syncthreads();
-  const long long at = at_s;
-  for (int r = warp; r < p.H + 2 * p.H_kv; r += kThreads / 32) {
-    const bool is_q = r < p.H, is_v = r >= p.H + p.H_kv;
-    const int h = is_q ? r : is_v ? r - p.H - p.H_kv : r - p.H;
-    if (!is_q && at < 0) continue;
-    const T *src;
-    T *dst;
-    if (is_q) {
-      src = static_cast<const T *>(p.q) + tok * p.q_stride + (long long)h * D;
-      dst = static_cast<T *>(p.q_out) + (tok * p.H + h) * D;
-    } else {
-      src = is_v ? static_cast<const T *>(p.v) + tok * p.v_stride + (long long)h * D
-                 : static_cast<const T *>(p.k) + tok * p.k_stride + (long long)h * D;
-      dst = static_cast<T *>(is_v ? p.v_cache : p.k_cache) + at + h * p.head_stride;
-    }
-    if (is_v) {
-      for (int d = lane; d < D; d += 32) dst[d] = src[d];
-      continue;
-    }
-    float sum = 0.f;
-    for (int d = lane; d < D; d += 32) {
-      const float x = to_f32(src[d]);
-      sum = fmaf(x, x, sum);
-    }
-#pragma unroll
-    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const float inv = 1.f / sqrtf(sum / D + n.eps);
-    const T *w = static_cast<const T *>(is_q ? n.qw : n.kw);
-    auto normed = [&](int d) {
-      const float y = to_f32(src[d]) * inv;
-      return w ? y * (n.offset + to_f32(w[d])) : y;
-    };
-    for (int d = lane; d < D; d += 32) {
-      float y = normed(d);
-      if (d < p.rot) {
-        const bool first = p.neighbours ? !(d & 1) : d < half;
-        const int f = p.neighbours ? d >> 1 : first ? d : d - half;
-        const float z = normed(p.neighbours ? d ^ 1 : first ? d + half : f);
-        y = first ? y * cs[f] - z * sn[f] : z * sn[f] + y * cs[f];
-      }
-      dst[d] = from_f32<T>(y);
-    }
-  }
-}
-
 // Persistent warps, each on its own: a warp's tokens pass through its ring of
-// kStages groups of tpb tokens in shared memory, by bulk copies both ways, and no
-// warp waits for another (with a block on a token, as in rope_append.cu, its 18
+// kStages units in shared memory, by bulk copies both ways; a unit is tpb tokens, or
+// one of `parts` runs of a long row's heads (of q, k and v in turn). No warp waits
+// for another (with a block on a token, as in rope_append.cu, its 18
 // heads of 256 made two unequal rounds between two barriers: 217 us on 34739
 // tokens). A head's row is the work of D / (2 x 16 bytes) lanes, each with two
 // vectors of 16 bytes that lie half a rotation apart (so that partners meet in one
 // lane), in registers from the sum of squares to the rotation.
 constexpr int kStages = 3;
 constexpr int kMostWarps = 16;
-constexpr int kStageBytes = 4 * 1024;  // of a group of tokens with short rows
+constexpr int kStageBytes = 4 * 1024;  // of a unit of short rows
+constexpr int kPartBytes = 5 * 1024;   // of a part of a long one: 14 warps have room
 constexpr int kMostTokens = 8;
 constexpr int kMostAngles = 4;         // of a lane and group
 constexpr int kRowsSmem = 220 * 1024;
@@ -123,8 +57,9 @@ enum Meet { kHalves, kNeighbours, kCut };
 
 template <typename T, int D, Meet MEET>
 __global__ void __launch_bounds__(32 * kMostWarps)
-    qknorm_rows_kernel(const RopeParams p, const NormParams n, uint32_t q_bytes, uint32_t kv_bytes,
-                       int tpb, int warp_bytes, FastDiv by_q, FastDiv by_kv, FastDiv by_half) {
+    qknorm_rows_kernel(const RopeParams p, const NormParams n, int tpb, int parts, int part_heads,
+                       int warp_bytes, FastDiv64 by_parts, FastDiv by_q, FastDiv by_kv,
+                       FastDiv by_half) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int VE = 16 / (int)sizeof(T), LPR = D / VE / 2;  // lanes of a head's row
   extern __shared__ __align__(128) unsigned char smem_all[];
@@ -132,7 +67,8 @@ __global__ void __launch_bounds__(32 * kMostWarps)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = p.rot >> 1;
   uint64_t *const full = full_all[warp];
   unsigned char *const smem = smem_all + (size_t)warp * warp_bytes;
-  const uint32_t row = q_bytes + 2 * kv_bytes, stage = tpb * row;
+  constexpr uint32_t kHead = D * sizeof(T);
+  const uint32_t row = part_heads * kHead, stage = tpb * row;
   // sines and cosines of a group of tokens, [tpb][half] each
   float *const cs0 = reinterpret_cast<float *>(smem + kStages * stage), *const sn0 = cs0 + tpb * half;
   if (lane == 0) {
@@ -141,35 +77,57 @@ __global__ void __launch_bounds__(32 * kMostWarps)
   }
   __syncwarp();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int groups = (p.n_tokens + tpb - 1) / tpb;
+  // the grid's units, token by token, taken in turn by its warps
+  const long long units = (long long)((p.n_tokens + tpb - 1) / tpb) * parts;
   const long long first = (long long)warp * gridDim.x + blockIdx.x,
                   step = (long long)gridDim.x * (blockDim.x >> 5);
-  auto group_of = [&](int it) { return first + it * step; };
-  auto tokens_of = [&](long long g) {
-    return g < groups ? min(tpb, p.n_tokens - (int)g * tpb) : 0;
+  struct Unit {
+    int tok, nt;  // first token, tokens (0: beyond the last unit)
+    int h0;       // first of its heads, those of q, k and v counted on
   };
-  // a lane for each token of a group
-  auto load = [&](int it) {
-    const long long g = group_of(it);
-    const int nt = tokens_of(g), s = it % kStages;
-    if (nt == 0) return;
-    if (lane == 0) mbar_arrive_expect_tx(&full[s], nt * row);
+  auto unit_of = [&](int it) {
+    const long long x = first + it * step;
+    if (x >= units) return Unit{0, 0, 0};
+    const int g = (int)(parts == 1 ? x : by_parts.div(x));
+    return Unit{g * tpb, min(tpb, p.n_tokens - g * tpb), (int)(x - (long long)g * parts) * part_heads};
+  };
+  // a unit's heads of those that begin at `from` and are n: the first and how many
+  auto heads_of = [&](const Unit &u, int from, int n) {
+    const int h = max(u.h0 - from, 0);
+    return make_int2(h, max(min(u.h0 + part_heads - from, n) - h, 0));
+  };
+  // a lane for each token of a unit
+  auto load = [&](const Unit &u, int it) {
+    const int s = it % kStages;
+    if (u.nt == 0) return;
+    const int2 q = heads_of(u, 0, p.H), k = heads_of(u, p.H, p.H_kv),
+               v = heads_of(u, p.H + p.H_kv, p.H_kv);
+    if (lane == 0) mbar_arrive_expect_tx(&full[s], u.nt * (q.y + k.y + v.y) * kHead);
     __syncwarp();
-    if (lane < nt) {
-      const long long tok = g * tpb + lane;
+    if (lane < u.nt) {
+      const long long tok = u.tok + lane;
       unsigned char *st = smem + s * stage + lane * row;
-      bulk_g2s(st, static_cast<const T *>(p.q) + tok * p.q_stride, q_bytes, &full[s]);
-      bulk_g2s(st + q_bytes, static_cast<const T *>(p.k) + tok * p.k_stride, kv_bytes, &full[s]);
-      bulk_g2s(st + q_bytes + kv_bytes, static_cast<const T *>(p.v) + tok * p.v_stride, kv_bytes,
-               &full[s]);
+      if (q.y)
+        bulk_g2s(st, static_cast<const T *>(p.q) + tok * p.q_stride + (long long)q.x * D,
+                 q.y * kHead, &full[s]);
+      if (k.y)
+        bulk_g2s(st + q.y * kHead,
+                 static_cast<const T *>(p.k) + tok * p.k_stride + (long long)k.x * D, k.y * kHead,
+                 &full[s]);
+      if (v.y)
+        bulk_g2s(st + (q.y + k.y) * kHead,
+                 static_cast<const T *>(p.v) + tok * p.v_stride + (long long)v.x * D, v.y * kHead,
+                 &full[s]);
     }
   };
-  auto slot_of = [&](int it) -> long long {
-    const long long g = group_of(it);
-    return lane < tokens_of(g) ? p.slots[g * tpb + lane] : -1;
+  auto slot_of = [&](const Unit &u) -> long long {
+    return lane < u.nt ? p.slots[u.tok + lane] : -1;
   };
-  for (int it = 0; it < kStages - 1; ++it) load(it);
-  long long slot = slot_of(0);
+  static_assert(kStages == 3, "two units ahead of the current one");
+  Unit u = unit_of(0), u1 = unit_of(1), u2 = unit_of(2);
+  load(u, 0);
+  load(u1, 1);
+  long long slot = slot_of(u);
   // the lane's two vectors of a head, from these elements on
   const int l = lane % LPR;
   int at_a = 2 * l * VE, at_b = at_a + VE;
@@ -200,33 +158,30 @@ __global__ void __launch_bounds__(32 * kMostWarps)
       freq[x] = p.inv_freq[i];
     }
   }
-  auto positions = [&](int it) {
-    const long long g = group_of(it);
-    const int nt = tokens_of(g);
+  auto positions = [&](const Unit &u) {
 #pragma unroll
     for (int x = 0; x < kMostAngles; ++x)
-      if (my_j[x] < nt)
-        pos[x] = p.positions[(long long)my_axis[x] * p.n_tokens + g * tpb + my_j[x]];
+      if (my_j[x] < u.nt)
+        pos[x] = p.positions[(long long)my_axis[x] * p.n_tokens + u.tok + my_j[x]];
   };
-  positions(0);
-  int it = 0;
-  for (long long g = first; g < groups; g += step, ++it) {
-    const int s = it % kStages, nt = tokens_of(g);
-    const long long next_slot = slot_of(it + 1);
+  positions(u);
+  for (int it = 0; u.nt > 0; ++it) {
+    const int s = it % kStages, nt = u.nt;
+    const long long next_slot = slot_of(u1);
 #pragma unroll
     for (int x = 0; x < kMostAngles; ++x)
       if (my_j[x] < nt)
         sincospif(2.f * reduced_turns(pos[x], freq[x]), &sn0[lane + 32 * x], &cs0[lane + 32 * x]);
-    positions(it + 1);
+    positions(u1);
     const bool ok = mbar_wait(&full[s], (it / kStages) & 1, p.err, kSiteRopeRow);
     if (!__all_sync(0xffffffffu, ok)) {
       if (lane == 0)  // the stages loaded ahead
-        for (int i = it; i < it + kStages - 1 && group_of(i) < groups; ++i)
+        for (int i = it; i < it + kStages - 1 && (i == it || u1.nt > 0); ++i)
           mbar_drain(&full[i % kStages], (i / kStages) & 1);
       break;
     }
     unsigned char *st = smem + s * stage;
-    // The rows of q (k) heads, h0 .. h0 + H of each token.
+    // H heads of each token of the unit, from its h0-th on.
     auto norm_rows = [&](int h0, int H, const FastDiv &by_H, const void *weight, const uint4 (&w)[2]) {
       // offset + weight, for the lane's two vectors; 1 without a weight
       float2 f[VE];
@@ -318,26 +273,32 @@ __global__ void __launch_bounds__(32 * kMostWarps)
         }
       }
     };
-    norm_rows(0, p.H, by_q, n.qw, wq);
-    norm_rows(p.H, p.H_kv, by_kv, n.kw, wk);
+    // (a part of a row has one token: all of its rows are below by_H's divisor)
+    const int2 qs = heads_of(u, 0, p.H), ks = heads_of(u, p.H, p.H_kv),
+               vs = heads_of(u, p.H + p.H_kv, p.H_kv);
+    norm_rows(0, qs.y, by_q, n.qw, wq);
+    norm_rows(qs.y, ks.y, by_kv, n.kw, wk);
     fence_proxy_async();
     __syncwarp();
     if (lane < nt) {
-      const long long tok = g * tpb + lane;
+      const long long tok = u.tok + lane;
       const unsigned char *src = st + lane * row;
-      bulk_s2g(static_cast<T *>(p.q_out) + tok * p.H * D, src, q_bytes);
+      if (qs.y)
+        bulk_s2g(static_cast<T *>(p.q_out) + (tok * p.H + qs.x) * D, src, qs.y * kHead);
       if (slot >= p.n_slots) {
         set_error(p.err, kDevBadSlot);
       } else if (slot >= 0) {
-        const long long at = slot_offset(p, slot);
-        T *kd = static_cast<T *>(p.k_cache) + at, *vd = static_cast<T *>(p.v_cache) + at;
         // a slot's heads are one run of the cache unless its layout parts them
-        const int runs = p.head_stride == D ? 1 : p.H_kv;
-        const uint32_t bytes = kv_bytes / runs;
-        for (int r = 0; r < runs; ++r) {
-          bulk_s2g(kd + r * p.head_stride, src + q_bytes + r * bytes, bytes);
-          bulk_s2g(vd + r * p.head_stride, src + q_bytes + kv_bytes + r * bytes, bytes);
-        }
+        const long long at = slot_offset(p, slot);
+        auto append = [&](void *cache, int2 heads, const unsigned char *from) {
+          T *to = static_cast<T *>(cache) + at + heads.x * p.head_stride;
+          const bool one = p.head_stride == D;
+          const int runs = one ? heads.y > 0 : heads.y;
+          const uint32_t bytes = one ? heads.y * kHead : kHead;
+          for (int r = 0; r < runs; ++r) bulk_s2g(to + r * p.head_stride, from + r * bytes, bytes);
+        };
+        append(p.k_cache, ks, src + qs.y * kHead);
+        append(p.v_cache, vs, src + (qs.y + ks.y) * kHead);
       }
     }
     bulk_commit();
@@ -346,7 +307,10 @@ __global__ void __launch_bounds__(32 * kMostWarps)
     // stores just issued have read theirs
     bulk_wait_read_but1();
     __syncwarp();
-    load(it + kStages - 1);
+    load(u2, it + 2);
+    u = u1;
+    u1 = u2;
+    u2 = unit_of(it + 3);
   }
   bulk_wait_all();
 }
@@ -356,18 +320,22 @@ cudaError_t launch_d(const RopeParams &p, const NormParams &n, cudaStream_t stre
   constexpr int VE = 16 / (int)sizeof(T);
   const long long row = (long long)(p.H + 2 * p.H_kv) * D * (int)sizeof(T);
   const int half = p.rot / 2;
-  // a warp's ring and its angles; bulk copies want 16 bytes
-  auto bytes_of = [&](long long tpb) { return row * kStages * tpb + (8 * tpb * half + 15) / 16 * 16; };
-  if (bytes_of(1) > kRowsSmem)  // rows too long for the ring
-    return launch_pdl(qknorm_kernel<T, D>, dim3(p.n_tokens), dim3(kThreads), 0, stream, p, n);
-  // tokens of a group: a warp each while there are warps for them
-  int tpb = kStageBytes / row < kMostTokens ? (int)(kStageBytes / row) : kMostTokens;
+  // parts of a token's row; tokens of a unit: a warp each while there are warps for them
+  const int heads = p.H + 2 * p.H_kv, head = D * (int)sizeof(T);
+  int parts = (int)((row + kPartBytes - 1) / kPartBytes);
+  const int part_heads = (heads + parts - 1) / parts;
+  parts = (heads + part_heads - 1) / part_heads;
+  int tpb = parts == 1 ? (int)(kStageBytes / row) : 1;
+  if (tpb > kMostTokens) tpb = kMostTokens;
   while (tpb > 1 && (p.n_tokens < kMostWarps * kSms * tpb || tpb * half > 32 * kMostAngles)) --tpb;
   if (tpb < 1) tpb = 1;
-  const int warp_bytes = (int)bytes_of(tpb), groups = (p.n_tokens + tpb - 1) / tpb;
+  const long long units = (long long)((p.n_tokens + tpb - 1) / tpb) * parts;
+  // a warp's ring and its angles; bulk copies want 16 bytes
+  const int warp_bytes = kStages * tpb * part_heads * head + (8 * tpb * half + 15) / 16 * 16;
   const int fit = kRowsSmem / warp_bytes, most = fit < kMostWarps ? fit : kMostWarps;
-  const int each = (groups + kSms - 1) / kSms, warps = each < most ? each : most;
-  const int blocks = (groups + warps - 1) / warps;
+  const long long each = (units + kSms - 1) / kSms;
+  const int warps = each < most ? (int)each : most;
+  const long long blocks = (units + warps - 1) / warps;
   auto kernel = p.neighbours     ? qknorm_rows_kernel<T, D, kNeighbours>
                 : half % VE == 0 ? qknorm_rows_kernel<T, D, kHalves>
                                  : qknorm_rows_kernel<T, D, kCut>;
@@ -378,9 +346,9 @@ cudaError_t launch_d(const RopeParams &p, const NormParams &n, cudaStream_t stre
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(kernel, dim3(blocks < kSms ? blocks : kSms), dim3(32 * warps), smem, stream, p, n,
-                    (uint32_t)(p.H * D * (int)sizeof(T)), (uint32_t)(p.H_kv * D * (int)sizeof(T)),
-                    tpb, warp_bytes, FastDiv(p.H), FastDiv(p.H_kv), FastDiv(half > 0 ? half : 1));
+  return launch_pdl(kernel, dim3(blocks < kSms ? (unsigned)blocks : kSms), dim3(32 * warps), smem,
+                    stream, p, n, tpb, parts, part_heads, warp_bytes, FastDiv64(parts), FastDiv(p.H),
+                    FastDiv(p.H_kv), FastDiv(half > 0 ? half : 1));
 }
 
 template <typename T>
