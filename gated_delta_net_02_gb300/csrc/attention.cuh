@@ -1371,6 +1371,453 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   if (warp == 8) tmem_dealloc(tm, C::TCOLS);
 }
 
+// ---- more rows (bf16): tiles of 128 rows and 128 keys, probabilities in tensor memory ----
+//
+// Rows x keys of more than a tile of 128 rows are bound by the products and the
+// exponentials together (128 rows, 128 keys, heads of 128: some 1,100 cycles of
+// products at the measured bf16 rate, 1,024 of exponentials), so neither may wait
+// for the other. Two tiles of scores are under way at any time: of two tiles of rows
+// (NQ = 2: every key and value then serves 256 rows), or, where the sums of one
+// tile fill half of tensor memory (heads of 256) or its rows are all there are, of
+// two tiles of keys. While one is turned into probabilities, the other's products
+// run. A lane of the four warps of a row tile has a whole row, so maximum and sum
+// need no other lane; probabilities go back to tensor memory over their scores, as
+// the next product's first operand, and cost no shared memory.
+// Scores overwrite the probabilities of the tile before (the one before that, with
+// two tiles of keys) once the product that reads those is over.
+template <int D_, int NQ_>
+struct WideCfg {
+  using In = __nv_bfloat16;
+  static constexpr bool kTensorMemory = true;
+  static constexpr int D = D_, NQ = NQ_, NS = NQ == 1 ? 2 : 1, KT = 128, ROWS = 128 * NQ;
+  // no more than three warps for each scheduler, so that a lane may hold a row's
+  // 128 scores
+  static constexpr int THREADS = 128 + 128 * NQ;
+  static constexpr int TILE = KT * D * 2, Q_BYTES = ROWS * D * 2;
+  static constexpr int FIT = (222 * 1024 - Q_BYTES) / TILE;
+  static constexpr int SLOTS = FIT > 8 ? 8 : FIT;  // tiles of K and V in turn
+  static constexpr int SMEM = SLOTS * TILE + Q_BYTES + 1024;
+  static constexpr int TCOLS = 512;  // sums, then two tiles of scores
+  static constexpr int PER_SM = 1;
+  static_assert(NQ * D + 256 <= TCOLS && SLOTS >= 2, "it fits");
+};
+
+// D[tmem] (+)= A[tmem] B[smem], A in the lanes of its rows, two bf16 a column; from a whole
+// converged warp, as umma_bf16_elect.
+__device__ __forceinline__ void umma_bf16_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                                   uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+
+// 64 columns in one load and one wait: a lane's values are valid when it retires.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]),
+        "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]),
+        "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]),
+        "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+        "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+        "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]),
+        "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
+        "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]),
+        "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
+        "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]),
+        "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
+        "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]),
+        "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Which of the 64 keys from `key` on a row sees, as bits (sees() for each).
+__device__ __forceinline__ unsigned long long seen64(int key, int lim, unsigned long long word) {
+  const int past = key - lim;  // of the limit
+  if (past <= -64) return ~0ull;
+  if (past < 0) return (word << -past) | ((1ull << -past) - 1);
+  return past < 64 ? word >> past : 0;
+}
+
+template <class C, bool TREE>
+__global__ void __launch_bounds__(C::THREADS, C::PER_SM)
+    attn_wide_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, int box) {
+  using T = __nv_bfloat16;
+  constexpr int D = C::D, KT = C::KT, NT = C::THREADS, U = C::SLOTS, NQ = C::NQ, NS = C::NS;
+  constexpr int CH = D / 8, CC = D / 64;  // 16-byte chunks and 64 columns of a row
+  extern __shared__ unsigned char raw[];
+  unsigned char *sm =
+      reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full[U], empty[U], s_full[2], p_full[2], o_done[NQ], o_free[NQ];
+  __shared__ uint64_t q_full, q_empty, landed, patched;
+  __shared__ long long warp_sum[NT / 32];
+  __shared__ Place place;
+  __shared__ uint32_t tm_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kIssuer = 3;  // warps: keys, queries (2), products, rows (4 NQ)
+  const uint32_t units_s = smem_u32(sm), q_s = units_s + U * C::TILE;
+  const int items_per_seq = p.H_kv * p.row_blocks.d;
+  if (tid == 0) {
+    for (int i = 0; i < U; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+    }
+    for (int i = 0; i < NQ; ++i) {
+      mbar_init(&o_done[i], 1);
+      mbar_init(&o_free[i], 4);
+    }
+    mbar_init(&q_full, 2);
+    mbar_init(&q_empty, 1);
+    mbar_init(&landed, 1);
+    mbar_init(&patched, 2);
+    fence_mbar_init();
+    prefetch_tmap(&mk);
+    prefetch_tmap(&mv);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // as attn_tc_kernel
+  if (warp == kIssuer) {
+    tmem_alloc(&tm_s, C::TCOLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tm = tm_s, tm_score = tm + NQ * D;
+
+  // Every role walks the block's items on its own.
+  Walk w{};
+  const bool any = w.begin<KT, NT>(p, items_per_seq, warp_sum, place);
+  if (!any && tid == 0 && !p.by_item) p.cut[blockIdx.x].x = -1;
+  int tb = 0, patches = 0;   // tiles and cleared tiles of the items before
+  int loaded = 0, used = 0;  // tiles of K and V loaded, and given back last, plus one
+  bool ok = any;
+  for (int seg = 0; ok && w.pos < w.end; ++seg) {
+    const int n = w.tiles(), s = w.s, len = w.len, tile0 = w.tile0;
+    const int kvh = p.row_blocks.div(w.x), r0 = (w.x - kvh * (int)p.row_blocks.d) * C::ROWS;
+    // the item's last tile is here, and ends inside a tile of V
+    const int patch_from = len - (tile0 + n - 1) * KT;
+    const bool patch = patch_from < KT;
+    if (warp == 0) {
+      if (lane == 0) w.list_join(p, items_per_seq, n);
+      // a lane's boxes of a tile: `box` tokens by 64 columns, CC of them side by side
+      const int32_t *table = p.table + (long long)s * p.max_pages;
+      const int boxes = KT / box * CC;
+      auto page_of = [&](int i, int e) -> int {
+        const int key = (tile0 + i) * KT + e / CC * box;
+        return e < boxes && i < n && key < len ? table[p.page_size.div(key)] : -1;
+      };
+      int page[2] = {page_of(0, lane), page_of(0, lane + 32)};
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        const int next[2] = {page_of(i + 1, lane), page_of(i + 1, lane + 32)};
+        bool live[2];
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int e = lane + 32 * x, key = (tile0 + i) * KT + e / CC * box;
+          live[x] = e < boxes && key < len;
+          if (live[x] && (page[x] < 0 || page[x] >= p.n_pages)) {
+            set_error(p.err, kDevBadPage);
+            live[x] = false;
+          }
+          bytes += __popc(__ballot_sync(0xffffffffu, live[x])) * box * 128;
+        }
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int u = 2 * (tb + i) + v, slot = u % U;
+          ok = ok && mbar_wait(&empty[slot], (u / U + 1) & 1, p.err, kSiteAttnTile);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+          __syncwarp();
+          loaded = u + 1;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int e = lane + 32 * x, j = e / CC, c = e % CC;
+            const int key = (tile0 + i) * KT + j * box;
+            if (live[x])
+              tma_load_4d(sm + slot * C::TILE + c * (KT * 128) + j * box * 128, v ? &mv : &mk, c * 64,
+                          kvh, key - p.page_size.div(key) * (int)p.page_size.d, page[x],
+                          &full[slot]);
+          }
+        }
+        page[0] = next[0];
+        page[1] = next[1];
+      }
+    } else if (warp < kIssuer) {
+      const int t64 = tid - 32;
+      const int nodes = TREE ? seq_nodes(p, s, w.x == 0 && tile0 == 0 && t64 == 0) : p.T;
+      ok = mbar_wait(&q_empty, (seg + 1) & 1, p.err, kSiteAttnTile);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+#pragma unroll 4
+        for (int e = t64; e < C::ROWS * CH; e += 64) {
+          const int r = e / CH, c = e % CH;
+          const long long row = out_row(p, s, kvh, r0 + r);
+          const bool live = row >= 0 && p.G.div(r0 + r) < nodes;
+          cp_async16(q_s + (r >> 7) * (128 * D * 2) + (c >> 3) * (128 * 128) + (r & 127) * 128 +
+                         (((c & 7) ^ (r & 7)) << 4),
+                     static_cast<const T *>(p.q) + (live ? row : 0) * D + c * 8, live);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full);
+      }
+      if (ok && patch) {
+        // told by the issuing warp, as in attn_tc_kernel
+        const int slot = (2 * (tb + n - 1) + 1) % U;
+        ok = mbar_wait(&landed, patches & 1, p.err, kSiteAttnTile);
+        ok = __all_sync(0xffffffffu, ok);
+        const int from = max(patch_from, 0);
+        if (ok)
+          for (int e = t64; e < (KT - from) * CH; e += 64) {
+            const int row = from + e / CH, c = e % CH;
+            *reinterpret_cast<uint4 *>(sm + slot * C::TILE + (c >> 3) * (KT * 128) + row * 128 +
+                                       ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&patched);
+      }
+    } else if (warp == kIssuer) {
+      // Tile t's product with V is over. Every phase of the barrier is waited for
+      // before the next can end: a parity tells neighbours apart and no more.
+      auto wait_sums = [&](int t, int q) {
+        ok = ok && mbar_wait(&o_done[q], t & 1, p.err, kSiteAttnSum);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      };
+      auto scores = [&](int i, int q) {  // S = Q K^T of tile i and row tile q
+        const int t = tb + i, b = NS == 2 ? t & 1 : q, slot = 2 * t % U;
+        if (NS == 1 && t > 0) wait_sums(t - 1, q);
+        if (!ok) return;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          umma_bf16_elect(tm_score + b * KT,
+                          sdesc_kmajor(q_s + q * (128 * D * 2) + (ks >> 2) * (128 * 128) + (ks & 3) * 32),
+                          sdesc_kmajor(units_s + slot * C::TILE + (ks >> 2) * (KT * 128) + (ks & 3) * 32),
+                          idesc_bf16_f32(128, KT, false, false), ks > 0);
+        umma_commit_elect(&s_full[b]);
+        if (q == NQ - 1) {
+          umma_commit_elect(&empty[slot]);
+          used = 2 * t + 1;
+          if (i == n - 1) umma_commit_elect(&q_empty);
+        }
+      };
+      auto wait_k = [&](int i) {
+        const int u = 2 * (tb + i);
+        ok = ok && mbar_wait(&full[u % U], (u / U) & 1, p.err, kSiteAttnTile);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      };
+      auto sums = [&](int i, int q) {  // O (+)= P V
+        const int t = tb + i, b = NS == 2 ? t & 1 : q, u = 2 * t + 1, slot = u % U;
+        ok = ok && mbar_wait_both(&p_full[b], (NS == 2 ? t >> 1 : t) & 1, &full[slot], (u / U) & 1,
+                                  p.err, kSiteAttnSum);
+        if (i == 0) ok = ok && mbar_wait(&o_free[q], (seg + 1) & 1, p.err, kSiteAttnSum);
+        ok = __all_sync(0xffffffffu, ok);
+        if (patch && i == n - 1 && q == 0) {
+          if (ok && lane == 0) mbar_arrive(&landed);
+          ok = ok && mbar_wait(&patched, patches & 1, p.err, kSiteAttnTile);
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < KT / 16; ++ks)
+          umma_bf16_ts_elect(tm + q * D, tm_score + b * KT + ks * 8,
+                             sdesc_mnmajor(units_s + slot * C::TILE + ks * 2048, KT * 128),
+                             idesc_bf16_f32(128, D, false, true), i > 0 || ks > 0);
+        if (q == NQ - 1) {
+          umma_commit_elect(&empty[slot]);
+          used = u + 1;
+        }
+        umma_commit_elect(&o_done[q]);
+      };
+      ok = mbar_wait(&q_full, seg & 1, p.err, kSiteAttnTile);
+      ok = __all_sync(0xffffffffu, ok);
+      wait_k(0);
+      if (ok) {
+        scores(0, 0);
+        if (NQ == 2 && ok) scores(0, NQ - 1);
+      }
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        if (NS == 2) {
+          if (tb + i > 0) wait_sums(tb + i - 1, 0);
+          if (ok && i + 1 < n) {
+            wait_k(i + 1);
+            if (ok) scores(i + 1, 0);
+          }
+          if (ok) sums(i, 0);
+        } else {
+          sums(i, 0);
+          if (ok && i + 1 < n) {
+            wait_k(i + 1);
+            if (ok) scores(i + 1, 0);
+          }
+          if (ok) sums(i, NQ - 1);
+          if (ok && i + 1 < n) scores(i + 1, NQ - 1);
+        }
+      }
+    } else {
+      // a row of this lane's
+      const int q = (warp - 4) >> 2, R = (warp & 3) * 32 + lane, row = r0 + q * 128 + R;
+      const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t tm_sum = tm + q * D + lanes;
+      const int nodes = TREE ? seq_nodes(p, s, false) : p.T;
+      const int t_row = p.G.div(row);
+      const bool mine = row < p.T * (int)p.G.d, absent = TREE && mine && t_row >= nodes;
+      // rows that are not there take part without a mask
+      const int lim = !mine || absent ? len : TREE ? len - nodes : len - p.T + t_row + 1;
+      const unsigned long long word = TREE && mine ? node_word(p, s, t_row, nodes) : 0;
+      float ref = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int t = tb + i, b = NS == 2 ? t & 1 : q;
+        ok = mbar_wait(&s_full[b], (NS == 2 ? t >> 1 : t) & 1, p.err, kSiteAttnScore);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t score = tm_score + b * KT + lanes;
+        float x[KT];
+#pragma unroll
+        for (int c = 0; c < KT; c += 64) tmem_ld64(score + c, x + c);
+        const int key0 = (tile0 + i) * KT;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (key0 + KT > lim) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const unsigned long long seen = seen64(key0 + 64 * h, lim, word);
+            const uint32_t part[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+              float &y = x[64 * h + j];
+              y = part[j >> 5] >> (j & 31) & 1 ? y * p.scale_log2 : -INFINITY;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < KT; ++j) x[j] *= p.scale_log2;
+        }
+#pragma unroll
+        for (int j = 0; j < KT; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool grow = top > ref + kMaxGrowth;
+        const float next = grow ? top : ref, alpha = grow ? exp2_ftz(ref - next) : 1.f;
+        ref = next;
+        l *= alpha;
+        if (i > 0 && __any_sync(0xffffffffu, grow)) {
+          // with two tiles of rows, these scores came after the last sums
+          if (NS == 2) {
+            ok = mbar_wait(&o_done[q], (t - 1) & 1, p.err, kSiteAttnSum);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+          }
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float o[16];
+            tmem_ld16(tm_sum + c, o);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] *= alpha;
+            tmem_st16(tm_sum + c, o);
+          }
+          tmem_wait_st();
+        }
+        const float base = ref == -INFINITY ? 0.f : ref;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < KT; c += 32) {
+          float pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float a = exp2_ftz(x[c + 2 * j] - base), e = exp2_ftz(x[c + 2 * j + 1] - base);
+            sum[j & 3] += a + e;
+            pk[j] = __uint_as_float(bf16x2(a, e));
+          }
+          tmem_st16(score + c / 2, pk);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[b]);
+      }
+      // one phase after the other: a wait for the last alone would be over before
+      // the one before it has begun
+      if (ok && NS == 2 && n > 1) ok = mbar_wait(&o_done[q], (tb + n - 2) & 1, p.err, kSiteAttnSum);
+      if (ok) ok = mbar_wait(&o_done[q], (tb + n - 1) & 1, p.err, kSiteAttnSum);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        tc_fence_after();
+        const bool whole = n == w.nt;
+        const long long to = mine ? out_row(p, s, kvh, row) : -1;
+        const long long piece = ((long long)blockIdx.x * 2 + (seg > 0)) * C::ROWS + q * 128 + R;
+        if (absent) l = 0.f;
+        // a row without keys has l = 0 and sums of 0: its output is 0
+        const float inv = absent ? 0.f : 1.f / (l == 0.f ? 1.f : l);
+        if (!whole && mine) p.part_ml[piece] = make_float2(absent ? -INFINITY : ref, l);
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tm_sum + c, o);
+          if (!mine) continue;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = absent ? 0.f : whole ? o[j] * inv : o[j];
+          if (whole) {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + to * D + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              dst[j] = make_uint4(bf16x2(o[8 * j], o[8 * j + 1]), bf16x2(o[8 * j + 2], o[8 * j + 3]),
+                                  bf16x2(o[8 * j + 4], o[8 * j + 5]), bf16x2(o[8 * j + 6], o[8 * j + 7]));
+          } else {
+            float4 *dst = reinterpret_cast<float4 *>(p.part_o + piece * D + c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[q]);
+      }
+    }
+    tb += n;
+    patches += patch;
+    w.next<KT>(p, items_per_seq, n);
+  }
+  if (any && !ok) {  // otherwise every copy and product has been waited for
+    if (warp == 0)
+      for (int u = max(loaded - U, 0); u < loaded; ++u) mbar_drain(&full[u % U], (u / U) & 1);
+    if (warp == kIssuer && used > 0) mbar_drain(&empty[(used - 1) % U], ((used - 1) / U) & 1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kIssuer) tmem_dealloc(tm, C::TCOLS);
+}
+
 // Joins the cut items: block (i, r) row r of the item listed at i. The W warps
 // take the pieces in turn, a lane D / 64 pairs of columns.
 template <typename T, int D, int ROWS, int W>
@@ -1455,10 +1902,14 @@ int box_of(const KvLayout &c) {
 // Calls f with the configuration of a head size, type and number of rows (T
 // x G of an item): the smallest block of rows that holds them all, or the
 // largest there is (each block of rows reads the keys again).
-template <typename T, int D, class F>
+template <typename T, int D, bool TREE, class F>
 auto with_rows(int rows, int box, F f) {
   if constexpr (sizeof(T) == 2) {
     if (rows <= 16) return f(Cfg<T, D, 1>{});
+    if constexpr (TREE) {
+      if (box && rows > 128) return f(WideCfg<D, D == 256 ? 1 : 2>{});
+      if (box && rows > 64) return f(WideCfg<D, 1>{});
+    }
     // Tensor memory where it measured faster or even (us, 64 sequences of 512 to
     // 8192, D = 128, or to 4096, D = 256, boxes of 16, 32 and 64 tokens;
     // warp-level kernel in brackets): 64 rows of D = 256 91, 86, 84 (110), 128
@@ -1479,17 +1930,22 @@ auto with_rows(int rows, int box, F f) {
     return f(Cfg<T, D, 4>{});
   }
 }
-template <typename T, class F>
+template <typename T, bool TREE, class F>
 auto with_d(int D, int rows, int box, F f) {
-  if (D == 64) return with_rows<T, 64>(rows, box, f);
-  if (D == 128) return with_rows<T, 128>(rows, box, f);
-  return with_rows<T, 256>(rows, box, f);
+  if (D == 64) return with_rows<T, 64, TREE>(rows, box, f);
+  if (D == 128) return with_rows<T, 128, TREE>(rows, box, f);
+  return with_rows<T, 256, TREE>(rows, box, f);
 }
-template <class F>
+template <bool TREE, class F>
 auto with_cfg(const KvLayout &c, int rows, F f) {
   const int box = box_of(c);
-  return c.bf16 ? with_d<__nv_bfloat16>(c.D, rows, box, f) : with_d<float>(c.D, rows, box, f);
+  return c.bf16 ? with_d<__nv_bfloat16, TREE>(c.D, rows, box, f)
+                : with_d<float, TREE>(c.D, rows, box, f);
 }
+template <class C>
+constexpr bool kIsWide = false;
+template <int D, int NQ>
+constexpr bool kIsWide<WideCfg<D, NQ>> = true;
 
 // A cache as (D, H_kv, page_size, n_pages); boxes of 64 columns x `box` tokens
 // of one head and page, 128-byte swizzle.
@@ -1550,11 +2006,13 @@ cudaError_t launch_cfg(const AttnParams &p, const KvLayout &c, int grid, cudaStr
     const int box = box_of(c);
     CUtensorMap mk, mv;
     if (!map_cache(&mk, p.k, c, box) || !map_cache(&mv, p.v, c, box)) return cudaErrorInvalidValue;
-    e = cudaFuncSetAttribute(attn_tc_kernel<C, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::SMEM);
+    constexpr auto kernel = [] {
+      if constexpr (kIsWide<C>) return attn_wide_kernel<C, TREE>;
+      else return attn_tc_kernel<C, TREE>;
+    }();
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_tc_kernel<C, TREE>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, p, mk, mv,
-                   box);
+    e = launch_pdl(kernel, dim3(grid), dim3(C::THREADS), C::SMEM, stream, p, mk, mv, box);
   } else {
     static_assert(C::SMEM + 4 * C::KT * 8 + 8 * C::ROWS + 128 <= 227 * 1024, "shared memory");
     static_assert((C::WK + 1) * C::ROWS * C::D * 4 + C::ROWS * 8 <= C::SMEM, "a piece fits");
@@ -1587,9 +2045,10 @@ cudaError_t launch_cfg(const AttnParams &p, const KvLayout &c, int grid, cudaStr
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+template <bool TREE>
 size_t workspace_size(const KvLayout &c, int n_seqs, int T, int H, int max_pages) {
   const int rows = T * (H / c.H_kv);
-  return with_cfg(c, rows, [&](auto cfg) -> size_t {
+  return with_cfg<TREE>(c, rows, [&](auto cfg) -> size_t {
     using C = decltype(cfg);
     const size_t g = (size_t)grid_of<C>(c, n_seqs, max_pages, (rows + C::ROWS - 1) / C::ROWS);
     return up256(g * 16) + up256(g * 2 * C::ROWS * 8) + g * 2 * C::ROWS * c.D * 4;
@@ -1611,7 +2070,7 @@ cudaError_t launch_attention(const AttnArgs &a, cudaStream_t stream) {
   p.grouped = a.grouped;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.err = a.err;
-  return with_cfg(c, rows, [&](auto cfg) -> cudaError_t {
+  return with_cfg<TREE>(c, rows, [&](auto cfg) -> cudaError_t {
     using C = decltype(cfg);
     p.row_blocks = FastDiv((rows + C::ROWS - 1) / C::ROWS);
     const int grid = grid_of<C>(c, a.n_seqs, a.max_pages, (int)p.row_blocks.d);

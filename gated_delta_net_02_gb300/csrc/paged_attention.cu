@@ -5,7 +5,7 @@
 namespace gdn {
 
 size_t attn_workspace_size(const KvLayout &c, int n_seqs, int T, int H, int max_pages) {
-  return workspace_size(c, n_seqs, T, H, max_pages);
+  return workspace_size<false>(c, n_seqs, T, H, max_pages);
 }
 
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream) {

@@ -134,6 +134,16 @@ def test_lengths_cut_between_blocks(gdn, dtype, H, T, lens):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("H,T", [(2, 50), (4, 64), (3, 64)])   # 100, 256 and 192 rows
+@pytest.mark.parametrize("lens", [[3000] * 60, [20000, 64, 9000, 127, 128, 129, 15000]])
+def test_many_rows_over_many_tiles(gdn, D, H, T, lens):
+    # several items in a block, of many tiles, of one and of two
+    nodes = [T - i % 4 for i in range(len(lens))]
+    c = TreeCase(gdn, lens, T, H, 1, D, 16, torch.bfloat16, seed=len(lens), nodes=nodes)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("page", [8, 16, 24, 32, 64, 128, 192])
 @pytest.mark.parametrize("layout", ["dense", "heads_first", "k_and_v_in_one"])
 def test_many_rows_pages_and_layouts(gdn, D, page, layout):
