@@ -1612,12 +1612,14 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         const int t = tb + i, b = NS == 2 ? t & 1 : q, slot = 2 * t % U;
         if (NS == 1 && t > 0) wait_sums(t - 1, q);
         if (!ok) return;
+#pragma unroll 1
+        for (int c = 0; c < CC; ++c)
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          umma_bf16_elect(tm_score + b * KT,
-                          sdesc_kmajor(q_s + q * (128 * D * 2) + (ks >> 2) * (128 * 128) + (ks & 3) * 32),
-                          sdesc_kmajor(units_s + slot * C::TILE + (ks >> 2) * (KT * 128) + (ks & 3) * 32),
-                          idesc_bf16_f32(128, KT, false, false), ks > 0);
+          for (int ks = 0; ks < 4; ++ks)
+            umma_bf16_elect(tm_score + b * KT,
+                            sdesc_kmajor(q_s + q * (128 * D * 2) + c * (128 * 128) + ks * 32),
+                            sdesc_kmajor(units_s + slot * C::TILE + c * (KT * 128) + ks * 32),
+                            idesc_bf16_f32(128, KT, false, false), c > 0 || ks > 0);
         umma_commit_elect(&s_full[b]);
         if (q == NQ - 1) {
           umma_commit_elect(&empty[slot]);
@@ -1644,9 +1646,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         }
         if (!ok) return;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 4
         for (int ks = 0; ks < KT / 16; ++ks)
-          umma_bf16_ts_elect(tm + q * D, tm_score + b * KT + ks * 8,
+          umma_bf16_ts_elect(tm + q * D, tm_score + b * KT + 64 + ks * 8,
                              sdesc_mnmajor(units_s + slot * C::TILE + ks * 2048, KT * 128),
                              idesc_bf16_f32(128, D, false, true), i > 0 || ks > 0);
         if (q == NQ - 1) {
@@ -1700,30 +1702,30 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        // In halves of 64 keys, read twice, by loops that are not unrolled: code for
+        // 128 scores at once is fetched anew for every tile, and the warp that
+        // issues products waits for its own behind it.
         const uint32_t score = tm_score + b * KT + lanes;
-        float x[KT];
-#pragma unroll
-        for (int c = 0; c < KT; c += 64) tmem_ld64(score + c, x + c);
         const int key0 = (tile0 + i) * KT;
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        if (key0 + KT > lim) {
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          float x[64];
+          tmem_ld64(score + 64 * h, x);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int j = 0; j < 64; ++j) x[j] *= p.scale_log2;
+          if (key0 + KT > lim) {
             const unsigned long long seen = seen64(key0 + 64 * h, lim, word);
             const uint32_t part[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
-              float &y = x[64 * h + j];
-              y = part[j >> 5] >> (j & 31) & 1 ? y * p.scale_log2 : -INFINITY;
-            }
+            for (int j = 0; j < 64; ++j)
+              x[j] = part[j >> 5] >> (j & 31) & 1 ? x[j] : -INFINITY;
           }
-        } else {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < KT; ++j) x[j] *= p.scale_log2;
+          for (int j = 0; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+          top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         }
-#pragma unroll
-        for (int j = 0; j < KT; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         const bool grow = top > ref + kMaxGrowth;
         const float next = grow ? top : ref, alpha = grow ? exp2_ftz(ref - next) : 1.f;
         ref = next;
@@ -1748,16 +1750,30 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         }
         const float base = ref == -INFINITY ? 0.f : ref;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // the later keys first: the probabilities take the place of their scores
+#pragma unroll 1
+        for (int h = 1; h >= 0; --h) {
+          float x[64];
+          tmem_ld64(score + 64 * h, x);
+          const bool cut = key0 + KT > lim;
+          const unsigned long long seen = cut ? seen64(key0 + 64 * h, lim, word) : ~0ull;
 #pragma unroll
-        for (int c = 0; c < KT; c += 32) {
-          float pk[16];
+          for (int j = 0; j < 64; ++j) x[j] = exp2_ftz(fmaf(x[j], p.scale_log2, -base));
+          if (cut) {
+            const uint32_t part[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float a = exp2_ftz(x[c + 2 * j] - base), e = exp2_ftz(x[c + 2 * j + 1] - base);
-            sum[j & 3] += a + e;
-            pk[j] = __uint_as_float(bf16x2(a, e));
+            for (int j = 0; j < 64; ++j) x[j] = part[j >> 5] >> (j & 31) & 1 ? x[j] : 0.f;
           }
-          tmem_st16(score + c / 2, pk);
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            float pk[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              sum[j & 3] += x[c + 2 * j] + x[c + 2 * j + 1];
+              pk[j] = __uint_as_float(bf16x2(x[c + 2 * j], x[c + 2 * j + 1]));
+            }
+            tmem_st16(score + 64 + 32 * h + c / 2, pk);
+          }
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
