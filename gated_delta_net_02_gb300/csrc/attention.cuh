@@ -782,22 +782,24 @@ __device__ __forceinline__ void finish_item(const AttnParams &p, const float *so
 // What a block holds: tiles of a run of items, walked item by item.
 struct Walk {
   long long pos, end, run;
-  int s, len, nt, x, tile0;
-  // The block's first item; false when there is nothing for this block.
+  int s, len, nt, x, tile0, block;
+  // The first item of block `block` of `blocks`; false when there is nothing for it.
   template <int KT, int NT>
   __device__ __forceinline__ bool begin(const AttnParams &p, int items_per_seq,
-                                        long long (&warp_sum)[NT / 32], Place &place) {
+                                        long long (&warp_sum)[NT / 32], Place &place, int block,
+                                        int blocks) {
+    this->block = block;
     long long total = 0;
     if (!find_place<NT>(
             p, KT, items_per_seq,
             [&](long long n) {
               total = n;
-              run = max(quotient(n + gridDim.x - 1, gridDim.x), (long long)kMinTiles);
-              return run * blockIdx.x;
+              run = max(quotient(n + blocks - 1, blocks), (long long)kMinTiles);
+              return run * block;
             },
             warp_sum, place))
       return false;
-    pos = run * blockIdx.x;
+    pos = run * block;
     end = min(pos + run, total);
     s = place.seq;
     len = place.len;
@@ -818,9 +820,9 @@ struct Walk {
     const int item = s * items_per_seq + x;
     int4 cut = make_int4(-1, 0, 0, 0);
     if (tile0 == 0 && n < nt)
-      cut = make_int4(item, 2 * blockIdx.x + (pos == run * blockIdx.x ? 0 : 1), nt - n,
+      cut = make_int4(item, 2 * block + (pos == run * block ? 0 : 1), nt - n,
                       (int)min(run, (long long)INT_MAX));
-    p.cut[p.by_item ? item : (int)blockIdx.x] = cut;
+    p.cut[p.by_item ? item : block] = cut;
   }
   template <int KT>
   __device__ __forceinline__ void next(const AttnParams &p, int items_per_seq, int n) {
@@ -872,7 +874,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     w.tile0 = rank * w.nt / split;
     w.pos = 0;
     w.end = (rank + 1) * w.nt / split - w.tile0;  // may be none
-  } else if (!w.begin<KT, NT>(p, items_per_seq, warp_sum, place)) {
+  } else if (!w.begin<KT, NT>(p, items_per_seq, warp_sum, place, blockIdx.x, gridDim.x)) {
     if (tid == 0 && !p.by_item) p.cut[blockIdx.x].x = -1;
     return;
   }
@@ -1122,7 +1124,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   const uint32_t tm = tm_s, tm_score = tm + D;
 
   Walk w{};
-  const bool any = w.begin<KT, NT>(p, items_per_seq, warp_sum, place);
+  const bool any =
+      w.begin<KT, NT>(p, items_per_seq, warp_sum, place, blockIdx.x, gridDim.x);
   if (!any && tid == 0 && !p.by_item) p.cut[blockIdx.x].x = -1;
   int tb = 0, patches = 0;  // tiles and cleared units of the items before
   int loaded = 0, used = 0;  // units that warp 0 has loaded, and warp 8 given back last, plus one
@@ -1384,22 +1387,29 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 // need no other lane; probabilities go back to tensor memory over their scores, as
 // the next product's first operand, and cost no shared memory.
 // Scores overwrite the probabilities of the tile before (the one before that, with
-// two tiles of keys) once the product that reads those is over.
+// two tiles of keys) once the product that reads those is over; each tile of rows
+// has a warp of its own to issue its products, so that one's wait is the other's turn.
+// The blocks of rows of an item (64 nodes x 8 heads of 256 are four) go to
+// neighbouring blocks of the grid with the same run of keys, which then pass from L2:
+// one behind the other they read memory 3.6 times over.
 template <int D_, int NQ_>
 struct WideCfg {
   using In = __nv_bfloat16;
   static constexpr bool kTensorMemory = true;
-  static constexpr int D = D_, NQ = NQ_, NS = NQ == 1 ? 2 : 1, KT = 128, ROWS = 128 * NQ;
-  // no more than three warps for each scheduler, so that a lane may hold a row's
-  // 128 scores
+  static constexpr int D = D_, NQ = NQ_, KT = 128 / NQ, ROWS = 128 * NQ;
+  // no more than three warps for each scheduler, so that a lane may hold 64 scores
   static constexpr int THREADS = 128 + 128 * NQ;
-  static constexpr int TILE = KT * D * 2, Q_BYTES = ROWS * D * 2;
-  static constexpr int FIT = (222 * 1024 - Q_BYTES) / TILE;
-  static constexpr int SLOTS = FIT > 8 ? 8 : FIT;  // tiles of K and V in turn
-  static constexpr int SMEM = SLOTS * TILE + Q_BYTES + 1024;
-  static constexpr int TCOLS = 512;  // sums, then two tiles of scores
+  // K and V arrive in units, each in a ring of its own: of K KA times 64 columns of
+  // the tile's keys, of V KV of its keys, which is what a few products read, so that
+  // a place is loaded again while the rest of its tile is still in use
+  static constexpr int TILE = KT * D * 2, CC = TILE > 16384 ? TILE / 16384 : 1, UNIT = TILE / CC;
+  static constexpr int KA = D / 64 / CC, KV = KT / CC;
+  static constexpr int Q_BYTES = ROWS * D * 2;
+  static constexpr int FIT = (222 * 1024 - Q_BYTES) / (2 * UNIT), U = FIT > 6 ? 6 : FIT;
+  static constexpr int SMEM = 2 * U * UNIT + Q_BYTES + 1024;
+  static constexpr int TCOLS = 512;  // sums, then two tiles of scores for each tile of rows
   static constexpr int PER_SM = 1;
-  static_assert(NQ * D + 256 <= TCOLS && SLOTS >= 2, "it fits");
+  static_assert(NQ * D + 256 <= TCOLS && U >= CC, "it fits");
 };
 
 // D[tmem] (+)= A[tmem] B[smem], A in the lanes of its rows, two bf16 a column; from a whole
@@ -1457,26 +1467,32 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     attn_wide_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, int box) {
   using T = __nv_bfloat16;
-  constexpr int D = C::D, KT = C::KT, NT = C::THREADS, U = C::SLOTS, NQ = C::NQ, NS = C::NS;
-  constexpr int CH = D / 8, CC = D / 64;  // 16-byte chunks and 64 columns of a row
+  constexpr int D = C::D, KT = C::KT, NT = C::THREADS, U = C::U, NQ = C::NQ;
+  constexpr int CH = D / 8, CC = C::CC, KA = C::KA, KV = C::KV;  // 16-byte chunks of a row; see WideCfg
   extern __shared__ unsigned char raw[];
   unsigned char *sm =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[U], empty[U], s_full[2], p_full[2], o_done[NQ], o_free[NQ];
-  __shared__ uint64_t q_full, q_empty, landed, patched;
+  __shared__ uint64_t full[2][U], empty[2][U];  // of K, of V
+  __shared__ uint64_t s_full[2 * NQ], p_full[2 * NQ], o_done[NQ], o_free[NQ];
+  __shared__ uint64_t q_first, q_full, q_empty, landed, patched;
   __shared__ long long warp_sum[NT / 32];
   __shared__ Place place;
   __shared__ uint32_t tm_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kIssuer = 3;  // warps: keys, queries (2), products, rows (4 NQ)
-  const uint32_t units_s = smem_u32(sm), q_s = units_s + U * C::TILE;
-  const int items_per_seq = p.H_kv * p.row_blocks.d;
+  // warps: K (and V), queries, (V or) products of the second tile of rows, products,
+  // rows (4 NQ)
+  constexpr int kIssuer = 3;
+  auto unit_at = [&](int v, int slot) { return (v * U + slot) * C::UNIT; };
+  const uint32_t units_s = smem_u32(sm), q_s = units_s + 2 * U * C::UNIT;
+  const int items_per_seq = p.H_kv, RB = p.row_blocks.d;
+  const int group = p.row_blocks.div(blockIdx.x), rb = blockIdx.x - group * RB;
+  const int groups = p.row_blocks.div(gridDim.x), r0 = rb * C::ROWS;
   if (tid == 0) {
-    for (int i = 0; i < U; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+    for (int i = 0; i < 2 * U; ++i) {
+      mbar_init(&full[0][0] + i, 1);
+      mbar_init(&empty[0][0] + i, NQ);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * NQ; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
     }
@@ -1484,10 +1500,11 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       mbar_init(&o_done[i], 1);
       mbar_init(&o_free[i], 4);
     }
-    mbar_init(&q_full, 2);
-    mbar_init(&q_empty, 1);
-    mbar_init(&landed, 1);
-    mbar_init(&patched, 2);
+    mbar_init(&q_first, 4 * NQ);
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, NQ);
+    mbar_init(&landed, NQ);
+    mbar_init(&patched, 1);
     fence_mbar_init();
     prefetch_tmap(&mk);
     prefetch_tmap(&mv);
@@ -1505,183 +1522,203 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 
   // Every role walks the block's items on its own.
   Walk w{};
-  const bool any = w.begin<KT, NT>(p, items_per_seq, warp_sum, place);
-  if (!any && tid == 0 && !p.by_item) p.cut[blockIdx.x].x = -1;
+  const bool any = w.begin<KT, NT>(p, items_per_seq, warp_sum, place, group, groups);
+  if (!any && tid == 0 && rb == 0 && !p.by_item) p.cut[group].x = -1;
   int tb = 0, patches = 0;   // tiles and cleared tiles of the items before
-  int loaded = 0, used = 0;  // tiles of K and V loaded, and given back last, plus one
+  int loaded[2] = {0, 0}, used[2] = {0, 0};  // units of K and V loaded, and given back
   bool ok = any;
   for (int seg = 0; ok && w.pos < w.end; ++seg) {
-    const int n = w.tiles(), s = w.s, len = w.len, tile0 = w.tile0;
-    const int kvh = p.row_blocks.div(w.x), r0 = (w.x - kvh * (int)p.row_blocks.d) * C::ROWS;
+    const int n = w.tiles(), s = w.s, len = w.len, tile0 = w.tile0, kvh = w.x;
     // the item's last tile is here, and ends inside a tile of V
     const int patch_from = len - (tile0 + n - 1) * KT;
     const bool patch = patch_from < KT;
-    if (warp == 0) {
-      if (lane == 0) w.list_join(p, items_per_seq, n);
-      // a lane's boxes of a tile: `box` tokens by 64 columns, CC of them side by side
+    // Rows of queries `from`, from + step .. to shared memory, 16 bytes a copy.
+    auto load_q = [&](int from, int step) {
+      const int nodes = TREE ? seq_nodes(p, s, false) : p.T;
+#pragma unroll 4
+      for (int e = from; e < C::ROWS * CH; e += step) {
+        const int r = e / CH, c = e % CH;
+        const long long row = out_row(p, s, kvh, r0 + r);
+        const bool live = row >= 0 && p.G.div(r0 + r) < nodes;
+        cp_async16(q_s + (r >> 7) * (128 * D * 2) + (c >> 3) * (128 * 128) + (r & 127) * 128 +
+                       (((c & 7) ^ (r & 7)) << 4),
+                   static_cast<const T *>(p.q) + (live ? row : 0) * D + c * 8, live);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async();
+      __syncwarp();
+    };
+    if (warp == 0 || (NQ == 1 && warp == 2)) {
+      if (lane == 0 && warp == 0 && rb == 0) w.list_join(p, items_per_seq, n);
+      // A lane's boxes of a tile, at most two: 64 columns of kbox keys of K, of vbox
+      // of V, unit by unit
       const int32_t *table = p.table + (long long)s * p.max_pages;
-      const int boxes = KT / box * CC;
-      auto page_of = [&](int i, int e) -> int {
-        const int key = (tile0 + i) * KT + e / CC * box;
-        return e < boxes && i < n && key < len ? table[p.page_size.div(key)] : -1;
+      const int kbox = box, vbox = min(box, KV);
+      const int per[2] = {KT / kbox * KA, KV / vbox * (D / 64)};  // boxes of a unit
+      auto key_of = [&](int v, int e) {                // first key of box e in its tile
+        return v ? e / per[1] * KV + e % per[1] / (D / 64) * vbox : e % per[0] / KA * kbox;
       };
-      int page[2] = {page_of(0, lane), page_of(0, lane + 32)};
-#pragma unroll 1
-      for (int i = 0; i < n && ok; ++i) {
-        const int next[2] = {page_of(i + 1, lane), page_of(i + 1, lane + 32)};
+      auto page_of = [&](int i, int v, int e) -> int {
+        const int key = (tile0 + i) * KT + key_of(v, e);
+        return e < CC * per[v] && i < n && key < len ? table[p.page_size.div(key)] : -1;
+      };
+      int page[2][2];
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        page[v][0] = page_of(0, v, lane);
+        page[v][1] = page_of(0, v, lane + 32);
+      }
+      auto load = [&](int i, int v) {  // K (V) of tile i
+        int next[2], at[2];
         bool live[2];
-        uint32_t bytes = 0;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int e = lane + 32 * x, key = (tile0 + i) * KT + e / CC * box;
-          live[x] = e < boxes && key < len;
-          if (live[x] && (page[x] < 0 || page[x] >= p.n_pages)) {
+          const int e = lane + 32 * x, key = (tile0 + i) * KT + key_of(v, e);
+          next[x] = page_of(i + 1, v, e);
+          live[x] = e < CC * per[v] && key < len;
+          if (live[x] && (page[v][x] < 0 || page[v][x] >= p.n_pages)) {
             set_error(p.err, kDevBadPage);
             live[x] = false;
           }
-          bytes += __popc(__ballot_sync(0xffffffffu, live[x])) * box * 128;
+          at[x] = key - p.page_size.div(key) * (int)p.page_size.d;
         }
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int u = 2 * (tb + i) + v, slot = u % U;
-          ok = ok && mbar_wait(&empty[slot], (u / U + 1) & 1, p.err, kSiteAttnTile);
+#pragma unroll 1
+        for (int c = 0; c < CC; ++c) {
+          const int u = (tb + i) * CC + c, slot = u % U;
+          ok = ok && mbar_wait(&empty[v][slot], (u / U + 1) & 1, p.err, kSiteAttnTile);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-          __syncwarp();
-          loaded = u + 1;
+          bool mine[2];
+          uint32_t boxes = 0;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int e = lane + 32 * x, j = e / CC, c = e % CC;
-            const int key = (tile0 + i) * KT + j * box;
-            if (live[x])
-              tma_load_4d(sm + slot * C::TILE + c * (KT * 128) + j * box * 128, v ? &mv : &mk, c * 64,
-                          kvh, key - p.page_size.div(key) * (int)p.page_size.d, page[x],
-                          &full[slot]);
+            mine[x] = live[x] && (lane + 32 * x) / per[v] == c;
+            boxes += __popc(__ballot_sync(0xffffffffu, mine[x]));
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&full[v][slot], boxes * (v ? vbox : kbox) * 128);
+          __syncwarp();
+          loaded[v] = u + 1;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int e = (lane + 32 * x) % per[v];
+            if (!mine[x]) continue;
+            unsigned char *dst = sm + unit_at(v, slot);
+            if (v)
+              tma_load_4d(dst + e % (D / 64) * (KV * 128) + e / (D / 64) * vbox * 128, &mv,
+                          e % (D / 64) * 64, kvh, at[x], page[v][x], &full[v][slot]);
+            else
+              tma_load_4d(dst + e % KA * (KT * 128) + e / KA * kbox * 128, &mk,
+                          (c * KA + e % KA) * 64, kvh, at[x], page[v][x], &full[v][slot]);
           }
         }
-        page[0] = next[0];
-        page[1] = next[1];
+        page[v][0] = next[0];
+        page[v][1] = next[1];
+      };
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
+        if (NQ == 2 || warp == 0) load(i, 0);
+        if (ok && (NQ == 2 || warp == 2)) load(i, 1);
       }
-    } else if (warp < kIssuer) {
-      const int t64 = tid - 32;
-      const int nodes = TREE ? seq_nodes(p, s, w.x == 0 && tile0 == 0 && t64 == 0) : p.T;
-      ok = mbar_wait(&q_empty, (seg + 1) & 1, p.err, kSiteAttnTile);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-#pragma unroll 4
-        for (int e = t64; e < C::ROWS * CH; e += 64) {
-          const int r = e / CH, c = e % CH;
-          const long long row = out_row(p, s, kvh, r0 + r);
-          const bool live = row >= 0 && p.G.div(r0 + r) < nodes;
-          cp_async16(q_s + (r >> 7) * (128 * D * 2) + (c >> 3) * (128 * 128) + (r & 127) * 128 +
-                         (((c & 7) ^ (r & 7)) << 4),
-                     static_cast<const T *>(p.q) + (live ? row : 0) * D + c * 8, live);
+    } else if (warp == 1) {
+      // queries of the items after the first, ahead of their turn
+      if (seg > 0) {
+        ok = mbar_wait(&q_empty, (seg - 1) & 1, p.err, kSiteAttnTile);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          load_q(lane, 32);
+          if (lane == 0) mbar_arrive(&q_full);
         }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full);
       }
+      if (TREE && lane == 0) seq_nodes(p, s, w.x == 0 && tile0 == 0);
       if (ok && patch) {
-        // told by the issuing warp, as in attn_tc_kernel
-        const int slot = (2 * (tb + n - 1) + 1) % U;
+        // told by the issuing warps, as in attn_tc_kernel
         ok = mbar_wait(&landed, patches & 1, p.err, kSiteAttnTile);
         ok = __all_sync(0xffffffffu, ok);
         const int from = max(patch_from, 0);
         if (ok)
-          for (int e = t64; e < (KT - from) * CH; e += 64) {
-            const int row = from + e / CH, c = e % CH;
-            *reinterpret_cast<uint4 *>(sm + slot * C::TILE + (c >> 3) * (KT * 128) + row * 128 +
-                                       ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          for (int e = lane; e < (KT - from) * CH; e += 32) {
+            const int key = from + e / CH, c = e % CH;
+            const int slot = ((tb + n - 1) * CC + key / KV) % U;
+            *reinterpret_cast<uint4 *>(sm + unit_at(1, slot) + (c >> 3) * (KV * 128) +
+                                       key % KV * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
           }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&patched);
       }
-    } else if (warp == kIssuer) {
+    } else if (warp <= kIssuer) {
+      const int q = NQ == 2 ? kIssuer - warp : 0;
       // Tile t's product with V is over. Every phase of the barrier is waited for
       // before the next can end: a parity tells neighbours apart and no more.
-      auto wait_sums = [&](int t, int q) {
+      auto wait_sums = [&](int t) {
         ok = ok && mbar_wait(&o_done[q], t & 1, p.err, kSiteAttnSum);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       };
-      auto scores = [&](int i, int q) {  // S = Q K^T of tile i and row tile q
-        const int t = tb + i, b = NS == 2 ? t & 1 : q, slot = 2 * t % U;
-        if (NS == 1 && t > 0) wait_sums(t - 1, q);
-        if (!ok) return;
-#pragma unroll 1
-        for (int c = 0; c < CC; ++c)
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_bf16_elect(tm_score + b * KT,
-                            sdesc_kmajor(q_s + q * (128 * D * 2) + c * (128 * 128) + ks * 32),
-                            sdesc_kmajor(units_s + slot * C::TILE + c * (KT * 128) + ks * 32),
-                            idesc_bf16_f32(128, KT, false, false), c > 0 || ks > 0);
-        umma_commit_elect(&s_full[b]);
-        if (q == NQ - 1) {
-          umma_commit_elect(&empty[slot]);
-          used = 2 * t + 1;
-          if (i == n - 1) umma_commit_elect(&q_empty);
-        }
-      };
-      auto wait_k = [&](int i) {
-        const int u = 2 * (tb + i);
-        ok = ok && mbar_wait(&full[u % U], (u / U) & 1, p.err, kSiteAttnTile);
+      auto arrived = [&](int v, int u) {  // unit u of K (V)
+        ok = ok && mbar_wait(&full[v][u % U], (u / U) & 1, p.err, kSiteAttnTile);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
       };
-      auto sums = [&](int i, int q) {  // O (+)= P V
-        const int t = tb + i, b = NS == 2 ? t & 1 : q, u = 2 * t + 1, slot = u % U;
-        ok = ok && mbar_wait_both(&p_full[b], (NS == 2 ? t >> 1 : t) & 1, &full[slot], (u / U) & 1,
-                                  p.err, kSiteAttnSum);
-        if (i == 0) ok = ok && mbar_wait(&o_free[q], (seg + 1) & 1, p.err, kSiteAttnSum);
-        ok = __all_sync(0xffffffffu, ok);
-        if (patch && i == n - 1 && q == 0) {
+      auto scores = [&](int i) {  // S = Q K^T of tile i
+        const int t = tb + i, b = 2 * q + (t & 1);
+#pragma unroll 1
+        for (int c = 0; c < CC; ++c) {
+          const int u = t * CC + c, slot = u % U;
+          arrived(0, u);
+          if (!ok) return;
+#pragma unroll
+          for (int ks = 0; ks < 4 * KA; ++ks)
+            umma_bf16_elect(tm_score + b * KT,
+                            sdesc_kmajor(q_s + q * (128 * D * 2) +
+                                         (c * KA + ks / 4) * (128 * 128) + ks % 4 * 32),
+                            sdesc_kmajor(units_s + unit_at(0, slot) + ks / 4 * (KT * 128) +
+                                         ks % 4 * 32),
+                            idesc_bf16_f32(128, KT, false, false), c > 0 || ks > 0);
+          umma_commit_elect(&empty[0][slot]);
+          used[0] = u + 1;
+        }
+        umma_commit_elect(&s_full[b]);
+        if (i == n - 1) umma_commit_elect(&q_empty);
+      };
+      auto sums = [&](int i) {  // O (+)= P V
+        const int t = tb + i, b = 2 * q + (t & 1);
+        if (patch && i == n - 1) {
+          for (int c = 0; c < CC; ++c) arrived(1, t * CC + c);
           if (ok && lane == 0) mbar_arrive(&landed);
           ok = ok && mbar_wait(&patched, patches & 1, p.err, kSiteAttnTile);
           ok = __all_sync(0xffffffffu, ok);
         }
-        if (!ok) return;
-        tc_fence_after();
-#pragma unroll 4
-        for (int ks = 0; ks < KT / 16; ++ks)
-          umma_bf16_ts_elect(tm + q * D, tm_score + b * KT + 64 + ks * 8,
-                             sdesc_mnmajor(units_s + slot * C::TILE + ks * 2048, KT * 128),
-                             idesc_bf16_f32(128, D, false, true), i > 0 || ks > 0);
-        if (q == NQ - 1) {
-          umma_commit_elect(&empty[slot]);
-          used = u + 1;
+        ok = ok && mbar_wait(&p_full[b], (t >> 1) & 1, p.err, kSiteAttnSum);
+        if (i == 0) ok = ok && mbar_wait(&o_free[q], (seg + 1) & 1, p.err, kSiteAttnSum);
+        ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+        for (int c = 0; c < CC; ++c) {
+          const int u = t * CC + c, slot = u % U;
+          arrived(1, u);
+          if (!ok) return;
+#pragma unroll
+          for (int ks = 0; ks < KV / 16; ++ks)
+            umma_bf16_ts_elect(tm + q * D, tm_score + b * KT + KT / 2 + (c * (KV / 16) + ks) * 8,
+                               sdesc_mnmajor(units_s + unit_at(1, slot) + ks * 2048, KV * 128),
+                               idesc_bf16_f32(128, D, false, true), i > 0 || c > 0 || ks > 0);
+          if (c == CC - 1) umma_commit_elect(&o_done[q]);
+          umma_commit_elect(&empty[1][slot]);
+          used[1] = u + 1;
         }
-        umma_commit_elect(&o_done[q]);
       };
-      ok = mbar_wait(&q_full, seg & 1, p.err, kSiteAttnTile);
+      if (seg == 0) ok = mbar_wait(&q_first, 0, p.err, kSiteAttnTile);
+      else ok = mbar_wait(&q_full, (seg - 1) & 1, p.err, kSiteAttnTile);
       ok = __all_sync(0xffffffffu, ok);
-      wait_k(0);
-      if (ok) {
-        scores(0, 0);
-        if (NQ == 2 && ok) scores(0, NQ - 1);
-      }
+      // scores take the place of those of the tile before the last, whose product is
+      // over
+      if (ok) scores(0);
 #pragma unroll 1
       for (int i = 0; i < n && ok; ++i) {
-        if (NS == 2) {
-          if (tb + i > 0) wait_sums(tb + i - 1, 0);
-          if (ok && i + 1 < n) {
-            wait_k(i + 1);
-            if (ok) scores(i + 1, 0);
-          }
-          if (ok) sums(i, 0);
-        } else {
-          sums(i, 0);
-          if (ok && i + 1 < n) {
-            wait_k(i + 1);
-            if (ok) scores(i + 1, 0);
-          }
-          if (ok) sums(i, NQ - 1);
-          if (ok && i + 1 < n) scores(i + 1, NQ - 1);
-        }
+        if (tb + i > 0) wait_sums(tb + i - 1);
+        if (ok && i + 1 < n) scores(i + 1);
+        if (ok) sums(i);
       }
     } else {
       // a row of this lane's
@@ -1694,27 +1731,31 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       // rows that are not there take part without a mask
       const int lim = !mine || absent ? len : TREE ? len - nodes : len - p.T + t_row + 1;
       const unsigned long long word = TREE && mine ? node_word(p, s, t_row, nodes) : 0;
+      if (seg == 0) {
+        load_q(tid - 128, 128 * NQ);
+        if (lane == 0) mbar_arrive(&q_first);
+      }
       float ref = -INFINITY, l = 0.f;
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
-        const int t = tb + i, b = NS == 2 ? t & 1 : q;
-        ok = mbar_wait(&s_full[b], (NS == 2 ? t >> 1 : t) & 1, p.err, kSiteAttnScore);
+        const int t = tb + i, b = 2 * q + (t & 1);
+        ok = mbar_wait(&s_full[b], (t >> 1) & 1, p.err, kSiteAttnScore);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        // In halves of 64 keys, read twice, by loops that are not unrolled: code for
-        // 128 scores at once is fetched anew for every tile, and the warp that
-        // issues products waits for its own behind it.
+        // In halves of 64 keys, read twice where a tile has two, by loops that are not
+        // unrolled: code for 128 scores at once is fetched anew for every tile, and
+        // the warp that issues products waits for its own behind it.
         const uint32_t score = tm_score + b * KT + lanes;
         const int key0 = (tile0 + i) * KT;
-        float top = -INFINITY;
+        const bool cut = key0 + KT > lim;
+        float x[64], top = -INFINITY;
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          float x[64];
+        for (int h = 0; h < KT / 64; ++h) {
           tmem_ld64(score + 64 * h, x);
 #pragma unroll
           for (int j = 0; j < 64; ++j) x[j] *= p.scale_log2;
-          if (key0 + KT > lim) {
+          if (cut) {
             const unsigned long long seen = seen64(key0 + 64 * h, lim, word);
             const uint32_t part[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
@@ -1731,13 +1772,10 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         ref = next;
         l *= alpha;
         if (i > 0 && __any_sync(0xffffffffu, grow)) {
-          // with two tiles of rows, these scores came after the last sums
-          if (NS == 2) {
-            ok = mbar_wait(&o_done[q], (t - 1) & 1, p.err, kSiteAttnSum);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-          }
+          ok = mbar_wait(&o_done[q], (t - 1) & 1, p.err, kSiteAttnSum);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 16) {
             float o[16];
@@ -1752,18 +1790,21 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         // the later keys first: the probabilities take the place of their scores
 #pragma unroll 1
-        for (int h = 1; h >= 0; --h) {
-          float x[64];
-          tmem_ld64(score + 64 * h, x);
-          const bool cut = key0 + KT > lim;
-          const unsigned long long seen = cut ? seen64(key0 + 64 * h, lim, word) : ~0ull;
+        for (int h = KT / 64 - 1; h >= 0; --h) {
+          if (KT > 64) {
+            tmem_ld64(score + 64 * h, x);
 #pragma unroll
-          for (int j = 0; j < 64; ++j) x[j] = exp2_ftz(fmaf(x[j], p.scale_log2, -base));
-          if (cut) {
-            const uint32_t part[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
+            for (int j = 0; j < 64; ++j) x[j] *= p.scale_log2;
+            if (cut) {
+              const unsigned long long seen = seen64(key0 + 64 * h, lim, word);
+              const uint32_t part[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
-            for (int j = 0; j < 64; ++j) x[j] = part[j >> 5] >> (j & 31) & 1 ? x[j] : 0.f;
+              for (int j = 0; j < 64; ++j)
+                x[j] = part[j >> 5] >> (j & 31) & 1 ? x[j] : -INFINITY;
+            }
           }
+#pragma unroll
+          for (int j = 0; j < 64; ++j) x[j] = exp2_ftz(x[j] - base);
 #pragma unroll
           for (int c = 0; c < 64; c += 32) {
             float pk[16];
@@ -1772,7 +1813,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
               sum[j & 3] += x[c + 2 * j] + x[c + 2 * j + 1];
               pk[j] = __uint_as_float(bf16x2(x[c + 2 * j], x[c + 2 * j + 1]));
             }
-            tmem_st16(score + 64 + 32 * h + c / 2, pk);
+            tmem_st16(score + KT / 2 + 32 * h + c / 2, pk);
           }
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -1783,18 +1824,21 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       }
       // one phase after the other: a wait for the last alone would be over before
       // the one before it has begun
-      if (ok && NS == 2 && n > 1) ok = mbar_wait(&o_done[q], (tb + n - 2) & 1, p.err, kSiteAttnSum);
+      if (ok && n > 1) ok = mbar_wait(&o_done[q], (tb + n - 2) & 1, p.err, kSiteAttnSum);
       if (ok) ok = mbar_wait(&o_done[q], (tb + n - 1) & 1, p.err, kSiteAttnSum);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after();
         const bool whole = n == w.nt;
         const long long to = mine ? out_row(p, s, kvh, row) : -1;
-        const long long piece = ((long long)blockIdx.x * 2 + (seg > 0)) * C::ROWS + q * 128 + R;
+        // pieces: [slot][row block][D / 4][row][4], a lane a row
+        const long long piece = ((long long)group * 2 + (seg > 0)) * RB + rb;
+        const int pr = q * 128 + R;
         if (absent) l = 0.f;
         // a row without keys has l = 0 and sums of 0: its output is 0
         const float inv = absent ? 0.f : 1.f / (l == 0.f ? 1.f : l);
-        if (!whole && mine) p.part_ml[piece] = make_float2(absent ? -INFINITY : ref, l);
+        if (!whole && mine)
+          p.part_ml[piece * C::ROWS + pr] = make_float2(absent ? -INFINITY : ref, l);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
@@ -1809,10 +1853,11 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
               dst[j] = make_uint4(bf16x2(o[8 * j], o[8 * j + 1]), bf16x2(o[8 * j + 2], o[8 * j + 3]),
                                   bf16x2(o[8 * j + 4], o[8 * j + 5]), bf16x2(o[8 * j + 6], o[8 * j + 7]));
           } else {
-            float4 *dst = reinterpret_cast<float4 *>(p.part_o + piece * D + c);
+            float4 *dst =
+                reinterpret_cast<float4 *>(p.part_o) + (piece * (D / 4) + c / 4) * C::ROWS + pr;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              dst[j * C::ROWS] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
           }
         }
         tc_fence_before();
@@ -1825,13 +1870,89 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     w.next<KT>(p, items_per_seq, n);
   }
   if (any && !ok) {  // otherwise every copy and product has been waited for
-    if (warp == 0)
-      for (int u = max(loaded - U, 0); u < loaded; ++u) mbar_drain(&full[u % U], (u / U) & 1);
-    if (warp == kIssuer && used > 0) mbar_drain(&empty[(used - 1) % U], ((used - 1) / U) & 1);
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      for (int u = max(loaded[v] - U, 0); u < loaded[v]; ++u)
+        mbar_drain(&full[v][u % U], (u / U) & 1);
+      if (used[v] > 0) mbar_drain(&empty[v][(used[v] - 1) % U], ((used[v] - 1) / U) & 1);
+    }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kIssuer) tmem_dealloc(tm, C::TCOLS);
+}
+
+// Joins the cut items of attn_wide_kernel: block (i, y) rows 8 y .. 8 y + 8 of the
+// item listed at i; the pieces are taken in turn by W groups of 128 threads, whose
+// sums are added in order. A thread has every 16th four columns of a row.
+template <class C, int W>
+__global__ void __launch_bounds__(128 * W) join_wide_kernel(const AttnParams p, int groups) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int D = C::D, VL = D / 64;
+  const int4 cut = p.cut[blockIdx.x];
+  // a main kernel that gave up (error word) may have left the list unwritten
+  if (cut.x < 0 || cut.x >= p.n_seqs * p.H_kv || cut.y < 0 || cut.z <= 0 || cut.w <= 0) return;
+  const int first = cut.y >> 1, np = (cut.z - 1) / cut.w + 2;  // blocks of the item
+  if (first + (long long)np > groups) return;
+  const int tid = threadIdx.x & 127, turn = threadIdx.x >> 7;
+  const int row = blockIdx.y * 8 + (tid & 7), rb = row / C::ROWS, r = row % C::ROWS, c4 = tid >> 3;
+  const int s = cut.x / p.H_kv, kvh = cut.x - s * p.H_kv;
+  auto slot = [&](int i) {  // as in join_kernel, of this block of rows
+    return (i == 0 ? (long long)cut.y : 2LL * (first + i)) * (int)p.row_blocks.d + rb;
+  };
+  const bool mine = row < p.T * (int)p.G.d;
+  float mm = -INFINITY, ll = 0.f;
+  float4 sum[VL];
+#pragma unroll
+  for (int j = 0; j < VL; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (mine) {
+#pragma unroll 4
+    for (int i = 0; i < np; ++i) mm = fmaxf(mm, p.part_ml[slot(i) * C::ROWS + r].x);
+    const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 4
+    for (int i = turn; i < np; i += W) {
+      const float2 ml = p.part_ml[slot(i) * C::ROWS + r];
+      const float f = exp2_ftz(ml.x - ref);
+      ll += f * ml.y;
+      const float4 *o = reinterpret_cast<const float4 *>(p.part_o) + slot(i) * (D / 4) * C::ROWS + r;
+#pragma unroll
+      for (int j = 0; j < VL; ++j) {
+        const float4 v = o[(j * 16 + c4) * C::ROWS];
+        sum[j].x = fmaf(f, v.x, sum[j].x);
+        sum[j].y = fmaf(f, v.y, sum[j].y);
+        sum[j].z = fmaf(f, v.z, sum[j].z);
+        sum[j].w = fmaf(f, v.w, sum[j].w);
+      }
+    }
+  }
+  if constexpr (W > 1) {
+    __shared__ float4 others[W - 1][VL][128];
+    __shared__ float sl[W - 1][128];
+    if (turn > 0) {
+#pragma unroll
+      for (int j = 0; j < VL; ++j) others[turn - 1][j][tid] = sum[j];
+      sl[turn - 1][tid] = ll;
+    }
+    __syncthreads();
+    if (turn > 0) return;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+      ll += sl[k][tid];
+#pragma unroll
+      for (int j = 0; j < VL; ++j) {
+        const float4 v = others[k][j][tid];
+        sum[j].x += v.x; sum[j].y += v.y; sum[j].z += v.z; sum[j].w += v.w;
+      }
+    }
+  }
+  if (!mine) return;
+  const float inv = 1.f / (ll == 0.f ? 1.f : ll);
+  __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + out_row(p, s, kvh, row) * D;
+#pragma unroll
+  for (int j = 0; j < VL; ++j)
+    store4(out + (j * 16 + c4) * 4,
+           make_float4(sum[j].x * inv, sum[j].y * inv, sum[j].z * inv, sum[j].w * inv));
 }
 
 // Joins the cut items: block (i, r) row r of the item listed at i. The W warps
@@ -1958,10 +2079,6 @@ auto with_cfg(const KvLayout &c, int rows, F f) {
   return c.bf16 ? with_d<__nv_bfloat16, TREE>(c.D, rows, box, f)
                 : with_d<float, TREE>(c.D, rows, box, f);
 }
-template <class C>
-constexpr bool kIsWide = false;
-template <int D, int NQ>
-constexpr bool kIsWide<WideCfg<D, NQ>> = true;
 
 // A cache as (D, H_kv, page_size, n_pages); boxes of 64 columns x `box` tokens
 // of one head and page, 128-byte swizzle.
@@ -1980,10 +2097,21 @@ bool map_cache(CUtensorMap *m, const void *base, const KvLayout &c, int box) {
 
 constexpr int kSms = 152;
 
+template <class C>
+constexpr bool kIsWide = false;
+template <int D, int NQ>
+constexpr bool kIsWide<WideCfg<D, NQ>> = true;
+
 // Blocks of the grid: all that fit the GPU, or as many as there can be tiles.
 template <class C>
 int grid_of(const KvLayout &c, int n_seqs, int max_pages, int row_blocks) {
   const long long tiles = ((long long)max_pages * c.page_size + C::KT - 1) / C::KT;
+  if constexpr (kIsWide<C>) {  // groups of blocks of rows side by side
+    const long long items = (long long)n_seqs * c.H_kv;
+    const int most = row_blocks < kSms ? kSms / row_blocks : 1;
+    const bool few = tiles < most && items * (tiles < 1 ? 1 : tiles) < most;
+    return row_blocks * (few ? (int)(items * (tiles < 1 ? 1 : tiles)) : most);
+  }
   const long long most = (long long)C::PER_SM * kSms;
   const long long items = (long long)n_seqs * c.H_kv * row_blocks;
   if (tiles < most && items * (tiles < 1 ? 1 : tiles) < most)
@@ -2021,7 +2149,9 @@ cudaError_t launch_cfg(const AttnParams &p, const KvLayout &c, int grid, cudaStr
     static_assert(C::SMEM + 4 * 1024 <= 227 * 1024, "shared memory");
     const int box = box_of(c);
     CUtensorMap mk, mv;
-    if (!map_cache(&mk, p.k, c, box) || !map_cache(&mv, p.v, c, box)) return cudaErrorInvalidValue;
+    int vbox = box;
+    if constexpr (kIsWide<C>) vbox = box < C::KV ? box : C::KV;
+    if (!map_cache(&mk, p.k, c, box) || !map_cache(&mv, p.v, c, vbox)) return cudaErrorInvalidValue;
     constexpr auto kernel = [] {
       if constexpr (kIsWide<C>) return attn_wide_kernel<C, TREE>;
       else return attn_tc_kernel<C, TREE>;
@@ -2046,6 +2176,15 @@ cudaError_t launch_cfg(const AttnParams &p, const KvLayout &c, int grid, cudaStr
     if (e != cudaSuccess) return e;
     e = launch_pdl(attn_kernel<C, false, TREE>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, p, 1);
   }
+  if constexpr (kIsWide<C>) {
+    const int groups = grid / (int)p.row_blocks.d, rows = p.T * (int)p.G.d;
+    if (e != cudaSuccess || groups == 1) return e;
+    const dim3 joins(p.joins, (rows + 7) / 8);
+    // as below
+    if (groups > 32LL * p.n_seqs * p.H_kv)
+      return launch_pdl(join_wide_kernel<C, 4>, joins, dim3(512), 0, stream, p, groups);
+    return launch_pdl(join_wide_kernel<C, 1>, joins, dim3(128), 0, stream, p, groups);
+  }
   if (e != cudaSuccess || grid == 1) return e;
   const int rows = p.row_blocks.d > 1 ? C::ROWS : p.T * (int)p.G.d;
   const long long items = (long long)p.n_seqs * p.H_kv * p.row_blocks.d;
@@ -2066,7 +2205,9 @@ size_t workspace_size(const KvLayout &c, int n_seqs, int T, int H, int max_pages
   const int rows = T * (H / c.H_kv);
   return with_cfg<TREE>(c, rows, [&](auto cfg) -> size_t {
     using C = decltype(cfg);
-    const size_t g = (size_t)grid_of<C>(c, n_seqs, max_pages, (rows + C::ROWS - 1) / C::ROWS);
+    const int row_blocks = (rows + C::ROWS - 1) / C::ROWS;
+    size_t g = (size_t)grid_of<C>(c, n_seqs, max_pages, row_blocks);
+    if (kIsWide<C> && (int)g == row_blocks) g = 1;  // one group: no item is cut
     return up256(g * 16) + up256(g * 2 * C::ROWS * 8) + g * 2 * C::ROWS * c.D * 4;
   });
 }
@@ -2098,6 +2239,11 @@ cudaError_t launch_attention(const AttnArgs &a, cudaStream_t stream) {
     const long long by_block = (long long)grid * (p.row_blocks.d > 1 ? C::ROWS : rows);
     p.by_item = items <= grid && by_block > 16 * kSms;
     p.joins = p.by_item ? (int)items : grid;
+    if constexpr (kIsWide<C>) {
+      const int groups = grid / (int)p.row_blocks.d;
+      p.by_item = (long long)a.n_seqs * c.H_kv <= groups;
+      p.joins = p.by_item ? a.n_seqs * c.H_kv : groups;
+    }
     unsigned char *ws = static_cast<unsigned char *>(a.workspace);
     p.cut = reinterpret_cast<int4 *>(ws);
     ws += up256((size_t)grid * 16);
