@@ -1397,19 +1397,20 @@ struct WideCfg {
   using In = __nv_bfloat16;
   static constexpr bool kTensorMemory = true;
   static constexpr int D = D_, NQ = NQ_, KT = 128 / NQ, ROWS = 128 * NQ;
-  // no more than three warps for each scheduler, so that a lane may hold 64 scores
-  static constexpr int THREADS = 128 + 128 * NQ;
+  // four warps of copies and products, one a row for each lane for each tile of rows,
+  // two of products for the second tile
+  static constexpr int THREADS = 256 + 192 * (NQ - 1);
   // K and V arrive in units, each in a ring of its own: of K KA times 64 columns of
   // the tile's keys, of V KV of its keys, which is what a few products read, so that
   // a place is loaded again while the rest of its tile is still in use
   static constexpr int TILE = KT * D * 2, CC = TILE > 16384 ? TILE / 16384 : 1, UNIT = TILE / CC;
   static constexpr int KA = D / 64 / CC, KV = KT / CC;
   static constexpr int Q_BYTES = ROWS * D * 2;
-  static constexpr int FIT = (222 * 1024 - Q_BYTES) / (2 * UNIT), U = FIT > 6 ? 6 : FIT;
+  static constexpr int U = 4;
   static constexpr int SMEM = 2 * U * UNIT + Q_BYTES + 1024;
   static constexpr int TCOLS = 512;  // sums, then two tiles of scores for each tile of rows
   static constexpr int PER_SM = 1;
-  static_assert(NQ * D + 256 <= TCOLS && U >= CC, "it fits");
+  static_assert(NQ * D + 256 <= TCOLS && U >= CC && SMEM <= 224 * 1024, "it fits");
 };
 
 // D[tmem] (+)= A[tmem] B[smem], A in the lanes of its rows, two bf16 a column; from a whole
@@ -1473,15 +1474,16 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   unsigned char *sm =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full[2][U], empty[2][U];  // of K, of V
-  __shared__ uint64_t s_full[2 * NQ], p_full[2 * NQ], o_done[NQ], o_free[NQ];
-  __shared__ uint64_t q_first, q_full, q_empty, landed, patched;
+  __shared__ uint64_t s_full[2 * NQ], p_full[2 * NQ], o_done[2 * NQ], o_free[NQ];
+  __shared__ uint64_t q_full[NQ], landed, patched, over[2 * NQ];
   __shared__ long long warp_sum[NT / 32];
   __shared__ Place place;
   __shared__ uint32_t tm_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // warps: K (and V), queries, (V or) products of the second tile of rows, products,
-  // rows (4 NQ)
-  constexpr int kIssuer = 3;
+  // warps: 0 K, 1 V, 2 and 12 products of queries and K, 3 and 13 of
+  // probabilities and V, 4 .. 4 + 4 NQ rows. A product's polls (some 200 cycles
+  // each, of phases long over too) and the copies it waits for then hold up no other's.
+  const bool scores = warp == 2 || warp == 12, sums = warp == 3 || warp == 13;
   auto unit_at = [&](int v, int slot) { return (v * U + slot) * C::UNIT; };
   const uint32_t units_s = smem_u32(sm), q_s = units_s + 2 * U * C::UNIT;
   const int items_per_seq = p.H_kv, RB = p.row_blocks.d;
@@ -1495,14 +1497,13 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     for (int i = 0; i < 2 * NQ; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
     }
     for (int i = 0; i < NQ; ++i) {
-      mbar_init(&o_done[i], 1);
       mbar_init(&o_free[i], 4);
+      mbar_init(&q_full[i], 4);
     }
-    mbar_init(&q_first, 4 * NQ);
-    mbar_init(&q_full, 1);
-    mbar_init(&q_empty, NQ);
+    for (int i = 0; i < 2 * NQ; ++i) mbar_init(&over[i], 1);
     mbar_init(&landed, NQ);
     mbar_init(&patched, 1);
     fence_mbar_init();
@@ -1510,7 +1511,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     prefetch_tmap(&mv);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // as attn_tc_kernel
-  if (warp == kIssuer) {
+  if (warp == 3) {
     tmem_alloc(&tm_s, C::TCOLS);
     tmem_relinquish();
   }
@@ -1525,59 +1526,58 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   const bool any = w.begin<KT, NT>(p, items_per_seq, warp_sum, place, group, groups);
   if (!any && tid == 0 && rb == 0 && !p.by_item) p.cut[group].x = -1;
   int tb = 0, patches = 0;   // tiles and cleared tiles of the items before
-  int loaded[2] = {0, 0}, used[2] = {0, 0};  // units of K and V loaded, and given back
+  int loaded = 0;  // units of K (of V) loaded
   bool ok = any;
   for (int seg = 0; ok && w.pos < w.end; ++seg) {
     const int n = w.tiles(), s = w.s, len = w.len, tile0 = w.tile0, kvh = w.x;
     // the item's last tile is here, and ends inside a tile of V
     const int patch_from = len - (tile0 + n - 1) * KT;
     const bool patch = patch_from < KT;
-    // Rows of queries `from`, from + step .. to shared memory, 16 bytes a copy.
-    auto load_q = [&](int from, int step) {
-      const int nodes = TREE ? seq_nodes(p, s, false) : p.T;
-#pragma unroll 4
-      for (int e = from; e < C::ROWS * CH; e += step) {
-        const int r = e / CH, c = e % CH;
-        const long long row = out_row(p, s, kvh, r0 + r);
-        const bool live = row >= 0 && p.G.div(r0 + r) < nodes;
-        cp_async16(q_s + (r >> 7) * (128 * D * 2) + (c >> 3) * (128 * 128) + (r & 127) * 128 +
-                       (((c & 7) ^ (r & 7)) << 4),
-                   static_cast<const T *>(p.q) + (live ? row : 0) * D + c * 8, live);
+    // Tile t of K (of V) has arrived, and phase `phase` of `bar` is over.
+    auto wait_tile = [&](int v, int t, uint64_t *bar, int phase) {
+      bool all = false;
+      for (uint32_t i = 0; i < kMaxPolls && !all; ++i) {
+        all = mbar_try_wait(bar, phase & 1);
+#pragma unroll
+        for (int c = 0; c < CC; ++c) {
+          const int u = t * CC + c;
+          all &= mbar_try_wait(&full[v][u % U], (u / U) & 1);
+        }
       }
-      cp_async_commit();
-      cp_async_wait<0>();
-      fence_proxy_async();
-      __syncwarp();
+      if (!all) set_error(p.err, kDevTimeout | (kSiteAttnTile << 8));
+      all = __all_sync(0xffffffffu, all);
+      tc_fence_after();
+      return all;
     };
-    if (warp == 0 || (NQ == 1 && warp == 2)) {
-      if (lane == 0 && warp == 0 && rb == 0) w.list_join(p, items_per_seq, n);
+    if (warp < 2) {
+      const int v = warp;  // K, V
+      if (v == 0 && lane == 0 && rb == 0) w.list_join(p, items_per_seq, n);
+      if (TREE && v == 1 && lane == 0) seq_nodes(p, s, w.x == 0 && tile0 == 0);
       // A lane's boxes of a tile, at most two: 64 columns of kbox keys of K, of vbox
       // of V, unit by unit
       const int32_t *table = p.table + (long long)s * p.max_pages;
-      const int kbox = box, vbox = min(box, KV);
-      const int per[2] = {KT / kbox * KA, KV / vbox * (D / 64)};  // boxes of a unit
-      auto key_of = [&](int v, int e) {                // first key of box e in its tile
-        return v ? e / per[1] * KV + e % per[1] / (D / 64) * vbox : e % per[0] / KA * kbox;
+      const int keys = v ? min(box, KV) : box;              // of a box
+      const int cols = v ? D / 64 : KA;                     // boxes side by side
+      const int per = (v ? KV : KT) / keys * cols;          // boxes of a unit
+      const int stride = (v ? KV : KT) * 128;               // of 64 columns of a unit
+      auto key_of = [&](int e) {                            // first key of box e in its tile
+        return (v ? e / per * KV : 0) + e % per / cols * keys;
       };
-      auto page_of = [&](int i, int v, int e) -> int {
-        const int key = (tile0 + i) * KT + key_of(v, e);
-        return e < CC * per[v] && i < n && key < len ? table[p.page_size.div(key)] : -1;
+      auto page_of = [&](int i, int e) -> int {
+        const int key = (tile0 + i) * KT + key_of(e);
+        return e < CC * per && i < n && key < len ? table[p.page_size.div(key)] : -1;
       };
-      int page[2][2];
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        page[v][0] = page_of(0, v, lane);
-        page[v][1] = page_of(0, v, lane + 32);
-      }
-      auto load = [&](int i, int v) {  // K (V) of tile i
+      int page[2] = {page_of(0, lane), page_of(0, lane + 32)};
+#pragma unroll 1
+      for (int i = 0; i < n && ok; ++i) {
         int next[2], at[2];
         bool live[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int e = lane + 32 * x, key = (tile0 + i) * KT + key_of(v, e);
-          next[x] = page_of(i + 1, v, e);
-          live[x] = e < CC * per[v] && key < len;
-          if (live[x] && (page[v][x] < 0 || page[v][x] >= p.n_pages)) {
+          const int e = lane + 32 * x, key = (tile0 + i) * KT + key_of(e);
+          next[x] = page_of(i + 1, e);
+          live[x] = e < CC * per && key < len;
+          if (live[x] && (page[x] < 0 || page[x] >= p.n_pages)) {
             set_error(p.err, kDevBadPage);
             live[x] = false;
           }
@@ -1593,46 +1593,26 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           uint32_t boxes = 0;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            mine[x] = live[x] && (lane + 32 * x) / per[v] == c;
+            mine[x] = live[x] && (lane + 32 * x) / per == c;
             boxes += __popc(__ballot_sync(0xffffffffu, mine[x]));
           }
-          if (lane == 0) mbar_arrive_expect_tx(&full[v][slot], boxes * (v ? vbox : kbox) * 128);
+          if (lane == 0) mbar_arrive_expect_tx(&full[v][slot], boxes * keys * 128);
           __syncwarp();
-          loaded[v] = u + 1;
+          loaded = u + 1;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int e = (lane + 32 * x) % per[v];
-            if (!mine[x]) continue;
-            unsigned char *dst = sm + unit_at(v, slot);
-            if (v)
-              tma_load_4d(dst + e % (D / 64) * (KV * 128) + e / (D / 64) * vbox * 128, &mv,
-                          e % (D / 64) * 64, kvh, at[x], page[v][x], &full[v][slot]);
-            else
-              tma_load_4d(dst + e % KA * (KT * 128) + e / KA * kbox * 128, &mk,
-                          (c * KA + e % KA) * 64, kvh, at[x], page[v][x], &full[v][slot]);
+            const int e = (lane + 32 * x) % per, col = e % cols;
+            if (mine[x])
+              tma_load_4d(sm + unit_at(v, slot) + col * stride + e / cols * keys * 128,
+                          v ? &mv : &mk, ((v ? 0 : c * KA) + col) * 64, kvh, at[x], page[x],
+                          &full[v][slot]);
           }
         }
-        page[v][0] = next[0];
-        page[v][1] = next[1];
-      };
-#pragma unroll 1
-      for (int i = 0; i < n && ok; ++i) {
-        if (NQ == 2 || warp == 0) load(i, 0);
-        if (ok && (NQ == 2 || warp == 2)) load(i, 1);
+        page[0] = next[0];
+        page[1] = next[1];
       }
-    } else if (warp == 1) {
-      // queries of the items after the first, ahead of their turn
-      if (seg > 0) {
-        ok = mbar_wait(&q_empty, (seg - 1) & 1, p.err, kSiteAttnTile);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          load_q(lane, 32);
-          if (lane == 0) mbar_arrive(&q_full);
-        }
-      }
-      if (TREE && lane == 0) seq_nodes(p, s, w.x == 0 && tile0 == 0);
-      if (ok && patch) {
-        // told by the issuing warps, as in attn_tc_kernel
+      if (v && ok && patch) {
+        // told by the warp of the products, as in attn_tc_kernel
         ok = mbar_wait(&landed, patches & 1, p.err, kSiteAttnTile);
         ok = __all_sync(0xffffffffu, ok);
         const int from = max(patch_from, 0);
@@ -1647,27 +1627,20 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         __syncwarp();
         if (lane == 0) mbar_arrive(&patched);
       }
-    } else if (warp <= kIssuer) {
-      const int q = NQ == 2 ? kIssuer - warp : 0;
-      // Tile t's product with V is over. Every phase of the barrier is waited for
-      // before the next can end: a parity tells neighbours apart and no more.
-      auto wait_sums = [&](int t) {
-        ok = ok && mbar_wait(&o_done[q], t & 1, p.err, kSiteAttnSum);
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after();
-      };
-      auto arrived = [&](int v, int u) {  // unit u of K (V)
-        ok = ok && mbar_wait(&full[v][u % U], (u / U) & 1, p.err, kSiteAttnTile);
-        ok = __all_sync(0xffffffffu, ok);
-        tc_fence_after();
-      };
-      auto scores = [&](int i) {  // S = Q K^T of tile i
-        const int t = tb + i, b = 2 * q + (t & 1);
+    } else if (scores) {  // S = Q K^T
+      const int q = warp > 3;
+      ok = mbar_wait(&q_full[q], seg & 1, p.err, kSiteAttnTile);
+      ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+      for (int t = tb; t < tb + n && ok; ++t) {
+        // in the place of the tile before the last, whose product is over (of the
+        // first two: a phase before the first is over)
+        const int b = 2 * q + (t & 1);
+        ok = wait_tile(0, t, &o_done[b], (t >> 1) + 1);
+        if (!ok) break;
 #pragma unroll 1
         for (int c = 0; c < CC; ++c) {
-          const int u = t * CC + c, slot = u % U;
-          arrived(0, u);
-          if (!ok) return;
+          const int slot = (t * CC + c) % U;
 #pragma unroll
           for (int ks = 0; ks < 4 * KA; ++ks)
             umma_bf16_elect(tm_score + b * KT,
@@ -1676,49 +1649,35 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
                             sdesc_kmajor(units_s + unit_at(0, slot) + ks / 4 * (KT * 128) +
                                          ks % 4 * 32),
                             idesc_bf16_f32(128, KT, false, false), c > 0 || ks > 0);
+          if (c == CC - 1) umma_commit_elect(&s_full[b]);
           umma_commit_elect(&empty[0][slot]);
-          used[0] = u + 1;
         }
-        umma_commit_elect(&s_full[b]);
-        if (i == n - 1) umma_commit_elect(&q_empty);
-      };
-      auto sums = [&](int i) {  // O (+)= P V
-        const int t = tb + i, b = 2 * q + (t & 1);
-        if (patch && i == n - 1) {
-          for (int c = 0; c < CC; ++c) arrived(1, t * CC + c);
+      }
+    } else if (sums) {  // O (+)= P V
+      const int q = warp > 3;
+      ok = mbar_wait(&o_free[q], (seg + 1) & 1, p.err, kSiteAttnSum);
+      ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+      for (int t = tb; t < tb + n && ok; ++t) {
+        const int b = 2 * q + (t & 1);
+        ok = wait_tile(1, t, &p_full[b], t >> 1);
+        if (patch && t == tb + n - 1) {
           if (ok && lane == 0) mbar_arrive(&landed);
           ok = ok && mbar_wait(&patched, patches & 1, p.err, kSiteAttnTile);
           ok = __all_sync(0xffffffffu, ok);
         }
-        ok = ok && mbar_wait(&p_full[b], (t >> 1) & 1, p.err, kSiteAttnSum);
-        if (i == 0) ok = ok && mbar_wait(&o_free[q], (seg + 1) & 1, p.err, kSiteAttnSum);
-        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
 #pragma unroll 1
         for (int c = 0; c < CC; ++c) {
-          const int u = t * CC + c, slot = u % U;
-          arrived(1, u);
-          if (!ok) return;
+          const int slot = (t * CC + c) % U;
 #pragma unroll
           for (int ks = 0; ks < KV / 16; ++ks)
             umma_bf16_ts_elect(tm + q * D, tm_score + b * KT + KT / 2 + (c * (KV / 16) + ks) * 8,
                                sdesc_mnmajor(units_s + unit_at(1, slot) + ks * 2048, KV * 128),
-                               idesc_bf16_f32(128, D, false, true), i > 0 || c > 0 || ks > 0);
-          if (c == CC - 1) umma_commit_elect(&o_done[q]);
+                               idesc_bf16_f32(128, D, false, true), t > tb || c > 0 || ks > 0);
+          if (c == CC - 1) umma_commit_elect(&o_done[b]);
           umma_commit_elect(&empty[1][slot]);
-          used[1] = u + 1;
         }
-      };
-      if (seg == 0) ok = mbar_wait(&q_first, 0, p.err, kSiteAttnTile);
-      else ok = mbar_wait(&q_full, (seg - 1) & 1, p.err, kSiteAttnTile);
-      ok = __all_sync(0xffffffffu, ok);
-      // scores take the place of those of the tile before the last, whose product is
-      // over
-      if (ok) scores(0);
-#pragma unroll 1
-      for (int i = 0; i < n && ok; ++i) {
-        if (tb + i > 0) wait_sums(tb + i - 1);
-        if (ok && i + 1 < n) scores(i + 1);
-        if (ok) sums(i);
       }
     } else {
       // a row of this lane's
@@ -1731,9 +1690,30 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       // rows that are not there take part without a mask
       const int lim = !mine || absent ? len : TREE ? len - nodes : len - p.T + t_row + 1;
       const unsigned long long word = TREE && mine ? node_word(p, s, t_row, nodes) : 0;
+      // This warp's 32 rows of queries of an item to shared memory, 16 bytes a copy: a
+      // lane knows where its row is.
+      auto load_q = [&](int s, int x) {
+        const int nodes = TREE ? seq_nodes(p, s, false) : p.T;
+        const long long from = mine && t_row < nodes ? out_row(p, s, x, row) : -1;
+#pragma unroll 8
+        for (int e = lane; e < 32 * CH; e += 32) {
+          const int i = e / CH, r = (warp & 3) * 32 + i, c = e % CH;
+          const long long at = __shfl_sync(0xffffffffu, from, i);
+          cp_async16(q_s + q * (128 * D * 2) + (c >> 3) * (128 * 128) + r * 128 +
+                         (((c & 7) ^ (r & 7)) << 4),
+                     static_cast<const T *>(p.q) + max(at, 0ll) * D + c * 8, at >= 0);
+        }
+        cp_async_commit();
+      };
+      auto q_loaded = [&] {
+        cp_async_wait<0>();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[q]);
+      };
       if (seg == 0) {
-        load_q(tid - 128, 128 * NQ);
-        if (lane == 0) mbar_arrive(&q_first);
+        load_q(s, kvh);
+        q_loaded();
       }
       float ref = -INFINITY, l = 0.f;
 #pragma unroll 1
@@ -1772,7 +1752,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         ref = next;
         l *= alpha;
         if (i > 0 && __any_sync(0xffffffffu, grow)) {
-          ok = mbar_wait(&o_done[q], (t - 1) & 1, p.err, kSiteAttnSum);
+          ok = mbar_wait(&o_done[2 * q + ((t - 1) & 1)], ((t - 1) >> 1) & 1, p.err, kSiteAttnSum);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -1822,11 +1802,17 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[b]);
       }
-      // one phase after the other: a wait for the last alone would be over before
-      // the one before it has begun
-      if (ok && n > 1) ok = mbar_wait(&o_done[q], (tb + n - 2) & 1, p.err, kSiteAttnSum);
-      if (ok) ok = mbar_wait(&o_done[q], (tb + n - 1) & 1, p.err, kSiteAttnSum);
+      // The item's last scores are over: the next one's queries may come.
+      Walk after = w;
+      after.next<KT>(p, items_per_seq, n);
+      const bool more = ok && after.pos < after.end;
+      if (more) load_q(after.s, after.x);
+      if (ok) {
+        const int t = tb + n - 1;
+        ok = mbar_wait(&o_done[2 * q + (t & 1)], (t >> 1) & 1, p.err, kSiteAttnSum);
+      }
       ok = __all_sync(0xffffffffu, ok);
+      if (more) q_loaded();
       if (ok) {
         tc_fence_after();
         const bool whole = n == w.nt;
@@ -1870,16 +1856,18 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     w.next<KT>(p, items_per_seq, n);
   }
   if (any && !ok) {  // otherwise every copy and product has been waited for
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      for (int u = max(loaded[v] - U, 0); u < loaded[v]; ++u)
-        mbar_drain(&full[v][u % U], (u / U) & 1);
-      if (used[v] > 0) mbar_drain(&empty[v][(used[v] - 1) % U], ((used[v] - 1) / U) & 1);
+    if (warp < 2)
+      for (int u = max(loaded - U, 0); u < loaded; ++u)
+        mbar_drain(&full[warp][u % U], (u / U) & 1);
+    if (scores || sums) {
+      const int i = 2 * (warp > 3) + sums;
+      umma_commit_elect(&over[i]);
+      mbar_drain(&over[i], 0);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssuer) tmem_dealloc(tm, C::TCOLS);
+  if (warp == 3) tmem_dealloc(tm, C::TCOLS);
 }
 
 // Joins the cut items of attn_wide_kernel: block (i, y) rows 8 y .. 8 y + 8 of the
