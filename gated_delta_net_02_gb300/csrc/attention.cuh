@@ -1463,6 +1463,13 @@ __device__ __forceinline__ unsigned long long seen64(int key, int lim, unsigned 
   return past < 64 ? word >> past : 0;
 }
 
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\t"
+      "add.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+
 template <class C, bool TREE>
 __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     attn_wide_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
@@ -1723,30 +1730,39 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        // In halves of 64 keys, read twice where a tile has two, by loops that are not
-        // unrolled: code for 128 scores at once is fetched anew for every tile, and
-        // the warp that issues products waits for its own behind it.
+        // What every tile runs is kept short, in halves of 64 keys (read twice where a
+        // tile has two) and by loops that are not unrolled: longer code is fetched anew
+        // for every tile, and the warps that issue products wait for theirs behind it.
         const uint32_t score = tm_score + b * KT + lanes;
         const int key0 = (tile0 + i) * KT;
-        const bool cut = key0 + KT > lim;
+        float factor = p.scale_log2;
+        if (factor < 0.f || __any_sync(0xffffffffu, key0 + KT > lim)) {
+          // scaled and masked in their place, so that the rest needs no mask
+#pragma unroll 1
+          for (int c = 0; c < KT; c += 16) {
+            const unsigned seen = (unsigned)seen64(key0 + c, lim, word);
+            float x[16];
+            tmem_ld16(score + c, x);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = seen >> j & 1 ? x[j] * factor : -INFINITY;
+            tmem_st16(score + c, x);
+          }
+          tmem_wait_st();
+          factor = 1.f;
+        }
         float x[64], top = -INFINITY;
 #pragma unroll 1
         for (int h = 0; h < KT / 64; ++h) {
           tmem_ld64(score + 64 * h, x);
-#pragma unroll
-          for (int j = 0; j < 64; ++j) x[j] *= p.scale_log2;
-          if (cut) {
-            const unsigned long long seen = seen64(key0 + 64 * h, lim, word);
-            const uint32_t part[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
-#pragma unroll
-            for (int j = 0; j < 64; ++j)
-              x[j] = part[j >> 5] >> (j & 31) & 1 ? x[j] : -INFINITY;
-          }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < 64; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+          for (int j = 0; j < 64; j += 2) {
+            float &m = mx[j >> 1 & 3];
+            m = fmaxf(fmaxf(m, x[j]), x[j + 1]);
+          }
           top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
         }
+        top *= factor;  // as the largest product: rounding keeps the order
         const bool grow = top > ref + kMaxGrowth;
         const float next = grow ? top : ref, alpha = grow ? exp2_ftz(ref - next) : 1.f;
         ref = next;
@@ -1771,27 +1787,18 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         // the later keys first: the probabilities take the place of their scores
 #pragma unroll 1
         for (int h = KT / 64 - 1; h >= 0; --h) {
-          if (KT > 64) {
-            tmem_ld64(score + 64 * h, x);
-#pragma unroll
-            for (int j = 0; j < 64; ++j) x[j] *= p.scale_log2;
-            if (cut) {
-              const unsigned long long seen = seen64(key0 + 64 * h, lim, word);
-              const uint32_t part[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
-#pragma unroll
-              for (int j = 0; j < 64; ++j)
-                x[j] = part[j >> 5] >> (j & 31) & 1 ? x[j] : -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 64; ++j) x[j] = exp2_ftz(x[j] - base);
+          if (KT > 64) tmem_ld64(score + 64 * h, x);
 #pragma unroll
           for (int c = 0; c < 64; c += 32) {
             float pk[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              sum[j & 3] += x[c + 2 * j] + x[c + 2 * j + 1];
-              pk[j] = __uint_as_float(bf16x2(x[c + 2 * j], x[c + 2 * j + 1]));
+              float y = -base, z = -base;
+              fma2(y, z, x[c + 2 * j], x[c + 2 * j + 1], factor, factor);
+              y = exp2_ftz(y);
+              z = exp2_ftz(z);
+              add2(sum[2 * (j & 1)], sum[2 * (j & 1) + 1], y, z);
+              pk[j] = __uint_as_float(bf16x2(y, z));
             }
             tmem_st16(score + KT / 2 + 32 * h + c / 2, pk);
           }
