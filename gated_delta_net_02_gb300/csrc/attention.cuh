@@ -1413,6 +1413,16 @@ struct WideCfg {
   static_assert(NQ * D + 256 <= TCOLS && U >= CC && SMEM <= 224 * 1024, "it fits");
 };
 
+__device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int c0, int c1,
+                                            int c2, int c3, int c4, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
 // D[tmem] (+)= A[tmem] B[smem], A in the lanes of its rows, two bf16 a column; from a whole
 // converged warp, as umma_bf16_elect.
 __device__ __forceinline__ void umma_bf16_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
@@ -1560,15 +1570,16 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
       const int v = warp;  // K, V
       if (v == 0 && lane == 0 && rb == 0) w.list_join(p, items_per_seq, n);
       if (TREE && v == 1 && lane == 0) seq_nodes(p, s, w.x == 0 && tile0 == 0);
-      // A lane's boxes of a tile, at most two: 64 columns of kbox keys of K, of vbox
-      // of V, unit by unit
+      // A lane's boxes of a tile, at most two, unit by unit: 64 columns of `keys` keys, or
+      // all of a unit's columns where a box has all of its keys (a copy takes some 250
+      // cycles to begin, whatever its size)
       const int32_t *table = p.table + (long long)s * p.max_pages;
-      const int keys = v ? min(box, KV) : box;              // of a box
-      const int cols = v ? D / 64 : KA;                     // boxes side by side
-      const int per = (v ? KV : KT) / keys * cols;          // boxes of a unit
-      const int stride = (v ? KV : KT) * 128;               // of 64 columns of a unit
-      auto key_of = [&](int e) {                            // first key of box e in its tile
-        return (v ? e / per * KV : 0) + e % per / cols * keys;
+      const int unit_keys = v ? KV : KT, keys = min(box, unit_keys);  // of a unit, of a box
+      const int cols = keys == unit_keys ? 1 : v ? D / 64 : KA;       // boxes side by side
+      const int per = unit_keys / keys * cols;                        // boxes of a unit
+      const int bytes = C::UNIT / per, log_cols = 31 - __clz(cols), log_per = 31 - __clz(per);
+      auto key_of = [&](int e) {  // first key of box e in its tile
+        return (v ? (e >> log_per) * KV : 0) + ((e & (per - 1)) >> log_cols) * keys;
       };
       auto page_of = [&](int i, int e) -> int {
         const int key = (tile0 + i) * KT + key_of(e);
@@ -1600,18 +1611,18 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
           uint32_t boxes = 0;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            mine[x] = live[x] && (lane + 32 * x) / per == c;
+            mine[x] = live[x] && (lane + 32 * x) >> log_per == c;
             boxes += __popc(__ballot_sync(0xffffffffu, mine[x]));
           }
-          if (lane == 0) mbar_arrive_expect_tx(&full[v][slot], boxes * keys * 128);
+          if (lane == 0) mbar_arrive_expect_tx(&full[v][slot], boxes * bytes);
           __syncwarp();
           loaded = u + 1;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int e = (lane + 32 * x) % per, col = e % cols;
+            const int e = (lane + 32 * x) & (per - 1), col = e & (cols - 1);
             if (mine[x])
-              tma_load_4d(sm + unit_at(v, slot) + col * stride + e / cols * keys * 128,
-                          v ? &mv : &mk, ((v ? 0 : c * KA) + col) * 64, kvh, at[x], page[x],
+              tma_load_5d(sm + unit_at(v, slot) + (col * unit_keys + (e >> log_cols) * keys) * 128,
+                          v ? &mv : &mk, 0, at[x], (v ? 0 : c * KA) + col, kvh, page[x],
                           &full[v][slot]);
           }
         }
@@ -2090,6 +2101,21 @@ bool map_cache(CUtensorMap *m, const void *base, const KvLayout &c, int box) {
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same as (64, page_size, D / 64, H_kv, n_pages); boxes of 64 columns x `box` tokens x
+// `cols` times 64 columns, which come to lie one behind the other.
+bool map_columns(CUtensorMap *m, const void *base, const KvLayout &c, int box, int cols) {
+  const cuuint64_t dims[5] = {64, (cuuint64_t)c.page_size, (cuuint64_t)c.D / 64,
+                              (cuuint64_t)c.H_kv, (cuuint64_t)c.n_pages};
+  const cuuint64_t strides[4] = {(cuuint64_t)c.token_stride * 2, 128, (cuuint64_t)c.head_stride * 2,
+                                 (cuuint64_t)c.page_stride * 2};
+  const cuuint32_t b[5] = {64, (cuuint32_t)box, (cuuint32_t)cols, 1, 1}, es[5] = {1, 1, 1, 1, 1};
+  return encode_fn() &&
+         encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims,
+                     strides, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kSms = 152;
 
 template <class C>
@@ -2144,9 +2170,15 @@ cudaError_t launch_cfg(const AttnParams &p, const KvLayout &c, int grid, cudaStr
     static_assert(C::SMEM + 4 * 1024 <= 227 * 1024, "shared memory");
     const int box = box_of(c);
     CUtensorMap mk, mv;
-    int vbox = box;
-    if constexpr (kIsWide<C>) vbox = box < C::KV ? box : C::KV;
-    if (!map_cache(&mk, p.k, c, box) || !map_cache(&mv, p.v, c, vbox)) return cudaErrorInvalidValue;
+    bool mapped;
+    if constexpr (kIsWide<C>) {
+      const int kbox = std::min(box, C::KT), vbox = std::min(box, C::KV);
+      mapped = map_columns(&mk, p.k, c, kbox, kbox == C::KT ? C::KA : 1) &&
+               map_columns(&mv, p.v, c, vbox, vbox == C::KV ? C::D / 64 : 1);
+    } else {
+      mapped = map_cache(&mk, p.k, c, box) && map_cache(&mv, p.v, c, box);
+    }
+    if (!mapped) return cudaErrorInvalidValue;
     constexpr auto kernel = [] {
       if constexpr (kIsWide<C>) return attn_wide_kernel<C, TREE>;
       else return attn_tc_kernel<C, TREE>;
