@@ -39,6 +39,7 @@ constexpr int kBins = 768, kFineBins = 512;  // of the first histograms and of a
 constexpr int kSms = 152;
 constexpr float kOctaves = 44.9f;     // further down, weights are 0
 constexpr int kGroups = 16;          // pieces of a warp's share with a mass of their own
+constexpr int kList = 1024;          // logits of the bin that is refined, of a block
 constexpr int kFine = 64, kCoarse = 184;  // table entries: 45 octaves x 256 points, by 64
 
 struct SampleParams {
@@ -187,6 +188,7 @@ struct Shared {
   u64 group[2][32];        // sums of 32 bins
   Small power[14];         // 2^(-2^k steps)
   float queue[kWarps][64];
+  float list[kList];
   u64 warp_part[kWarps], warp_part2[kWarps];
   u64 seg_mass[kWarps][kGroups];
   uint32_t seg_ties[kWarps][kGroups];
@@ -197,7 +199,7 @@ struct Shared {
   float depth;             // logits from the largest to weight 0
   double min_drop;         // temperature * log(min_p)
   float warp_top[kWarps];
-  int found;
+  int found, listed;
   u64 before, there, goal, total;
 };
 
@@ -312,6 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   clear(0);
   clear(1);
+  if (tid == 0) sh.listed = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   Share<T> share;
@@ -514,18 +517,35 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float lo = fmaxf(of_key(key_of((edge - 15) * sh.step + grid.from) - 8), low);
     const float hi = fminf(of_key(key_of((edge + 1) * sh.step + grid.from) + 8), top);
     uint32_t khi = key_of(hi) >> kLow, klo = key_of(lo) >> kLow;
-    for (;;) {
+    for (bool first = true;; first = false) {
       int shift = 0;
       while ((khi - klo) >> shift >= (uint32_t)kFineBins) ++shift;
-      share.each_between(lo, hi, 0, chunks, [&](float x) {
-        const uint32_t k = key_of(x) >> kLow;
-        if (bin_of(x) != bin || k > khi || k < klo) return;
+      auto add = [&](float x, uint32_t k) {
         const int i = (int)((khi - k) >> shift);
         auto &h = sh.hist[buf].fine;
         atomicAdd(&h.count[i], 1u);
         atomicMax(&h.most[i], k);
         if (by_mass) atomicAdd(&h.mass[i], grid.weight(x));
-      });
+      };
+      // the first pass lists the bin's logits, the others need only those
+      const int listed = sh.listed;
+      if (first || listed > kList) {
+        share.each_between(lo, hi, 0, chunks, [&](float x) {
+          const uint32_t k = key_of(x) >> kLow;
+          if (bin_of(x) != bin || k > khi || k < klo) return;
+          add(x, k);
+          if (first) {
+            const int at = atomicAdd(&sh.listed, 1);
+            if (at < kList) sh.list[at] = x;
+          }
+        });
+      } else {
+        for (int i = tid; i < listed; i += kThreads) {
+          const float x = sh.list[i];
+          const uint32_t k = key_of(x) >> kLow;
+          if (k <= khi && k >= klo) add(x, k);
+        }
+      }
       if (by_mass) {
         pass_done(kFineBins, mass_in);
         search(have, [&](u64) { return want; }, far_mass);
@@ -548,7 +568,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         key <<= kLow;
         if constexpr (kLow > 0) key |= (int)key < 0 ? 0u : 0xffffu;
         cut = of_key(key);
-        if (tid == 0) sh.there = there;
+        if (tid == 0) {
+          sh.there = there;
+          sh.listed = 0;
+        }
         __syncthreads();
         return;
       }
@@ -755,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // Bytes of a row's share in shared memory: two blocks on an SM up to the first;
 // the second is what 8 blocks need of the longest rows (2^18 fp32).
-constexpr int kShareTwo = 80 * 1024, kShareMost = 136 * 1024;
+constexpr int kShareTwo = 76 * 1024, kShareMost = 136 * 1024;
 static_assert(2 * (kShareTwo + sizeof(Shared) + 1024) <= 228 * 1024, "two blocks");
 static_assert(((1 << 18) * 4 / 16 + 8 * kWarps) / (8 * kWarps) * kWarps * 16 <= kShareMost, "fits");
 
