@@ -39,7 +39,7 @@ constexpr int kBins = 768, kFineBins = 512;  // of the first histograms and of a
 constexpr int kSms = 152;
 constexpr float kOctaves = 44.9f;     // further down, weights are 0
 constexpr int kGroups = 16;          // pieces of a warp's share with a mass of their own
-constexpr int kList = 1024;          // logits of the bin that is refined, of a block
+constexpr int kList = 1024;          // logits that a block lists
 constexpr int kFine = 64, kCoarse = 184;  // table entries: 45 octaves x 256 points, by 64
 
 struct SampleParams {
@@ -314,7 +314,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   };
   clear(0);
   clear(1);
-  if (tid == 0) sh.listed = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   Share<T> share;
@@ -507,6 +506,26 @@ __global__ void __launch_bounds__(kThreads, 2)
            ((u64)ld_cluster_u32(&sh.hist[buf].part[2][i], k) << 32);
   };
 
+  // f(x) for the block's logits lo <= x <= hi, by all of its threads: from the list where
+  // it has them all; or by the row, and then (`list`) they are listed.
+  float list_lo = INFINITY, list_hi = -INFINITY;  // what the list was made of
+  auto visit = [&](float lo, float hi, bool list, auto f) {
+    if (!list && list_lo <= lo && hi <= list_hi && sh.listed <= kList) {
+      const int n = sh.listed;
+      for (int i = tid; i < n; i += kThreads) {
+        const float x = sh.list[i];
+        if (x >= lo && x <= hi) f(x);
+      }
+      return;
+    }
+    share.each_between(lo, hi, 0, chunks, [&](float x) {
+      f(x);
+      if (list) {
+        const int at = atomicAdd(&sh.listed, 1);
+        if (at < kList) sh.list[at] = x;
+      }
+    });
+  };
   // The value at which the order's running count (BY_MASS: mass) first reaches
   // `want`, among the logits from `low` on in bin `bin`; `have` = what comes
   // before that bin. Leaves the value in cut, what comes before it in sh.before
@@ -517,35 +536,27 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float lo = fmaxf(of_key(key_of((edge - 15) * sh.step + grid.from) - 8), low);
     const float hi = fminf(of_key(key_of((edge + 1) * sh.step + grid.from) + 8), top);
     uint32_t khi = key_of(hi) >> kLow, klo = key_of(lo) >> kLow;
-    for (bool first = true;; first = false) {
+    for (;;) {
       int shift = 0;
       while ((khi - klo) >> shift >= (uint32_t)kFineBins) ++shift;
-      auto add = [&](float x, uint32_t k) {
+      // the last of a count has few before it, which the masses are made of: they
+      // are listed with the bin's
+      const bool list = !(list_lo <= lo && hi <= list_hi);
+      if (list) {
+        list_lo = lo;
+        list_hi = !by_mass && have <= kList ? top : hi;
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+      }
+      visit(lo, list ? list_hi : hi, list, [&](float x) {
+        const uint32_t k = key_of(x) >> kLow;
+        if (bin_of(x) != bin || k > khi || k < klo) return;
         const int i = (int)((khi - k) >> shift);
         auto &h = sh.hist[buf].fine;
         atomicAdd(&h.count[i], 1u);
         atomicMax(&h.most[i], k);
         if (by_mass) atomicAdd(&h.mass[i], grid.weight(x));
-      };
-      // the first pass lists the bin's logits, the others need only those
-      const int listed = sh.listed;
-      if (first || listed > kList) {
-        share.each_between(lo, hi, 0, chunks, [&](float x) {
-          const uint32_t k = key_of(x) >> kLow;
-          if (bin_of(x) != bin || k > khi || k < klo) return;
-          add(x, k);
-          if (first) {
-            const int at = atomicAdd(&sh.listed, 1);
-            if (at < kList) sh.list[at] = x;
-          }
-        });
-      } else {
-        for (int i = tid; i < listed; i += kThreads) {
-          const float x = sh.list[i];
-          const uint32_t k = key_of(x) >> kLow;
-          if (k <= khi && k >= klo) add(x, k);
-        }
-      }
+      });
       if (by_mass) {
         pass_done(kFineBins, mass_in);
         search(have, [&](u64) { return want; }, far_mass);
@@ -568,10 +579,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         key <<= kLow;
         if constexpr (kLow > 0) key |= (int)key < 0 ? 0u : 0xffffu;
         cut = of_key(key);
-        if (tid == 0) {
-          sh.there = there;
-          sh.listed = 0;
-        }
+        if (tid == 0) sh.there = there;
         __syncthreads();
         return;
       }
@@ -604,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (top_p < 1.f) {
       const float low = fmaxf(grid.low, of_key(key_of(cut) + 1));
-      share.each_between(low, top, 0, chunks, [&](float x) {
+      visit(low, top, false, [&](float x) {
         int j;
         const u64 w = grid.weight(x, j);
         auto &part = sh.hist[buf].part;

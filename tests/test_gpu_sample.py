@@ -250,3 +250,16 @@ def test_frequencies_follow_the_weights(gdn):
     p = torch.softmax(x[0].double().cpu(), 0)
     count = torch.bincount(tokens.cpu().long(), minlength=5).double()
     assert bool(((count - n * p).abs() <= 5 * (n * p * (1 - p)).sqrt()).all())
+
+
+@pytest.mark.parametrize("spread", [2.0 ** -10, 2.0 ** -4])
+def test_many_logits_of_one_bin(gdn, spread):
+    # more values between the bounds of one bin than a block lists, and some rows
+    # with fewer; the last kept one takes several rounds to find
+    g = torch.Generator("cuda").manual_seed(13)
+    torch.manual_seed(13)
+    x = torch.randn(7, 60000, generator=g, device="cuda") * spread
+    k = torch.tensor([3, 900, 1023, 1025, 5000, 59999, 0], dtype=torch.int32)
+    run(gdn, x, top_k=k)
+    run(gdn, x, top_k=k, top_p=0.2 + 0.7 * torch.rand(7))
+    run(gdn, x, top_p=0.2 + 0.7 * torch.rand(7))
