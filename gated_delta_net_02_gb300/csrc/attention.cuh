@@ -1379,19 +1379,30 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 // Rows x keys of more than a tile of 128 rows are bound by the products and the
 // exponentials together (128 rows, 128 keys, heads of 128: some 1,100 cycles of
 // products at the measured bf16 rate, 1,024 of exponentials), so neither may wait
-// for the other. Two tiles of scores are under way at any time: of two tiles of rows
-// (NQ = 2: every key and value then serves 256 rows), or, where the sums of one
-// tile fill half of tensor memory (heads of 256) or its rows are all there are, of
-// two tiles of keys. While one is turned into probabilities, the other's products
-// run. A lane of the four warps of a row tile has a whole row, so maximum and sum
-// need no other lane; probabilities go back to tensor memory over their scores, as
-// the next product's first operand, and cost no shared memory.
-// Scores overwrite the probabilities of the tile before (the one before that, with
-// two tiles of keys) once the product that reads those is over; each tile of rows
-// has a warp of its own to issue its products, so that one's wait is the other's turn.
+// for the other. Two tiles of scores are under way for every tile of rows: while one
+// is turned into probabilities, the other's products run. With two tiles of rows
+// (NQ = 2: every key and value then serves 256 rows) tensor memory has room for
+// tiles of 64 keys; with one (heads of 256, whose sums fill half of it, or up to
+// 128 rows) for 128. One tile of 128 keys a tile of rows instead of two of 64 was
+// slower (32 sequences x 32 nodes, below: 71 us for 66).
+// A lane of the four warps of a row tile has a whole row, so maximum and sum need
+// no other lane; probabilities go back to tensor memory over their scores, as the
+// next product's first operand, and cost no shared memory. Scores overwrite the
+// probabilities of the tile before the last once the product that reads those is
+// over.
+// Every wait costs some 200 to 500 cycles, so each kind of work has a warp of its
+// own: one that polls for all made 90 us of the 66. Lanes that poll alone, the rest
+// of the warp waiting, were slower yet (75).
+// A copy takes some 250 cycles to begin, whatever its size: a unit of V has all its
+// columns in one where pages allow (338 us for 447, below).
 // The blocks of rows of an item (64 nodes x 8 heads of 256 are four) go to
 // neighbouring blocks of the grid with the same run of keys, which then pass from L2:
-// one behind the other they read memory 3.6 times over.
+// one behind the other they read memory 3.6 times over (645 us for 524, then).
+//
+// Measured (16 heads on 2, bf16): 32 sequences of 512 to 8192 with 32 nodes, heads
+// of 128, pages of 16: 58 us (22.2 by bytes, 19.1 by products; the warp-level kernel
+// for up to 128 rows took 225); 8 of 30k to 65k with 64 nodes, heads of 256: 338 us,
+// 1.18 PFLOP/s of 1.92 (985).
 template <int D_, int NQ_>
 struct WideCfg {
   using In = __nv_bfloat16;

@@ -133,7 +133,7 @@ struct QkNormArgs {
 };
 cudaError_t launch_qknorm_rope(const QkNormArgs &a, cudaStream_t stream);
 
-// Attention over a paged cache; see paged_attention.cu.
+// Attention over a paged cache; see attention.cuh.
 struct AttnArgs {
   KvLayout cache;
   const void *q, *k_cache, *v_cache;

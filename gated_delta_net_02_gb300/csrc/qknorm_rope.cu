@@ -6,7 +6,9 @@
 //
 // Bound by HBM: each element is read once and written once. The sum of a
 // head's squares, the norm and the rotation are in fp32, with one rounding at
-// the end.
+// the end. Measured on one GB300: 34739 tokens x (16 + 2 + 2) heads of 256, bf16, 64
+// rotated, 117 us (104.9 by bytes, 6.1 TB/s); 64 tokens x 20 x 128 11.6 us, of which the
+// host takes 9.
 #include "rope.cuh"
 
 namespace gdn {

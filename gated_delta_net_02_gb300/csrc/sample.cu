@@ -6,7 +6,10 @@
 //   token = first kept index, by index, whose running mass passes u * mass
 //
 // Bound by HBM: a row is read once; a cluster of up to 8 blocks holds it in
-// shared memory and makes all further passes there.
+// shared memory and makes all further passes there. Measured on one GB300 (bytes at
+// the copy rate in brackets): 64 rows of 131072 bf16, top k and top p 37.4 us (2.5);
+// 512 rows of 150001 fp32, top p and min p, 523 us (45.2): some 140 instructions a
+// logit, and a third of the time at barriers of blocks and clusters.
 //  * Masses decide between tokens by whole numbers: a weight is an integer in
 //    units of 2^-44 of (about) the largest, so a sum has the same value in any
 //    order, and with it the token. Logits lie on a grid of 2^-8 to 2^-7 octaves of
@@ -20,6 +23,8 @@
 //  * The first histogram of masses adds a weight as three numbers of 16 bits,
 //    by 32-bit atomics that are skipped where they are 0, as the upper ones
 //    mostly are; one 64-bit addition to shared memory is a loop.
+//  * The last bin's logits are listed while they are counted (and those before
+//    it, where a count left few), and later passes go by the list.
 //  * A bin is looked for in sums of 32 bins first, then in those 32: blocks read
 //    one another's shared memory slowly (all bins by all blocks took 6 us).
 #include <cuda_bf16.h>

@@ -11,7 +11,15 @@
 // product of 0, and no range of gates is out of reach.
 //
 // Bound by HBM: the first state is read once (the token loop with a slot for
-// each node would write as many states as there are nodes).
+// each node would write as many states as there are nodes). Heads of 128 x 128 on one
+// GB300 (bytes at the copy rate in brackets): 32 sequences x 16 heads x 8 nodes, bf16,
+// one decay a head 16.9 us (6.0); 64 x 32 x 32 nodes, a decay for each row of
+// the state, 153 us (42). From 34 and 981 with the state through the CUDA cores;
+// with it on the matrix instruction 186, with keys by asynchronous copies 157.
+// The rest is the chain in a block: words, products of keys, products with the
+// state, the levels of the tree (some 450 cycles each), and the dots along the
+// paths where decays have rows. The commit: 32 x 16 states of 8 nodes 14.5 us
+// (10.1), 128 x 32 of 32 nodes 107 (86.0).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

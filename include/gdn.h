@@ -601,8 +601,9 @@ gdn_status gdn_tree_commit(const gdn_shape *shape, const void *k, const float *g
  * others 0. A row with nothing above -infinity gives token -1, prob 0.
  * top_k <= 0, top_p >= 1, min_p <= 0 or NaN: no such limit.
  * Weights and masses are whole numbers of 2^-44 of the largest weight (a
- * weight is off by some 2^-40; below 2^-45 it is 0), so the result is the same
- * bits every time and its place between two tokens is that of 64-bit sums.
+ * weight is off by some 2^-30 of itself; below 2^-44.9 it is 0), so the result is
+ * the same bits every time and its place between two tokens is that of exact
+ * sums. Temperatures below 1e-30 count as 1e-30, those above 3e33 as 3e33.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int rows;             /* >= 0, at most 2^24 */

@@ -1,10 +1,11 @@
 """gdn_sample against its definition in 64 bits, row by row on the CPU.
 
-Tokens have to be equal: weights are off by some 2^-40 of the largest and their
-sums are exact, so a token differs from the definition's only where u * mass
-lies that near the edge between two tokens (for these inputs some 1e-6 of all
-rows). prob = w / mass: 2^-24 for its own rounding, 2^-38 for the weight (a few
-units of 2^-40), and what tokens below 2^-45 leave out of the mass, 2^18 x 2^-45 of it:
+Tokens have to be equal: weights are off by at most some 2^-29 of themselves and
+their sums are exact, so a token differs from the definition's only where u * mass
+lies that near the edge between two tokens (2^-29 of the mass for each of some
+1000 tokens with weight: 2e-6 of all rows). prob = w / mass: 2^-24 for its own
+rounding, 2^-28 for the weight and the mass, a unit of 2^-44 of the largest, and
+what tokens below 2^-44.9 leave out of the mass, 2^18 x 2^-44.9 of it (2^-26.9): less than
 2^-22 prob + 2^-38 in all."""
 import math
 

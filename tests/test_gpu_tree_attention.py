@@ -225,3 +225,12 @@ def test_captured_and_replayed(gdn):
         graph.replay()
         torch.cuda.synchronize()
         c.check(out)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,H", [(64, 40), (33, 96), (64, 640)])
+def test_more_blocks_of_rows_than_fit(gdn, D, T, H):
+    # one kv head: up to 40960 rows, more blocks of them than the GPU runs at once
+    c = TreeCase(gdn, [T + 70, 200, T], T, H, 1, D, 16, torch.bfloat16, seed=H,
+                 nodes=[T, T - 1, 1])
+    c.check(c.run())
