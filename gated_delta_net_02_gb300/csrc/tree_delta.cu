@@ -151,6 +151,24 @@ __device__ __forceinline__ void get(const float *p, float (&v)[N]) {
   }
 }
 
+// Two numbers to an instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, u, v;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\t"
+      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 w, u, v, w;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
 // Sizes of a block's shared memory, in bytes, for n nodes.
 template <typename T_, int DK_, int DV_, bool KDA_>
 struct Form {
@@ -386,22 +404,25 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
         for (int x = 0; x < 4; ++x) {
           const int j = left ? 63 - __clzll(left) : -1;
           js[x] = j;
-          float a = 0.f, b = 0.f;
+          float2 a = {0.f, 0.f}, b = a;
           if (j >= 0) {
             left &= ~(1ull << j);
             float kj[PER], aj[PER];
             get(raw_k + j * DK + lane * PER, kj);
             if constexpr (KDA) get(raw_a + j * DK + lane * PER, aj);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-              const float y = w[i] * kj[i];
-              a = fmaf(kt[i], y, a);
-              b = fmaf(qt[i], y, b);
-              w[i] *= KDA ? aj[i] : alpha[j];
+            for (int i = 0; i < PER; i += 2) {
+              float2 c = {w[i], w[i + 1]};
+              const float2 y = mul2(c, float2{kj[i], kj[i + 1]});
+              a = fma2(float2{kt[i], kt[i + 1]}, y, a);
+              b = fma2(float2{qt[i], qt[i + 1]}, y, b);
+              c = mul2(c, KDA ? float2{aj[i], aj[i + 1]} : float2{alpha[j], alpha[j]});
+              w[i] = c.x;
+              w[i + 1] = c.y;
             }
           }
-          sum[x] = a;
-          sum[4 + x] = b;
+          sum[x] = a.x + a.y;
+          sum[4 + x] = b.x + b.y;
         }
 #pragma unroll
         for (int half = 4; half; half >>= 1) {
@@ -443,9 +464,11 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   }
   __syncthreads();
 
-  // ---- S_0^T of the operands, 16 nodes at a time
+  // ---- S_0^T of the operands, 16 or 32 nodes at a time: GROUPS tiles of keys, then of
+  // queries
+  constexpr int GROUPS = TILES == 4 ? 2 : 1;
   const uint32_t op_s = smem_u32(op);
-  for (int c0 = 0; c0 < n; c0 += 16) {
+  for (int c0 = 0; c0 < n; c0 += 16 * GROUPS) {
     float acc[TILES][4][4] = {}, scale = 1.f;
     if (S) {
       if (c0 > 0) {
@@ -498,7 +521,9 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
         if (ks + AHEAD < KS) load(ks + AHEAD);
 #pragma unroll
         for (int m = 0; m < TILES; ++m) {
-          const uint32_t at = op_s + (c0 + m * NT + (lane & 15)) * F::PITCH +
+          const int g0 = c0 + m % GROUPS * 16;
+          if (GROUPS > 1 && g0 >= n) continue;
+          const uint32_t at = op_s + (g0 + m / GROUPS * NT + (lane & 15)) * F::PITCH +
                               (half * HALF + ks * 16 + (lane >> 4) * 8) * 2;
 #pragma unroll
           for (int pa = 0; pa < F::PARTS; ++pa) {
@@ -527,7 +552,7 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const int r = (lane >> 2) + 8 * y;
-            int t = c0 + r, is_q = m;
+            int t = c0 + m % GROUPS * 16 + r, is_q = m / GROUPS;
             if (TILES == 1) {
               is_q = r >= NT;
               t = is_q ? r - NT : r;
@@ -713,7 +738,9 @@ cudaError_t forward_tiles(const TreeParams &p, cudaStream_t stream) {
 }
 template <class F>
 cudaError_t forward(const TreeParams &p, cudaStream_t stream) {
-  return p.T <= 8 ? forward_tiles<F, 1>(p, stream) : forward_tiles<F, 2>(p, stream);
+  return p.T <= 8    ? forward_tiles<F, 1>(p, stream)
+         : p.T <= 16 ? forward_tiles<F, 2>(p, stream)
+                     : forward_tiles<F, 4>(p, stream);
 }
 
 template <typename T, int DK, int DV, bool KDA>
