@@ -14,8 +14,9 @@
 // each node would write as many states as there are nodes). Heads of 128 x 128 on one
 // GB300 (bytes at the copy rate in brackets): 32 sequences x 16 heads x 8 nodes, bf16,
 // one decay a head 16.9 us (6.0); 64 x 32 x 32 nodes, a decay for each row of
-// the state, 153 us (42). From 34 and 981 with the state through the CUDA cores;
-// with it on the matrix instruction 186, with keys by asynchronous copies 157.
+// the state, 139 us (42). From 34 and 981 with the state through the CUDA cores;
+// with it on the matrix instruction 186, with keys by asynchronous copies 157, with
+// 32 nodes at a time 147 (16 at a time read and split the state twice).
 // The rest is the chain in a block: words, products of keys, products with the
 // state, the levels of the tree (some 450 cycles each), and the dots along the
 // paths where decays have rows. The commit: 32 x 16 states of 8 nodes 14.5 us
@@ -105,20 +106,21 @@ __device__ __forceinline__ float inverse(float s) {
   return e == 254 ? 0x1p-127f : __int_as_float((254 - e) << 23);
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4 *u, float (&v)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float4 u = reinterpret_cast<const float4 *>(p)[i];
-    v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
+    for (int i = 0; i < 2; ++i) {
+      v[4 * i] = __uint_as_float(u[i].x); v[4 * i + 1] = __uint_as_float(u[i].y);
+      v[4 * i + 2] = __uint_as_float(u[i].z); v[4 * i + 3] = __uint_as_float(u[i].w);
+    }
   }
 }
 
@@ -543,7 +545,21 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
     }
     const float unscale = F::kPlain ? 1.f : inverse(scale);
     // a lane's 8 columns of rows lane / 4 and + 8: the halves of the state are added
-    // in turn
+    // in turn; the values come while the other half writes
+    constexpr int VL = 8 * (int)sizeof(T) / 16;
+    uint4 vs[GROUPS][2][VL];
+    if (half == 0) {
+#pragma unroll
+      for (int m = 0; m < GROUPS; ++m)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int t = min(c0 + m * 16 + (lane >> 2) + 8 * y, n - 1);
+          const uint4 *from =
+              reinterpret_cast<const uint4 *>(vt + t * v_step + col0 + (lane & 3) * 8);
+#pragma unroll
+          for (int i = 0; i < VL; ++i) vs[m][y][i] = from[i];
+        }
+    }
 #pragma unroll
     for (int turn = 1; turn >= 0; --turn) {
       if (half == turn) {
@@ -576,7 +592,7 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
               o[6] = (o[6] + u1.z) * w; o[7] = (o[7] + u1.w) * w;
               if (!is_q) {
                 float v[8];
-                load8(vt + t * v_step + c, v);
+                unpack8<T>(vs[m % GROUPS][y], v);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) o[i] = v[i] - o[i];
               }
