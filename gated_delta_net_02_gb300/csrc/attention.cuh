@@ -1417,11 +1417,13 @@ struct WideCfg {
   static constexpr int TILE = KT * D * 2, CC = TILE > 16384 ? TILE / 16384 : 1, UNIT = TILE / CC;
   static constexpr int KA = D / 64 / CC, KV = KT / CC;
   static constexpr int Q_BYTES = ROWS * D * 2;
-  static constexpr int U = 4;
-  static constexpr int SMEM = 2 * U * UNIT + Q_BYTES + 1024;
+  // places of the rings: a tile of heads of 256 is all four of K's, and a product starts
+  // with the first unit of V while the last is on its way
+  static constexpr int UK = 4, UV = D == 256 ? 6 : 4;
+  static constexpr int SMEM = (UK + UV) * UNIT + Q_BYTES + 1024;
   static constexpr int TCOLS = 512;  // sums, then two tiles of scores for each tile of rows
   static constexpr int PER_SM = 1;
-  static_assert(NQ * D + 256 <= TCOLS && U >= CC && SMEM <= 224 * 1024, "it fits");
+  static_assert(NQ * D + 256 <= TCOLS && UK >= CC && UV >= CC && SMEM <= 225 * 1024, "it fits");
 };
 
 __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, int c0, int c1,
@@ -1496,12 +1498,12 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     attn_wide_kernel(const AttnParams p, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, int box) {
   using T = __nv_bfloat16;
-  constexpr int D = C::D, KT = C::KT, NT = C::THREADS, U = C::U, NQ = C::NQ;
+  constexpr int D = C::D, KT = C::KT, NT = C::THREADS, NQ = C::NQ, UK = C::UK, UV = C::UV;
   constexpr int CH = D / 8, CC = C::CC, KA = C::KA, KV = C::KV;  // 16-byte chunks of a row; see WideCfg
   extern __shared__ unsigned char raw[];
   unsigned char *sm =
       reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full[2][U], empty[2][U];  // of K, of V
+  __shared__ uint64_t full[2][UV], empty[2][UV];  // of K, of V
   __shared__ uint64_t s_full[2 * NQ], p_full[2 * NQ], o_done[2 * NQ], o_free[NQ];
   __shared__ uint64_t q_full[NQ], landed, patched, over[2 * NQ];
   __shared__ long long warp_sum[NT / 32];
@@ -1512,13 +1514,17 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   // probabilities and V, 4 .. 4 + 4 NQ rows. A product's polls (some 200 cycles
   // each, of phases long over too) and the copies it waits for then hold up no other's.
   const bool scores = warp == 2 || warp == 12, sums = warp == 3 || warp == 13;
-  auto unit_at = [&](int v, int slot) { return (v * U + slot) * C::UNIT; };
-  const uint32_t units_s = smem_u32(sm), q_s = units_s + 2 * U * C::UNIT;
+  static_assert(UV >= UK, "places of either");
+  // unit u of K (of V): its place, there and in shared memory, and the round of the ring
+  auto slot_of = [](int v, int u) { return v ? u % UV : u % UK; };
+  auto round_of = [](int v, int u) { return v ? u / UV : u / UK; };
+  auto unit_at = [](int v, int slot) { return (v * UK + slot) * C::UNIT; };
+  const uint32_t units_s = smem_u32(sm), q_s = units_s + (UK + UV) * C::UNIT;
   const int items_per_seq = p.H_kv, RB = p.row_blocks.d;
   const int group = p.row_blocks.div(blockIdx.x), rb = blockIdx.x - group * RB;
   const int groups = p.row_blocks.div(gridDim.x), r0 = rb * C::ROWS;
   if (tid == 0) {
-    for (int i = 0; i < 2 * U; ++i) {
+    for (int i = 0; i < 2 * UV; ++i) {
       mbar_init(&full[0][0] + i, 1);
       mbar_init(&empty[0][0] + i, NQ);
     }
@@ -1561,22 +1567,22 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
     // the item's last tile is here, and ends inside a tile of V
     const int patch_from = len - (tile0 + n - 1) * KT;
     const bool patch = patch_from < KT;
-    // Tile t of K (of V) has arrived, and phase `phase` of `bar` is over.
-    auto wait_tile = [&](int v, int t, uint64_t *bar, int phase) {
+    // `count` units of K (of V) from u on have arrived, and phase `phase` of `bar` is over.
+    auto wait_units = [&](int v, int u0, auto count, uint64_t *bar, int phase) {
       bool all = false;
       for (uint32_t i = 0; i < kMaxPolls && !all; ++i) {
-        all = mbar_try_wait(bar, phase & 1);
+        all = !bar || mbar_try_wait(bar, phase & 1);
 #pragma unroll
-        for (int c = 0; c < CC; ++c) {
-          const int u = t * CC + c;
-          all &= mbar_try_wait(&full[v][u % U], (u / U) & 1);
-        }
+        for (int c = 0; c < count; ++c)
+          all &= mbar_try_wait(&full[v][slot_of(v, u0 + c)], round_of(v, u0 + c) & 1);
       }
       if (!all) set_error(p.err, kDevTimeout | (kSiteAttnTile << 8));
       all = __all_sync(0xffffffffu, all);
       tc_fence_after();
       return all;
     };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, CC> whole_tile;
     if (warp < 2) {
       const int v = warp;  // K, V
       if (v == 0 && lane == 0 && rb == 0) w.list_join(p, items_per_seq, n);
@@ -1614,8 +1620,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         }
 #pragma unroll 1
         for (int c = 0; c < CC; ++c) {
-          const int u = (tb + i) * CC + c, slot = u % U;
-          ok = ok && mbar_wait(&empty[v][slot], (u / U + 1) & 1, p.err, kSiteAttnTile);
+          const int u = (tb + i) * CC + c, slot = slot_of(v, u);
+          ok = ok && mbar_wait(&empty[v][slot], (round_of(v, u) + 1) & 1, p.err, kSiteAttnTile);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           bool mine[2];
@@ -1648,7 +1654,7 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         if (ok)
           for (int e = lane; e < (KT - from) * CH; e += 32) {
             const int key = from + e / CH, c = e % CH;
-            const int slot = ((tb + n - 1) * CC + key / KV) % U;
+            const int slot = slot_of(1, (tb + n - 1) * CC + key / KV);
             *reinterpret_cast<uint4 *>(sm + unit_at(1, slot) + (c >> 3) * (KV * 128) +
                                        key % KV * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
           }
@@ -1665,11 +1671,11 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         // in the place of the tile before the last, whose product is over (of the
         // first two: a phase before the first is over)
         const int b = 2 * q + (t & 1);
-        ok = wait_tile(0, t, &o_done[b], (t >> 1) + 1);
+        ok = wait_units(0, t * CC, whole_tile, &o_done[b], (t >> 1) + 1);
         if (!ok) break;
 #pragma unroll 1
         for (int c = 0; c < CC; ++c) {
-          const int slot = (t * CC + c) % U;
+          const int slot = slot_of(0, t * CC + c);
 #pragma unroll
           for (int ks = 0; ks < 4 * KA; ++ks)
             umma_bf16_elect(tm_score + b * KT,
@@ -1689,8 +1695,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 #pragma unroll 1
       for (int t = tb; t < tb + n && ok; ++t) {
         const int b = 2 * q + (t & 1);
-        ok = wait_tile(1, t, &p_full[b], t >> 1);
+        ok = wait_units(1, t * CC, one, &p_full[b], t >> 1);
         if (patch && t == tb + n - 1) {
+          ok = ok && wait_units(1, t * CC, whole_tile, nullptr, 0);
           if (ok && lane == 0) mbar_arrive(&landed);
           ok = ok && mbar_wait(&patched, patches & 1, p.err, kSiteAttnTile);
           ok = __all_sync(0xffffffffu, ok);
@@ -1698,7 +1705,11 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
         if (!ok) break;
 #pragma unroll 1
         for (int c = 0; c < CC; ++c) {
-          const int slot = (t * CC + c) % U;
+          const int slot = slot_of(1, t * CC + c);
+          if (c > 0) {
+            ok = wait_units(1, t * CC + c, one, nullptr, 0);
+            if (!ok) break;
+          }
 #pragma unroll
           for (int ks = 0; ks < KV / 16; ++ks)
             umma_bf16_ts_elect(tm + q * D, tm_score + b * KT + KT / 2 + (c * (KV / 16) + ks) * 8,
@@ -1886,8 +1897,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
   }
   if (any && !ok) {  // otherwise every copy and product has been waited for
     if (warp < 2)
-      for (int u = max(loaded - U, 0); u < loaded; ++u)
-        mbar_drain(&full[warp][u % U], (u / U) & 1);
+      for (int u = max(loaded - (warp ? UV : UK), 0); u < loaded; ++u)
+        mbar_drain(&full[warp][slot_of(warp, u)], round_of(warp, u) & 1);
     if (scores || sums) {
       const int i = 2 * (warp > 3) + sums;
       umma_commit_elect(&over[i]);
@@ -2178,7 +2189,7 @@ template <class C, bool TREE>
 cudaError_t launch_cfg(const AttnParams &p, const KvLayout &c, int grid, cudaStream_t stream) {
   cudaError_t e;
   if constexpr (C::kTensorMemory) {
-    static_assert(C::SMEM + 4 * 1024 <= 227 * 1024, "shared memory");
+    static_assert(C::SMEM + (kIsWide<C> ? 2 : 4) * 1024 <= 227 * 1024, "shared memory");
     const int box = box_of(c);
     CUtensorMap mk, mv;
     bool mapped;
