@@ -1394,15 +1394,17 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 // own: one that polls for all made 90 us of the 66. Lanes that poll alone, the rest
 // of the warp waiting, were slower yet (75).
 // A copy takes some 250 cycles to begin, whatever its size: a unit of V has all its
-// columns in one where pages allow (338 us for 447, below).
+// columns in one where pages allow (338 us for 447, the last case below).
 // The blocks of rows of an item (64 nodes x 8 heads of 256 are four) go to
 // neighbouring blocks of the grid with the same run of keys, which then pass from L2:
-// one behind the other they read memory 3.6 times over (645 us for 524, then).
+// one behind the other they read memory 3.6 times over (645 us for 524, then). Copies
+// shared by two of them (a cluster, each loading every other box for both) were
+// slower, 349 us for 327: each then waits for the other's places.
 //
 // Measured (16 heads on 2, bf16): 32 sequences of 512 to 8192 with 32 nodes, heads
-// of 128, pages of 16: 58 us (22.2 by bytes, 19.1 by products; the warp-level kernel
-// for up to 128 rows took 225); 8 of 30k to 65k with 64 nodes, heads of 256: 338 us,
-// 1.18 PFLOP/s of 1.92 (985).
+// of 128, pages of 16: 55 us (22.2 by bytes, 19.1 by products; the warp-level kernel
+// for up to 128 rows took 225); 8 of 30k to 65k with 64 nodes, heads of 256: 327 us,
+// 1.22 PFLOP/s of 1.92 (985).
 template <int D_, int NQ_>
 struct WideCfg {
   using In = __nv_bfloat16;
