@@ -234,3 +234,11 @@ def test_more_blocks_of_rows_than_fit(gdn, D, T, H):
     c = TreeCase(gdn, [T + 70, 200, T], T, H, 1, D, 16, torch.bfloat16, seed=H,
                  nodes=[T, T - 1, 1])
     c.check(c.run())
+
+
+@pytest.mark.parametrize("D,H", [(64, 4), (128, 4), (256, 3)])
+@pytest.mark.parametrize("scale", [-0.07, 1e-4])
+def test_scales_of_many_rows(gdn, D, H, scale):
+    c = TreeCase(gdn, [64, 700, 321, 130], 64, H, 1, D, 16, torch.bfloat16, words="any",
+                 nodes=[64, 50, 64, 1], scale=scale, seed=D)
+    c.check(c.run())
