@@ -1391,8 +1391,9 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 // probabilities of the tile before the last once the product that reads those is
 // over.
 // Every wait costs some 200 to 500 cycles, so each kind of work has a warp of its
-// own: one that polls for all made 90 us of the 66. Lanes that poll alone, the rest
-// of the warp waiting, were slower yet (75).
+// own (the first case below took 90 us with one warp for a tile's products and one
+// for all copies, 66 with these). Polls by one lane, the others of its warp waiting,
+// were slower (75).
 // A copy takes some 250 cycles to begin, whatever its size: a unit of V has all its
 // columns in one where pages allow (338 us for 447, the last case below).
 // The blocks of rows of an item (64 nodes x 8 heads of 256 are four) go to
