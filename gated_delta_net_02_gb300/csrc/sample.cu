@@ -65,6 +65,12 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float of_key(uint32_t k) {
   return __uint_as_float(k ^ ((int)k < 0 ? 0x80000000u : 0xffffffffu));
 }
+// The largest value below x. The key before 0's is no value's (it would be -0): the
+// largest negative number's is the one before that.
+__device__ __forceinline__ float below(float x) {
+  const uint32_t k = key_of(x) - 1;
+  return of_key(k == 0x7fffffffu ? 0x7ffffffeu : k);
+}
 
 __device__ __forceinline__ u64 ld_cluster_u64(const void *local, uint32_t rank) {
   u64 v;
@@ -652,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncthreads();
       const float least = sh.least;
       if (least > cut) {  // all of that value: what is below it goes
-        cut = of_key(key_of(least) - 1);
+        cut = below(least);
         ties = 0;
       }
     }
