@@ -14,15 +14,14 @@
 // each node would write as many states as there are nodes). Heads of 128 x 128 on one
 // GB300 (bytes at the copy rate in brackets): 32 sequences x 16 heads x 8 nodes, bf16,
 // one decay a head 16.9 us (6.0); 64 x 32 x 32 nodes, a decay for each row of
-// the state, 139 us (42). From 34 and 981 with the state through the CUDA cores;
-// with it on the matrix instruction 186, with keys by asynchronous copies 157, with
-// 32 nodes at a time 147 (16 at a time read and split the state twice).
+// the state, 152 us (42). From 34 and 981 with the state through the CUDA cores;
+// with it on the matrix instruction 186, with keys by asynchronous copies 157. 32
+// nodes are taken at a time: 16 would read and split the state twice.
 // The rest is the chain in a block: words, products of keys, products with the
 // state, the levels of the tree (some 450 cycles each), and the dots along the
 // paths where decays have rows. The commit: 32 x 16 states of 8 nodes 14.5 us
 // (10.1), 128 x 32 of 32 nodes 107 (86.0).
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include "kernels.h"
 #include "layer.cuh"
@@ -63,17 +62,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                             uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Two numbers as three bf16 parts each (8 bits of each number in turn: together
-// its 24), packed in pairs.
+// its 24, whatever the size of others), packed in pairs.
 __device__ __forceinline__ void split(float x, float y, uint32_t (&part)[3]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -81,29 +71,6 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&part)[3]) {
     x -= __uint_as_float(part[i] << 16);
     y -= __uint_as_float(part[i] & 0xffff0000u);
   }
-}
-// As two fp16 parts (11 bits in turn, in all 23 with the second's sign), of numbers
-// scaled to below 2^15: what the second cannot hold is below 2^-25.
-__device__ __forceinline__ void split(float x, float y, uint32_t (&part)[2]) {
-  const __half2 hi = __floats2half2_rn(x, y);
-  const float2 f = __half22float2(hi);
-  const __half2 lo = __floats2half2_rn(x - f.x, y - f.y);
-  part[0] = *reinterpret_cast<const uint32_t *>(&hi);
-  part[1] = *reinterpret_cast<const uint32_t *>(&lo);
-}
-// The power of two that takes the largest of a warp's finite numbers (m: the
-// largest size of this lane's) to 8 .. 16; 1 for zeros.
-__device__ __forceinline__ float scale_of(float m) {
-#pragma unroll
-  for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  if (m == 0.f) return 1.f;
-  return __int_as_float(min(254 + 3 - (__float_as_int(m) >> 23), 254) << 23);
-}
-__device__ __forceinline__ float finite(float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.f; }
-// 1 / s of a power of two, which may lie below the normal numbers.
-__device__ __forceinline__ float inverse(float s) {
-  const int e = __float_as_int(s) >> 23;
-  return e == 254 ? 0x1p-127f : __int_as_float((254 - e) << 23);
 }
 
 template <typename T>
@@ -178,10 +145,10 @@ struct Form {
   static constexpr int DK = DK_, DV = DV_;
   static constexpr bool KDA = KDA_;
   // rows of c k and c q: bf16 keys are their own operand (the scalar c is
-  // multiplied afterwards), against three bf16 parts of the state; otherwise two fp16
-  // parts against two
+  // multiplied afterwards), against the three parts of the state; otherwise three
+  // parts of their own against those
   static constexpr bool kPlain = sizeof(In) == 2 && !KDA;
-  static constexpr int PARTS = kPlain ? 1 : 2, STATE_PARTS = kPlain ? 3 : 2;
+  static constexpr int PARTS = kPlain ? 1 : 3;
   static constexpr int PITCH = DK * 2 + 16;  // of an operand's row: conflict-free ldmatrix
   static constexpr int UP = DV + 4;          // of a row of sums, in floats
   static constexpr int THREADS = DV * 2;     // a warp: 32 columns of one half of the rows
@@ -208,8 +175,11 @@ struct Form {
 //    multiplied on the way), and the operands c k and c q.
 //  * Then S_0^T (c k), S_0^T (c q): a warp takes 32 columns and half of the
 //    rows of the state, straight from memory into fragments (a lane's 16 bytes
-//    are one row's columns of four products), and splits it into parts that
-//    hold its 24 bits. Of products of parts all are kept whose size is above 2^-23.
+//    are one row's columns of four products), and splits each element into three
+//    bf16 parts that hold its own 24 bits: a sum is as exact beside large elements
+//    as without them. (Two fp16 parts under one scale for a warp's elements took 139
+//    us for 152 on the second case above, and lost what is small beside the largest.)
+//    Of a product's nine pairs of parts the three below 2^-23 of it are left out.
 //  * d then goes from the root downwards, nodes of one depth together; a warp
 //    has 16 columns, which need no other warp.
 // TILES: of 16 rows of the operands taken at once; 1 (up to 8 nodes): keys and
@@ -222,9 +192,7 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   constexpr bool KDA = F::KDA;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ u64 words[64];
-  // what a node's sums with the state are multiplied by: bf16 keys by c, others by
-  // what undoes their rows' scales
-  __shared__ float root[2][64], beta[64], alpha[64];
+  __shared__ float root[64], beta[64], alpha[64];  // root: bf16 keys' c(t)
   __shared__ int depth[64], order[64], level_end[65], bad;
   __shared__ alignas(4) unsigned char path[64][64];  // ancestors, the parent first
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -276,7 +244,9 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   n = min(max(n, 0), NT);
   // the state's first fragments to registers, the rest to L2
   constexpr int COLS = DV / 32, HALF = DK / 2, KS = HALF / 16;
-  constexpr int AHEAD = TILES == 1 ? KS : 2;  // steps of the state in registers
+  // Steps of the state in registers. Where 32 nodes meet operands in parts, a second
+  // one makes a lane spill (64 x 32 x 32 nodes, fp32, row gates: 185 us, 170 with one).
+  constexpr int AHEAD = TILES == 1 ? KS : TILES == 4 && !F::kPlain ? 1 : 2;
   const int col0 = warp % COLS * 32, half = warp / COLS;
   if (S) S += (long long)h * DK * DV;
   const float *mine = S ? S + (long long)(half * HALF + (lane & 3) * 2) * DV + col0 + (lane >> 2) * 4
@@ -386,7 +356,7 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
           w *= a[i];
         }
       }
-      root[0][tid] = root[1][tid] = w;
+      root[tid] = w;
     }
   } else {
     // one path a warp
@@ -444,23 +414,15 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
       // the operands: c k and c q in parts
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        float y[PER], m = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          y[i] = (x ? qt[i] : kt[i]) * w[i];
-          m = fmaxf(m, finite(y[i]));
-        }
-        const float scale = scale_of(m);
 #pragma unroll
         for (int i = 0; i < PER; i += 2) {
-          uint32_t part[2];
-          split(y[i] * scale, y[i + 1] * scale, part);
+          uint32_t part[3];
+          split((x ? qt[i] : kt[i]) * w[i], (x ? qt[i + 1] : kt[i + 1]) * w[i + 1], part);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < 3; ++k)
             *reinterpret_cast<uint32_t *>(op + k * op_bytes + (x * NT + t) * F::PITCH +
                                           (lane * PER + i) * 2) = part[k];
         }
-        if (lane == 0) root[x][t] = inverse(scale);
       }
     }
   }
@@ -471,7 +433,7 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
   constexpr int GROUPS = TILES == 4 ? 2 : 1;
   const uint32_t op_s = smem_u32(op);
   for (int c0 = 0; c0 < n; c0 += 16 * GROUPS) {
-    float acc[TILES][4][4] = {}, scale = 1.f;
+    float acc[TILES][4][4] = {};
     if (S) {
       if (c0 > 0) {
 #pragma unroll
@@ -479,39 +441,9 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
       }
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        float4 (&xs)[4] = x[ks % AHEAD];
-        if constexpr (!F::kPlain) {
-          // numbers up to 2^15 after scaling; the scale follows the state's size
-          float m = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            m = fmaxf(fmaxf(m, fmaxf(fabsf(xs[i].x), fabsf(xs[i].y))),
-                      fmaxf(fabsf(xs[i].z), fabsf(xs[i].w)));
-          if (__any_sync(0xffffffffu, ks == 0 || !(m * scale < 32768.f))) {
-            m = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              m = fmaxf(fmaxf(m, fmaxf(finite(xs[i].x), finite(xs[i].y))),
-                        fmaxf(finite(xs[i].z), finite(xs[i].w)));
-            const float next = scale_of(m);
-            if (ks == 0 || next < scale) {
-              const float f = ks == 0 ? 1.f : next * inverse(scale);
-              scale = next;
-#pragma unroll
-              for (int t = 0; t < TILES; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) acc[t][i][y] *= f;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            xs[i].x *= scale; xs[i].y *= scale; xs[i].z *= scale; xs[i].w *= scale;
-          }
-        }
+        const float4 (&xs)[4] = x[ks % AHEAD];
         // column product i, k pair y: parts
-        uint32_t b[4][2][F::STATE_PARTS];
+        uint32_t b[4][2][3];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
           const float4 &lo = xs[2 * y], &hi = xs[2 * y + 1];
@@ -532,18 +464,14 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
             uint32_t a[4];
             ldsm4(a, at + pa * op_bytes);
 #pragma unroll
-            for (int pb = 0; pb < F::STATE_PARTS; ++pb) {
+            for (int pb = 0; pb < 3 - pa; ++pb) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if constexpr (F::kPlain) mma16816(acc[m][i], a, b[i][0][pb], b[i][1][pb]);
-                else if (pa + pb < 2) mma16816_f16(acc[m][i], a, b[i][0][pb], b[i][1][pb]);
-              }
+              for (int i = 0; i < 4; ++i) mma16816(acc[m][i], a, b[i][0][pb], b[i][1][pb]);
             }
           }
         }
       }
     }
-    const float unscale = F::kPlain ? 1.f : inverse(scale);
     // a lane's 8 columns of rows lane / 4 and + 8: the halves of the state are added
     // in turn; the values come while the other half writes
     constexpr int VL = 8 * (int)sizeof(T) / 16;
@@ -579,12 +507,12 @@ __global__ void __launch_bounds__(F::THREADS, 2) tree_forward_kernel(const TreeP
             float o[8];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              o[i] = acc[m][i][2 * y] * unscale;
-              o[4 + i] = acc[m][i][2 * y + 1] * unscale;
+              o[i] = acc[m][i][2 * y];
+              o[4 + i] = acc[m][i][2 * y + 1];
             }
             float4 *d4 = reinterpret_cast<float4 *>(dst);
             if (turn == 0) {
-              const float w = root[is_q][t];
+              const float w = F::kPlain ? root[t] : 1.f;
               const float4 u0 = d4[0], u1 = d4[1];
               o[0] = (o[0] + u0.x) * w; o[1] = (o[1] + u0.y) * w;
               o[2] = (o[2] + u0.z) * w; o[3] = (o[3] + u0.w) * w;
