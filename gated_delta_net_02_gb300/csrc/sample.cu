@@ -434,7 +434,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     // less the largest, all that have weight are exact
     grid.from = fabsf(top) > 32.f * sh.depth ? top : 0.f;
     grid.magic = 12582912.f * sh.step;
-    grid.low = top - sh.depth;
+    // upwards: rounded down it could admit the logit before the largest, further than
+    // the table's octaves below it, or -inf
+    grid.low = __fsub_ru(top, sh.depth);
     grid.top = __float_as_int(__fadd_rd(top - grid.from, grid.magic));
     grid.ln_step = sh.ln_step;
     grid.coarse = sh.coarse;
