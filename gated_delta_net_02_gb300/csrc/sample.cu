@@ -208,7 +208,7 @@ struct Shared {
   alignas(16) uint32_t warp_ties[kWarps];
   float top, step, ln_step, least;
   float depth;             // logits from the largest to weight 0
-  double min_drop;         // temperature * log(min_p)
+  double min_drop;         // t * log(min_p)
   float warp_top[kWarps];
   int found, listed;
   u64 before, there, goal, total;
@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     share.queue = sh.queue[warp];
   }
   const float temperature = p.temperature ? p.temperature[r] : 1.f;
+  const float t = fminf(fmaxf(temperature, 1e-30f), 3e33f);  // as weights count it
   const float top_p = p.top_p ? p.top_p[r] : 1.f, min_p = p.min_p ? p.min_p[r] : 0.f;
   const int top_k = p.top_k ? p.top_k[r] : 0;
   const float u = p.uniform[r];
@@ -349,9 +350,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   // 64-bit floating point is two operations a cycle of an SM, and slow to
   // return: where it is needed, one thread does it.
   if (tid == 0) {
-    // octaves of weight for each unit of logit, log2(e) / temperature, as the sum
-    // of two floats; steps stay inside fp32's range
-    const float t = fminf(fmaxf(temperature, 1e-30f), 3e33f);
+    // octaves of weight for each unit of logit, log2(e) / t, as the sum of two
+    // floats; steps stay inside fp32's range
     const float c = 1.442695041f / t;
     const float c_lo = (fmaf(-c, t, 1.442695041f) + 1.925963033e-8f) / t;
     const int e = (__float_as_int(c) >> 23) - 127;
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   if (tid == kThreads - 1 && min_p > 0.f)
-    sh.min_drop = (double)fminf(temperature, 3e33f) * log((double)min_p);
+    sh.min_drop = (double)t * log((double)min_p);
   __syncthreads();
   if (tid < kCoarse + kFine) {
     const int i = tid < kCoarse ? tid * kFine : tid - kCoarse;

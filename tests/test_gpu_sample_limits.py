@@ -76,3 +76,14 @@ def test_the_lowest_numbers_beside_minus_infinity(gdn, more):
         got = run(gdn, x, temperature=torch.full((4,), t), u=torch.tensor([0.1, 0.5, 0.9, 0.3]),
                   check=t <= 3e33, **args)
         assert bool((x[torch.arange(4), got[0].long()] > -math.inf).all())
+
+
+def test_min_p_with_temperatures_that_count_as_the_least(gdn):
+    # 1e-35 counts as 1e-30 for the weights and for min_p's bound alike
+    x = torch.tensor([[0.0, -1e-31, -5e-31, -2e-30, -1.0],
+                      [-1e-31, -3e-31, 0.0, -8e-31, -1e-30]], device="cuda").repeat(6, 1)
+    m = torch.full((12,), 0.5)
+    u = torch.linspace(0.0, 0.99, 12)
+    want = run(gdn, x, temperature=torch.full((12,), 1e-30), min_p=m, u=u)
+    got = run(gdn, x, temperature=torch.full((12,), 1e-35), min_p=m, u=u, check=False)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
