@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(32 * kMostWarps)
           mbar_drain(&full[i % kStages], (i / kStages) & 1);
       break;
     }
+    __syncwarp();  // a vote orders no memory: other lanes read the sines stored above
     unsigned char *st = smem + s * stage;
     // H heads of each token of the unit, from its h0-th on.
     auto norm_rows = [&](int h0, int H, const FastDiv &by_H, const void *weight, const uint4 (&w)[2]) {
