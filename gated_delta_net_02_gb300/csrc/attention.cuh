@@ -1404,8 +1404,8 @@ __global__ void __launch_bounds__(C::THREADS, C::PER_SM)
 //
 // Measured (16 heads on 2, bf16): 32 sequences of 512 to 8192 with 32 nodes, heads
 // of 128, pages of 16: 55 us (22.2 by bytes, 19.1 by products; the warp-level kernel
-// for up to 128 rows took 225); 8 of 30k to 65k with 64 nodes, heads of 256: 327 us,
-// 1.22 PFLOP/s of 1.92 (985).
+// for up to 128 rows took 225); 8 of 30k to 65k with 64 nodes, heads of 256: 331 us,
+// 1.20 PFLOP/s of 1.92 (985).
 template <int D_, int NQ_>
 struct WideCfg {
   using In = __nv_bfloat16;
@@ -2075,6 +2075,12 @@ auto with_rows(int rows, int box, F f) {
   if constexpr (sizeof(T) == 2) {
     if (rows <= 16) return f(Cfg<T, D, 1>{});
     if constexpr (TREE) {
+      // us, 64 sequences of 512 to 8192 (D = 256: to 4096), 2 kv heads, pages of 16 and
+      // 64 tokens; what follows below in brackets. 72, 128 and 256 rows: D = 64 42 and
+      // 40 (80, 76), 37 and 40 (73, 80), 61 and 50 (160, 127); D = 128 53 and 48 (241,
+      // 203), 52 and 56 (163, 173), 71 and 68 (294, 260); D = 256 59 and 61 (150, 166),
+      // 67 and 65 (127, 135), 98 and 92 (229, 235). Pages without a box (24, 100 or 7
+      // tokens), D = 128, 256 rows: 217 to 235, by the warp-level kernel; fp32 1290.
       if (box && rows > 128) return f(WideCfg<D, D == 256 ? 1 : 2>{});
       if (box && rows > 64) return f(WideCfg<D, 1>{});
     }

@@ -8,7 +8,9 @@
 // Bound by HBM as long as a kv head has few rows (nodes x query heads), by the
 // products beyond some 280 (4 rows D flops for 4 D bytes). Up to 64 rows take the
 // kernels of a line of tokens, with the word as their mask; more rows in bf16
-// attn_wide_kernel (attention.cuh, where both stand with what they measured).
+// attn_wide_kernel, where boxes of a tensor map fit the pages (tokens of a page a
+// multiple of 64, or 8, 16 or 32); what is left, and fp32, the warp-level kernel
+// (attention.cuh, where all stand with what they measured).
 #include "attention.cuh"
 
 namespace gdn {

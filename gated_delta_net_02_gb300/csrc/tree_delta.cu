@@ -14,7 +14,7 @@
 // each node would write as many states as there are nodes). Heads of 128 x 128 on one
 // GB300 (bytes at the copy rate in brackets): 32 sequences x 16 heads x 8 nodes, bf16,
 // one decay a head 16.9 us (6.0); 64 x 32 x 32 nodes, a decay for each row of
-// the state, 152 us (42). From 34 and 981 with the state through the CUDA cores;
+// the state, 151 us (42). From 34 and 981 with the state through the CUDA cores;
 // with it on the matrix instruction 186, with keys by asynchronous copies 157. 32
 // nodes are taken at a time: 16 would read and split the state twice.
 // The rest is the chain in a block: words, products of keys, products with the
@@ -98,6 +98,8 @@ template <int BYTES>
 __device__ __forceinline__ void prefetch_l2(const void *p) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "n"(BYTES));
 }
+// Blocks that run at a time: two of an SM, one beyond some 40 nodes with operands in
+// parts. (There 152 instead measured the same: 32 x 32 x 64 nodes 242 us.)
 constexpr int kBlocksAtOnce = 2 * 152;
 
 // N consecutive elements of shared memory as fp32.
@@ -178,7 +180,7 @@ struct Form {
 //    are one row's columns of four products), and splits each element into three
 //    bf16 parts that hold its own 24 bits: a sum is as exact beside large elements
 //    as without them. (Two fp16 parts under one scale for a warp's elements took 139
-//    us for 152 on the second case above, and lost what is small beside the largest.)
+//    us for 151 on the second case above, and lost what is small beside the largest.)
 //    Of a product's nine pairs of parts the three below 2^-23 of it are left out.
 //  * d then goes from the root downwards, nodes of one depth together; a warp
 //    has 16 columns, which need no other warp.

@@ -529,6 +529,8 @@ size_t gdn_tree_attention_workspace_size(const gdn_attn_shape *shape, const gdn_
  * shape->T    nodes of each sequence, at most 64
  * n_nodes out of range is cut to it and reported as GDN_ERR_DEVICE_ARG by
  * gdn_check_device_error.
+ * Any page size is taken; for bf16 and more than 64 rows of a kv head (T x H / H_kv),
+ * pages of 8, 16, 32 or a multiple of 64 tokens are some 3 times as fast as others.
  */
 gdn_status gdn_tree_attention(const gdn_attn_shape *shape, const gdn_kv_cache *cache,
                               const void *q, const void *k_cache, const void *v_cache,
@@ -543,8 +545,10 @@ gdn_status gdn_tree_attention(const gdn_attn_shape *shape, const gdn_kv_cache *c
  * (decay as gdn_forward). No state is written: o and d follow from state_in,
  * the keys of the ancestors and their d, and gdn_tree_commit forms the one
  * state that is wanted from the d once a branch is accepted. All products and
- * sums are as exact as fp32 ones, for bf16 inputs too; any gate is computed,
- * -inf included.
+ * sums are as exact as fp32 ones, for bf16 inputs too, whatever the size of the
+ * state's other elements; any gate is computed, -inf included. An element of the
+ * state, or of a key or query times its decays, that is not finite or above 3.38e38
+ * makes the sums that it enters NaN.
  * shape       as gdn_forward, T = nodes of each sequence, at most 64
  * q, k, v, g, beta, state_in  as gdn_forward (token s*T+t is node t)
  * n_nodes     device int32 [n_seqs], or NULL
@@ -569,7 +573,9 @@ gdn_status gdn_tree_forward(const gdn_shape *shape, const void *q, const void *k
  * and tree as gdn_tree_forward's and the updates that it wrote:
  *   S = state_in, then for each ancestor of the leaf and the leaf in turn
  *   S = decay(S) + k d^T
- * leaf        device int32 [n_seqs]; -1: no node, the state is state_in
+ * leaf        device int32 [n_seqs], one of the nodes that the sequence has; -1: no
+ *             node, the state is state_in. (n_nodes is not given: a leaf in the
+ *             padding is reported only where its word could be no node's.)
  * state_out   device fp32 [n_seqs][H][D_k][D_v]. state_in[s] may be the place
  *             of sequence s in it (in place); any other overlap is reported as
  *             GDN_ERR_DEVICE_ARG and that sequence's state is not written.
